@@ -1,4 +1,5 @@
-"""ctypes loader for ``libkda.so`` (the C ABI of include/kda.h).
+"""ctypes loader for ``libkda.so`` (the C ABI of include/kda.h and
+include/kda_layer.h).
 
 The library is built in-tree by ``python -m gated_delta_rule_81_amd.build``.
 There is no fallback: if the library is missing, every call raises.
@@ -50,6 +51,26 @@ SIGNATURES = {
     "kda_abi_version": ([], ctypes.c_int),
 }
 
+# The operators around the recurrence: include/kda_layer.h, in its order.
+_f32 = ctypes.c_float
+LAYER_SIGNATURES = {
+    "kda_short_conv_fwd": ([_vp, _fp, _fp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i64, _i64,
+                            _i32, _i32, _i32, _vp], ctypes.c_int),
+    "kda_short_conv_bwd": ([_vp, _fp, _fp, _vp, _vp, _vp, _vp, _vp, _fp, _fp, _vp, _i32, _i32,
+                            _i32, _i32, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _i64, _vp],
+                           ctypes.c_int),
+    "kda_short_conv_bwd_workspace_size": ([_i32, _i32, _i32, _i32], _i64),
+    "kda_short_conv_step": ([_vp, _fp, _fp, _vp, _vp, _i32, _i32, _i32, _i64, _i64, _i32, _i32,
+                             _vp], ctypes.c_int),
+    "kda_qk_norm_fwd": ([_vp, _vp, _fp, _fp, _fp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+                         _i32, _i64, _i64, _i64, _i64, _f32, _i32, _i32, _i32, _vp],
+                        ctypes.c_int),
+    "kda_qk_norm_bwd": ([_vp, _vp, _fp, _fp, _fp, _vp, _vp, _vp, _vp, _vp, _fp, _fp, _i32, _i32,
+                         _i32, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _f32, _i32,
+                         _i32, _i32, _vp, _i64, _vp], ctypes.c_int),
+    "kda_qk_norm_bwd_workspace_size": ([_i32, _i32, _i32, _i32], _i64),
+}
+
 _lib = None
 
 
@@ -71,7 +92,7 @@ def lib():
                 f"{LIB_PATH} is not built; run `python -m gated_delta_rule_81_amd.build`")
         import torch  # noqa: F401
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in SIGNATURES.items():
+        for name, (args, res) in {**SIGNATURES, **LAYER_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = res

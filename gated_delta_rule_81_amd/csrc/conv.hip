@@ -1,0 +1,484 @@
+// conv.hip -- short depthwise causal convolution: forward, backward and the
+// single-token step.
+//
+//   z[t] = bias + sum_j w[j] r[t - (W-1) + j],  out = z or z sigmoid(z),
+//
+// with r = the sequence's rows and, before them, its state's W - 1 rows.  Every
+// value is read once and written once with about 2 W operations in between, so
+// HBM bounds all three.  A lane keeps VEC neighbouring channels and walks a
+// run of tokens with the last W - 1 rows in registers; a wave therefore reads
+// and writes whole 1 KiB pieces of a row, and the only rows read twice are the
+// W - 1 before each run.  Sequence boundaries inside a run are a wave-uniform
+// branch per token that reloads the window from the next sequence's state.
+#include "layer_device.h"
+
+namespace kda {
+namespace {
+
+constexpr int kWaves = 4;  // runs of one workgroup (one per wave)
+
+// Row `r` of the sequence that begins at token `beg`, as floats: a token's, or
+// row r - beg + W - 1 of the sequence's state for the W - 1 rows before it.
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void seq_row(const T *x, int64_t xs, const T *state0, int64_t n, int C,
+                                        int c, int r, int beg, float (&f)[VEC]) {
+    typedef Row<T, VEC> R;
+    if (r >= beg) {
+        R::get(R::raw(x + (int64_t)r * xs + c), f);
+    } else if (state0) {
+        R::get(R::raw(state0 + (n * (W - 1) + (r - beg + W - 1)) * (int64_t)C + c), f);
+    } else {
+        R::get(R::zero(), f);
+    }
+}
+
+// The channels' taps and biases, in 16-byte pieces where VEC allows.
+template <int VEC, int W>
+__device__ __forceinline__ void load_params(const ConvArgs &a, int c, float (&w)[W][VEC],
+                                            float (&b)[VEC]) {
+    const float *wp = a.weight + (int64_t)c * W;
+    if constexpr (VEC % 4 == 0) {
+        f32x4 v[VEC * W / 4];
+#pragma unroll
+        for (int i = 0; i < VEC * W / 4; ++i) v[i] = *reinterpret_cast<const f32x4 *>(wp + 4 * i);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = v[(i * W + j) / 4][(i * W + j) % 4];
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+            const f32x4 q = a.bias ? *reinterpret_cast<const f32x4 *>(a.bias + c + i) : zero4();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[i + e] = q[e];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = wp[i * W + j];
+            b[i] = a.bias ? a.bias[c + i] : 0.f;
+        }
+    }
+}
+
+// A workgroup is 64 channel vectors x kWaves runs of `run` tokens; workgroups
+// at and past `run_blocks` copy the final states, kWaves rows each.
+template <typename T, int VEC, int W>
+__global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs a, int cblocks,
+                                                               int run_blocks, int run) {
+    typedef Row<T, VEC> R;
+    constexpr int U = 8;  // rows in flight
+    const T *x = static_cast<const T *>(a.x), *state0 = static_cast<const T *>(a.state0);
+    const int C = a.channels;
+    const int c = ((int)(blockIdx.x % cblocks) * 64 + (int)threadIdx.x) * VEC;
+    if (c >= C) return;
+    const int64_t blk = blockIdx.x / cblocks;
+    if (blk >= run_blocks) {
+        const int64_t unit = (blk - run_blocks) * kWaves + threadIdx.y;
+        const int64_t n = unit / (W - 1);
+        const int j = (int)(unit % (W - 1));
+        if (n >= a.seqs.num) return;
+        const int beg = (int)seq_first_token(a.seqs.cu, a.seqs.seq_len, a.seqs.total, (int)n);
+        int end = seq_end_token(a.seqs, (int)n);
+        end = end < beg ? beg : end;
+        float f[VEC];
+        // row j of the last W - 1 of (state, x)
+        seq_row<T, VEC, W>(x, a.x_stride, state0, n, C, c, end - (W - 1) + j, beg, f);
+        R::put(static_cast<T *>(a.final_state) + (n * (W - 1) + j) * (int64_t)C + c, f);
+        return;
+    }
+    const int64_t first = (blk * kWaves + threadIdx.y) * (int64_t)run;
+    if (first >= a.seqs.total) return;
+    const int t0 = (int)first;
+    const int t1 = first + run < a.seqs.total ? (int)(first + run) : a.seqs.total;
+    T *out = static_cast<T *>(a.out);
+
+    float w[W][VEC], b[VEC], win[W][VEC];  // win: rows t - (W-1) .. t
+    load_params<VEC, W>(a, c, w, b);
+    int beg = 0, end = t0, n = -1;
+    for (int t = t0; t < t1; t += U) {
+        typename R::vec raw[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            raw[i] = t + i < t1 ? R::raw(x + (int64_t)(t + i) * a.x_stride + c) : R::zero();
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int tt = t + i;
+            if (tt >= t1) break;
+            if (tt >= end) {  // a sequence begins here, or the run does
+                n = seq_of_token(a.seqs, tt, &beg, &end);
+                if (n < 0) {
+                    end = tt + 1;
+                    continue;
+                }
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+                    seq_row<T, VEC, W>(x, a.x_stride, state0, n, C, c, tt - (W - 1) + j, beg,
+                                       win[j]);
+            }
+            R::get(raw[i], win[W - 1]);
+            float y[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float z = b[e];
+#pragma unroll
+                for (int j = 0; j < W; ++j) z += w[j][e] * win[j][e];
+                y[e] = a.silu ? z * sigmoid(z) : z;
+            }
+            R::put(out + (int64_t)tt * a.out_stride + c, y);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+        }
+    }
+}
+
+// d(out)/dz times d_out, from the window ending at the token.
+template <int VEC, int W>
+__device__ __forceinline__ void grad_z(const float (&w)[W][VEC], const float (&b)[VEC],
+                                       const float (&win)[W][VEC], bool silu, float (&g)[VEC]) {
+    if (!silu) return;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        float z = b[e];
+#pragma unroll
+        for (int j = 0; j < W; ++j) z += w[j][e] * win[j][e];
+        const float s = sigmoid(z);
+        g[e] *= s * (1.f + z * (1.f - s));
+    }
+}
+
+// dz[t] = d_out act'(z); dx[s] = sum_j w[j] dz[s + (W-1) - j] over its own
+// sequence (+ d_final for the last W - 1 rows); dw[j] = sum_t dz[t] r[t-(W-1)+j].
+// A run emits dx of its own tokens, so it walks W - 1 tokens past its end (dz
+// only); dw and db of the run go to the workgroup's row of `partial`
+// ([row][W + 1][C]), summed afterwards in row order.
+template <typename T, int VEC, int W>
+__global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int cblocks,
+                                                               int run_blocks, int run) {
+    typedef Row<T, VEC> R;
+    constexpr int U = 4;
+    __shared__ float sum[kWaves - 1][W + 1][VEC][64];
+    const T *x = static_cast<const T *>(a.x), *state0 = static_cast<const T *>(a.state0);
+    const T *dy = static_cast<const T *>(a.d_out), *d_final = static_cast<const T *>(a.d_final);
+    const int C = a.channels;
+    const int c = ((int)(blockIdx.x % cblocks) * 64 + (int)threadIdx.x) * VEC;
+    const bool on = c < C;
+    const int64_t blk = blockIdx.x / cblocks;
+    float w[W][VEC], b[VEC];
+    if (on) load_params<VEC, W>(a, c, w, b);
+
+    if (blk >= run_blocks) {  // gradient of the initial states: kWaves sequences each
+        const int64_t n = (blk - run_blocks) * kWaves + threadIdx.y;
+        if (!on || n >= a.seqs.num) return;
+        const int beg = (int)seq_first_token(a.seqs.cu, a.seqs.seq_len, a.seqs.total, (int)n);
+        int end = seq_end_token(a.seqs, (int)n);
+        const int len = end < beg ? 0 : end - beg;
+        float dz[W - 1][VEC];  // of the first W - 1 tokens
+#pragma unroll
+        for (int t = 0; t < W - 1; ++t) {
+            R::get(R::zero(), dz[t]);
+            if (t < len) {
+                float win[W][VEC];
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    seq_row<T, VEC, W>(x, a.x_stride, state0, n, C, c, beg + t - (W - 1) + j, beg,
+                                       win[j]);
+                R::get(R::raw(dy + (int64_t)(beg + t) * a.d_out_stride + c), dz[t]);
+                grad_z<VEC, W>(w, b, win, a.silu, dz[t]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            float g[VEC];
+            R::get(R::zero(), g);
+            if (d_final && j >= len)  // this row is still there in the final state
+                R::get(R::raw(d_final + (n * (W - 1) + (j - len)) * (int64_t)C + c), g);
+#pragma unroll
+            for (int i = 0; i <= j; ++i)  // tap i of token j - i
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) g[e] += w[i][e] * dz[j - i][e];
+            R::put(static_cast<T *>(a.d_state0) + (n * (W - 1) + j) * (int64_t)C + c, g);
+        }
+        return;
+    }
+
+    const int64_t first = (blk * kWaves + threadIdx.y) * (int64_t)run;
+    float dw[W][VEC], db[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        db[e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
+    }
+    if (on && first < a.seqs.total) {
+        const int t0 = (int)first;
+        const int t1 = first + run < a.seqs.total ? (int)(first + run) : a.seqs.total;
+        const int t2 = t1 + (W - 1) < a.seqs.total ? t1 + (W - 1) : a.seqs.total;
+        T *dx = static_cast<T *>(a.dx);
+        float win[W][VEC], dz[W][VEC];  // dz: of tokens t - (W-1) .. t
+        int beg = 0, end = t0, n = -1;
+
+        // dx of token s, whose dz window begins at s
+        auto emit = [&](int s, int row) {
+            float g[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) g[e] = 0.f;
+            if (row >= 0 && d_final)
+                R::get(R::raw(d_final + ((int64_t)n * (W - 1) + row) * C + c), g);
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) g[e] += w[W - 1 - i][e] * dz[i][e];
+            R::put(dx + (int64_t)s * a.dx_stride + c, g);
+        };
+        auto shift = [&]() {
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) dz[i][e] = dz[i + 1][e];
+        };
+        // the last W - 1 rows of the sequence that ends: no dz behind it
+        auto flush = [&]() {
+            for (int k = 0; k < W - 1; ++k) {
+                shift();
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) dz[W - 1][e] = 0.f;
+                const int s = end - (W - 1) + k;
+                if (s >= beg && s >= t0 && s < t1) emit(s, k);
+            }
+        };
+
+        bool done = false;
+        for (int t = t0; t < t2 && !done; t += U) {
+            typename R::vec rx[U], rg[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const bool in = t + i < t2;
+                rx[i] = in ? R::raw(x + (int64_t)(t + i) * a.x_stride + c) : R::zero();
+                rg[i] = in ? R::raw(dy + (int64_t)(t + i) * a.d_out_stride + c) : R::zero();
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int tt = t + i;
+                if (tt >= t2 || done) break;
+                if (tt >= end) {
+                    if (n >= 0) flush();
+                    if (tt >= t1) {  // what follows is another sequence's
+                        n = -1;
+                        done = true;
+                        break;
+                    }
+                    n = seq_of_token(a.seqs, tt, &beg, &end);
+                    if (n < 0) {
+                        end = tt + 1;
+                        continue;
+                    }
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j)
+                        seq_row<T, VEC, W>(x, a.x_stride, state0, n, C, c, tt - (W - 1) + j, beg,
+                                           win[j]);
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) dz[j][e] = 0.f;
+                }
+                if (n < 0) continue;
+                R::get(rx[i], win[W - 1]);
+                shift();
+                R::get(rg[i], dz[W - 1]);
+                grad_z<VEC, W>(w, b, win, a.silu, dz[W - 1]);
+                if (tt < t1) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        db[e] += dz[W - 1][e];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j][e] += dz[W - 1][e] * win[j][e];
+                    }
+                }
+                const int s = tt - (W - 1);
+                if (s >= beg && s >= t0) emit(s, -1);
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+            }
+        }
+        // the walk ended where its sequence does (t2 = total, or the next begins at t2)
+        if (!done && n >= 0 && end <= t2) flush();
+    }
+    if (threadIdx.y > 0) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            sum[threadIdx.y - 1][W][e][threadIdx.x] = db[e];
+#pragma unroll
+            for (int j = 0; j < W; ++j) sum[threadIdx.y - 1][j][e][threadIdx.x] = dw[j][e];
+        }
+    }
+    __syncthreads();
+    if (threadIdx.y == 0 && on) {
+        float *p = a.partial + blk * (W + 1) * (int64_t)C + c;
+#pragma unroll
+        for (int j = 0; j <= W; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float v = j < W ? dw[j][e] : db[e];
+#pragma unroll
+                for (int k = 0; k < kWaves - 1; ++k) v += sum[k][j][e][threadIdx.x];
+                p[j * (int64_t)C + e] = v;
+            }
+    }
+}
+
+// dweight and dbias: the rows of `partial` summed, 16 rows side by side.
+__global__ __launch_bounds__(1024) void conv_reduce_kernel(const float *partial, int rows, int C,
+                                                           int W, float *dweight, float *dbias) {
+    __shared__ float part[16][64];
+    const int64_t col = (int64_t)blockIdx.x * 64 + threadIdx.x, cols = (int64_t)(W + 1) * C;
+    float s = 0.f;
+    if (col < cols)
+        for (int r = threadIdx.y; r < rows; r += 16) s += partial[r * cols + col];
+    part[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y || col >= cols) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s += part[k][threadIdx.x];
+    const int j = (int)(col / C);
+    const int64_t c = col % C;
+    if (j < W)
+        dweight[c * W + j] = s;
+    else if (dbias)
+        dbias[c] = s;
+}
+
+template <typename T, int VEC, int W>
+__global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, T *state, int cblocks,
+                                                        int batch) {
+    typedef Row<T, VEC> R;
+    const int C = a.channels;
+    const int c = ((int)(blockIdx.x % cblocks) * 64 + (int)threadIdx.x) * VEC;
+    const int64_t n = (int64_t)(blockIdx.x / cblocks) * kWaves + threadIdx.y;
+    if (c >= C || n >= batch) return;
+    T *st = state + n * (W - 1) * (int64_t)C + c;
+    typename R::vec raw[W];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) raw[j] = R::raw(st + j * (int64_t)C);
+    raw[W - 1] = R::raw(static_cast<const T *>(a.x) + n * a.x_stride + c);
+    float w[W][VEC], y[VEC];
+    load_params<VEC, W>(a, c, w, y);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        float f[VEC];
+        R::get(raw[j], f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) y[e] += w[j][e] * f[e];
+        if (j > 0) *reinterpret_cast<typename R::vec *>(st + (j - 1) * (int64_t)C) = raw[j];
+    }
+    if (a.silu)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) y[e] *= sigmoid(y[e]);
+    R::put(static_cast<T *>(a.out) + n * a.out_stride + c, y);
+}
+
+int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Tokens of one wave's run.  Long runs read fewer rows twice, short ones fill
+// the chip when there is little to do: about 8 waves per SIMD's worth of runs,
+// 8 to 128 tokens each.
+int run_tokens(int64_t total, int cblocks) {
+    int64_t run = total * cblocks / (256 * 32);
+    run = (run + 7) / 8 * 8;
+    return (int)(run < 8 ? 8 : (run > 128 ? 128 : run));
+}
+constexpr int kBwdRun = 64;  // at most; the workspace is sized without cblocks
+int bwd_run_tokens(int64_t total, int cblocks) {
+    const int run = run_tokens(total, cblocks);
+    return run < 16 ? 16 : (run > kBwdRun ? kBwdRun : run);
+}
+
+template <typename T, int VEC, int W> int fwd(const ConvArgs &a, hipStream_t stream) {
+    const int cb = div_up(a.channels, 64 * VEC);
+    const int run = run_tokens(a.seqs.total, cb);
+    const int rb = div_up(a.seqs.total, (int64_t)run * kWaves);
+    const int sb = a.final_state ? div_up((int64_t)a.seqs.num * (W - 1), kWaves) : 0;
+    if (rb + sb == 0) return 0;
+    hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, W>), dim3((unsigned)cb * (unsigned)(rb + sb)),
+                       dim3(64, kWaves), 0, stream, a, cb, rb, run);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+template <typename T, int VEC, int W> int bwd(const ConvArgs &a, hipStream_t stream) {
+    const int cb = div_up(a.channels, 64 * VEC);
+    const int run = bwd_run_tokens(a.seqs.total, cb);
+    const int rb = div_up(a.seqs.total, (int64_t)run * kWaves);
+    const int sb = a.d_state0 ? div_up(a.seqs.num, kWaves) : 0;
+    if (rb + sb > 0)
+        hipLaunchKernelGGL((conv_bwd_kernel<T, VEC, W>), dim3((unsigned)cb * (unsigned)(rb + sb)),
+                           dim3(64, kWaves), 0, stream, a, cb, rb, run);
+    hipLaunchKernelGGL(conv_reduce_kernel, dim3(div_up((int64_t)a.channels * (W + 1), 64)),
+                       dim3(64, 16), 0, stream, a.partial, rb, a.channels, W, a.dweight, a.dbias);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+template <typename T, int VEC, int W>
+int step(const ConvArgs &a, void *state, int batch, hipStream_t stream) {
+    const int cb = div_up(a.channels, 64 * VEC);
+    hipLaunchKernelGGL((conv_step_kernel<T, VEC, W>),
+                       dim3((unsigned)cb * (unsigned)div_up(batch, kWaves)), dim3(64, kWaves), 0,
+                       stream, a, static_cast<T *>(state), cb, batch);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+// Whether every row of every tensor of the call starts on a multiple of
+// VEC elements (16 bytes, or 8 for the bf16 backward) and holds whole vectors.
+bool wide(const ConvArgs &a, const void *state, int vec) {
+    const int esz = a.dtype == kDtypeBf16 ? 2 : 4;
+    const void *p[] = {a.x, a.state0, a.d_out, a.d_final, a.out, a.final_state, a.dx, a.d_state0,
+                       state};
+    for (const void *q : p)
+        if (reinterpret_cast<uintptr_t>(q) % (uintptr_t)(vec * esz)) return false;
+    if ((reinterpret_cast<uintptr_t>(a.weight) | reinterpret_cast<uintptr_t>(a.bias)) % 16)
+        return false;
+    return a.channels % vec == 0 && a.x_stride % vec == 0 && a.out_stride % vec == 0 &&
+           a.d_out_stride % vec == 0 && a.dx_stride % vec == 0;
+}
+
+#define KDA_CONV_WIDTHS(fn, T, VEC, ...)                       \
+    (a.width == 4   ? fn<T, VEC, 4>(__VA_ARGS__)               \
+     : a.width == 3 ? fn<T, VEC, 3>(__VA_ARGS__)               \
+                    : fn<T, VEC, 2>(__VA_ARGS__))
+
+}  // namespace
+
+int launch_conv_fwd(const ConvArgs &a, hipStream_t stream) {
+    if (a.dtype == kDtypeBf16)
+        return wide(a, nullptr, 8) ? KDA_CONV_WIDTHS(fwd, bf16, 8, a, stream)
+                                   : KDA_CONV_WIDTHS(fwd, bf16, 1, a, stream);
+    return wide(a, nullptr, 4) ? KDA_CONV_WIDTHS(fwd, float, 4, a, stream)
+                               : KDA_CONV_WIDTHS(fwd, float, 1, a, stream);
+}
+
+int launch_conv_bwd(const ConvArgs &a, hipStream_t stream) {
+    if (a.dtype == kDtypeBf16)
+        return wide(a, nullptr, 4) ? KDA_CONV_WIDTHS(bwd, bf16, 4, a, stream)
+                                   : KDA_CONV_WIDTHS(bwd, bf16, 1, a, stream);
+    return wide(a, nullptr, 4) ? KDA_CONV_WIDTHS(bwd, float, 4, a, stream)
+                               : KDA_CONV_WIDTHS(bwd, float, 1, a, stream);
+}
+
+int64_t conv_bwd_workspace_floats(int64_t total, int64_t channels, int width) {
+    // runs are 16 tokens or longer (bwd_run_tokens)
+    const int64_t rows = (total + 16 * kWaves - 1) / (16 * kWaves);
+    return rows * channels * (width + 1);
+}
+
+int launch_conv_step(const ConvArgs &a, void *state, int32_t batch, hipStream_t stream) {
+    if (a.dtype == kDtypeBf16)
+        return wide(a, state, 8) ? KDA_CONV_WIDTHS(step, bf16, 8, a, state, batch, stream)
+                                 : KDA_CONV_WIDTHS(step, bf16, 1, a, state, batch, stream);
+    return wide(a, state, 4) ? KDA_CONV_WIDTHS(step, float, 4, a, state, batch, stream)
+                             : KDA_CONV_WIDTHS(step, float, 1, a, state, batch, stream);
+}
+
+}  // namespace kda

@@ -1,0 +1,342 @@
+// layer_api.cpp -- the C ABI declared in include/kda_layer.h: argument
+// validation on the host, then the launches on the caller's stream.
+//
+// Validation order as in kda_api.cpp: sizes, NULL pointers, supported
+// configurations, alignment, aliasing (host checks only), then the device,
+// then (debug mode) the offsets, then the launch.
+#include "kda_api_common.h"
+#include "kda_layer.h"
+#include "layer_internal.h"
+
+namespace {
+
+bool aligned_to(const void *p, uint64_t bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+int elem_size(int32_t dtype) {
+    return dtype == kda::kDtypeBf16 ? 2 : (dtype == kda::kDtypeF32 ? 4 : 0);
+}
+
+// Bytes from the first to the last element of `rows` rows of `len` elements.
+Range rows_range(const void *p, int64_t rows, int64_t len, int64_t stride, int esz) {
+    return {p, rows > 0 && len > 0 ? (uint64_t)((rows - 1) * stride + len) * esz : 0};
+}
+
+// No output may overlap another output or an input.
+int check_alias(const Range *outs, int n_out, const Range *ins, int n_in) {
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = i + 1; j < n_out; ++j)
+            if (overlap(outs[i], outs[j])) return KDA_ERR_ALIAS;
+        for (int j = 0; j < n_in; ++j)
+            if (overlap(outs[i], ins[j])) return KDA_ERR_ALIAS;
+    }
+    return KDA_OK;
+}
+template <int NO, int NI> int check_alias(const Range (&outs)[NO], const Range (&ins)[NI]) {
+    return check_alias(outs, NO, ins, NI);
+}
+
+// Sizes of a call over sequences; *seqs receives them.
+int check_seqs(const int32_t *cu, int32_t batch, int32_t seq_len, int32_t num_seqs,
+               kda::Seqs *seqs) {
+    if (batch < 0 || seq_len < 0) return KDA_ERR_SHAPE;
+    if (cu && (batch != 1 || num_seqs < 0)) return KDA_ERR_SHAPE;
+    const int64_t tokens = (int64_t)batch * seq_len;
+    if (tokens > INT32_MAX) return KDA_ERR_SHAPE;
+    *seqs = {cu, cu ? num_seqs : batch, seq_len, (int32_t)tokens};
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ------------------------------------------------------------ short convolution
+int kda_short_conv_fwd(const void *x, const float *weight, const float *bias,
+                       const void *initial_state, const int32_t *cu_seqlens, void *out,
+                       void *final_state, int32_t batch, int32_t seq_len, int32_t channels,
+                       int32_t width, int64_t x_stride, int64_t out_stride, int32_t num_seqs,
+                       int32_t activation, int32_t dtype, hipStream_t stream) {
+    kda::Seqs seqs;
+    int st = check_seqs(cu_seqlens, batch, seq_len, num_seqs, &seqs);
+    if (st != KDA_OK) return st;
+    if (channels < 0 || width < 1) return KDA_ERR_SHAPE;
+    const int esz = elem_size(dtype);
+    if (!esz) return KDA_ERR_UNSUPPORTED;
+    const bool work = seqs.total > 0 && channels > 0;
+    if (work && (x_stride < channels || out_stride < channels)) return KDA_ERR_SHAPE;
+    if (work && (!x || !weight || !out)) return KDA_ERR_NULL;
+    if (width < 2 || width > 4) return KDA_ERR_UNSUPPORTED;
+    if (activation != KDA_ACT_NONE && activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
+    if (!aligned_to(x, esz) || !aligned_to(out, esz) || !aligned_to(initial_state, esz) ||
+        !aligned_to(final_state, esz) || !aligned4(weight) || !aligned4(bias) ||
+        !aligned4(cu_seqlens))
+        return KDA_ERR_ALIGN;
+    const uint64_t state = (uint64_t)seqs.num * (width - 1) * channels * esz;
+    const Range outs[] = {rows_range(out, seqs.total, channels, out_stride, esz),
+                          {final_state, state}};
+    const Range ins[] = {rows_range(x, seqs.total, channels, x_stride, esz),
+                         {weight, (uint64_t)channels * width * 4},
+                         {bias, (uint64_t)channels * 4},
+                         {initial_state, state},
+                         {cu_seqlens, (uint64_t)(seqs.num + 1) * 4}};
+    if ((st = check_alias(outs, ins)) != KDA_OK) return st;
+    if (seqs.num == 0 || channels == 0) return KDA_OK;
+    if ((st = check_device()) != KDA_OK) return st;
+    const char *where = "kda_short_conv_fwd";
+    if (debug_mode() &&
+        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
+        return st;
+    kda::ConvArgs a = {};
+    a.x = x, a.state0 = initial_state, a.weight = weight, a.bias = bias, a.out = out;
+    a.final_state = final_state, a.seqs = seqs, a.channels = channels, a.width = width;
+    a.silu = activation == KDA_ACT_SILU, a.dtype = dtype;
+    a.x_stride = x_stride, a.out_stride = out_stride;
+    return launch_status(kda::launch_conv_fwd(a, stream), stream, where);
+}
+
+int64_t kda_short_conv_bwd_workspace_size(int32_t batch, int32_t seq_len, int32_t channels,
+                                          int32_t width) {
+    if (batch < 0 || seq_len < 0 || channels < 0 || width < 2 || width > 4) return -1;
+    const int64_t tokens = (int64_t)batch * seq_len;
+    if (tokens > INT32_MAX) return -1;
+    return 4 * kda::conv_bwd_workspace_floats(tokens, channels, width);
+}
+
+int kda_short_conv_bwd(const void *x, const float *weight, const float *bias,
+                       const void *initial_state, const int32_t *cu_seqlens, const void *d_out,
+                       const void *d_final_state, void *dx, float *dweight, float *dbias,
+                       void *d_initial_state, int32_t batch, int32_t seq_len, int32_t channels,
+                       int32_t width, int64_t x_stride, int64_t d_out_stride, int64_t dx_stride,
+                       int32_t num_seqs, int32_t activation, int32_t dtype, void *workspace,
+                       int64_t workspace_bytes, hipStream_t stream) {
+    kda::Seqs seqs;
+    int st = check_seqs(cu_seqlens, batch, seq_len, num_seqs, &seqs);
+    if (st != KDA_OK) return st;
+    if (channels < 0 || width < 1) return KDA_ERR_SHAPE;
+    const int esz = elem_size(dtype);
+    if (!esz) return KDA_ERR_UNSUPPORTED;
+    const bool work = seqs.total > 0 && channels > 0;
+    if (work && (x_stride < channels || d_out_stride < channels || dx_stride < channels))
+        return KDA_ERR_SHAPE;
+    if (work && (!x || !d_out || !dx)) return KDA_ERR_NULL;
+    if (channels > 0 && (!weight || !dweight)) return KDA_ERR_NULL;
+    if (width < 2 || width > 4) return KDA_ERR_UNSUPPORTED;
+    if (activation != KDA_ACT_NONE && activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
+    const int64_t need = 4 * kda::conv_bwd_workspace_floats(seqs.total, channels, width);
+    if (need > 0 && !workspace) return KDA_ERR_NULL;
+    if (workspace_bytes < need) return KDA_ERR_SHAPE;
+    if (!aligned_to(x, esz) || !aligned_to(d_out, esz) || !aligned_to(dx, esz) ||
+        !aligned_to(initial_state, esz) || !aligned_to(d_final_state, esz) ||
+        !aligned_to(d_initial_state, esz) || !aligned4(weight) || !aligned4(bias) ||
+        !aligned4(dweight) || !aligned4(dbias) || !aligned4(cu_seqlens) || !aligned16(workspace))
+        return KDA_ERR_ALIGN;
+    const uint64_t state = (uint64_t)seqs.num * (width - 1) * channels * esz;
+    const uint64_t wb = (uint64_t)channels * width * 4, bb = (uint64_t)channels * 4;
+    const Range outs[] = {rows_range(dx, seqs.total, channels, dx_stride, esz),
+                          {dweight, wb},
+                          {dbias, bb},
+                          {d_initial_state, state},
+                          {workspace, (uint64_t)need}};
+    const Range ins[] = {rows_range(x, seqs.total, channels, x_stride, esz),
+                         rows_range(d_out, seqs.total, channels, d_out_stride, esz),
+                         {weight, wb},
+                         {bias, bb},
+                         {initial_state, state},
+                         {d_final_state, state},
+                         {cu_seqlens, (uint64_t)(seqs.num + 1) * 4}};
+    if ((st = check_alias(outs, ins)) != KDA_OK) return st;
+    if (channels == 0) return KDA_OK;
+    if ((st = check_device()) != KDA_OK) return st;
+    const char *where = "kda_short_conv_bwd";
+    if (debug_mode() &&
+        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
+        return st;
+    if (seqs.num == 0) seqs.total = 0;  // no sequence holds a token
+    kda::ConvArgs a = {};
+    a.x = x, a.state0 = initial_state, a.d_out = d_out, a.d_final = d_final_state;
+    a.weight = weight, a.bias = bias, a.dx = dx, a.d_state0 = d_initial_state;
+    a.dweight = dweight, a.dbias = dbias, a.partial = static_cast<float *>(workspace);
+    a.seqs = seqs, a.channels = channels, a.width = width;
+    a.silu = activation == KDA_ACT_SILU, a.dtype = dtype;
+    a.x_stride = x_stride, a.d_out_stride = d_out_stride, a.dx_stride = dx_stride;
+    return launch_status(kda::launch_conv_bwd(a, stream), stream, where);
+}
+
+int kda_short_conv_step(const void *x, const float *weight, const float *bias, void *state,
+                        void *out, int32_t batch, int32_t channels, int32_t width,
+                        int64_t x_stride, int64_t out_stride, int32_t activation, int32_t dtype,
+                        hipStream_t stream) {
+    if (batch < 0 || channels < 0 || width < 1) return KDA_ERR_SHAPE;
+    const int esz = elem_size(dtype);
+    if (!esz) return KDA_ERR_UNSUPPORTED;
+    const bool work = batch > 0 && channels > 0;
+    if (work && (x_stride < channels || out_stride < channels)) return KDA_ERR_SHAPE;
+    if (work && (!x || !weight || !state || !out)) return KDA_ERR_NULL;
+    if (width < 2 || width > 4) return KDA_ERR_UNSUPPORTED;
+    if (activation != KDA_ACT_NONE && activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
+    if (!aligned_to(x, esz) || !aligned_to(out, esz) || !aligned_to(state, esz) ||
+        !aligned4(weight) || !aligned4(bias))
+        return KDA_ERR_ALIGN;
+    const Range outs[] = {rows_range(out, batch, channels, out_stride, esz),
+                          {state, (uint64_t)batch * (width - 1) * channels * esz}};
+    const Range ins[] = {rows_range(x, batch, channels, x_stride, esz),
+                         {weight, (uint64_t)channels * width * 4},
+                         {bias, (uint64_t)channels * 4}};
+    int st = check_alias(outs, ins);
+    if (st != KDA_OK) return st;
+    if (!work) return KDA_OK;
+    if ((st = check_device()) != KDA_OK) return st;
+    kda::ConvArgs a = {};
+    a.x = x, a.weight = weight, a.bias = bias, a.out = out;
+    a.channels = channels, a.width = width, a.silu = activation == KDA_ACT_SILU, a.dtype = dtype;
+    a.x_stride = x_stride, a.out_stride = out_stride;
+    return launch_status(kda::launch_conv_step(a, state, batch, stream), stream,
+                         "kda_short_conv_step");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ norm and rotation
+namespace {
+
+// Checks shared by both directions; the ranges of q, k, weights, table and
+// positions go to `ins` (six of them).
+int check_qk(const void *q, const void *k, const float *q_weight, const float *k_weight,
+             const float *table, const int32_t *positions, int32_t tokens, int32_t q_heads,
+             int32_t k_heads, int32_t head_dim, int32_t rotary_dim, int32_t table_rows,
+             int64_t q_stride, int64_t k_stride, float eps, int32_t norm, int32_t dtype,
+             Range (&ins)[6]) {
+    if (tokens < 0 || q_heads < 0 || k_heads < 0 || head_dim <= 0 || rotary_dim < 0)
+        return KDA_ERR_SHAPE;
+    if ((int64_t)q_heads + k_heads > INT32_MAX) return KDA_ERR_SHAPE;
+    if (rotary_dim > head_dim || !(eps >= 0.f)) return KDA_ERR_SHAPE;
+    const int esz = elem_size(dtype);
+    if (!esz) return KDA_ERR_UNSUPPORTED;
+    const int64_t ql = (int64_t)q_heads * head_dim, kl = (int64_t)k_heads * head_dim;
+    const bool any_q = tokens > 0 && q_heads > 0, any_k = tokens > 0 && k_heads > 0;
+    if ((any_q && q_stride < ql) || (any_k && k_stride < kl)) return KDA_ERR_SHAPE;
+    if ((any_q && !q) || (any_k && !k)) return KDA_ERR_NULL;
+    if (rotary_dim > 0 && (any_q || any_k)) {
+        if (!table || !positions) return KDA_ERR_NULL;
+        if (table_rows < 1) return KDA_ERR_SHAPE;
+    }
+    if (head_dim != 64 && head_dim != 128) return KDA_ERR_UNSUPPORTED;
+    if (rotary_dim % 16 != 0) return KDA_ERR_UNSUPPORTED;
+    if (norm != KDA_NORM_L2 && norm != KDA_NORM_RMS) return KDA_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(table) || !aligned4(positions) ||
+        !aligned4(q_weight) || !aligned4(k_weight) || (any_q && q_stride * esz % 16 != 0) ||
+        (any_k && k_stride * esz % 16 != 0))
+        return KDA_ERR_ALIGN;
+    const bool rot = rotary_dim > 0;
+    ins[0] = rows_range(q, tokens, ql, q_stride, esz);
+    ins[1] = rows_range(k, tokens, kl, k_stride, esz);
+    ins[2] = {q_weight, (uint64_t)head_dim * 4};
+    ins[3] = {k_weight, (uint64_t)head_dim * 4};
+    ins[4] = {rot ? table : nullptr, rot ? (uint64_t)table_rows * rotary_dim * 4 : 0};
+    ins[5] = {rot ? positions : nullptr, (uint64_t)tokens * 4};
+    return KDA_OK;
+}
+
+// One more pair of tensors laid out like q and k.
+int check_qk_rows(const void *q, const void *k, int32_t tokens, int32_t q_heads, int32_t k_heads,
+                  int32_t head_dim, int64_t q_stride, int64_t k_stride, int32_t dtype, Range *r) {
+    const int esz = elem_size(dtype);
+    const int64_t ql = (int64_t)q_heads * head_dim, kl = (int64_t)k_heads * head_dim;
+    const bool any_q = tokens > 0 && q_heads > 0, any_k = tokens > 0 && k_heads > 0;
+    if ((any_q && q_stride < ql) || (any_k && k_stride < kl)) return KDA_ERR_SHAPE;
+    if ((any_q && !q) || (any_k && !k)) return KDA_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || (any_q && q_stride * esz % 16 != 0) ||
+        (any_k && k_stride * esz % 16 != 0))
+        return KDA_ERR_ALIGN;
+    r[0] = rows_range(q, tokens, ql, q_stride, esz);
+    r[1] = rows_range(k, tokens, kl, k_stride, esz);
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_qk_norm_fwd(const void *q, const void *k, const float *q_weight, const float *k_weight,
+                    const float *table, const int32_t *positions, void *out_q, void *out_k,
+                    int32_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                    int32_t rotary_dim, int32_t table_rows, int64_t q_stride, int64_t k_stride,
+                    int64_t out_q_stride, int64_t out_k_stride, float eps, int32_t norm,
+                    int32_t interleaved, int32_t dtype, hipStream_t stream) {
+    Range ins[6], outs[2];
+    int st = check_qk(q, k, q_weight, k_weight, table, positions, tokens, q_heads, k_heads,
+                      head_dim, rotary_dim, table_rows, q_stride, k_stride, eps, norm, dtype, ins);
+    if (st != KDA_OK) return st;
+    st = check_qk_rows(out_q, out_k, tokens, q_heads, k_heads, head_dim, out_q_stride,
+                       out_k_stride, dtype, outs);
+    if (st != KDA_OK) return st;
+    if ((st = check_alias(outs, ins)) != KDA_OK) return st;
+    if (tokens == 0 || (q_heads == 0 && k_heads == 0)) return KDA_OK;
+    if ((st = check_device()) != KDA_OK) return st;
+    const kda::QkArgs a = {{q, k},       {nullptr, nullptr}, {out_q, out_k},
+                           {q_weight, k_weight}, {nullptr, nullptr}, nullptr,
+                           table,        positions,          tokens,
+                           {q_heads, k_heads}, head_dim,     rotary_dim,
+                           table_rows,   {q_stride, k_stride}, {0, 0},
+                           {out_q_stride, out_k_stride}, eps, norm == KDA_NORM_RMS,
+                           interleaved != 0, dtype};
+    return launch_status(kda::launch_qk_norm_fwd(a, stream), stream, "kda_qk_norm_fwd");
+}
+
+int64_t kda_qk_norm_bwd_workspace_size(int32_t tokens, int32_t q_heads, int32_t k_heads,
+                                       int32_t head_dim) {
+    if (tokens < 0 || q_heads < 0 || k_heads < 0 || (head_dim != 64 && head_dim != 128) ||
+        (int64_t)q_heads + k_heads > INT32_MAX)
+        return -1;
+    return 4 * kda::qk_norm_bwd_workspace_floats(tokens, (int64_t)q_heads + k_heads, head_dim);
+}
+
+int kda_qk_norm_bwd(const void *q, const void *k, const float *q_weight, const float *k_weight,
+                    const float *table, const int32_t *positions, const void *d_out_q,
+                    const void *d_out_k, void *dq, void *dk, float *dq_weight, float *dk_weight,
+                    int32_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                    int32_t rotary_dim, int32_t table_rows, int64_t q_stride, int64_t k_stride,
+                    int64_t d_out_q_stride, int64_t d_out_k_stride, int64_t dq_stride,
+                    int64_t dk_stride, float eps, int32_t norm, int32_t interleaved,
+                    int32_t dtype, void *workspace, int64_t workspace_bytes, hipStream_t stream) {
+    Range ins[8], outs[5], base[6];
+    int st = check_qk(q, k, q_weight, k_weight, table, positions, tokens, q_heads, k_heads,
+                      head_dim, rotary_dim, table_rows, q_stride, k_stride, eps, norm, dtype,
+                      base);
+    if (st != KDA_OK) return st;
+    // the gradient of a weight that was not given has no meaning
+    if ((dq_weight && !q_weight) || (dk_weight && !k_weight)) return KDA_ERR_NULL;
+    for (int i = 0; i < 6; ++i) ins[i] = base[i];
+    st = check_qk_rows(d_out_q, d_out_k, tokens, q_heads, k_heads, head_dim, d_out_q_stride,
+                       d_out_k_stride, dtype, ins + 6);
+    if (st != KDA_OK) return st;
+    st = check_qk_rows(dq, dk, tokens, q_heads, k_heads, head_dim, dq_stride, dk_stride, dtype,
+                       outs);
+    if (st != KDA_OK) return st;
+    const bool weights = dq_weight || dk_weight;
+    const int64_t need =
+        weights ? kda_qk_norm_bwd_workspace_size(tokens, q_heads, k_heads, head_dim) : 0;
+    if (need > 0 && !workspace) return KDA_ERR_NULL;
+    if (workspace_bytes < need) return KDA_ERR_SHAPE;
+    if (!aligned4(dq_weight) || !aligned4(dk_weight) || !aligned16(workspace))
+        return KDA_ERR_ALIGN;
+    outs[2] = {dq_weight, (uint64_t)head_dim * 4};
+    outs[3] = {dk_weight, (uint64_t)head_dim * 4};
+    outs[4] = {workspace, (uint64_t)need};
+    if ((st = check_alias(outs, ins)) != KDA_OK) return st;
+    const bool none = tokens == 0 || (q_heads == 0 && k_heads == 0);
+    if (none && !weights) return KDA_OK;
+    if ((st = check_device()) != KDA_OK) return st;
+    kda::QkArgs a = {{q, k},       {d_out_q, d_out_k}, {dq, dk},
+                     {q_weight, k_weight}, {dq_weight, dk_weight}, static_cast<float *>(workspace),
+                     table,        positions,          none ? 0 : tokens,
+                     {q_heads, k_heads}, head_dim,     rotary_dim,
+                     table_rows,   {q_stride, k_stride}, {d_out_q_stride, d_out_k_stride},
+                     {dq_stride, dk_stride}, eps,      norm == KDA_NORM_RMS,
+                     interleaved != 0, dtype};
+    return launch_status(kda::launch_qk_norm_bwd(a, stream), stream, "kda_qk_norm_bwd");
+}
+
+}  // extern "C"

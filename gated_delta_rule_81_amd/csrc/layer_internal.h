@@ -1,0 +1,50 @@
+// layer_internal.h -- host-side launch functions of the operators around the
+// recurrence (not part of the public ABI; see include/kda_layer.h).  Arguments
+// are already validated.  Each returns 0, or -1 if a launch failed.
+#pragma once
+
+#include "kda_internal.h"
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+namespace kda {
+
+// Sequences of a call: num_seqs rows of seq_len tokens (cu == NULL), or the
+// packed offsets cu; total tokens in all.
+struct Seqs {
+    const int32_t *cu;
+    int32_t num, seq_len, total;
+};
+
+struct ConvArgs {
+    const void *x, *state0, *d_out, *d_final;
+    const float *weight, *bias;
+    void *out, *final_state, *dx, *d_state0;
+    float *dweight, *dbias, *partial;
+    Seqs seqs;
+    int32_t channels, width, silu, dtype;
+    int64_t x_stride, out_stride, d_out_stride, dx_stride;
+};
+int launch_conv_fwd(const ConvArgs &a, hipStream_t stream);
+int launch_conv_bwd(const ConvArgs &a, hipStream_t stream);
+int64_t conv_bwd_workspace_floats(int64_t total, int64_t channels, int width);
+int launch_conv_step(const ConvArgs &a, void *state, int32_t batch, hipStream_t stream);
+
+struct QkArgs {
+    const void *x[2], *dy[2];    // q, k and the gradients of their outputs
+    void *y[2];                  // outputs, or dq and dk
+    const float *weight[2];
+    float *dweight[2], *partial;
+    const float *table;
+    const int32_t *positions;
+    int32_t tokens, heads[2], head_dim, rot, table_rows;
+    int64_t x_stride[2], dy_stride[2], y_stride[2];
+    float eps;
+    int32_t rms, interleaved, dtype;
+};
+int launch_qk_norm_fwd(const QkArgs &a, hipStream_t stream);
+int launch_qk_norm_bwd(const QkArgs &a, hipStream_t stream);
+int64_t qk_norm_bwd_workspace_floats(int64_t tokens, int64_t heads, int head_dim);
+
+}  // namespace kda

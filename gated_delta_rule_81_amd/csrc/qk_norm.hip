@@ -1,0 +1,294 @@
+// qk_norm.hip -- queries and keys divided by each head's norm, weighted, and
+// rotated by position in the same pass; forward and backward.
+//
+//   y = R (x w inv),  inv = 1 / sqrt(ss / m + eps),  m = 1 (L2) or d (RMS);
+//   backward: g = R^T dy, dw = sum g x inv, h = g w,
+//             dx = inv h - x inv^3 (h . x) / m.
+//
+// Every value is read once and written once (backward: two reads, one write),
+// so HBM bounds both.  A head is d / 8 lanes with eight channels each (16 bytes
+// of bf16); a wave works on 64 / (d / 8) heads of ONE token at a time, so the
+// token's cos | sin row is read once into registers for all of its heads, q's
+// and k's alike.  The sum over a head stays in its 8 or 16 lanes (DPP); pairs
+// half the rotated width apart come from the partner lane.
+#include "layer_device.h"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256, kWavesPerBlock = 4;
+constexpr int kPasses = 4;  // passes (of 4 or 8 heads each) whose loads are in flight together
+
+// Sum over aligned groups of LPR (8 or 16) lanes, in every lane of the group.
+template <int LPR> __device__ __forceinline__ float head_sum(float x) {
+    auto dpp = [](float v, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value,
+                                                          0xf, 0xf, true));
+    };
+    x += dpp(x, std::integral_constant<int, 0xB1>{});   // quad_perm [1,0,3,2]
+    x += dpp(x, std::integral_constant<int, 0x4E>{});   // quad_perm [2,3,0,1]
+    x += dpp(x, std::integral_constant<int, 0x141>{});  // row_half_mirror: the other quad of 8
+    if constexpr (LPR == 16) x += dpp(x, std::integral_constant<int, 0x140>{});  // row_mirror
+    return x;
+}
+
+// What a lane does to its eight channels: cos and sin per channel (or per
+// channel pair when interleaved) and the lane that holds the other halves.
+struct Turn {
+    float cs[8], sn[8];  // sn carries the sign of the sine's term
+    int partner;
+    bool on;
+};
+
+template <int D>
+__device__ __forceinline__ Turn load_turn(const QkArgs &a, int64_t token, int lane, bool back) {
+    constexpr int LPR = D / 8;
+    Turn r;
+    const int e0 = 8 * (lane % LPR), half = a.rot / 2;
+    r.on = e0 < a.rot;
+    r.partner = lane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.cs[i] = 1.f, r.sn[i] = 0.f;
+    if (!r.on) return r;
+    int pos = a.positions[token];
+    pos = pos < 0 ? 0 : (pos >= a.table_rows ? a.table_rows - 1 : pos);
+    const float *row = a.table + (int64_t)pos * a.rot;
+    if (a.interleaved) {
+        const f32x4 c = *reinterpret_cast<const f32x4 *>(row + e0 / 2);
+        const f32x4 s = *reinterpret_cast<const f32x4 *>(row + half + e0 / 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            r.cs[i] = c[i / 2];
+            r.sn[i] = (i % 2 == 0) != back ? -s[i / 2] : s[i / 2];
+        }
+        return r;
+    }
+    const bool low = e0 < half;
+    const int at = low ? e0 : e0 - half;
+    r.partner = low ? lane + half / 8 : lane - half / 8;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const f32x4 c = *reinterpret_cast<const f32x4 *>(row + at + i);
+        const f32x4 s = *reinterpret_cast<const f32x4 *>(row + half + at + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r.cs[i + e] = c[e];
+            r.sn[i + e] = low != back ? -s[e] : s[e];
+        }
+    }
+    return r;
+}
+
+// y <- R y (or R^T y when the turn was loaded so).  Every lane of the wave
+// takes part in the exchange.
+__device__ __forceinline__ void rotate(const Turn &r, int interleaved, float (&y)[8]) {
+    float o[8];
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = y[i ^ 1];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = __shfl(y[i], r.partner, 64);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = r.on ? y[i] * r.cs[i] + o[i] * r.sn[i] : y[i];
+}
+
+__device__ __forceinline__ float inv_norm(float ss, bool rms, int d, float eps) {
+    return __builtin_amdgcn_rsqf((rms ? ss * (1.f / d) : ss) + eps);
+}
+
+template <typename T>
+__device__ __forceinline__ const T *head_at(const void *const (&p)[2], const int64_t (&stride)[2],
+                                            int which, int64_t token, int h, int d) {
+    return static_cast<const T *>(p[which]) + token * stride[which] + (int64_t)h * d;
+}
+
+// Unit: (token, group of kPasses passes).  One wave per unit.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkArgs a, int groups) {
+    constexpr int LPR = D / 8, HPP = 64 / LPR;  // lanes per head, heads per pass
+    const int lane = threadIdx.x & 63;
+    const int64_t unit = (int64_t)blockIdx.x * kWavesPerBlock + (threadIdx.x >> 6);
+    const int64_t token = unit / groups;
+    if (token >= a.tokens) return;
+    const int h0 = (int)(unit % groups) * (kPasses * HPP) + lane / LPR;
+    const int heads = a.heads[0] + a.heads[1], e0 = 8 * (lane % LPR);
+    typename Vec8<T>::raw raw[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int h = h0 + i * HPP, which = h >= a.heads[0];
+        raw[i] = h < heads ? load8(head_at<T>(a.x, a.x_stride, which, token,
+                                              which ? h - a.heads[0] : h, D) + e0)
+                           : Vec8<T>::zero();
+    }
+    Turn turn;
+    if (a.rot) turn = load_turn<D>(a, token, lane, false);
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int h = h0 + i * HPP, which = h >= a.heads[0];
+        float x[8];
+        Vec8<T>::to_float(raw[i], x);
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+        const float inv = inv_norm(head_sum<LPR>(ss), a.rms, D, a.eps);
+        const float *w = a.weight[which];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= inv;
+        if (w) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= w[e0 + e];
+        }
+        if (a.rot) rotate(turn, a.interleaved, x);
+        if (h < heads)
+            store8(const_cast<T *>(head_at<T>({a.y[0], a.y[1]}, a.y_stride, which, token,
+                                              which ? h - a.heads[0] : h, D)) + e0, x);
+    }
+}
+
+// The same walk; the gradients of the two weights of all of a workgroup's heads go
+// to its row of `partial` ([row][2][D]), summed afterwards in row order.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkArgs a, int groups) {
+    constexpr int LPR = D / 8, HPP = 64 / LPR;
+    __shared__ float sum[kWavesPerBlock][2][HPP][D];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int heads = a.heads[0] + a.heads[1], e0 = 8 * (lane % LPR);
+    const int64_t units = (int64_t)a.tokens * groups;
+    float dw[2][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
+    for (int64_t unit = (int64_t)blockIdx.x * kWavesPerBlock + wave; unit < units;
+         unit += (int64_t)gridDim.x * kWavesPerBlock) {
+        const int64_t token = unit / groups;
+        const int h0 = (int)(unit % groups) * (kPasses * HPP) + lane / LPR;
+        typename Vec8<T>::raw rx[kPasses], rg[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int h = h0 + i * HPP, which = h >= a.heads[0];
+            const int hh = which ? h - a.heads[0] : h;
+            const bool in = h < heads;
+            rx[i] = in ? load8(head_at<T>(a.x, a.x_stride, which, token, hh, D) + e0)
+                       : Vec8<T>::zero();
+            rg[i] = in ? load8(head_at<T>(a.dy, a.dy_stride, which, token, hh, D) + e0)
+                       : Vec8<T>::zero();
+        }
+        Turn turn;
+        if (a.rot) turn = load_turn<D>(a, token, lane, true);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int h = h0 + i * HPP, which = h >= a.heads[0];
+            float x[8], g[8];
+            Vec8<T>::to_float(rx[i], x);
+            Vec8<T>::to_float(rg[i], g);
+            if (a.rot) rotate(turn, a.interleaved, g);
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+            const float inv = inv_norm(head_sum<LPR>(ss), a.rms, D, a.eps);
+            const float *w = a.weight[which];
+            if (w) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = h < heads ? g[e] * x[e] * inv : 0.f;
+                    dw[0][e] += which ? 0.f : v;
+                    dw[1][e] += which ? v : 0.f;
+                    g[e] *= w[e0 + e];
+                }
+            }
+            float dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot += g[e] * x[e];
+            // inv^2 first: x inv stays in range where inv^3 may not
+            const float k = head_sum<LPR>(dot) * inv * (a.rms ? 1.f / D : 1.f) * inv;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = inv * (g[e] - x[e] * k);
+            if (h < heads)
+                store8(const_cast<T *>(head_at<T>({a.y[0], a.y[1]}, a.y_stride, which, token,
+                                                  which ? h - a.heads[0] : h, D)) + e0, x);
+        }
+    }
+    if (!a.partial) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        sum[wave][0][lane / LPR][e0 + e] = dw[0][e];
+        sum[wave][1][lane / LPR][e0 + e] = dw[1][e];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int wv = 0; wv < kWavesPerBlock; ++wv)
+#pragma unroll
+            for (int r = 0; r < HPP; ++r) s += sum[wv][i / D][r][i % D];
+        a.partial[(int64_t)blockIdx.x * 2 * D + i] = s;
+    }
+}
+
+// dq_weight and dk_weight: `rows` rows of [2][D], eight columns per workgroup.
+__global__ __launch_bounds__(512) void qk_reduce_kernel(const float *partial, int rows, int D,
+                                                        float *dq, float *dk) {
+    __shared__ float part[64][8];
+    const int col = blockIdx.x * 8 + threadIdx.x;
+    float s = 0.f;
+    for (int r = threadIdx.y; r < rows; r += 64) s += partial[(int64_t)r * 2 * D + col];
+    part[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y) return;
+    for (int k = 1; k < 64; ++k) s += part[k][threadIdx.x];
+    float *out = col < D ? dq : dk;
+    if (out) out[col % D] = s;
+}
+
+int groups_of(int heads, int d) {
+    const int hpp = 512 / d;  // heads per pass
+    return (heads + kPasses * hpp - 1) / (kPasses * hpp);
+}
+// Workgroups of the backward: enough to fill the chip several times over,
+// few enough that their partial sums stay small beside the data.
+constexpr int kBwdBlocks = 2048;
+int bwd_blocks(int64_t units) {
+    const int64_t b = (units + kWavesPerBlock - 1) / kWavesPerBlock;
+    return (int)(b < kBwdBlocks ? b : kBwdBlocks);
+}
+
+template <typename T, int D> int fwd(const QkArgs &a, hipStream_t stream) {
+    const int groups = groups_of(a.heads[0] + a.heads[1], D);
+    const int64_t units = (int64_t)a.tokens * groups;
+    hipLaunchKernelGGL((qk_norm_fwd_kernel<T, D>),
+                       dim3((unsigned)((units + kWavesPerBlock - 1) / kWavesPerBlock)),
+                       dim3(kThreads), 0, stream, a, groups);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+template <typename T, int D> int bwd(const QkArgs &args, hipStream_t stream) {
+    QkArgs a = args;
+    const bool weights = a.dweight[0] || a.dweight[1];
+    if (!weights) a.partial = nullptr;
+    const int groups = groups_of(a.heads[0] + a.heads[1], D);
+    const int blocks = bwd_blocks((int64_t)a.tokens * groups);
+    if (blocks > 0)
+        hipLaunchKernelGGL((qk_norm_bwd_kernel<T, D>), dim3(blocks), dim3(kThreads), 0, stream, a,
+                           groups);
+    if (weights)
+        hipLaunchKernelGGL(qk_reduce_kernel, dim3(2 * D / 8), dim3(8, 64), 0, stream, a.partial,
+                           blocks, D, a.dweight[0], a.dweight[1]);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+#define KDA_QK_DISPATCH(fn)                                                      \
+    (a.dtype == kDtypeBf16                                                       \
+         ? (a.head_dim == 128 ? fn<bf16, 128>(a, stream) : fn<bf16, 64>(a, stream)) \
+         : (a.head_dim == 128 ? fn<float, 128>(a, stream) : fn<float, 64>(a, stream)))
+
+}  // namespace
+
+int launch_qk_norm_fwd(const QkArgs &a, hipStream_t stream) { return KDA_QK_DISPATCH(fwd); }
+int launch_qk_norm_bwd(const QkArgs &a, hipStream_t stream) { return KDA_QK_DISPATCH(bwd); }
+
+int64_t qk_norm_bwd_workspace_floats(int64_t tokens, int64_t heads, int head_dim) {
+    return (int64_t)bwd_blocks(tokens * groups_of((int)heads, head_dim)) * 2 * head_dim;
+}
+
+}  // namespace kda

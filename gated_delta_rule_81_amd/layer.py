@@ -1,0 +1,309 @@
+"""PyTorch front end of the operators around the recurrence
+(include/kda_layer.h): argument marshalling only, as in ``ops``.
+
+Tensors with one row per token ([B, T, ...] or [B, ...] for a single token) may
+be slices of wider rows: everything behind the token axis has to be contiguous
+and consecutive tokens a fixed distance apart.  Calls run on the current stream
+of the tensors' own device, whichever device is current.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from ._lib import check, lib
+from .ops import _DTYPES, _expect, _ptr
+
+_ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
+_NORMS = {"l2": 0, "rms": 1}
+
+
+def _rows(t, name, dtype, shape, device, lead: int) -> int:
+    """Check a tensor whose first ``lead`` axes count tokens; returns the
+    distance in elements between consecutive tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    width = 1
+    for size, stride in reversed(list(zip(t.shape[lead:], t.stride()[lead:]))):
+        if size != 1 and stride != width:
+            raise ValueError(f"{name}: the values of a token must be contiguous")
+        width *= size
+    row, count = None, 1  # distance between tokens; tokens behind the axis looked at
+    for size, stride in reversed(list(zip(t.shape[:lead], t.stride()[:lead]))):
+        if size != 1:
+            if row is None:
+                row = stride
+            elif stride != row * count:
+                raise ValueError(f"{name}: tokens must be a fixed distance apart")
+        count *= size
+    row = width if row is None or t.numel() == 0 else row
+    if row < width:
+        raise ValueError(f"{name}: the rows of two tokens overlap")
+    return row
+
+
+def _dtype(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _num_seqs(cu_seqlens, batch, device):
+    if cu_seqlens is None:
+        return batch
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or not len(cu_seqlens):
+        raise ValueError("cu_seqlens must be a 1-D tensor")
+    _expect(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, device)
+    if batch != 1:
+        raise ValueError("packed sequences need a batch of 1")
+    return cu_seqlens.shape[0] - 1
+
+
+def _call(name, device, *args):
+    """Call a library function on ``device``'s current stream."""
+    if device.type != "cuda":
+        raise ValueError(f"{name} needs tensors on a GPU, got {device}")
+    with torch.cuda.device(device):
+        rc = getattr(lib(), name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    check(rc, name)
+
+
+def _workspace(workspace, need, device):
+    if need < 0:
+        raise ValueError("invalid sizes")
+    if workspace is None:
+        return torch.empty(max(int(need), 1), dtype=torch.uint8, device=device)
+    _expect(workspace, "workspace", torch.uint8, (workspace.numel(),), device)
+    return workspace
+
+
+def _out(t, like_shape, dtype, device):
+    return torch.empty(like_shape, dtype=dtype, device=device) if t is None else t
+
+
+# ---------------------------------------------------------------- short convolution
+def _conv_common(x, weight, bias, activation):
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be 'silu' or 'none', got {activation!r}")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [C, width]")
+    C = x.shape[2]
+    _expect(weight, "weight", torch.float32, (C, weight.shape[1]), x.device)
+    _expect(bias, "bias", torch.float32, (C,), x.device)
+    return _ACTIVATIONS[activation]
+
+
+def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               initial_state: Optional[torch.Tensor] = None,
+               cu_seqlens: Optional[torch.Tensor] = None, *, activation: Optional[str] = "silu",
+               out: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+               output_final_state: bool = True
+               ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Depthwise causal convolution over a few tokens (``kda_short_conv_fwd``),
+    the stage before a recurrence's q, k and v (or x, B and C).
+
+    x: [B, T, C] float32 or bfloat16 (may be a slice of wider rows); weight:
+    [C, width] fp32, width 2 to 4, the last tap is the token itself; bias: [C]
+    fp32 or None; initial_state: [N, width - 1, C] rows before each sequence's
+    first token, dtype of x, or None (zeros); cu_seqlens as for ``chunk_fwd``;
+    activation "silu" or "none".  Returns (out [B, T, C], final_state
+    [N, width - 1, C] or None): the rows the next call continues from.
+    """
+    dt = _dtype(x, "x")
+    act = _conv_common(x, weight, bias, activation)
+    (B, T, C), W, dev = x.shape, weight.shape[1], x.device
+    xs = _rows(x, "x", x.dtype, x.shape, dev, 2)
+    N = _num_seqs(cu_seqlens, B, dev)
+    state = (N, W - 1, C)
+    _expect(initial_state, "initial_state", x.dtype, state, dev)
+    out = _out(out, x.shape, x.dtype, dev)
+    os = _rows(out, "out", x.dtype, x.shape, dev, 2)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(state, dtype=x.dtype, device=dev)
+    _expect(final_state, "final_state", x.dtype, state, dev)
+    _call("kda_short_conv_fwd", dev, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state),
+          _ptr(cu_seqlens), _ptr(out), _ptr(final_state), B, T, C, W, xs, os,
+          N if cu_seqlens is not None else 0, act, dt)
+    return out, final_state
+
+
+def short_conv_bwd_workspace_size(batch: int, seq_len: int, channels: int, width: int) -> int:
+    """Bytes of workspace ``short_conv_bwd`` needs."""
+    n = lib().kda_short_conv_bwd_workspace_size(batch, seq_len, channels, width)
+    if n < 0:
+        raise ValueError("invalid sizes")
+    return int(n)
+
+
+def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, d_out: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None,
+                   d_final_state: Optional[torch.Tensor] = None,
+                   initial_state: Optional[torch.Tensor] = None,
+                   cu_seqlens: Optional[torch.Tensor] = None, *,
+                   activation: Optional[str] = "silu", workspace: Optional[torch.Tensor] = None,
+                   grads: Optional[dict] = None,
+                   output_initial_state_grad: bool = True) -> dict:
+    """Gradients of ``short_conv`` (``kda_short_conv_bwd``): given dL/d out and
+    dL/d final_state (None = zero), a dict with dx (dtype of x), dweight, dbias
+    (fp32; dbias None without a bias) and d_initial_state (dtype of x, or None
+    when ``output_initial_state_grad`` is False).  ``grads`` may hold
+    preallocated outputs under the same names, ``workspace`` a uint8 tensor of
+    ``short_conv_bwd_workspace_size`` bytes.
+    """
+    dt = _dtype(x, "x")
+    act = _conv_common(x, weight, bias, activation)
+    (B, T, C), W, dev = x.shape, weight.shape[1], x.device
+    xs = _rows(x, "x", x.dtype, x.shape, dev, 2)
+    gs = _rows(d_out, "d_out", x.dtype, x.shape, dev, 2)
+    N = _num_seqs(cu_seqlens, B, dev)
+    state = (N, W - 1, C)
+    _expect(initial_state, "initial_state", x.dtype, state, dev)
+    _expect(d_final_state, "d_final_state", x.dtype, state, dev)
+    g = dict(grads or {})
+    g["dx"] = _out(g.get("dx"), x.shape, x.dtype, dev)
+    dxs = _rows(g["dx"], "dx", x.dtype, x.shape, dev, 2)
+    g["dweight"] = _out(g.get("dweight"), (C, W), torch.float32, dev)
+    _expect(g["dweight"], "dweight", torch.float32, (C, W), dev)
+    g["dbias"] = None if bias is None else _out(g.get("dbias"), (C,), torch.float32, dev)
+    _expect(g["dbias"], "dbias", torch.float32, (C,), dev)
+    g.setdefault("d_initial_state", None)
+    if g["d_initial_state"] is None and output_initial_state_grad:
+        g["d_initial_state"] = torch.empty(state, dtype=x.dtype, device=dev)
+    _expect(g["d_initial_state"], "d_initial_state", x.dtype, state, dev)
+    ws = _workspace(workspace, lib().kda_short_conv_bwd_workspace_size(B, T, C, W), dev)
+    _call("kda_short_conv_bwd", dev, _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state),
+          _ptr(cu_seqlens), _ptr(d_out), _ptr(d_final_state), _ptr(g["dx"]), _ptr(g["dweight"]),
+          _ptr(g["dbias"]), _ptr(g["d_initial_state"]), B, T, C, W, xs, gs, dxs,
+          N if cu_seqlens is not None else 0, act, dt, _ptr(ws), ws.numel())
+    return g
+
+
+def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor,
+                    bias: Optional[torch.Tensor] = None, *, activation: Optional[str] = "silu",
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``short_conv`` for one token per session (``kda_short_conv_step``): x
+    [B, C], state [B, width - 1, C] moved on by one row in place.  Returns out
+    [B, C]."""
+    dt = _dtype(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [B, C]")
+    act = _conv_common(x[None], weight, bias, activation)
+    (B, C), W, dev = x.shape, weight.shape[1], x.device
+    xs = _rows(x, "x", x.dtype, x.shape, dev, 1)
+    if state is None:
+        raise TypeError("state must be a tensor")
+    _expect(state, "state", x.dtype, (B, W - 1, C), dev)
+    out = _out(out, x.shape, x.dtype, dev)
+    os = _rows(out, "out", x.dtype, x.shape, dev, 1)
+    _call("kda_short_conv_step", dev, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(out),
+          B, C, W, xs, os, act, dt)
+    return out
+
+
+# ---------------------------------------------------------------- norm and rotation
+def _qk_common(q, k, q_weight, k_weight, table, positions, kind):
+    if kind not in _NORMS:
+        raise ValueError(f"kind must be 'l2' or 'rms', got {kind!r}")
+    if q.dim() < 2 or k.dim() != q.dim() or q.shape[:-2] != k.shape[:-2]:
+        raise ValueError("q and k must be [..., heads, d] with the same leading axes")
+    d, dev, lead = q.shape[-1], q.device, q.dim() - 2
+    strides = (_rows(q, "q", q.dtype, q.shape, dev, lead),
+               _rows(k, "k", q.dtype, (*k.shape[:-1], d), dev, lead))
+    _expect(q_weight, "q_weight", torch.float32, (d,), dev)
+    _expect(k_weight, "k_weight", torch.float32, (d,), dev)
+    rot = rows = 0
+    if (table is None) != (positions is None):
+        raise ValueError("a rotation needs both table and positions")
+    if table is not None:
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must be [rows, rotary_dim]")
+        rows, rot = table.shape
+        _expect(table, "table", torch.float32, (rows, rot), dev)
+        _expect(positions, "positions", torch.int32, q.shape[:-2], dev)
+    tokens = 1
+    for n in q.shape[:-2]:
+        tokens *= n
+    return tokens, q.shape[-2], k.shape[-2], d, rot, rows, strides, lead
+
+
+def qk_norm(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+            k_weight: Optional[torch.Tensor] = None, table: Optional[torch.Tensor] = None,
+            positions: Optional[torch.Tensor] = None, *, kind: str = "l2", eps: float = 1e-6,
+            interleaved: bool = False, out_q: Optional[torch.Tensor] = None,
+            out_k: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Every head of q and k over its norm, times a weight, its first channels
+    rotated by position (``kda_qk_norm_fwd``): what ``chunk_fwd`` and
+    ``decode_step`` expect of their q and k with ``kind="l2"`` alone.
+
+    q: [..., Hq, d], k: [..., Hk, d], the same leading axes ([B, T] for a
+    prompt, [B] for one token each), one dtype, d 64 or 128 (may be slices of
+    wider rows); weights [d] fp32 or None; ``kind`` "l2" (root of the sum of
+    squares) or "rms" (of their mean).  ``table`` [rows, rotary_dim] fp32 holds
+    cos, then sin, of each position's angles and ``positions`` (int32, the
+    leading axes' shape) the row of each token: any frequencies or scaling,
+    rotary_dim a multiple of 16 up to d.  Pairs are (i, i + rotary_dim / 2), or
+    (2 i, 2 i + 1) with ``interleaved``.  Returns (q', k').
+    """
+    dt = _dtype(q, "q")
+    n, hq, hk, d, rot, rows, (qs, ks), lead = _qk_common(q, k, q_weight, k_weight, table,
+                                                         positions, kind)
+    out_q = _out(out_q, q.shape, q.dtype, q.device)
+    out_k = _out(out_k, k.shape, q.dtype, q.device)
+    oqs = _rows(out_q, "out_q", q.dtype, q.shape, q.device, lead)
+    oks = _rows(out_k, "out_k", q.dtype, k.shape, q.device, lead)
+    _call("kda_qk_norm_fwd", q.device, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+          _ptr(table), _ptr(positions), _ptr(out_q), _ptr(out_k), n, hq, hk, d, rot, rows, qs, ks,
+          oqs, oks, eps, _NORMS[kind], int(bool(interleaved)), dt)
+    return out_q, out_k
+
+
+def qk_norm_bwd_workspace_size(tokens: int, q_heads: int, k_heads: int, head_dim: int) -> int:
+    """Bytes of workspace ``qk_norm_bwd`` needs when it returns weights' gradients."""
+    n = lib().kda_qk_norm_bwd_workspace_size(tokens, q_heads, k_heads, head_dim)
+    if n < 0:
+        raise ValueError("invalid sizes")
+    return int(n)
+
+
+def qk_norm_bwd(q: torch.Tensor, k: torch.Tensor, d_out_q: torch.Tensor, d_out_k: torch.Tensor,
+                q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                table: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, *,
+                kind: str = "l2", eps: float = 1e-6, interleaved: bool = False,
+                workspace: Optional[torch.Tensor] = None, grads: Optional[dict] = None) -> dict:
+    """Gradients of ``qk_norm`` (``kda_qk_norm_bwd``): a dict with dq, dk (dtype
+    of q), dq_weight and dk_weight (fp32, None where there is no weight).
+    ``grads`` may hold preallocated outputs, ``workspace`` a uint8 tensor of
+    ``qk_norm_bwd_workspace_size`` bytes."""
+    dt = _dtype(q, "q")
+    n, hq, hk, d, rot, rows, (qs, ks), lead = _qk_common(q, k, q_weight, k_weight, table,
+                                                         positions, kind)
+    dev = q.device
+    gqs = _rows(d_out_q, "d_out_q", q.dtype, q.shape, dev, lead)
+    gks = _rows(d_out_k, "d_out_k", q.dtype, k.shape, dev, lead)
+    g = dict(grads or {})
+    for name, like in (("dq", q), ("dk", k)):
+        g[name] = _out(g.get(name), like.shape, q.dtype, dev)
+    dqs = _rows(g["dq"], "dq", q.dtype, q.shape, dev, lead)
+    dks = _rows(g["dk"], "dk", q.dtype, k.shape, dev, lead)
+    for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
+        g[name] = None if w is None else _out(g.get(name), (d,), torch.float32, dev)
+        _expect(g[name], name, torch.float32, (d,), dev)
+    if q_weight is not None or k_weight is not None or workspace is not None:
+        workspace = _workspace(workspace, lib().kda_qk_norm_bwd_workspace_size(n, hq, hk, d), dev)
+    _call("kda_qk_norm_bwd", dev, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(table),
+          _ptr(positions), _ptr(d_out_q), _ptr(d_out_k), _ptr(g["dq"]), _ptr(g["dk"]),
+          _ptr(g["dq_weight"]), _ptr(g["dk_weight"]), n, hq, hk, d, rot, rows, qs, ks, gqs, gks,
+          dqs, dks, eps, _NORMS[kind], int(bool(interleaved)), dt, _ptr(workspace),
+          0 if workspace is None else workspace.numel())
+    return g

@@ -1,0 +1,150 @@
+/*
+ * kda_layer.h -- C ABI of libkda, the operators around the KDA recurrence of a
+ * layer (AMD Instinct MI355X, gfx950, hand-written HIP):
+ *
+ *   - the short causal convolution that a layer's q, k and v (or x, B and C)
+ *     pass through before the recurrence (kda_short_conv_*);
+ *   - the per-head norm of queries and keys with the position rotation in the
+ *     same pass (kda_qk_norm_*);
+ *   - the selective state space scan, the recurrence with one decay per token
+ *     and head and no delta rule (kda_ssm_*).
+ *
+ * Conventions shared by every entry point (those of kda.h, where both apply):
+ *   - Status codes, element types (enum kda_dtype), packed sequences
+ *     (cu_seqlens: a DEVICE int32 array of num_seqs + 1 offsets, 0 first, not
+ *     decreasing, T last; NULL = batch rows of seq_len tokens), streams and the
+ *     debug mode are as in kda.h.  Malformed offsets give wrong results, never
+ *     an access out of bounds.  Tokens behind the last offset are in no
+ *     sequence: their outputs are left as they were.
+ *   - Tensors with one row per token may be slices of wider rows: `*_stride`
+ *     is the distance in elements between consecutive tokens (token t of batch
+ *     row b is row b * seq_len + t), at least the row's own length.  Everything
+ *     else is dense.  Offsets are 64-bit.
+ *   - Parameters (weights, biases, A, D), dt and scan states are fp32; sums,
+ *     norms and states are held in fp32; outputs are rounded once.
+ *   - A workspace is the caller's, 16-byte aligned, of at least the size its
+ *     `_workspace_size` returns (-1: invalid sizes).  Nothing in it has to
+ *     survive a call and no call reads what an earlier one left.  Calls that
+ *     may overlap in time (two streams, two captured graphs) need one each.
+ *   - Nothing is allocated and no host memory is read after the call returns:
+ *     every call may be captured into a graph.  Results do not depend on the
+ *     order in which workgroups run.
+ *   - An output must not overlap an input or another output
+ *     (KDA_ERR_ALIAS) except where said.
+ */
+#ifndef KDA_LAYER_H_
+#define KDA_LAYER_H_
+
+#include "kda.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Activation behind the short convolution. */
+enum kda_activation { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 };
+
+/* What kda_qk_norm_* divides a head by: the root of its sum of squares, or of
+ * their mean. */
+enum kda_norm { KDA_NORM_L2 = 0, KDA_NORM_RMS = 1 };
+
+/*
+ * kda_short_conv_fwd -- depthwise causal convolution of width 2, 3 or 4 with
+ * an optional bias and activation:
+ *     z[t,c] = bias[c] + sum_j weight[c,j] * r[t - (width - 1) + j, c],
+ *     out[t,c] = z, or z * sigmoid(z) (KDA_ACT_SILU),
+ * where r holds the sequence's rows x and, before its first token, the
+ * width - 1 rows of initial_state (zeros when NULL).
+ *
+ *   x, out          [batch, seq_len, channels]      dtype (rows x_stride, out_stride apart)
+ *   weight          [channels, width]               fp32
+ *   bias            [channels] or NULL              fp32
+ *   initial_state,
+ *   final_state     [N, width - 1, channels] or NULL  dtype
+ *
+ * final_state receives the last width - 1 rows of (initial_state, x) of each
+ * sequence, unrounded copies: a sequence shorter than that keeps rows of its
+ * initial state, an empty one all of them.  Any number of channels; rows whose
+ * starts and lengths are multiples of 16 bytes are read in 16-byte pieces.
+ */
+int kda_short_conv_fwd(const void *x, const float *weight, const float *bias,
+                       const void *initial_state, const int32_t *cu_seqlens, void *out,
+                       void *final_state, int32_t batch, int32_t seq_len, int32_t channels,
+                       int32_t width, int64_t x_stride, int64_t out_stride, int32_t num_seqs,
+                       int32_t activation, int32_t dtype, hipStream_t stream);
+
+/*
+ * kda_short_conv_bwd -- gradients of kda_short_conv_fwd for d_out (of out) and
+ * d_final_state (of final_state; NULL = zero).  z is computed again from x.
+ *   dx               [batch, seq_len, channels]        dtype
+ *   dweight          [channels, width]                 fp32
+ *   dbias            [channels] or NULL                fp32
+ *   d_initial_state  [N, width - 1, channels] or NULL  dtype
+ */
+int kda_short_conv_bwd(const void *x, const float *weight, const float *bias,
+                       const void *initial_state, const int32_t *cu_seqlens, const void *d_out,
+                       const void *d_final_state, void *dx, float *dweight, float *dbias,
+                       void *d_initial_state, int32_t batch, int32_t seq_len, int32_t channels,
+                       int32_t width, int64_t x_stride, int64_t d_out_stride, int64_t dx_stride,
+                       int32_t num_seqs, int32_t activation, int32_t dtype, void *workspace,
+                       int64_t workspace_bytes, hipStream_t stream);
+int64_t kda_short_conv_bwd_workspace_size(int32_t batch, int32_t seq_len, int32_t channels,
+                                          int32_t width);
+
+/*
+ * kda_short_conv_step -- one token of each of `batch` sessions: out as above
+ * from (state, x), then state moves on by one row, in place.
+ *   x, out  [batch, channels] dtype;  state  [batch, width - 1, channels] dtype
+ */
+int kda_short_conv_step(const void *x, const float *weight, const float *bias, void *state,
+                        void *out, int32_t batch, int32_t channels, int32_t width,
+                        int64_t x_stride, int64_t out_stride, int32_t activation, int32_t dtype,
+                        hipStream_t stream);
+
+/*
+ * kda_qk_norm_fwd -- every head of q and k divided by its norm, times a weight
+ * per channel, then its first rotary_dim channels rotated by the token's
+ * position, in one pass:
+ *     y = x * weight / sqrt(ss + eps),  ss = sum x^2 (L2) or mean x^2 (RMS),
+ *     (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin) for each pair i,
+ * with pairs (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when
+ * interleaved != 0, i < rotary_dim / 2, and cos | sin taken from row
+ * positions[token] of the table:
+ *   q, out_q   [tokens, q_heads, head_dim]   dtype (rows *_stride apart)
+ *   k, out_k   [tokens, k_heads, head_dim]   dtype; k_heads may be 0
+ *   q_weight, k_weight  [head_dim] or NULL (ones)                fp32
+ *   table      [table_rows, rotary_dim]: cos, then sin           fp32
+ *   positions  [tokens]  int32; values outside the table are moved into it
+ * head_dim is 64 or 128; rotary_dim a multiple of 16, at most head_dim, 0 = no
+ * rotation (table and positions are then not read).  Row starts of q, k and
+ * the outputs and the table are 16-byte aligned.
+ */
+int kda_qk_norm_fwd(const void *q, const void *k, const float *q_weight, const float *k_weight,
+                    const float *table, const int32_t *positions, void *out_q, void *out_k,
+                    int32_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                    int32_t rotary_dim, int32_t table_rows, int64_t q_stride, int64_t k_stride,
+                    int64_t out_q_stride, int64_t out_k_stride, float eps, int32_t norm,
+                    int32_t interleaved, int32_t dtype, hipStream_t stream);
+
+/*
+ * kda_qk_norm_bwd -- gradients of kda_qk_norm_fwd for d_out_q and d_out_k,
+ * from its inputs:
+ *   dq, dk like q and k;  dq_weight, dk_weight [head_dim] fp32 or NULL.
+ * The workspace is read only when a weight's gradient is asked for.
+ */
+int kda_qk_norm_bwd(const void *q, const void *k, const float *q_weight, const float *k_weight,
+                    const float *table, const int32_t *positions, const void *d_out_q,
+                    const void *d_out_k, void *dq, void *dk, float *dq_weight, float *dk_weight,
+                    int32_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                    int32_t rotary_dim, int32_t table_rows, int64_t q_stride, int64_t k_stride,
+                    int64_t d_out_q_stride, int64_t d_out_k_stride, int64_t dq_stride,
+                    int64_t dk_stride, float eps, int32_t norm, int32_t interleaved,
+                    int32_t dtype, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+int64_t kda_qk_norm_bwd_workspace_size(int32_t tokens, int32_t q_heads, int32_t k_heads,
+                                       int32_t head_dim);
+
+#ifdef __cplusplus
+} /* extern "C" */
+#endif
+
+#endif /* KDA_LAYER_H_ */
