@@ -340,3 +340,173 @@ int kda_qk_norm_bwd(const void *q, const void *k, const float *q_weight, const f
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------ state space scan
+namespace {
+
+// Sizes and supported configurations of the scan.
+int check_ssm_dims(int32_t heads, int32_t groups, int32_t p, int32_t n, int32_t dtype) {
+    if (heads < 0 || groups < 0 || p <= 0 || n <= 0) return KDA_ERR_SHAPE;
+    if (heads > 0 && (groups == 0 || heads % groups != 0)) return KDA_ERR_SHAPE;
+    if (!elem_size(dtype)) return KDA_ERR_UNSUPPORTED;
+    if ((p != 64 && p != 128) || (n != 64 && n != 128)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+// A tensor of `rows` token rows of `len` elements: stride and alignment.
+int check_ssm_rows(const void *t, int64_t rows, int64_t len, int64_t stride, int esz) {
+    if (rows > 0 && len > 0) {
+        if (stride < len) return KDA_ERR_SHAPE;
+        if (!t) return KDA_ERR_NULL;
+        if (stride * esz % 16 != 0) return KDA_ERR_ALIGN;
+    }
+    return aligned16(t) ? KDA_OK : KDA_ERR_ALIGN;
+}
+
+// How a call's sequences are cut (host rule, from sizes alone): pieces of
+// `len` tokens, or one piece per sequence (split = false).
+struct PiecePlan {
+    bool split;
+    int32_t len;
+};
+PiecePlan piece_plan(const kda::Seqs &s, int32_t heads) {
+    const int64_t want = 1024;  // workgroups in flight that fill the chip
+    // equal rows: every (sequence, head) is as long as the others
+    const bool enough = !s.cu && (int64_t)s.num * heads >= want / 2;
+    int64_t len = ((int64_t)s.total * heads + want - 1) / want;
+    len = (len + 63) / 64 * 64;
+    if (len < 256) len = 256;
+    if (len > (1 << 20)) len = 1 << 20;
+    const int64_t longest = s.cu ? s.total : s.seq_len;
+    if (enough || longest <= len) {
+        int64_t whole = (longest + 63) / 64 * 64;
+        return {false, (int32_t)(whole < 64 ? 64 : (whole > INT32_MAX - 63 ? INT32_MAX - 63 : whole))};
+    }
+    return {true, (int32_t)len};
+}
+struct SsmSpace {
+    int64_t states, decay;  // floats of the piece states, doubles of their decays
+    int64_t bytes() const { return 8 * ((decay + 1) / 2 * 2) + 4 * states; }
+};
+SsmSpace ssm_space(const kda::Seqs &s, int32_t heads, int32_t p, int32_t n) {
+    const PiecePlan plan = piece_plan(s, heads);
+    if (!plan.split || s.num == 0) return {0, 0};
+    const int64_t count = ((int64_t)s.total / plan.len + s.num + 1) * heads;
+    return {count * p * n, count};
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t kda_ssm_chunk_fwd_workspace_size(int32_t batch, int32_t seq_len, int32_t num_seqs,
+                                         int32_t num_heads, int32_t head_dim, int32_t state_dim) {
+    static const int32_t packed = 0;  // stands for offsets; never read
+    kda::Seqs seqs;
+    if (check_seqs(num_seqs > 0 ? &packed : nullptr, batch, seq_len, num_seqs, &seqs) != KDA_OK ||
+        check_ssm_dims(num_heads, 1, head_dim, state_dim, kda::kDtypeF32) != KDA_OK)
+        return -1;
+    return ssm_space(seqs, num_heads, head_dim, state_dim).bytes();
+}
+
+int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void *B,
+                      const void *C, const float *D, const float *initial_state,
+                      const int32_t *cu_seqlens, void *out, float *final_state, int32_t batch,
+                      int32_t seq_len, int32_t num_heads, int32_t num_groups, int32_t head_dim,
+                      int32_t state_dim, int64_t x_stride, int64_t b_stride, int64_t c_stride,
+                      int64_t out_stride, int32_t num_seqs, int32_t dtype, void *workspace,
+                      int64_t workspace_bytes, hipStream_t stream) {
+    kda::Seqs seqs;
+    int st = check_seqs(cu_seqlens, batch, seq_len, num_seqs, &seqs);
+    if (st != KDA_OK) return st;
+    if ((st = check_ssm_dims(num_heads, num_groups, head_dim, state_dim, dtype)) != KDA_OK)
+        return st;
+    const int esz = elem_size(dtype);
+    const int64_t xl = (int64_t)num_heads * head_dim;
+    const int64_t bl = num_heads > 0 ? (int64_t)num_groups * state_dim : 0;
+    const int64_t th = (int64_t)seqs.total * num_heads;
+    if (th > 0 && (!dt || !A)) return KDA_ERR_NULL;
+    if ((st = check_ssm_rows(x, seqs.total, xl, x_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(B, seqs.total, bl, b_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(C, seqs.total, bl, c_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(out, seqs.total, xl, out_stride, esz)) != KDA_OK)
+        return st;
+    const SsmSpace space = ssm_space(seqs, num_heads, head_dim, state_dim);
+    if (space.bytes() > 0 && !workspace) return KDA_ERR_NULL;
+    if (workspace_bytes < space.bytes()) return KDA_ERR_SHAPE;
+    if (!aligned4(dt) || !aligned4(A) || !aligned4(D) || !aligned16(initial_state) ||
+        !aligned16(final_state) || !aligned4(cu_seqlens) || !aligned16(workspace))
+        return KDA_ERR_ALIGN;
+    const uint64_t state = (uint64_t)seqs.num * xl * state_dim * 4;
+    const Range outs[] = {rows_range(out, seqs.total, xl, out_stride, esz),
+                          {workspace, (uint64_t)space.bytes()},
+                          {final_state, state}};
+    const Range ins[] = {rows_range(x, seqs.total, xl, x_stride, esz),
+                         rows_range(B, seqs.total, bl, b_stride, esz),
+                         rows_range(C, seqs.total, bl, c_stride, esz),
+                         {dt, (uint64_t)th * 4},
+                         {A, (uint64_t)num_heads * 4},
+                         {D, (uint64_t)num_heads * 4},
+                         {cu_seqlens, (uint64_t)(seqs.num + 1) * 4},
+                         {final_state == initial_state ? nullptr : initial_state, state}};
+    if ((st = check_alias(outs, ins)) != KDA_OK) return st;
+    if (final_state == initial_state &&  // in place: still apart from the other outputs
+        (overlap(outs[0], {initial_state, state}) || overlap(outs[1], {initial_state, state})))
+        return KDA_ERR_ALIAS;
+    if (seqs.num == 0 || num_heads == 0) return KDA_OK;
+    if ((st = check_device()) != KDA_OK) return st;
+    const char *where = "kda_ssm_chunk_fwd";
+    if (debug_mode() &&
+        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
+        return st;
+    kda::SsmScan a = {};
+    a.x = x, a.k = B, a.c = C, a.dt = dt, a.A = A, a.D = D, a.state0 = initial_state;
+    a.out = out, a.final_state = final_state, a.seqs = seqs;
+    a.heads = num_heads, a.groups = num_groups, a.p = head_dim, a.n = state_dim;
+    a.piece = piece_plan(seqs, num_heads).len;
+    a.x_stride = x_stride, a.k_stride = b_stride, a.c_stride = c_stride;
+    a.out_stride = out_stride;
+    if (space.states > 0) {
+        a.seg_decay = static_cast<double *>(workspace);
+        a.seg_states = reinterpret_cast<float *>(a.seg_decay + (space.decay + 1) / 2 * 2);
+    }
+    return launch_status(kda::launch_ssm_scan(a, kda::kSsmOut, dtype, stream), stream, where);
+}
+
+int kda_ssm_decode_step(const void *x, const float *dt, const float *A, const void *B,
+                        const void *C, const float *D, float *state, void *out, int32_t batch,
+                        int32_t num_heads, int32_t num_groups, int32_t head_dim,
+                        int32_t state_dim, int64_t x_stride, int64_t b_stride, int64_t c_stride,
+                        int64_t out_stride, int32_t dtype, hipStream_t stream) {
+    if (batch < 0) return KDA_ERR_SHAPE;
+    int st = check_ssm_dims(num_heads, num_groups, head_dim, state_dim, dtype);
+    if (st != KDA_OK) return st;
+    const int esz = elem_size(dtype);
+    const int64_t xl = (int64_t)num_heads * head_dim;
+    const int64_t bl = num_heads > 0 ? (int64_t)num_groups * state_dim : 0;
+    const uint64_t units = (uint64_t)batch * num_heads;
+    if (units > INT32_MAX / 4) return KDA_ERR_UNSUPPORTED;
+    if (units > 0 && (!dt || !A || !state)) return KDA_ERR_NULL;
+    if ((st = check_ssm_rows(x, batch, xl, x_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(B, batch, bl, b_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(C, batch, bl, c_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(out, batch, xl, out_stride, esz)) != KDA_OK)
+        return st;
+    if (!aligned4(dt) || !aligned4(A) || !aligned4(D) || !aligned16(state)) return KDA_ERR_ALIGN;
+    const Range outs[] = {rows_range(out, batch, xl, out_stride, esz),
+                          {state, units * head_dim * state_dim * 4}};
+    const Range ins[] = {rows_range(x, batch, xl, x_stride, esz),
+                         rows_range(B, batch, bl, b_stride, esz),
+                         rows_range(C, batch, bl, c_stride, esz),
+                         {dt, units * 4},
+                         {A, (uint64_t)num_heads * 4},
+                         {D, (uint64_t)num_heads * 4}};
+    if ((st = check_alias(outs, ins)) != KDA_OK) return st;
+    if (units == 0) return KDA_OK;
+    if ((st = check_device()) != KDA_OK) return st;
+    const kda::SsmStep a = {x, B, C, dt, A, D, state, out, batch, num_heads, num_groups,
+                            head_dim, state_dim, x_stride, b_stride, c_stride, out_stride};
+    return launch_status(kda::launch_ssm_step(a, dtype, stream), stream, "kda_ssm_decode_step");
+}
+
+}  // extern "C"

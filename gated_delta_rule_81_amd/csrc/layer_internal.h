@@ -47,4 +47,35 @@ int launch_qk_norm_fwd(const QkArgs &a, hipStream_t stream);
 int launch_qk_norm_bwd(const QkArgs &a, hipStream_t stream);
 int64_t qk_norm_bwd_workspace_floats(int64_t tokens, int64_t heads, int head_dim);
 
+// The scan's walk over the sequences.  kSsmOut: y (and final states).
+// kSsmStates: the state entering every block, in block_states.  kSsmStatesRev:
+// the same from the right for the loss gradient of the state (x = d_out, k = C,
+// state0 = d_final_state, final_state = d_initial_state): what arrives at every
+// block's end.  With seg_states the sequences are cut into pieces of `piece`
+// tokens that run at once (seg_states: a state per piece number and head,
+// seg_decay: a double each); without, `piece` is at least every sequence's
+// length.
+constexpr int kSsmOut = 0, kSsmStates = 1, kSsmStatesRev = 2;
+struct SsmScan {
+    const void *x, *k, *c;
+    const float *dt, *A, *D, *state0;
+    void *out;
+    float *final_state, *seg_states, *block_states;
+    double *seg_decay;
+    Seqs seqs;
+    int32_t heads, groups, p, n, piece;
+    int64_t x_stride, k_stride, c_stride, out_stride;
+};
+int launch_ssm_scan(const SsmScan &a, int mode, int dtype, hipStream_t stream);
+
+struct SsmStep {
+    const void *x, *B, *C;
+    const float *dt, *A, *D;
+    float *state;
+    void *out;
+    int32_t batch, heads, groups, p, n;
+    int64_t x_stride, b_stride, c_stride, out_stride;
+};
+int launch_ssm_step(const SsmStep &a, int dtype, hipStream_t stream);
+
 }  // namespace kda

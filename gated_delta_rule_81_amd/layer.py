@@ -307,3 +307,95 @@ def qk_norm_bwd(q: torch.Tensor, k: torch.Tensor, d_out_q: torch.Tensor, d_out_k
           dqs, dks, eps, _NORMS[kind], int(bool(interleaved)), dt, _ptr(workspace),
           0 if workspace is None else workspace.numel())
     return g
+
+
+# ---------------------------------------------------------------- state space scan
+def _ssm_common(x, dt, A, B, C, D, lead):
+    H, P = x.shape[lead:]
+    if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
+        raise ValueError("B must be [..., G, N] with the leading axes of x")
+    G, N = B.shape[lead:]
+    dev, dtype = x.device, x.dtype
+    if H % max(G, 1) or (H and not G):
+        raise ValueError(f"{H} heads cannot share {G} groups of B and C")
+    strides = (_rows(x, "x", dtype, x.shape, dev, lead),
+               _rows(B, "B", dtype, (*x.shape[:lead], G, N), dev, lead),
+               _rows(C, "C", dtype, (*x.shape[:lead], G, N), dev, lead))
+    for t, name, shape in ((dt, "dt", x.shape[: lead + 1]), (A, "A", (H,))):
+        if t is None:
+            raise TypeError(f"{name} must be a tensor")
+        _expect(t, name, torch.float32, shape, dev)
+    _expect(D, "D", torch.float32, (H,), dev)
+    return H, P, G, N, strides
+
+
+def ssm_workspace_size(batch: int, seq_len: int, num_heads: int, head_dim: int, state_dim: int,
+                       num_seqs: int = 0) -> int:
+    """Bytes of workspace ``ssm_chunk_fwd`` needs (``num_seqs``: packed sequences,
+    0 for a batch of equal rows)."""
+    n = lib().kda_ssm_chunk_fwd_workspace_size(batch, seq_len, num_seqs, num_heads, head_dim,
+                                               state_dim)
+    if n < 0:
+        raise ValueError("invalid sizes")
+    return int(n)
+
+
+def ssm_chunk_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                  C: torch.Tensor, D: Optional[torch.Tensor] = None,
+                  initial_state: Optional[torch.Tensor] = None,
+                  cu_seqlens: Optional[torch.Tensor] = None, *,
+                  workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  final_state: Optional[torch.Tensor] = None, output_final_state: bool = True
+                  ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Selective state space scan over whole sequences (``kda_ssm_chunk_fwd``):
+    S_t = exp(dt_t A) S_{t-1} + dt_t x_t B_t^T, y_t = S_t C_t + D x_t per head.
+
+    x: [B, T, H, P], B, C: [B, T, G, N] float32 or bfloat16 (may be slices of
+    wider rows), P and N 64 or 128, H a multiple of G (heads H / G * j .. share
+    row j); dt: [B, T, H] fp32 as it enters the formula; A: [H], D: [H] or None,
+    fp32, dt * A <= 0; initial_state: [n, H, P, N] fp32 or None; cu_seqlens as
+    for ``chunk_fwd``.  Returns (out [B, T, H, P], final_state or None);
+    ``final_state`` may be ``initial_state`` itself.
+    """
+    dtc = _dtype(x, "x")
+    if x.dim() != 4:
+        raise ValueError("x must be [B, T, H, P]")
+    b, T = x.shape[:2]
+    dev = x.device
+    H, P, G, N, (xs, bs, cs) = _ssm_common(x, dt, A, B, C, D, 2)
+    n = _num_seqs(cu_seqlens, b, dev)
+    state = (n, H, P, N)
+    _expect(initial_state, "initial_state", torch.float32, state, dev)
+    out = _out(out, x.shape, x.dtype, dev)
+    os = _rows(out, "out", x.dtype, x.shape, dev, 2)
+    if final_state is None and output_final_state:
+        final_state = torch.empty(state, dtype=torch.float32, device=dev)
+    _expect(final_state, "final_state", torch.float32, state, dev)
+    packed = n if cu_seqlens is not None else 0
+    need = lib().kda_ssm_chunk_fwd_workspace_size(b, T, packed, H, P, N)
+    ws = _workspace(workspace, max(need, 0), dev) if need or workspace is not None else None
+    _call("kda_ssm_chunk_fwd", dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+          _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state), b, T, H, G, P, N,
+          xs, bs, cs, os, packed, dtc, _ptr(ws), 0 if ws is None else ws.numel())
+    return out, final_state
+
+
+def ssm_decode_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                    C: torch.Tensor, state: torch.Tensor, D: Optional[torch.Tensor] = None, *,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``ssm_chunk_fwd`` for one token per session (``kda_ssm_decode_step``): x
+    [B, H, P], dt [B, H], B, C [B, G, N], state [B, H, P, N] fp32 updated in
+    place.  Returns out [B, H, P]."""
+    dtc = _dtype(x, "x")
+    if x.dim() != 3:
+        raise ValueError("x must be [B, H, P]")
+    b, dev = x.shape[0], x.device
+    H, P, G, N, (xs, bs, cs) = _ssm_common(x, dt, A, B, C, D, 1)
+    if state is None:
+        raise TypeError("state must be a tensor")
+    _expect(state, "state", torch.float32, (b, H, P, N), dev)
+    out = _out(out, x.shape, x.dtype, dev)
+    os = _rows(out, "out", x.dtype, x.shape, dev, 1)
+    _call("kda_ssm_decode_step", dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+          _ptr(state), _ptr(out), b, H, G, P, N, xs, bs, cs, os, dtc)
+    return out

@@ -143,6 +143,49 @@ int kda_qk_norm_bwd(const void *q, const void *k, const float *q_weight, const f
 int64_t kda_qk_norm_bwd_workspace_size(int32_t tokens, int32_t q_heads, int32_t k_heads,
                                        int32_t head_dim);
 
+/*
+ * kda_ssm_chunk_fwd -- the selective state space scan over whole sequences:
+ * per head, with one decay per token,
+ *     S_t = exp(dt_t A) S_{t-1} + dt_t x_t B_t^T,   y_t = S_t C_t + D x_t,
+ * computed in blocks of 64 tokens (fp32 inputs: 32), in parallel inside a block
+ * and, for long sequences, in several pieces at once.
+ *
+ *   x, out   [batch, seq_len, num_heads, head_dim]    dtype (rows *_stride apart)
+ *   B, C     [batch, seq_len, num_groups, state_dim]  dtype (rows *_stride apart)
+ *   dt       [batch, seq_len, num_heads]              fp32
+ *   A        [num_heads] fp32;  D  [num_heads] fp32 or NULL (zero)
+ *   initial_state, final_state  [N, num_heads, head_dim, state_dim] fp32
+ *                               (the [.., d_v, d_k] layout of every state) or NULL
+ *
+ * Heads num_heads / num_groups * j .. share row j of B and C.  head_dim and
+ * state_dim are 64 or 128 each.  dt and A are finite, dt * A <= 0 (any size: a
+ * decay of zero included); a token with dt = 0 leaves the state as it is.
+ * NaN and infinities in x, B or C propagate, but may also turn into NaN where
+ * the formula has an infinity.  Row starts of x, B, C and out are 16-byte
+ * aligned.  final_state may be initial_state itself.
+ */
+int64_t kda_ssm_chunk_fwd_workspace_size(int32_t batch, int32_t seq_len, int32_t num_seqs,
+                                         int32_t num_heads, int32_t head_dim, int32_t state_dim);
+int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void *B,
+                      const void *C, const float *D, const float *initial_state,
+                      const int32_t *cu_seqlens, void *out, float *final_state, int32_t batch,
+                      int32_t seq_len, int32_t num_heads, int32_t num_groups, int32_t head_dim,
+                      int32_t state_dim, int64_t x_stride, int64_t b_stride, int64_t c_stride,
+                      int64_t out_stride, int32_t num_seqs, int32_t dtype, void *workspace,
+                      int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * kda_ssm_decode_step -- one token of each of `batch` sessions, the state
+ * updated in place.  x, out [batch, num_heads, head_dim], B, C [batch,
+ * num_groups, state_dim], dt [batch, num_heads], state [batch, num_heads,
+ * head_dim, state_dim] fp32; everything else as above.
+ */
+int kda_ssm_decode_step(const void *x, const float *dt, const float *A, const void *B,
+                        const void *C, const float *D, float *state, void *out, int32_t batch,
+                        int32_t num_heads, int32_t num_groups, int32_t head_dim,
+                        int32_t state_dim, int64_t x_stride, int64_t b_stride, int64_t c_stride,
+                        int64_t out_stride, int32_t dtype, hipStream_t stream);
+
 #ifdef __cplusplus
 } /* extern "C" */
 #endif
