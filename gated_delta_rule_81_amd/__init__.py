@@ -16,8 +16,8 @@ The operators around the recurrence (include/kda_layer.h):
 """
 from ._lib import KdaError, lib
 from .layer import (qk_norm, qk_norm_bwd, qk_norm_bwd_workspace_size, short_conv, short_conv_bwd,
-                    short_conv_bwd_workspace_size, short_conv_step, ssm_chunk_fwd,
-                    ssm_decode_step, ssm_workspace_size)
+                    short_conv_bwd_workspace_size, short_conv_step, ssm_bwd_workspace_size,
+                    ssm_chunk_bwd, ssm_chunk_fwd, ssm_decode_step, ssm_workspace_size)
 from .ops import (bwd_workspace_size, chunk_bwd, chunk_fwd, chunk_fwd_segmented,
                   chunk_fwd_segmented_noalloc, chunk_fwd_snapshots, decode_step,
                   segmented_workspace_size)
@@ -26,5 +26,5 @@ __all__ = ["chunk_fwd", "chunk_fwd_segmented", "chunk_fwd_segmented_noalloc",
            "chunk_fwd_snapshots", "chunk_bwd", "decode_step", "segmented_workspace_size",
            "bwd_workspace_size", "short_conv", "short_conv_bwd",
            "short_conv_bwd_workspace_size", "short_conv_step", "qk_norm", "qk_norm_bwd",
-           "qk_norm_bwd_workspace_size", "ssm_chunk_fwd", "ssm_decode_step",
-           "ssm_workspace_size", "KdaError", "lib"]
+           "qk_norm_bwd_workspace_size", "ssm_chunk_fwd", "ssm_chunk_bwd", "ssm_decode_step",
+           "ssm_workspace_size", "ssm_bwd_workspace_size", "KdaError", "lib"]

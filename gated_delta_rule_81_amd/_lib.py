@@ -73,6 +73,10 @@ LAYER_SIGNATURES = {
     "kda_ssm_chunk_fwd": ([_vp, _fp, _fp, _vp, _vp, _fp, _fp, _vp, _vp, _fp, _i32, _i32, _i32,
                            _i32, _i32, _i32, _i64, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp],
                           ctypes.c_int),
+    "kda_ssm_chunk_bwd_workspace_size": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32], _i64),
+    "kda_ssm_chunk_bwd": ([_vp, _fp, _fp, _vp, _vp, _fp, _fp, _vp, _vp, _fp, _vp, _fp, _fp, _vp,
+                           _vp, _fp, _fp, _i32, _i32, _i32, _i32, _i32, _i32, _i64, _i64, _i64,
+                           _i64, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _vp], ctypes.c_int),
     "kda_ssm_decode_step": ([_vp, _fp, _fp, _vp, _vp, _fp, _fp, _vp, _i32, _i32, _i32, _i32, _i32,
                              _i64, _i64, _i64, _i64, _i32, _vp], ctypes.c_int),
 }

@@ -473,6 +473,151 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
     return launch_status(kda::launch_ssm_scan(a, kda::kSsmOut, dtype, stream), stream, where);
 }
 
+}  // extern "C"
+
+namespace {
+
+// The backward's workspace: piece decays and states (as the forward's), the
+// states at every block from both sides, the parts of dA and dD, and with
+// several sets of heads the parts of dB and dC.
+struct SsmBwdSpace {
+    SsmSpace pieces;
+    int64_t blocks, states, params, bc;  // block numbers; floats of each part
+    int32_t sets;
+    int64_t bytes() const { return pieces.bytes() + 4 * (2 * states + params + bc); }
+};
+SsmBwdSpace ssm_bwd_space(const kda::Seqs &s, int32_t heads, int32_t groups, int32_t p, int32_t n,
+                          int32_t dtype) {
+    SsmBwdSpace w = {};
+    if (s.num == 0 || heads == 0) return w;
+    w.pieces = ssm_space(s, heads, p, n);
+    const int64_t block = dtype == kda::kDtypeBf16 ? 64 : 32;
+    w.blocks = (int64_t)s.total / block + s.num + 1;
+    w.states = w.blocks * heads * p * n;
+    w.params = (2 * w.blocks * heads + 3) / 4 * 4;
+    // sets: enough workgroups to fill the chip twice over
+    const int64_t units = w.blocks * groups, per_group = heads / groups;
+    int64_t sets = (512 + units - 1) / units;
+    sets = sets > per_group ? per_group : sets;
+    const int64_t per_set = (per_group + sets - 1) / sets;
+    w.sets = (int32_t)((per_group + per_set - 1) / per_set);
+    w.bc = w.sets > 1 ? 2 * w.sets * (int64_t)s.total * groups * n : 0;
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t kda_ssm_chunk_bwd_workspace_size(int32_t batch, int32_t seq_len, int32_t num_seqs,
+                                         int32_t num_heads, int32_t num_groups, int32_t head_dim,
+                                         int32_t state_dim, int32_t dtype) {
+    static const int32_t packed = 0;  // stands for offsets; never read
+    kda::Seqs seqs;
+    if (check_seqs(num_seqs > 0 ? &packed : nullptr, batch, seq_len, num_seqs, &seqs) != KDA_OK ||
+        check_ssm_dims(num_heads, num_groups, head_dim, state_dim, dtype) != KDA_OK)
+        return -1;
+    return ssm_bwd_space(seqs, num_heads, num_groups, head_dim, state_dim, dtype).bytes();
+}
+
+int kda_ssm_chunk_bwd(const void *x, const float *dt, const float *A, const void *B,
+                      const void *C, const float *D, const float *initial_state,
+                      const int32_t *cu_seqlens, const void *d_out, const float *d_final_state,
+                      void *dx, float *ddt, float *dA, void *dB, void *dC, float *dD,
+                      float *d_initial_state, int32_t batch, int32_t seq_len, int32_t num_heads,
+                      int32_t num_groups, int32_t head_dim, int32_t state_dim, int64_t x_stride,
+                      int64_t b_stride, int64_t c_stride, int64_t d_out_stride,
+                      int64_t dx_stride, int64_t db_stride, int64_t dc_stride, int32_t num_seqs,
+                      int32_t dtype, void *workspace, int64_t workspace_bytes,
+                      hipStream_t stream) {
+    kda::Seqs seqs;
+    int st = check_seqs(cu_seqlens, batch, seq_len, num_seqs, &seqs);
+    if (st != KDA_OK) return st;
+    if ((st = check_ssm_dims(num_heads, num_groups, head_dim, state_dim, dtype)) != KDA_OK)
+        return st;
+    const int esz = elem_size(dtype);
+    const int64_t xl = (int64_t)num_heads * head_dim;
+    const int64_t bl = num_heads > 0 ? (int64_t)num_groups * state_dim : 0;
+    const int64_t th = (int64_t)seqs.total * num_heads;
+    if (th > 0 && (!dt || !ddt)) return KDA_ERR_NULL;
+    if (num_heads > 0 && (!A || !dA)) return KDA_ERR_NULL;
+    if (dD && !D) return KDA_ERR_NULL;  // the gradient of what was not given
+    if ((st = check_ssm_rows(x, seqs.total, xl, x_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(B, seqs.total, bl, b_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(C, seqs.total, bl, c_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(d_out, seqs.total, xl, d_out_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(dx, seqs.total, xl, dx_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(dB, seqs.total, bl, db_stride, esz)) != KDA_OK ||
+        (st = check_ssm_rows(dC, seqs.total, bl, dc_stride, esz)) != KDA_OK)
+        return st;
+    const SsmBwdSpace w =
+        ssm_bwd_space(seqs, num_heads, num_groups, head_dim, state_dim, dtype);
+    if (w.bytes() > 0 && !workspace) return KDA_ERR_NULL;
+    if (workspace_bytes < w.bytes()) return KDA_ERR_SHAPE;
+    if (!aligned4(dt) || !aligned4(A) || !aligned4(D) || !aligned16(initial_state) ||
+        !aligned16(d_final_state) || !aligned16(d_initial_state) || !aligned4(cu_seqlens) ||
+        !aligned4(ddt) || !aligned4(dA) || !aligned4(dD) || !aligned16(workspace))
+        return KDA_ERR_ALIGN;
+    const uint64_t state = (uint64_t)seqs.num * xl * state_dim * 4, hb = (uint64_t)num_heads * 4;
+    const Range outs[] = {rows_range(dx, seqs.total, xl, dx_stride, esz),
+                          rows_range(dB, seqs.total, bl, db_stride, esz),
+                          rows_range(dC, seqs.total, bl, dc_stride, esz),
+                          {ddt, (uint64_t)th * 4},
+                          {dA, hb},
+                          {dD, hb},
+                          {d_initial_state, state},
+                          {workspace, (uint64_t)w.bytes()}};
+    const Range ins[] = {rows_range(x, seqs.total, xl, x_stride, esz),
+                         rows_range(B, seqs.total, bl, b_stride, esz),
+                         rows_range(C, seqs.total, bl, c_stride, esz),
+                         rows_range(d_out, seqs.total, xl, d_out_stride, esz),
+                         {dt, (uint64_t)th * 4},
+                         {A, hb},
+                         {D, hb},
+                         {cu_seqlens, (uint64_t)(seqs.num + 1) * 4},
+                         {initial_state, state},
+                         {d_final_state, state}};
+    if ((st = check_alias(outs, ins)) != KDA_OK) return st;
+    if (num_heads == 0) return KDA_OK;
+    if ((st = check_device()) != KDA_OK) return st;
+    const char *where = "kda_ssm_chunk_bwd";
+    if (debug_mode() &&
+        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
+        return st;
+    kda::SsmGrad g = {};
+    g.dA = dA, g.dD = dD, g.seqs = seqs, g.heads = num_heads, g.groups = num_groups;
+    if (seqs.num > 0) {
+        kda::SsmScan a = {};
+        a.x = x, a.k = B, a.dt = dt, a.A = A, a.state0 = initial_state;
+        a.seqs = seqs, a.heads = num_heads, a.groups = num_groups;
+        a.p = head_dim, a.n = state_dim, a.piece = piece_plan(seqs, num_heads).len;
+        a.x_stride = x_stride, a.k_stride = b_stride;
+        char *at = static_cast<char *>(workspace);
+        if (w.pieces.states > 0) {
+            a.seg_decay = reinterpret_cast<double *>(at);
+            a.seg_states = reinterpret_cast<float *>(a.seg_decay + (w.pieces.decay + 1) / 2 * 2);
+        }
+        float *s_states = reinterpret_cast<float *>(at + w.pieces.bytes());
+        float *e_states = s_states + w.states;
+        a.block_states = s_states;
+        int rc = kda::launch_ssm_scan(a, kda::kSsmStates, dtype, stream);
+        a.x = d_out, a.k = C, a.x_stride = d_out_stride, a.k_stride = c_stride;
+        a.state0 = d_final_state, a.final_state = d_initial_state, a.block_states = e_states;
+        if (rc == 0) rc = kda::launch_ssm_scan(a, kda::kSsmStatesRev, dtype, stream);
+        if (rc != 0) return launch_status(rc, stream, where);
+        g.x = x, g.B = B, g.C = C, g.dy = d_out, g.dt = dt, g.A = A, g.D = D;
+        g.s_states = s_states, g.e_states = e_states;
+        g.dx = dx, g.dB = dB, g.dC = dC, g.ddt = ddt;
+        g.part_a = e_states + w.states, g.part_d = g.part_a + w.blocks * num_heads;
+        g.part_bc = g.part_a + w.params;
+        g.p = head_dim, g.n = state_dim, g.sets = w.sets, g.blocks = w.blocks;
+        g.x_stride = x_stride, g.b_stride = b_stride, g.c_stride = c_stride;
+        g.dy_stride = d_out_stride, g.dx_stride = dx_stride;
+        g.db_stride = db_stride, g.dc_stride = dc_stride;
+    }
+    return launch_status(kda::launch_ssm_grad(g, dtype, stream), stream, where);
+}
+
 int kda_ssm_decode_step(const void *x, const float *dt, const float *A, const void *B,
                         const void *C, const float *D, float *state, void *out, int32_t batch,
                         int32_t num_heads, int32_t num_groups, int32_t head_dim,

@@ -68,6 +68,22 @@ struct SsmScan {
 };
 int launch_ssm_scan(const SsmScan &a, int mode, int dtype, hipStream_t stream);
 
+// The gradients from the states entering every block (s_states) and the loss
+// gradients behind every block (e_states), both [block number][head][n][p]:
+// a.blocks block numbers of 64 (bf16) or 32 tokens.  The heads of a group are
+// worked on in `sets` sets; part_bc (sets > 1): dB and dC of each set, fp32
+// [set][2][token][group][n]; part_a, part_d: [block number][head].
+struct SsmGrad {
+    const void *x, *B, *C, *dy;
+    const float *dt, *A, *D, *s_states, *e_states;
+    void *dx, *dB, *dC;
+    float *ddt, *dA, *dD, *part_a, *part_d, *part_bc;
+    Seqs seqs;
+    int32_t heads, groups, p, n, sets;
+    int64_t blocks, x_stride, b_stride, c_stride, dy_stride, dx_stride, db_stride, dc_stride;
+};
+int launch_ssm_grad(const SsmGrad &a, int dtype, hipStream_t stream);
+
 struct SsmStep {
     const void *x, *B, *C;
     const float *dt, *A, *D;

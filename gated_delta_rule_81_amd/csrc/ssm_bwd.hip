@@ -1,0 +1,484 @@
+// ssm_bwd.hip -- gradients of the state space scan.
+//
+// With S0 the state entering a block of L tokens, E the loss gradient of the
+// state behind it, G = C B^T, dP = dY X^T (both L x L) and L_ts = e^{cum_t - cum_s},
+// s <= t (ssm_scan.hip):
+//   du_s = e^{cum_L - cum_s} E B_s + sum_t G_ts L_ts dy_t,    dx = dt du + D dy
+//   dC_t = e^{cum_t} S0^T dy_t + sum_s Q_ts B_s,   Q_ts = dP_ts L_ts dt_s
+//   dB_s = dt_s e^{cum_L - cum_s} E^T x_s + sum_t Q_ts C_t
+//   dl_r = sum_{s < r <= t} G_ts Q_ts + sum_{t >= r} z_t + sum_{s < r} v_s
+//          + e^{cum_L} <E, S0>            (l_r = dt_r A)
+//     z_t = e^{cum_t} dy_t . S0 C_t,  v_s = dt_s e^{cum_L - cum_s} x_s . E B_s
+//   ddt = x . du + A dl,  dA = sum dt dl,  dD = sum x . dy
+// dB and dC summed over the heads of the group.  dl adds the pairs that l_r
+// stands between: no term is added and taken away again, so it is exact at any
+// decay (as a suffix sum of dy y - u du it would lose e^-l of its digits).
+//
+// Three steps.  The scan (ssm_scan.hip) writes S0 of every block, then, from the
+// right, E of every block, both fp32 and transposed ([N][P]).  Then one
+// workgroup per (block, group, set of heads) loops over its heads with dB and dC
+// in registers: 8 waves, each the owner of 16 columns n of dB and dC and of a
+// 16-token s-tile of du, where G, dP, M and Q never leave registers except Q
+// (to dB's and dC's waves) and E (read by columns n, needed by rows too), as
+// bf16 parts in LDS.  A head of 128 rows is two of 64 that share dt and A: every
+// sum above is linear in the rows.
+#include "ssm_device.h"
+
+namespace kda {
+namespace {
+
+constexpr int kPB = 64;        // state rows a workgroup works on at a time
+constexpr int kGradWaves = 8;
+
+template <typename T, int N>
+__global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
+    constexpr int L = kSsmBlock<T>, NT = kGradWaves * 64, NI = sizeof(T) == 2 ? 1 : 3;
+    constexpr int KQ = sizeof(T) == 2 ? 2 : 3;   // parts of Q (dB and dC only)
+    constexpr int TL = L / 16, PT = TL / 2;      // token tiles; row tiles of du a wave owns
+    constexpr int NTN = N / 16, TG = kGradWaves / NTN, TPW = TL / TG;  // tiles of dB, dC a wave owns
+    constexpr int KT = L / 32;                   // 32-wide steps over tokens
+    typedef Tile<NI, L, N> TK;
+    typedef Tile<NI, L, kPB> TX;
+    typedef Tile<KQ, L, L> TQ;
+    typedef Tile<3, N, kPB> TE;
+    __shared__ __attribute__((aligned(16))) bf16 sb[TK::ELEMS];
+    __shared__ __attribute__((aligned(16))) bf16 sc[TK::ELEMS];
+    __shared__ __attribute__((aligned(16))) bf16 sx[TX::ELEMS];
+    __shared__ __attribute__((aligned(16))) bf16 sy[TX::ELEMS];
+    __shared__ __attribute__((aligned(16))) bf16 sq[TQ::ELEMS];  // Q^T: [s][t]
+    __shared__ __attribute__((aligned(16))) bf16 se[TE::ELEMS];  // E: [n][p]
+    __shared__ __attribute__((aligned(16))) double s_cum[2][L];
+    __shared__ __attribute__((aligned(16))) float s_dt[2][L], s_out[2][L], s_in[2][L];
+    __shared__ float s_all[2];
+    __shared__ float s_pair[TL][L], s_z[NTN][L], s_xdu[8 / TL][L], s_v[8 / TL][L];
+    __shared__ float s_k[NTN], s_d[TL];
+
+    const int64_t units = a.blocks * a.groups * a.sets;
+    const int64_t unit = xcd_unit(units);
+    if (unit < 0) return;
+    const int set = (int)(unit % a.sets), group = (int)(unit / a.sets % a.groups);
+    const int64_t number = unit / a.sets / a.groups;
+    const int per_group = a.heads / a.groups, per_set = (per_group + a.sets - 1) / a.sets;
+    const int h0 = group * per_group + set * per_set;
+    const int h1 = set * per_set + per_set < per_group ? h0 + per_set : (group + 1) * per_group;
+    const Piece pc = find_piece(a.seqs, number, L);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int n = pc.any ? pc.end - pc.beg : 0, t0 = pc.beg;
+    if (n <= 0) {  // no token: nothing to add to dA and dD
+        for (int h = h0 + tid; h < h1; h += NT) {
+            a.part_a[number * a.heads + h] = 0.f;
+            a.part_d[number * a.heads + h] = 0.f;
+        }
+        return;
+    }
+    const int P = a.p, halves = P / kPB;
+    const int count = (h1 > h0 ? h1 - h0 : 0) * halves;  // (head, 64 of its rows) to work on
+    const int is = wave % TL, pg = wave / TL;            // s-tile and row tiles of du
+    const int nt = wave % NTN, tg = wave / NTN;          // columns and token tiles of dB, dC
+    const bool weigher = wave == kGradWaves - 1;
+
+    const T *x = static_cast<const T *>(a.x) + t0 * a.x_stride;
+    const T *dy = static_cast<const T *>(a.dy) + t0 * a.dy_stride;
+    Stage<T, L, kPB, NT> rx, ry;
+    auto load_rows = [&](int i) {
+        const int64_t off = (int64_t)(h0 + i / halves) * P + (i % halves) * kPB;
+        rx.load(x + off, a.x_stride, n, tid);
+        ry.load(dy + off, a.dy_stride, n, tid);
+    };
+    // operand of index n (columns 16 nt ..), k = rows p, of a state stored [N][P]
+    auto load_state = [&](const float *states, int i, float (&f)[kPB / 32][8]) {
+        const float *at = states + (number * a.heads + h0 + i / halves) * (int64_t)(P * N) +
+                          (int64_t)(16 * nt + r) * P + (i % halves) * kPB + 4 * g;
+#pragma unroll
+        for (int ks = 0; ks < kPB / 32; ++ks)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const f32x4 v = __builtin_nontemporal_load(
+                    reinterpret_cast<const f32x4 *>(at + 32 * ks + 16 * q));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[ks][4 * q + e] = v[e];
+            }
+    };
+    float rdt = 0.f, A2 = 0.f, An = 0.f;  // the weigher's head
+    auto load_dt = [&](int i) {
+        const int h = h0 + i / halves;
+        rdt = lane < n ? a.dt[(int64_t)(t0 + lane) * a.heads + h] : 0.f;
+        A2 = a.A[h];
+    };
+    auto weights = [&](int buf) {
+        const double step = (double)rdt * ((double)A2 * kLog2eD);
+        const double cum = wave_prefix(step < -400.0 ? -400.0 : step, lane);
+        const double all = __shfl(cum, 63, 64);
+        if (lane < L) {
+            s_cum[buf][lane] = cum;
+            s_dt[buf][lane] = rdt;
+            s_in[buf][lane] = fast_exp2((float)cum);
+            s_out[buf][lane] = fast_exp2((float)(all - cum));
+        }
+        if (lane == 0) s_all[buf] = fast_exp2((float)all);
+    };
+    float ev[kPB / 32][8], sv[kPB / 32][8];
+    Parts<3> ep[kPB / 32];
+    auto store_e = [&]() {  // E's parts: kept for dB, and to LDS for du
+#pragma unroll
+        for (int ks = 0; ks < kPB / 32; ++ks) {
+            ep[ks] = split<3>(ev[ks]);
+            if (tg == 0)
+#pragma unroll
+                for (int q = 0; q < 3; ++q) {
+                    bf16 *at = se + q * TE::PLANE + (16 * nt + r) * TE::LD + 32 * ks + 4 * g;
+                    const bf16x8 v = ep[ks].v[q];
+                    *reinterpret_cast<bf16x4 *>(at) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+                    *reinterpret_cast<bf16x4 *>(at + 16) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+                }
+        }
+    };
+
+    // the group's rows, and the first head's
+    {
+        Stage<T, L, N, NT> rb, rc;
+        rb.load(static_cast<const T *>(a.B) + t0 * a.b_stride + (int64_t)group * N, a.b_stride, n, tid);
+        rc.load(static_cast<const T *>(a.C) + t0 * a.c_stride + (int64_t)group * N, a.c_stride, n, tid);
+        if (count > 0) {
+            load_rows(0);
+            load_state(a.e_states, 0, ev);
+            load_state(a.s_states, 0, sv);
+            if (weigher) load_dt(0);
+        }
+        rb.template store<TK>(sb, tid);
+        rc.template store<TK>(sc, tid);
+        for (int i = tid; i < TQ::ELEMS; i += NT) sq[i] = static_cast<bf16>(0.f);
+        if (count > 0) {
+            rx.template store<TX>(sx, tid);
+            ry.template store<TX>(sy, tid);
+            store_e();
+            if (weigher) weights(0);
+        }
+    }
+    lds_barrier();
+
+    // G[t][s] of this wave's s-tile (rows t = 16 it + 4 g + e, column s = 16 is + r)
+    f32x4 G[TL];
+#pragma unroll
+    for (int it = 0; it < TL; ++it) {
+        G[it] = zero4();
+        if (it >= is)
+#pragma unroll
+            for (int ks = 0; ks < N / 32; ++ks)
+                G[it] = mma(read_rows<TK, NI>(sc, 16 * it, ks, lane),
+                            read_rows<TK, NI>(sb, 16 * is, ks, lane), G[it]);
+    }
+    // B^T and C^T operands of this wave's columns n
+    Parts<NI> bt[KT], ct[KT];
+#pragma unroll
+    for (int ks = 0; ks < KT; ++ks) {
+        bt[ks] = read_cols<TK, NI>(sb, ks, 16 * nt, lane);
+        ct[ks] = read_cols<TK, NI>(sc, ks, 16 * nt, lane);
+    }
+    f32x4 dB[TPW], dC[TPW];  // rows n = 16 nt + 4 g + e, column token 16 (tg TPW + i) + r
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) dB[i] = dC[i] = zero4();
+    float sum_dl = 0.f, sum_xdu = 0.f, sum_d = 0.f;  // the weigher's, over a head's halves
+
+    for (int i = 0; i < count; ++i) {
+        const int buf = i & 1, h = h0 + i / halves;
+        const bool more = i + 1 < count;
+        if (weigher) An = A2;
+        float kdot = 0.f;
+        // ---- phase A: everything but the products with Q
+        {   // dC_t += e^{cum_t} S0^T dy_t and z_t;  dB_s += dt_s e^{cum_L - cum_s} E^T x_s
+            Parts<3> sp[kPB / 32];
+#pragma unroll
+            for (int ks = 0; ks < kPB / 32; ++ks) {
+                sp[ks] = split<3>(sv[ks]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) kdot += sv[ks][e] * (to_f32(ep[ks].v[0][e]) +
+                                                                 to_f32(ep[ks].v[1][e]) +
+                                                                 to_f32(ep[ks].v[2][e]));
+            }
+            if (more) {
+                load_rows(i + 1);
+                load_state(a.e_states, i + 1, ev);
+                load_state(a.s_states, i + 1, sv);
+                if (weigher) load_dt(i + 1);
+            }
+#pragma unroll
+            for (int q = 0; q < TPW; ++q) {
+                const int it = tg * TPW + q, t = 16 * it + r;
+                f32x4 u = zero4(), v = zero4();
+#pragma unroll
+                for (int ks = 0; ks < kPB / 32; ++ks) {
+                    u = mma(sp[ks], read_rows<TX, NI>(sy, 16 * it, ks, lane), u);
+                    v = mma(ep[ks], read_rows<TX, NI>(sx, 16 * it, ks, lane), v);
+                }
+                const float win = s_in[buf][t];
+                const bf16 *row = sc + t * TK::LD + 16 * nt + 4 * g;
+                float z = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float cv = to_f32(row[e]);
+                    if constexpr (NI == 3)
+                        cv += to_f32(row[TK::PLANE + e]) + to_f32(row[2 * TK::PLANE + e]);
+                    u[e] *= win;
+                    z += u[e] * cv;
+                }
+                z = rows4_sum(z);
+                if (g == 0) s_z[nt][t] = z;
+                dC[q] += u;
+                dB[q] += v * (s_out[buf][t] * s_dt[buf][t]);
+            }
+            kdot = rows4_sum(row16_total(kdot));
+            if (tg == 0 && lane == 0) s_k[nt] = kdot;
+        }
+        {   // this wave's s-tile: dP, M, Q, the pairs, and du
+            const int s = 16 * is + r;
+            const double cs = s_cum[buf][s];
+            const float dts = s_dt[buf][s];
+            f32x4 M[TL], W[TL];
+            float diag = 0.f;
+#pragma unroll
+            for (int it = 0; it < TL; ++it) {
+                M[it] = W[it] = zero4();
+                if (it < is) continue;
+                f32x4 dp = zero4();
+#pragma unroll
+                for (int ks = 0; ks < kPB / 32; ++ks)
+                    dp = mma(read_rows<TX, NI>(sy, 16 * it, ks, lane),
+                             read_rows<TX, NI>(sx, 16 * is, ks, lane), dp);
+                float qv[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 16 * it + 4 * g + e;
+                    const float w = s <= t ? fast_exp2((float)(s_cum[buf][t] - cs)) : 0.f;
+                    diag += s == t ? dp[e] : 0.f;
+                    qv[e] = s <= t ? dp[e] * w * dts : 0.f;
+                    M[it][e] = s <= t ? G[it][e] * w : 0.f;
+                    W[it][e] = s <= t ? G[it][e] * qv[e] : 0.f;
+                }
+                if (pg == 0)
+#pragma unroll
+                    for (int part = 0; part < KQ; ++part) {
+                        bf16x4 o;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float f = part < KQ - 1 ? top_bits(qv[e]) : qv[e];
+                            o[e] = static_cast<bf16>(f);
+                            qv[e] -= f;
+                        }
+                        *reinterpret_cast<bf16x4 *>(sq + part * TQ::PLANE + s * TQ::LD + 16 * it +
+                                                    4 * g) = o;
+                    }
+            }
+            if (pg == 0) {
+                diag = rows4_sum(row16_total(diag));
+                if (lane == 0) s_d[is] = diag;
+                float tail = 0.f;  // of the tiles below, per column s
+#pragma unroll
+                for (int it = TL - 1; it >= 0; --it) {
+                    if (it < is) continue;
+                    float R[4];
+                    R[3] = W[it][3];
+#pragma unroll
+                    for (int e = 2; e >= 0; --e) R[e] = W[it][e] + R[e + 1];
+                    float v[4];
+                    rows4_gather(R[0], v);
+                    const float below = (g < 1 ? v[1] : 0.f) + (g < 2 ? v[2] : 0.f) +
+                                        (g < 3 ? v[3] : 0.f) + tail;
+                    tail += v[0] + v[1] + v[2] + v[3];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = 16 * it + 4 * g + e;
+                        const float sum = row16_total(s < t ? R[e] + below : 0.f);
+                        if (r == 0) s_pair[is][t] = sum;
+                    }
+                }
+            }
+            Parts<3> mp[KT];
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = M[2 * kt][e], f[4 + e] = M[2 * kt + 1][e];
+                mp[kt] = split<3>(f);
+            }
+            float xdu = 0.f, vs = 0.f;
+            const float wout = s_out[buf][s], D = a.D ? a.D[h] : 0.f;
+            T *dx = static_cast<T *>(a.dx) + (int64_t)(t0 + s) * a.dx_stride + (int64_t)h * P +
+                    (i % halves) * kPB;
+#pragma unroll
+            for (int q = 0; q < PT; ++q) {
+                const int pt = pg * PT + q;
+                f32x4 du = zero4();
+#pragma unroll
+                for (int ks = 0; ks < N / 32; ++ks)
+                    du = mma(read_cols<TE, 3>(se, ks, 16 * pt, lane),
+                             read_rows<TK, NI>(sb, 16 * is, ks, lane), du);
+                du *= wout;
+                const int at = s * TX::LD + 16 * pt + 4 * g;
+                float xv[4], yv[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    xv[e] = to_f32(sx[at + e]);
+                    yv[e] = to_f32(sy[at + e]);
+                    if constexpr (NI == 3) {
+                        xv[e] += to_f32(sx[TX::PLANE + at + e]) + to_f32(sx[2 * TX::PLANE + at + e]);
+                        yv[e] += to_f32(sy[TX::PLANE + at + e]) + to_f32(sy[2 * TX::PLANE + at + e]);
+                    }
+                    vs += du[e] * xv[e];
+                }
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+                    if (2 * kt + 1 >= is)
+                        du = mma(read_cols<TX, NI>(sy, kt, 16 * pt, lane), mp[kt], du);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) xdu += du[e] * xv[e];
+                if (s < n)
+                    store4(dx + 16 * pt + 4 * g, dts * du[0] + D * yv[0], dts * du[1] + D * yv[1],
+                           dts * du[2] + D * yv[2], dts * du[3] + D * yv[3]);
+            }
+            xdu = rows4_sum(xdu);
+            vs = rows4_sum(vs);
+            if (g == 0) s_xdu[pg][s] = xdu, s_v[pg][s] = vs * dts;
+        }
+        lds_barrier();
+        // ---- phase B: the products with Q, the sums of dt's gradient, and the
+        // next head's rows into LDS
+#pragma unroll
+        for (int q = 0; q < TPW; ++q) {
+            const int it = tg * TPW + q;
+#pragma unroll
+            for (int ks = 0; ks < KT; ++ks) {
+                if (ks <= it / 2) dC[q] = mma(bt[ks], read_cols<TQ, KQ>(sq, ks, 16 * it, lane), dC[q]);
+                if (ks >= it / 2) dB[q] = mma(ct[ks], read_rows<TQ, KQ>(sq, 16 * it, ks, lane), dB[q]);
+            }
+        }
+        if (weigher) {
+            float dl = 0.f, xdu = 0.f, z = 0.f, v = 0.f, k = 0.f;
+            if (lane < L) {
+#pragma unroll
+                for (int q = 0; q < TL; ++q) dl += q <= lane / 16 ? s_pair[q][lane] : 0.f;
+#pragma unroll
+                for (int q = 0; q < NTN; ++q) z += s_z[q][lane];
+#pragma unroll
+                for (int q = 0; q < 8 / TL; ++q) xdu += s_xdu[q][lane], v += s_v[q][lane];
+            }
+#pragma unroll
+            for (int q = 0; q < NTN; ++q) k += s_k[q];
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const float zo = __shfl_down(z, d, 64), vo = __shfl_up(v, d, 64);
+                z += lane + d < 64 ? zo : 0.f;
+                v += lane >= d ? vo : 0.f;
+            }
+            v = __shfl_up(v, 1, 64);
+            dl += z + (lane > 0 ? v : 0.f) + s_all[buf] * k;
+            float dd = 0.f;
+#pragma unroll
+            for (int q = 0; q < TL; ++q) dd += s_d[q];
+            const bool fresh = i % halves == 0;
+            sum_dl = fresh ? dl : sum_dl + dl;
+            sum_xdu = fresh ? xdu : sum_xdu + xdu;
+            sum_d = fresh ? dd : sum_d + dd;
+            if (i % halves == halves - 1) {
+                if (lane < n) a.ddt[(int64_t)(t0 + lane) * a.heads + h] = sum_xdu + An * sum_dl;
+                const float pa = lane < n ? s_dt[buf][lane] * sum_dl : 0.f;
+                const float tot = rows4_sum(row16_total(pa));
+                if (lane == 0) {
+                    a.part_a[number * a.heads + h] = tot;
+                    a.part_d[number * a.heads + h] = sum_d;
+                }
+            }
+            if (more) weights(buf ^ 1);
+        }
+        if (more) {
+            rx.template store<TX>(sx, tid);
+            ry.template store<TX>(sy, tid);
+            store_e();
+        }
+        lds_barrier();
+    }
+    // dB and dC of this group, or of this set of its heads
+#pragma unroll
+    for (int q = 0; q < TPW; ++q) {
+        const int t = 16 * (tg * TPW + q) + r;
+        if (t >= n) continue;
+        const int64_t token = t0 + t, col = (int64_t)group * N + 16 * nt + 4 * g;
+        if (a.sets == 1) {
+            store4(static_cast<T *>(a.dB) + token * a.db_stride + col, dB[q][0], dB[q][1], dB[q][2],
+                   dB[q][3]);
+            store4(static_cast<T *>(a.dC) + token * a.dc_stride + col, dC[q][0], dC[q][1], dC[q][2],
+                   dC[q][3]);
+        } else {
+            const int64_t row = (int64_t)a.groups * N;
+            float *p = a.part_bc + (2 * set * (int64_t)a.seqs.total + token) * row + col;
+            *reinterpret_cast<f32x4 *>(p) = dB[q];
+            *reinterpret_cast<f32x4 *>(p + a.seqs.total * row) = dC[q];
+        }
+    }
+}
+
+// dB and dC: the sets' parts summed in order, four values a thread.
+template <typename T> __global__ __launch_bounds__(256) void ssm_sets_kernel(SsmGrad a) {
+    const int64_t row = (int64_t)a.groups * a.n, values = (int64_t)a.seqs.total * row;
+    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (at >= 2 * values) return;
+    const int which = at >= values;
+    const int64_t v = at - which * values, token = v / row, col = v % row;
+    if (token >= seq_end_token(a.seqs, a.seqs.num - 1)) return;  // in no sequence
+    const float *p = a.part_bc + at;
+    f32x4 s = zero4();
+    for (int k = 0; k < a.sets; ++k) s += *reinterpret_cast<const f32x4 *>(p + 2 * k * values);
+    T *out = which ? static_cast<T *>(a.dC) + token * a.dc_stride : static_cast<T *>(a.dB) + token * a.db_stride;
+    store4(out + col, s[0], s[1], s[2], s[3]);
+}
+
+// dA and dD of one head: its blocks' parts summed in fp64, 256 side by side.
+__global__ __launch_bounds__(256) void ssm_params_kernel(SsmGrad a) {
+    __shared__ double sum[2][256];
+    const int h = blockIdx.x, tid = threadIdx.x;
+    double s = 0.0, d = 0.0;
+    for (int64_t i = tid; i < a.blocks; i += 256) {
+        s += a.part_a[i * a.heads + h];
+        d += a.part_d[i * a.heads + h];
+    }
+    sum[0][tid] = s;
+    sum[1][tid] = d;
+    __syncthreads();
+    for (int k = 128; k > 0; k >>= 1) {
+        if (tid < k)
+            for (int q = 0; q < 2; ++q) sum[q][tid] += sum[q][tid + k];
+        __syncthreads();
+    }
+    if (tid == 0) {
+        a.dA[h] = (float)sum[0][0];
+        if (a.dD) a.dD[h] = (float)sum[1][0];
+    }
+}
+
+template <typename T> int grad(const SsmGrad &a, hipStream_t stream) {
+    if (a.blocks == 0) {  // no sequence: dA and dD are zero
+        hipLaunchKernelGGL(ssm_params_kernel, dim3(a.heads), dim3(256), 0, stream, a);
+        return hipGetLastError() == hipSuccess ? 0 : -1;
+    }
+    const unsigned blocks = xcd_blocks(a.blocks * a.groups * a.sets);
+    if (a.n == 64)
+        hipLaunchKernelGGL((ssm_grad_kernel<T, 64>), dim3(blocks), dim3(kGradWaves * 64), 0, stream, a);
+    else
+        hipLaunchKernelGGL((ssm_grad_kernel<T, 128>), dim3(blocks), dim3(kGradWaves * 64), 0, stream, a);
+    if (a.sets > 1) {
+        const int64_t quads = 2 * (int64_t)a.seqs.total * a.groups * a.n / 4;
+        if (quads > 0)
+            hipLaunchKernelGGL((ssm_sets_kernel<T>), dim3((unsigned)((quads + 255) / 256)), dim3(256),
+                               0, stream, a);
+    }
+    hipLaunchKernelGGL(ssm_params_kernel, dim3(a.heads), dim3(256), 0, stream, a);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+int launch_ssm_grad(const SsmGrad &a, int dtype, hipStream_t stream) {
+    return dtype == kDtypeBf16 ? grad<bf16>(a, stream) : grad<float>(a, stream);
+}
+
+}  // namespace kda

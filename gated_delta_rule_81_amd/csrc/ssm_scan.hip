@@ -59,9 +59,13 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
     const double A = (double)a.A[h] * kLog2eD;
     const int blocks = (pc.end - pc.beg + L - 1) / L;
 
-    // S^T tiles: rows n = 16 t + 4 g + e, column p = 16 wave + r
+    // S^T tiles: rows n = 16 t + 4 g + e, column p = 16 wave + r.  kStates, which
+    // forms no outputs, keeps S tiles (rows p, column n = 16 t + r) instead: its
+    // states are stored [N][P], four rows p a lane.
     f32x4 S[N / 16];
-    const int64_t lane_off = (int64_t)(16 * wave + r) * N + 4 * g;
+    constexpr bool TR = MODE == kStates;
+    const int64_t lane_off = TR ? (int64_t)(16 * wave + 4 * g) * N + r
+                                : (int64_t)(16 * wave + r) * N + 4 * g;
     const float *enter = nullptr;
     if (MODE != kLocal) {
         const bool edge = REV ? pc.last : pc.first;
@@ -70,8 +74,12 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
                     : (a.state0 ? a.state0 + ((int64_t)pc.seq * a.heads + h) * (P * N) : nullptr);
     }
 #pragma unroll
-    for (int t = 0; t < N / 16; ++t)
-        S[t] = enter ? *reinterpret_cast<const f32x4 *>(enter + lane_off + 16 * t) : zero4();
+    for (int t = 0; t < N / 16; ++t) {
+        const float *at = enter + lane_off + 16 * t;
+        S[t] = !enter ? zero4()
+               : TR   ? f32x4{at[0], at[N], at[2 * N], at[3 * N]}
+                      : *reinterpret_cast<const f32x4 *>(at);
+    }
 
     Stage<T, L, N, NT> rk, rc;
     Stage<T, L, P, NT> rx;
@@ -123,10 +131,12 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
             if (weigher) load_dt(i + 1);
         }
         if constexpr (MODE == kStates) {
-            const int64_t number64 = pc.seq_beg / L + pc.seq + (t0 - pc.seq_beg) / L;
-            float *to = a.block_states + (number64 * a.heads + h) * (int64_t)(P * N) + lane_off;
+            const int64_t block = pc.seq_beg / L + pc.seq + (t0 - pc.seq_beg) / L;
+            float *to = a.block_states + (block * a.heads + h) * (int64_t)(P * N) +
+                        (int64_t)r * P + 16 * wave + 4 * g;
 #pragma unroll
-            for (int t = 0; t < N / 16; ++t) *reinterpret_cast<f32x4 *>(to + 16 * t) = S[t];
+            for (int t = 0; t < N / 16; ++t)
+                *reinterpret_cast<f32x4 *>(to + (int64_t)16 * t * P) = S[t];
         }
         f32x4 y[L / 16];
         if constexpr (OUT) {
@@ -227,7 +237,8 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
             S[t] *= decay;
 #pragma unroll
             for (int ks = 0; ks < L / 32; ++ks)
-                S[t] = mma(read_cols<TK, NI>(sk, ks, 16 * t, lane), xw[ks], S[t]);
+                S[t] = TR ? mma(xw[ks], read_cols<TK, NI>(sk, ks, 16 * t, lane), S[t])
+                          : mma(read_cols<TK, NI>(sk, ks, 16 * t, lane), xw[ks], S[t]);
         }
         if (weigher && i + 1 < blocks) weights(buf ^ 1);
         lds_barrier();  // the tiles are read: the next block's may be written
@@ -241,8 +252,14 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
     }
     if (to)
 #pragma unroll
-        for (int t = 0; t < N / 16; ++t)
-            *reinterpret_cast<f32x4 *>(to + lane_off + 16 * t) = S[t];
+        for (int t = 0; t < N / 16; ++t) {
+            float *at = to + lane_off + 16 * t;
+            if constexpr (TR)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) at[e * N] = S[t][e];
+            else
+                *reinterpret_cast<f32x4 *>(at) = S[t];
+        }
 }
 
 // The pieces' own final states turned in place into entering states:

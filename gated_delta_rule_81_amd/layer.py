@@ -380,6 +380,67 @@ def ssm_chunk_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.T
     return out, final_state
 
 
+def ssm_bwd_workspace_size(batch: int, seq_len: int, num_heads: int, num_groups: int,
+                           head_dim: int, state_dim: int, dtype: torch.dtype,
+                           num_seqs: int = 0) -> int:
+    """Bytes of workspace ``ssm_chunk_bwd`` needs (``num_seqs``: packed sequences,
+    0 for a batch of equal rows)."""
+    n = lib().kda_ssm_chunk_bwd_workspace_size(batch, seq_len, num_seqs, num_heads, num_groups,
+                                               head_dim, state_dim, _DTYPES[dtype])
+    if n < 0:
+        raise ValueError("invalid sizes")
+    return int(n)
+
+
+def ssm_chunk_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                  C: torch.Tensor, d_out: torch.Tensor, D: Optional[torch.Tensor] = None,
+                  d_final_state: Optional[torch.Tensor] = None,
+                  initial_state: Optional[torch.Tensor] = None,
+                  cu_seqlens: Optional[torch.Tensor] = None, *,
+                  workspace: Optional[torch.Tensor] = None, grads: Optional[dict] = None,
+                  output_initial_state_grad: bool = True) -> dict:
+    """Gradients of ``ssm_chunk_fwd`` (``kda_ssm_chunk_bwd``): given dL/d out and
+    dL/d final_state (None = zero), a dict with dx, dB, dC (dtype of x), ddt, dA,
+    dD (fp32; dD None without D) and d_initial_state (fp32, or None when
+    ``output_initial_state_grad`` is False).  ``grads`` may hold preallocated
+    outputs, ``workspace`` a uint8 tensor of ``ssm_bwd_workspace_size`` bytes.
+    """
+    dtc = _dtype(x, "x")
+    if x.dim() != 4:
+        raise ValueError("x must be [B, T, H, P]")
+    b, T = x.shape[:2]
+    dev = x.device
+    H, P, G, N, (xs, bs, cs) = _ssm_common(x, dt, A, B, C, D, 2)
+    gs = _rows(d_out, "d_out", x.dtype, x.shape, dev, 2)
+    n = _num_seqs(cu_seqlens, b, dev)
+    state = (n, H, P, N)
+    _expect(initial_state, "initial_state", torch.float32, state, dev)
+    _expect(d_final_state, "d_final_state", torch.float32, state, dev)
+    g = dict(grads or {})
+    rows = []
+    for name, like in (("dx", x), ("dB", B), ("dC", C)):
+        g[name] = _out(g.get(name), like.shape, x.dtype, dev)
+        rows.append(_rows(g[name], name, x.dtype, like.shape, dev, 2))
+    for name, shape in (("ddt", (b, T, H)), ("dA", (H,))):
+        g[name] = _out(g.get(name), shape, torch.float32, dev)
+        _expect(g[name], name, torch.float32, shape, dev)
+    g["dD"] = None if D is None else _out(g.get("dD"), (H,), torch.float32, dev)
+    _expect(g["dD"], "dD", torch.float32, (H,), dev)
+    g.setdefault("d_initial_state", None)
+    if g["d_initial_state"] is None and output_initial_state_grad:
+        g["d_initial_state"] = torch.empty(state, dtype=torch.float32, device=dev)
+    _expect(g["d_initial_state"], "d_initial_state", torch.float32, state, dev)
+    packed = n if cu_seqlens is not None else 0
+    need = lib().kda_ssm_chunk_bwd_workspace_size(b, T, packed, H, G, P, N, dtc)
+    ws = _workspace(workspace, max(need, 0), dev)
+    _call("kda_ssm_chunk_bwd", dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+          _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_out), _ptr(d_final_state), _ptr(g["dx"]),
+          _ptr(g["ddt"]), _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]),
+          _ptr(g["d_initial_state"]), b, T, H, G, P, N, xs, bs, cs, gs, *rows, packed, dtc,
+          _ptr(ws), ws.numel())
+    return g
+
+
 def ssm_decode_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                     C: torch.Tensor, state: torch.Tensor, D: Optional[torch.Tensor] = None, *,
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:

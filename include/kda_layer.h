@@ -175,6 +175,29 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
                       int64_t workspace_bytes, hipStream_t stream);
 
 /*
+ * kda_ssm_chunk_bwd -- gradients of kda_ssm_chunk_fwd for d_out (of out) and
+ * d_final_state (of final_state; NULL = zero), from its inputs:
+ *   dx  like x;  dB, dC  like B and C (summed over the heads that share a row)
+ *   ddt [batch, seq_len, num_heads], dA [num_heads], dD [num_heads] or NULL  fp32
+ *   d_initial_state like initial_state, or NULL
+ * The workspace holds the state at every block of 64 (fp32: 32) tokens twice:
+ * about seq_len / 32 states per head.
+ */
+int64_t kda_ssm_chunk_bwd_workspace_size(int32_t batch, int32_t seq_len, int32_t num_seqs,
+                                         int32_t num_heads, int32_t num_groups, int32_t head_dim,
+                                         int32_t state_dim, int32_t dtype);
+int kda_ssm_chunk_bwd(const void *x, const float *dt, const float *A, const void *B,
+                      const void *C, const float *D, const float *initial_state,
+                      const int32_t *cu_seqlens, const void *d_out, const float *d_final_state,
+                      void *dx, float *ddt, float *dA, void *dB, void *dC, float *dD,
+                      float *d_initial_state, int32_t batch, int32_t seq_len, int32_t num_heads,
+                      int32_t num_groups, int32_t head_dim, int32_t state_dim, int64_t x_stride,
+                      int64_t b_stride, int64_t c_stride, int64_t d_out_stride,
+                      int64_t dx_stride, int64_t db_stride, int64_t dc_stride, int32_t num_seqs,
+                      int32_t dtype, void *workspace, int64_t workspace_bytes,
+                      hipStream_t stream);
+
+/*
  * kda_ssm_decode_step -- one token of each of `batch` sessions, the state
  * updated in place.  x, out [batch, num_heads, head_dim], B, C [batch,
  * num_groups, state_dim], dt [batch, num_heads], state [batch, num_heads,

@@ -61,16 +61,16 @@ def qk_ref(x, w, table, pos, kind, eps, inter):
     return out
 
 
-def ssm_ref(x, dt, A, B, C, D, state, seqs):
+def ssm_ref(x, dt, A, B, C, D, state, seqs, raw=False):
     """x [B, T, H, P], dt [B, T, H], B, C [B, T, G, N], state [n, H, P, N]:
-    (y, final state), token by token."""
+    (y, final state), token by token.  raw: x already holds dt x."""
     per = x.shape[2] // B.shape[2]
     Bh, Ch = (v.repeat_interleave(per, 2) for v in (B, C))
     out, fin = [], []
     for n, (b, t0, t1) in enumerate(seqs):
         S = state[n]
         for t in range(t0, t1):
-            u = dt[b, t, :, None] * x[b, t]
+            u = x[b, t] if raw else dt[b, t, :, None] * x[b, t]
             S = torch.exp(dt[b, t] * A)[:, None, None] * S + u[..., None] * Bh[b, t][:, None]
             y = (S * Ch[b, t][:, None]).sum(-1)
             out.append(y if D is None else y + D[:, None] * x[b, t])

@@ -99,6 +99,83 @@ def test_forward(case):
     within(out, ref, h * ref.abs() + fy * (1 + h) * m + 1e-37, "out")
 
 
+BWD_CASES = CASES + [
+    # several sets of a group's heads, their parts of dB and dC summed
+    (1, 200, None, 7, 1, 64, 64, True, True, 0, "bf16", 1.0),
+    (1, 0, [40, 0, 70], 6, 2, 128, 128, True, True, 8, "f32", 1.0),
+]
+
+
+def grad_magnitudes(f, d_out, d_final):
+    """The gradients' sums over absolute values: autograd of the definition on
+    |x|, |B|, |C|, |D|, |state|, |d_out|, |d_final| with the decays' own signs
+    turned so that every path adds (dA, ddt: |x . du| + |A| dl)."""
+    ab = lambda v: None if v is None else v.abs().requires_grad_()
+    x, B, C, D, st = ab(f["x"]), ab(f["B"]), ab(f["C"]), ab(f["D"]), ab(f["state"])
+    # decay and input weight apart: exp(-(dt |A|)) enters with a slope of its own
+    dt_in, dt_l = f["dt"].clone().requires_grad_(), f["dt"].clone().requires_grad_()
+    A = f["A"].clone().requires_grad_()
+    l = dt_l * A
+    ones = torch.ones_like(f["A"])
+    y, fin = ssm_ref(x * dt_in[..., None], l, ones, B / 1.0, C, None, st, f["seqs"], raw=True)
+    if D is not None:
+        y = y + D[:, None] * x
+    leaves = [x, dt_in, dt_l, A, B, C, st] + ([] if D is None else [D])
+    g = torch.autograd.grad([y, fin], leaves, [d_out.abs(), d_final.abs()])
+    out = dict(dx=g[0], ddt=g[1] + g[2].abs(), dA=g[3].abs(), dB=g[4], dC=g[5], d_initial_state=g[6])
+    out["dD"] = None if D is None else g[7]
+    return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", BWD_CASES, ids=str)
+def test_backward(case):
+    """Each gradient against autograd of the definition.  Its products chain two
+    block sums (G with dP, M with dy, the states with dy or x), each as the
+    forward's: twice the forward's factors; bf16 dB and dC take Q as two bf16
+    parts (2^-15)."""
+    dt = DTYPES[case[10]]
+    dev, f = make(case, 2)
+    g = torch.Generator().manual_seed(77)
+    d_out = torch.randn(f["x"].shape, generator=g).to(dt)
+    d_fin = torch.randn(f["state"].shape, generator=g) if case[7] else None
+    say("ssm_chunk_bwd", case)
+    got = kda.ssm_chunk_bwd(dev["x"], dev["dt"], dev["A"], dev["B"], dev["C"], d_out.to(DEV),
+                            dev["D"], None if d_fin is None else d_fin.to(DEV), dev["state"], dev["cu"])
+    torch.cuda.synchronize()
+    leaf = lambda k: None if f[k] is None else f[k].clone().requires_grad_()
+    names = ["x", "dt", "A", "B", "C", "state"] + ([] if f["D"] is None else ["D"])
+    v = {k: leaf(k) for k in ("x", "dt", "A", "B", "C", "D", "state")}
+    y, fin = ssm_ref(v["x"], v["dt"], v["A"], v["B"], v["C"], v["D"], v["state"], f["seqs"])
+    df = torch.zeros_like(fin) if d_fin is None else d_fin.double()
+    ref = dict(zip(names, torch.autograd.grad([y, fin], [v[k] for k in names], [d_out.double(), df])))
+    mag = grad_magnitudes(f, d_out.double(), df)
+    blocks = f["x"].shape[1] // 32 + 1
+    _, fs = factors(torch.float32, blocks)
+    fy, _ = factors(torch.float32, blocks)
+    h = HALF[dt]
+    for name, key in (("dx", "x"), ("ddt", "dt"), ("dA", "A"), ("dB", "B"), ("dC", "C"),
+                      ("dD", "D"), ("d_initial_state", "state")):
+        if ref.get(key) is None:
+            assert got[name] is None
+            continue
+        rounded = name in ("dx", "dB", "dC")
+        two = 2 * 2.0 ** -15 if name in ("dB", "dC") and dt == torch.bfloat16 else 0
+        bound = (2 * fy + two) * mag[name] * (1 + h) + (h * ref[key].abs() if rounded else 0) + 1e-37
+        within(got[name], ref[key], bound, name)
+
+
+def test_reference_gradient_by_differences():
+    """The 64-bit reference's gradient against central differences."""
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(s, generator=g, dtype=torch.float64).requires_grad_()
+    seqs = spans(1, 6, [3, 0, 1, 2])
+    dt = (torch.rand(1, 6, 2, generator=g, dtype=torch.float64) + 0.1).requires_grad_()
+    f = lambda x, t, A, B, C, D, s: ssm_ref(x, t, -A.abs(), B, C, D, s, seqs)
+    assert torch.autograd.gradcheck(f, (r(1, 6, 2, 3), dt, r(2), r(1, 6, 1, 2), r(1, 6, 1, 2), r(2),
+                                        r(4, 2, 3, 2)))
+
+
 @pytest.mark.gpu
 def test_far_decays():
     """Steps of e^-1000 and e^-1e30 between ordinary ones: what lies before them
