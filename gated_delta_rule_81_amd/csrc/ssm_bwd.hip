@@ -62,7 +62,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     const int h0 = group * per_group + set * per_set;
     const int h1 = set * per_set + per_set < per_group ? h0 + per_set : (group + 1) * per_group;
     const Piece pc = find_piece(a.seqs, number, L);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane0 = tid & 63, wave = tid >> 6;
+    int lane = lane0, r = lane & 15, g = lane >> 4;
     const int n = pc.any ? pc.end - pc.beg : 0, t0 = pc.beg;
     if (n <= 0) {  // no token: nothing to add to dA and dD
         for (int h = h0 + tid; h < h1; h += NT) {
@@ -126,10 +127,12 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
             if (tg == 0)
 #pragma unroll
                 for (int q = 0; q < 3; ++q) {
-                    bf16 *at = se + q * TE::PLANE + (16 * nt + r) * TE::LD + 32 * ks + 4 * g;
+                    bf16 *at = se + q * TE::PLANE;
                     const bf16x8 v = ep[ks].v[q];
-                    *reinterpret_cast<bf16x4 *>(at) = __builtin_shufflevector(v, v, 0, 1, 2, 3);
-                    *reinterpret_cast<bf16x4 *>(at + 16) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+                    *reinterpret_cast<bf16x4 *>(at + TE::at(16 * nt + r, 32 * ks + 4 * g)) =
+                        __builtin_shufflevector(v, v, 0, 1, 2, 3);
+                    *reinterpret_cast<bf16x4 *>(at + TE::at(16 * nt + r, 32 * ks + 16 + 4 * g)) =
+                        __builtin_shufflevector(v, v, 4, 5, 6, 7);
                 }
         }
     };
@@ -167,13 +170,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
             for (int ks = 0; ks < N / 32; ++ks)
                 G[it] = mma(read_rows<TK, NI>(sc, 16 * it, ks, lane),
                             read_rows<TK, NI>(sb, 16 * is, ks, lane), G[it]);
-    }
-    // B^T and C^T operands of this wave's columns n
-    Parts<NI> bt[KT], ct[KT];
-#pragma unroll
-    for (int ks = 0; ks < KT; ++ks) {
-        bt[ks] = read_cols<TK, NI>(sb, ks, 16 * nt, lane);
-        ct[ks] = read_cols<TK, NI>(sc, ks, 16 * nt, lane);
+        __builtin_amdgcn_sched_barrier(0);
     }
     f32x4 dB[TPW], dC[TPW];  // rows n = 16 nt + 4 g + e, column token 16 (tg TPW + i) + r
 #pragma unroll
@@ -183,6 +180,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     for (int i = 0; i < count; ++i) {
         const int buf = i & 1, h = h0 + i / halves;
         const bool more = i + 1 < count;
+        lane = here(lane0), r = lane & 15, g = lane >> 4;
         if (weigher) An = A2;
         float kdot = 0.f;
         // ---- phase A: everything but the products with Q
@@ -196,12 +194,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                                                                  to_f32(ep[ks].v[1][e]) +
                                                                  to_f32(ep[ks].v[2][e]));
             }
-            if (more) {
-                load_rows(i + 1);
-                load_state(a.e_states, i + 1, ev);
-                load_state(a.s_states, i + 1, sv);
-                if (weigher) load_dt(i + 1);
-            }
+            if (more) load_rows(i + 1);
 #pragma unroll
             for (int q = 0; q < TPW; ++q) {
                 const int it = tg * TPW + q, t = 16 * it + r;
@@ -212,7 +205,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                     v = mma(ep[ks], read_rows<TX, NI>(sx, 16 * it, ks, lane), v);
                 }
                 const float win = s_in[buf][t];
-                const bf16 *row = sc + t * TK::LD + 16 * nt + 4 * g;
+                const bf16 *row = sc + TK::at(t, 16 * nt + 4 * g);
                 float z = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -226,80 +219,80 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 if (g == 0) s_z[nt][t] = z;
                 dC[q] += u;
                 dB[q] += v * (s_out[buf][t] * s_dt[buf][t]);
+                __builtin_amdgcn_sched_barrier(0);
             }
             kdot = rows4_sum(row16_total(kdot));
             if (tg == 0 && lane == 0) s_k[nt] = kdot;
         }
+        __builtin_amdgcn_sched_barrier(0);
         {   // this wave's s-tile: dP, M, Q, the pairs, and du
             const int s = 16 * is + r;
             const double cs = s_cum[buf][s];
             const float dts = s_dt[buf][s];
-            f32x4 M[TL], W[TL];
-            float diag = 0.f;
+            Parts<3> mp[KT];
+            float mf[8], diag = 0.f, tail = 0.f;  // tail: pairs of the tiles below, per column s
 #pragma unroll
-            for (int it = 0; it < TL; ++it) {
-                M[it] = W[it] = zero4();
-                if (it < is) continue;
-                f32x4 dp = zero4();
+            for (int it = TL - 1; it >= 0; --it) {
+                float *m = mf + 4 * (it % 2);
 #pragma unroll
-                for (int ks = 0; ks < kPB / 32; ++ks)
-                    dp = mma(read_rows<TX, NI>(sy, 16 * it, ks, lane),
-                             read_rows<TX, NI>(sx, 16 * is, ks, lane), dp);
-                float qv[4];
+                for (int e = 0; e < 4; ++e) m[e] = 0.f;
+                if (it >= is) {
+                    f32x4 dp = zero4();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 16 * it + 4 * g + e;
-                    const float w = s <= t ? fast_exp2((float)(s_cum[buf][t] - cs)) : 0.f;
-                    diag += s == t ? dp[e] : 0.f;
-                    qv[e] = s <= t ? dp[e] * w * dts : 0.f;
-                    M[it][e] = s <= t ? G[it][e] * w : 0.f;
-                    W[it][e] = s <= t ? G[it][e] * qv[e] : 0.f;
-                }
-                if (pg == 0)
+                    for (int ks = 0; ks < kPB / 32; ++ks)
+                        dp = mma(read_rows<TX, NI>(sy, 16 * it, ks, lane),
+                                 read_rows<TX, NI>(sx, 16 * is, ks, lane), dp);
+                    float qv[4], w[4];
 #pragma unroll
-                    for (int part = 0; part < KQ; ++part) {
-                        bf16x4 o;
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = 16 * it + 4 * g + e;
+                        const float z = (float)(s_cum[buf][t] - cs);
+                        const float d = fast_exp2(s <= t ? z : -1e30f);  // 0 above the diagonal
+                        diag += s == t ? dp[e] : 0.f;
+                        qv[e] = dp[e] * d * dts;
+                        m[e] = G[it][e] * d;
+                        w[e] = G[it][e] * qv[e];
+                    }
+                    if (pg == 0) {
+#pragma unroll
+                        for (int part = 0; part < KQ; ++part) {
+                            bf16x4 o;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float f = part < KQ - 1 ? top_bits(qv[e]) : qv[e];
+                                o[e] = static_cast<bf16>(f);
+                                qv[e] -= f;
+                            }
+                            *reinterpret_cast<bf16x4 *>(sq + part * TQ::PLANE +
+                                                        TQ::at(s, 16 * it + 4 * g)) = o;
+                        }
+                        // sum over t' >= t of this column, then over the columns s < t
+#pragma unroll
+                        for (int e = 2; e >= 0; --e) w[e] += w[e + 1];
+                        float v[4];
+                        rows4_gather(w[0], v);
+                        const float below = (g < 1 ? v[1] : 0.f) + (g < 2 ? v[2] : 0.f) +
+                                            (g < 3 ? v[3] : 0.f) + tail;
+                        tail += v[0] + v[1] + v[2] + v[3];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float f = part < KQ - 1 ? top_bits(qv[e]) : qv[e];
-                            o[e] = static_cast<bf16>(f);
-                            qv[e] -= f;
+                            const int t = 16 * it + 4 * g + e;
+                            const float sum = row16_total(s < t ? w[e] + below : 0.f);
+                            if (r == 0) s_pair[is][t] = sum;
                         }
-                        *reinterpret_cast<bf16x4 *>(sq + part * TQ::PLANE + s * TQ::LD + 16 * it +
-                                                    4 * g) = o;
                     }
+                }
+                if (it % 2 == 0) mp[it / 2] = split<3>(mf);
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (pg == 0) {
                 diag = rows4_sum(row16_total(diag));
                 if (lane == 0) s_d[is] = diag;
-                float tail = 0.f;  // of the tiles below, per column s
-#pragma unroll
-                for (int it = TL - 1; it >= 0; --it) {
-                    if (it < is) continue;
-                    float R[4];
-                    R[3] = W[it][3];
-#pragma unroll
-                    for (int e = 2; e >= 0; --e) R[e] = W[it][e] + R[e + 1];
-                    float v[4];
-                    rows4_gather(R[0], v);
-                    const float below = (g < 1 ? v[1] : 0.f) + (g < 2 ? v[2] : 0.f) +
-                                        (g < 3 ? v[3] : 0.f) + tail;
-                    tail += v[0] + v[1] + v[2] + v[3];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = 16 * it + 4 * g + e;
-                        const float sum = row16_total(s < t ? R[e] + below : 0.f);
-                        if (r == 0) s_pair[is][t] = sum;
-                    }
-                }
             }
-            Parts<3> mp[KT];
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = M[2 * kt][e], f[4 + e] = M[2 * kt + 1][e];
-                mp[kt] = split<3>(f);
+            if (more) {  // in flight through du and phase B
+                load_state(a.e_states, i + 1, ev);
+                load_state(a.s_states, i + 1, sv);
+                if (weigher) load_dt(i + 1);
             }
             float xdu = 0.f, vs = 0.f;
             const float wout = s_out[buf][s], D = a.D ? a.D[h] : 0.f;
@@ -313,8 +306,9 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 for (int ks = 0; ks < N / 32; ++ks)
                     du = mma(read_cols<TE, 3>(se, ks, 16 * pt, lane),
                              read_rows<TK, NI>(sb, 16 * is, ks, lane), du);
+                __builtin_amdgcn_sched_barrier(0);
                 du *= wout;
-                const int at = s * TX::LD + 16 * pt + 4 * g;
+                const int at = TX::at(s, 16 * pt + 4 * g);
                 float xv[4], yv[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -335,6 +329,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 if (s < n)
                     store4(dx + 16 * pt + 4 * g, dts * du[0] + D * yv[0], dts * du[1] + D * yv[1],
                            dts * du[2] + D * yv[2], dts * du[3] + D * yv[3]);
+                __builtin_amdgcn_sched_barrier(0);
             }
             xdu = rows4_sum(xdu);
             vs = rows4_sum(vs);
@@ -343,6 +338,12 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
         lds_barrier();
         // ---- phase B: the products with Q, the sums of dt's gradient, and the
         // next head's rows into LDS
+        Parts<NI> bt[KT], ct[KT];  // B^T and C^T of this wave's columns n
+#pragma unroll
+        for (int ks = 0; ks < KT; ++ks) {
+            bt[ks] = read_cols<TK, NI>(sb, ks, 16 * nt, lane);
+            ct[ks] = read_cols<TK, NI>(sc, ks, 16 * nt, lane);
+        }
 #pragma unroll
         for (int q = 0; q < TPW; ++q) {
             const int it = tg * TPW + q;
@@ -351,6 +352,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 if (ks <= it / 2) dC[q] = mma(bt[ks], read_cols<TQ, KQ>(sq, ks, 16 * it, lane), dC[q]);
                 if (ks >= it / 2) dB[q] = mma(ct[ks], read_rows<TQ, KQ>(sq, 16 * it, ks, lane), dB[q]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (weigher) {
             float dl = 0.f, xdu = 0.f, z = 0.f, v = 0.f, k = 0.f;

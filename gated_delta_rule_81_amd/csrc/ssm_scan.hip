@@ -51,7 +51,8 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
     const Piece pc = find_piece(a.seqs, number, a.piece);
     if (!pc.any) return;
     if (MODE == kLocal && (REV ? pc.first : pc.last)) return;  // nothing enters from it
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane0 = tid & 63, wave = tid >> 6;
+    int lane = lane0, r = lane & 15, g = lane >> 4;
     const int group = h / (a.heads / a.groups);
     const T *x = static_cast<const T *>(a.x) + (int64_t)h * P;
     const T *k = static_cast<const T *>(a.k) + (int64_t)group * N;
@@ -122,6 +123,7 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
     }
     for (int i = 0; i < blocks; ++i) {
         const int buf = i & 1, t0 = first_token(i);
+        lane = here(lane0), r = lane & 15, g = lane >> 4;
         rk.template store<TK>(sk, tid);
         rx.template store<TX>(sx, tid);
         if constexpr (OUT) rc.template store<TK>(sc, tid);
@@ -157,9 +159,10 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        v[e] = s + e <= t ? m[e] * fast_exp2((float)(ct - s_cum[buf][s + e])) *
-                                                s_dt[buf][s + e]
-                                          : 0.f;
+                    {
+                        const float z = (float)(ct - s_cum[buf][s + e]);  // 0 above the diagonal
+                        v[e] = m[e] * fast_exp2(s + e <= t ? z : -1e30f) * s_dt[buf][s + e];
+                    }
 #pragma unroll
                     for (int part = 0; part < KP; ++part) {
                         bf16x4 o;
@@ -169,7 +172,7 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
                             o[e] = static_cast<bf16>(f);
                             v[e] -= f;
                         }
-                        *reinterpret_cast<bf16x4 *>(sm + part * TM::PLANE + t * TM::LD + s) = o;
+                        *reinterpret_cast<bf16x4 *>(sm + part * TM::PLANE + TM::at(t, s)) = o;
                     }
                 }
             // y^T = S C^T e^{cum}: rows p, columns t
@@ -217,7 +220,7 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
                     y[it] = mma(xt[ks], read_rows<TM, KP>(sm, 16 * it, ks, lane), y[it]);
                 const int t = 16 * it + r;
                 if (a.D) {
-                    const bf16 *row = sx + t * TX::LD + 16 * wave + 4 * g;
+                    const bf16 *row = sx + TX::at(t, 16 * wave + 4 * g);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float v = to_f32(row[e]);
