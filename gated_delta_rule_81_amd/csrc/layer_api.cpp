@@ -358,6 +358,8 @@ int check_ssm_rows(const void *t, int64_t rows, int64_t len, int64_t stride, int
     if (rows > 0 && len > 0) {
         if (stride < len) return KDA_ERR_SHAPE;
         if (!t) return KDA_ERR_NULL;
+        // the kernels address 64 rows with 32-bit byte offsets
+        if (stride > INT32_MAX / (64 * esz)) return KDA_ERR_UNSUPPORTED;
         if (stride * esz % 16 != 0) return KDA_ERR_ALIGN;
     }
     return aligned16(t) ? KDA_OK : KDA_ERR_ALIGN;

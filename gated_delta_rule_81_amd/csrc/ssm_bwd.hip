@@ -49,7 +49,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     __shared__ __attribute__((aligned(16))) bf16 se[TE::ELEMS];  // E: [n][p]
     __shared__ __attribute__((aligned(16))) double s_cum[2][L];
     __shared__ __attribute__((aligned(16))) float s_dt[2][L], s_out[2][L], s_in[2][L];
-    __shared__ float s_all[2];
+    __shared__ __attribute__((aligned(16))) float s_g[TL * (TL + 1) / 2][64][4];  // G's tiles
+    __shared__ float s_all[2], s_D[2];
     __shared__ float s_pair[TL][L], s_z[NTN][L], s_xdu[8 / TL][L], s_v[8 / TL][L];
     __shared__ float s_k[NTN], s_d[TL];
 
@@ -100,11 +101,12 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 for (int e = 0; e < 4; ++e) f[ks][4 * q + e] = v[e];
             }
     };
-    float rdt = 0.f, A2 = 0.f, An = 0.f;  // the weigher's head
+    float rdt = 0.f, A2 = 0.f, An = 0.f, rD = 0.f;  // the weigher's head
     auto load_dt = [&](int i) {
         const int h = h0 + i / halves;
         rdt = lane < n ? a.dt[(int64_t)(t0 + lane) * a.heads + h] : 0.f;
         A2 = a.A[h];
+        rD = a.D ? a.D[h] : 0.f;
     };
     auto weights = [&](int buf) {
         const double step = (double)rdt * ((double)A2 * kLog2eD);
@@ -116,19 +118,18 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
             s_in[buf][lane] = fast_exp2((float)cum);
             s_out[buf][lane] = fast_exp2((float)(all - cum));
         }
-        if (lane == 0) s_all[buf] = fast_exp2((float)all);
+        if (lane == 0) s_all[buf] = fast_exp2((float)all), s_D[buf] = rD;
     };
     float ev[kPB / 32][8], sv[kPB / 32][8];
-    Parts<3> ep[kPB / 32];
-    auto store_e = [&]() {  // E's parts: kept for dB, and to LDS for du
+    auto store_e = [&]() {  // E's parts to LDS
 #pragma unroll
         for (int ks = 0; ks < kPB / 32; ++ks) {
-            ep[ks] = split<3>(ev[ks]);
+            const Parts<3> ep = split<3>(ev[ks]);
             if (tg == 0)
 #pragma unroll
                 for (int q = 0; q < 3; ++q) {
                     bf16 *at = se + q * TE::PLANE;
-                    const bf16x8 v = ep[ks].v[q];
+                    const bf16x8 v = ep.v[q];
                     *reinterpret_cast<bf16x4 *>(at + TE::at(16 * nt + r, 32 * ks + 4 * g)) =
                         __builtin_shufflevector(v, v, 0, 1, 2, 3);
                     *reinterpret_cast<bf16x4 *>(at + TE::at(16 * nt + r, 32 * ks + 16 + 4 * g)) =
@@ -160,18 +161,23 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     }
     lds_barrier();
 
-    // G[t][s] of this wave's s-tile (rows t = 16 it + 4 g + e, column s = 16 is + r)
-    f32x4 G[TL];
+    // G's tiles it >= is (rows t = 16 it + 4 g + e, column s = 16 is + r), by lane
+    auto tile_of = [](int it, int js) { return it * (it + 1) / 2 + js; };
+    {
+        const RowsAt<TK> krow(lane);
 #pragma unroll
-    for (int it = 0; it < TL; ++it) {
-        G[it] = zero4();
-        if (it >= is)
+        for (int it = 0; it < TL; ++it) {
+            if (it < is || pg != it % (8 / TL)) continue;
+            f32x4 v = zero4();
 #pragma unroll
             for (int ks = 0; ks < N / 32; ++ks)
-                G[it] = mma(read_rows<TK, NI>(sc, 16 * it, ks, lane),
-                            read_rows<TK, NI>(sb, 16 * is, ks, lane), G[it]);
-        __builtin_amdgcn_sched_barrier(0);
+                v = mma(read_rows<TK, NI>(sc, 16 * it, ks, krow),
+                        read_rows<TK, NI>(sb, 16 * is, ks, krow), v);
+            *reinterpret_cast<f32x4 *>(s_g[tile_of(it, is)][lane]) = v;
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
+    lds_barrier();
     f32x4 dB[TPW], dC[TPW];  // rows n = 16 nt + 4 g + e, column token 16 (tg TPW + i) + r
 #pragma unroll
     for (int i = 0; i < TPW; ++i) dB[i] = dC[i] = zero4();
@@ -181,14 +187,18 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
         const int buf = i & 1, h = h0 + i / halves;
         const bool more = i + 1 < count;
         lane = here(lane0), r = lane & 15, g = lane >> 4;
+        const RowsAt<TK> krow(lane);
+        const RowsAt<TX> xrow(lane);
         if (weigher) An = A2;
         float kdot = 0.f;
         // ---- phase A: everything but the products with Q
         {   // dC_t += e^{cum_t} S0^T dy_t and z_t;  dB_s += dt_s e^{cum_L - cum_s} E^T x_s
-            Parts<3> sp[kPB / 32];
+            Parts<3> sp[kPB / 32], ep[kPB / 32];
+            const RowsAt<TE> erow(lane);
 #pragma unroll
             for (int ks = 0; ks < kPB / 32; ++ks) {
                 sp[ks] = split<3>(sv[ks]);
+                ep[ks] = read_rows<TE, 3>(se, 16 * nt, ks, erow);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) kdot += sv[ks][e] * (to_f32(ep[ks].v[0][e]) +
                                                                  to_f32(ep[ks].v[1][e]) +
@@ -201,8 +211,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 f32x4 u = zero4(), v = zero4();
 #pragma unroll
                 for (int ks = 0; ks < kPB / 32; ++ks) {
-                    u = mma(sp[ks], read_rows<TX, NI>(sy, 16 * it, ks, lane), u);
-                    v = mma(ep[ks], read_rows<TX, NI>(sx, 16 * it, ks, lane), v);
+                    u = mma(sp[ks], read_rows<TX, NI>(sy, 16 * it, ks, xrow), u);
+                    v = mma(ep[ks], read_rows<TX, NI>(sx, 16 * it, ks, xrow), v);
                 }
                 const float win = s_in[buf][t];
                 const bf16 *row = sc + TK::at(t, 16 * nt + 4 * g);
@@ -240,8 +250,9 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                     f32x4 dp = zero4();
 #pragma unroll
                     for (int ks = 0; ks < kPB / 32; ++ks)
-                        dp = mma(read_rows<TX, NI>(sy, 16 * it, ks, lane),
-                                 read_rows<TX, NI>(sx, 16 * is, ks, lane), dp);
+                        dp = mma(read_rows<TX, NI>(sy, 16 * it, ks, xrow),
+                                 read_rows<TX, NI>(sx, 16 * is, ks, xrow), dp);
+                    const f32x4 G = *reinterpret_cast<const f32x4 *>(s_g[tile_of(it, is)][lane]);
                     float qv[4], w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -250,8 +261,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                         const float d = fast_exp2(s <= t ? z : -1e30f);  // 0 above the diagonal
                         diag += s == t ? dp[e] : 0.f;
                         qv[e] = dp[e] * d * dts;
-                        m[e] = G[it][e] * d;
-                        w[e] = G[it][e] * qv[e];
+                        m[e] = G[e] * d;
+                        w[e] = G[e] * qv[e];
                     }
                     if (pg == 0) {
 #pragma unroll
@@ -295,7 +306,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 if (weigher) load_dt(i + 1);
             }
             float xdu = 0.f, vs = 0.f;
-            const float wout = s_out[buf][s], D = a.D ? a.D[h] : 0.f;
+            const float wout = s_out[buf][s], D = s_D[buf];
             T *dx = static_cast<T *>(a.dx) + (int64_t)(t0 + s) * a.dx_stride + (int64_t)h * P +
                     (i % halves) * kPB;
 #pragma unroll
@@ -304,8 +315,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 f32x4 du = zero4();
 #pragma unroll
                 for (int ks = 0; ks < N / 32; ++ks)
-                    du = mma(read_cols<TE, 3>(se, ks, 16 * pt, lane),
-                             read_rows<TK, NI>(sb, 16 * is, ks, lane), du);
+                    du = mma(read_cols<TE, 3>(se, ks, cols_at<TE>(16 * pt, lane)),
+                             read_rows<TK, NI>(sb, 16 * is, ks, krow), du);
                 __builtin_amdgcn_sched_barrier(0);
                 du *= wout;
                 const int at = TX::at(s, 16 * pt + 4 * g);
@@ -323,7 +334,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt)
                     if (2 * kt + 1 >= is)
-                        du = mma(read_cols<TX, NI>(sy, kt, 16 * pt, lane), mp[kt], du);
+                        du = mma(read_cols<TX, NI>(sy, kt, cols_at<TX>(16 * pt, lane)), mp[kt], du);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) xdu += du[e] * xv[e];
                 if (s < n)
@@ -341,16 +352,16 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
         Parts<NI> bt[KT], ct[KT];  // B^T and C^T of this wave's columns n
 #pragma unroll
         for (int ks = 0; ks < KT; ++ks) {
-            bt[ks] = read_cols<TK, NI>(sb, ks, 16 * nt, lane);
-            ct[ks] = read_cols<TK, NI>(sc, ks, 16 * nt, lane);
+            bt[ks] = read_cols<TK, NI>(sb, ks, cols_at<TK>(16 * nt, lane));
+            ct[ks] = read_cols<TK, NI>(sc, ks, cols_at<TK>(16 * nt, lane));
         }
 #pragma unroll
         for (int q = 0; q < TPW; ++q) {
             const int it = tg * TPW + q;
 #pragma unroll
             for (int ks = 0; ks < KT; ++ks) {
-                if (ks <= it / 2) dC[q] = mma(bt[ks], read_cols<TQ, KQ>(sq, ks, 16 * it, lane), dC[q]);
-                if (ks >= it / 2) dB[q] = mma(ct[ks], read_rows<TQ, KQ>(sq, 16 * it, ks, lane), dB[q]);
+                if (ks <= it / 2) dC[q] = mma(bt[ks], read_cols<TQ, KQ>(sq, ks, cols_at<TQ>(16 * it, lane)), dC[q]);
+                if (ks >= it / 2) dB[q] = mma(ct[ks], read_rows<TQ, KQ>(sq, 16 * it, ks, RowsAt<TQ>(lane)), dB[q]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }

@@ -78,62 +78,88 @@ template <int NP, int ROWS, int COLS> struct Tile {
     }
 };
 
-// Operand with outer index = row: rows row0 + l % 16, k = columns 32 ks ...
-// row0 is a multiple of 16.
+// Where a lane's pieces of an operand lie: element offsets that depend on the
+// lane alone, formed once and used for every row tile (rows) or row step
+// (columns) by immediate offsets, since turn() repeats after 16 rows.
+//   rows:    outer index = row row0 + l % 16 (row0 a multiple of 16), k =
+//            columns 32 ks ..; two 8-byte pieces
+//   columns: outer index = column col0 + l % 16, k = rows 32 ks ..; two
+//            transposing reads (lane l of 16 receives column l of the four rows
+//            whose 8-byte pieces lanes l / 4 + 4 e address, e = 0..3)
+template <typename TL> struct RowsAt {
+    int o[TL::LD / 32][2];
+    __device__ __forceinline__ explicit RowsAt(int lane) {
+#pragma unroll
+        for (int ks = 0; ks < TL::LD / 32; ++ks)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                o[ks][q] = TL::at(lane & 15, 32 * ks + 16 * q + 4 * (lane >> 4));
+    }
+};
+template <typename TL> __device__ __forceinline__ int cols_at(int col0, int lane) {
+    return TL::at(4 * (lane >> 4) + ((lane & 15) >> 2), col0 + 4 * (lane & 3));
+}
+
+typedef __attribute__((address_space(3))) const bf16 lds_bf16;
+typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+
 template <typename TL, int NP>
-__device__ __forceinline__ Parts<NP> read_rows(const bf16 *tile, int row0, int ks, int lane) {
+__device__ __forceinline__ Parts<NP> read_rows(const bf16 *tile, int row0, int ks,
+                                               const RowsAt<TL> &at) {
     Parts<NP> p;
-    const bf16 *at = tile + TL::at(row0 + (lane & 15), 32 * ks + 4 * (lane >> 4));
-    const bf16 *up = tile + TL::at(row0 + (lane & 15), 32 * ks + 16 + 4 * (lane >> 4));
+    lds_bf16 *a = (lds_bf16 *)tile + at.o[ks][0], *b = (lds_bf16 *)tile + at.o[ks][1];
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
-        const bf16x4 a = *reinterpret_cast<const bf16x4 *>(at + q * TL::PLANE);
-        const bf16x4 b = *reinterpret_cast<const bf16x4 *>(up + q * TL::PLANE);
-        p.v[q] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        const bf16x4 u = *(lds_bf16x4 *)(a + (q * TL::PLANE + row0 * TL::LD));
+        const bf16x4 v = *(lds_bf16x4 *)(b + (q * TL::PLANE + row0 * TL::LD));
+        p.v[q] = __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     return p;
 }
 
-// Operand with outer index = column: columns col0 + l % 16, k = rows 32 ks ...
-// (transposing LDS reads: lane l of 16 receives column l of the four rows whose
-// 8-byte pieces lanes l / 4 + 4 e address, e = 0..3).
+// at = cols_at<TL>(col0, lane)
 template <typename TL, int NP>
-__device__ __forceinline__ Parts<NP> read_cols(const bf16 *tile, int ks, int col0, int lane) {
-    typedef __attribute__((address_space(3))) bf16x4 lds4;
+__device__ __forceinline__ Parts<NP> read_cols(const bf16 *tile, int ks, int at) {
     Parts<NP> p;
-    const int row = 4 * (lane >> 4) + ((lane & 15) >> 2);
-    const bf16 *at = tile + 32 * ks * TL::LD + TL::at(row, col0 + 4 * (lane & 3));
-    const bf16 *up = at + 16 * TL::LD;  // turn() repeats after 16 rows
+    lds_bf16 *a = (lds_bf16 *)tile + at;
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
-        const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4 *)(at + q * TL::PLANE));
-        const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4 *)(up + q * TL::PLANE));
-        p.v[q] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+        const bf16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+            (lds_bf16x4 *)(a + (q * TL::PLANE + 32 * ks * TL::LD)));
+        const bf16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+            (lds_bf16x4 *)(a + (q * TL::PLANE + (32 * ks + 16) * TL::LD)));
+        p.v[q] = __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     return p;
 }
 
 // ROWS x COLS values of T, row r at p + r * stride, staged by NT threads:
 // global to registers in 16-byte pieces (rows at and past `valid` as zeros),
-// later registers to LDS as parts.
+// later registers to LDS as parts.  A thread's pieces lie RS rows apart in one
+// column: one 32-bit offset serves them all beside a uniform base (64 rows of a
+// tensor span less than 2^31 bytes).
 template <typename T, int ROWS, int COLS, int NT> struct Stage {
     static constexpr int E = 16 / sizeof(T), PER_ROW = COLS / E, COUNT = ROWS * PER_ROW / NT;
-    static_assert(COUNT * NT == ROWS * PER_ROW, "pieces over threads");
+    static constexpr int RS = NT / PER_ROW;
+    static_assert(COUNT * NT == ROWS * PER_ROW && RS * PER_ROW == NT, "pieces over threads");
     u32x4 r[COUNT];
     __device__ __forceinline__ void load(const T *p, int64_t stride, int valid, int tid) {
+        const int row = tid / PER_ROW;
+        const unsigned off = (unsigned)(row * (int)stride + tid % PER_ROW * E) * (unsigned)sizeof(T);
+        const char *base = reinterpret_cast<const char *>(p);
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
-            const int piece = tid + i * NT, row = piece / PER_ROW;
-            r[i] = row < valid ? *reinterpret_cast<const u32x4 *>(p + row * stride +
-                                                                   piece % PER_ROW * E)
-                               : u32x4{0u, 0u, 0u, 0u};
+            r[i] = row + i * RS < valid
+                       ? *reinterpret_cast<const u32x4 *>(base + (int64_t)(i * RS) * stride *
+                                                                     (int)sizeof(T) + off)
+                       : u32x4{0u, 0u, 0u, 0u};
         }
     }
     template <typename TL> __device__ __forceinline__ void store(bf16 *tile, int tid) const {
+        const int row = tid / PER_ROW, col = tid % PER_ROW * E, first = TL::at(row, col);
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) {
-            const int piece = tid + i * NT, row = piece / PER_ROW;
-            bf16 *at = tile + TL::at(row, piece % PER_ROW * E);
+            bf16 *at = tile + (RS % 16 == 0 ? first + i * RS * TL::LD : TL::at(row + i * RS, col));
             if constexpr (sizeof(T) == 2) {
                 *reinterpret_cast<u32x4 *>(at) = r[i];
             } else {

@@ -21,6 +21,14 @@
 // once more and does 4 P N of the second's 4 P N + 2 L (P + N) operations a token.
 #include "ssm_device.h"
 
+#ifndef SCAN_OCC
+#define SCAN_OCC (P == 64 && sizeof(T) == 2 ? 3 : 2)
+#endif
+#ifdef SCAN_SB
+#define SB __builtin_amdgcn_sched_barrier(0)
+#else
+#define SB
+#endif
 namespace kda {
 namespace {
 
@@ -29,13 +37,15 @@ enum Mode { kLocal, kOut, kStates };
 // REV walks the blocks from the last to the first and the tokens' weights from
 // the right: the gradient's recurrence E_{t-1} = e^{dt_t A} (E_t + x_t k_t^T).
 template <typename T, int P, int N, int MODE, bool REV>
-__global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
+__global__ __launch_bounds__(P * 4, SCAN_OCC) void ssm_scan_kernel(SsmScan a) {
     constexpr int L = kSsmBlock<T>, NT = P * 4, NI = sizeof(T) == 2 ? 1 : 3;
-    constexpr int KP = sizeof(T) == 2 ? 2 : 3;  // parts of y's fp32 operands (M and S)
+    // Parts of y's fp32 operands, the block's weights M and the state: two for a
+    // bf16 y (2^-15, nothing beside its own rounding), three for an fp32 one.
+    constexpr int KM = sizeof(T) == 2 ? 2 : 3, KP = KM;
     constexpr bool OUT = MODE == kOut;
     typedef Tile<NI, L, N> TK;
     typedef Tile<NI, L, P> TX;
-    typedef Tile<KP, L, L> TM;
+    typedef Tile<KM, L, L> TM;
     __shared__ __attribute__((aligned(16))) bf16 sk[TK::ELEMS];
     __shared__ __attribute__((aligned(16))) bf16 sc[OUT ? TK::ELEMS : 8];
     __shared__ __attribute__((aligned(16))) bf16 sx[TX::ELEMS];
@@ -51,8 +61,13 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
     const Piece pc = find_piece(a.seqs, number, a.piece);
     if (!pc.any) return;
     if (MODE == kLocal && (REV ? pc.first : pc.last)) return;  // nothing enters from it
-    const int tid = threadIdx.x, lane0 = tid & 63, wave = tid >> 6;
-    int lane = lane0, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const RowsAt<TK> krow(lane);
+    const RowsAt<TM> mrow(lane);
+    int kcol[N / 16];
+#pragma unroll
+    for (int t = 0; t < N / 16; ++t) kcol[t] = cols_at<TK>(16 * t, lane);
+    const int xcol = cols_at<TX>(16 * wave, lane);
     const int group = h / (a.heads / a.groups);
     const T *x = static_cast<const T *>(a.x) + (int64_t)h * P;
     const T *k = static_cast<const T *>(a.k) + (int64_t)group * N;
@@ -123,7 +138,6 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
     }
     for (int i = 0; i < blocks; ++i) {
         const int buf = i & 1, t0 = first_token(i);
-        lane = here(lane0), r = lane & 15, g = lane >> 4;
         rk.template store<TK>(sk, tid);
         rx.template store<TX>(sx, tid);
         if constexpr (OUT) rc.template store<TK>(sc, tid);
@@ -141,6 +155,7 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
                 *reinterpret_cast<f32x4 *>(to + (int64_t)16 * t * P) = S[t];
         }
         f32x4 y[L / 16];
+        const int ln = here(lane), r = ln & 15, g = ln >> 4;
         if constexpr (OUT) {
             // M[t][s] = e^{cum_t - cum_s} (C_t . B_s) dt_s, s <= t, formed as tiles of M^T
             int q = 0;
@@ -152,8 +167,8 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
                     f32x4 m = zero4();
 #pragma unroll
                     for (int ks = 0; ks < N / 32; ++ks)
-                        m = mma(read_rows<TK, NI>(sk, 16 * is, ks, lane),
-                                read_rows<TK, NI>(sc, 16 * it, ks, lane), m);
+                        m = mma(read_rows<TK, NI>(sk, 16 * is, ks, krow),
+                                read_rows<TK, NI>(sc, 16 * it, ks, krow), m);
                     const int t = 16 * it + r, s = 16 * is + 4 * g;
                     const double ct = s_cum[buf][t];
                     float v[4];
@@ -164,16 +179,17 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
                         v[e] = m[e] * fast_exp2(s + e <= t ? z : -1e30f) * s_dt[buf][s + e];
                     }
 #pragma unroll
-                    for (int part = 0; part < KP; ++part) {
+                    for (int part = 0; part < KM; ++part) {
                         bf16x4 o;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float f = part < KP - 1 ? top_bits(v[e]) : v[e];
+                            const float f = part < KM - 1 ? top_bits(v[e]) : v[e];
                             o[e] = static_cast<bf16>(f);
                             v[e] -= f;
                         }
                         *reinterpret_cast<bf16x4 *>(sm + part * TM::PLANE + TM::at(t, s)) = o;
                     }
+                    SB;
                 }
             // y^T = S C^T e^{cum}: rows p, columns t
 #pragma unroll
@@ -186,7 +202,8 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
                 const Parts<KP> sp = split<KP>(f);
 #pragma unroll
                 for (int it = 0; it < L / 16; ++it)
-                    y[it] = mma(sp, read_rows<TK, NI>(sc, 16 * it, ks, lane), y[it]);
+                    y[it] = mma(sp, read_rows<TK, NI>(sc, 16 * it, ks, krow), y[it]);
+                SB;
             }
 #pragma unroll
             for (int it = 0; it < L / 16; ++it) y[it] *= s_in[buf][16 * it + r];
@@ -197,7 +214,7 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
         Parts<3> xw[L / 32];
 #pragma unroll
         for (int ks = 0; ks < L / 32; ++ks) {
-            xt[ks] = read_cols<TX, NI>(sx, ks, 16 * wave, lane);
+            xt[ks] = read_cols<TX, NI>(sx, ks, xcol);
             const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&s_w[buf][32 * ks + 4 * g]);
             const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&s_w[buf][32 * ks + 16 + 4 * g]);
             float f[8];
@@ -208,6 +225,7 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
                 f[e] = v * (e < 4 ? w0[e % 4] : w1[e % 4]);
             }
             xw[ks] = split<3>(f);
+            SB;
         }
         if constexpr (OUT) {
             const int n = pc.end - t0;
@@ -217,7 +235,7 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
             for (int it = 0; it < L / 16; ++it) {
 #pragma unroll
                 for (int ks = 0; ks <= it / 2; ++ks)
-                    y[it] = mma(xt[ks], read_rows<TM, KP>(sm, 16 * it, ks, lane), y[it]);
+                    y[it] = mma(xt[ks], read_rows<TM, KM>(sm, 16 * it, ks, mrow), y[it]);
                 const int t = 16 * it + r;
                 if (a.D) {
                     const bf16 *row = sx + TX::at(t, 16 * wave + 4 * g);
@@ -232,6 +250,7 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
                 if (t < n)
                     store4(out + (int64_t)(t0 + t) * a.out_stride, y[it][0], y[it][1], y[it][2],
                            y[it][3]);
+                SB;
             }
         }
         const float decay = fast_exp2((float)s_tot[buf]);
@@ -240,8 +259,8 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_scan_kernel(SsmScan a) {
             S[t] *= decay;
 #pragma unroll
             for (int ks = 0; ks < L / 32; ++ks)
-                S[t] = TR ? mma(xw[ks], read_cols<TK, NI>(sk, ks, 16 * t, lane), S[t])
-                          : mma(read_cols<TK, NI>(sk, ks, 16 * t, lane), xw[ks], S[t]);
+                S[t] = TR ? mma(xw[ks], read_cols<TK, NI>(sk, ks, kcol[t]), S[t])
+                          : mma(read_cols<TK, NI>(sk, ks, kcol[t]), xw[ks], S[t]);
         }
         if (weigher && i + 1 < blocks) weights(buf ^ 1);
         lds_barrier();  // the tiles are read: the next block's may be written

@@ -28,21 +28,23 @@ def _rows(t, name, dtype, shape, device, lead: int) -> int:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    width = 1
-    for size, stride in reversed(list(zip(t.shape[lead:], t.stride()[lead:]))):
-        if size != 1 and stride != width:
+    if t.is_contiguous():
+        return t.shape[lead:].numel()
+    sizes, strides, width = t.shape, t.stride(), 1
+    for i in range(len(sizes) - 1, lead - 1, -1):
+        if strides[i] != width and sizes[i] != 1:
             raise ValueError(f"{name}: the values of a token must be contiguous")
-        width *= size
+        width *= sizes[i]
     row, count = None, 1  # distance between tokens; tokens behind the axis looked at
-    for size, stride in reversed(list(zip(t.shape[:lead], t.stride()[:lead]))):
-        if size != 1:
+    for i in range(lead - 1, -1, -1):
+        if sizes[i] != 1:
             if row is None:
-                row = stride
-            elif stride != row * count:
+                row = strides[i]
+            elif strides[i] != row * count:
                 raise ValueError(f"{name}: tokens must be a fixed distance apart")
-        count *= size
+            count *= sizes[i]
     row = width if row is None or t.numel() == 0 else row
     if row < width:
         raise ValueError(f"{name}: the rows of two tokens overlap")
@@ -72,9 +74,15 @@ def _call(name, device, *args):
     """Call a library function on ``device``'s current stream."""
     if device.type != "cuda":
         raise ValueError(f"{name} needs tensors on a GPU, got {device}")
-    with torch.cuda.device(device):
-        rc = getattr(lib(), name)(*args, torch.cuda.current_stream(device).cuda_stream)
-    check(rc, name)
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)  # no Stream object for a handle
+    if torch.cuda.current_device() == index:
+        rc = getattr(lib(), name)(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = getattr(lib(), name)(*args, stream)
+    if rc:
+        check(rc, name)
 
 
 def _workspace(workspace, need, device):
@@ -86,8 +94,12 @@ def _workspace(workspace, need, device):
     return workspace
 
 
-def _out(t, like_shape, dtype, device):
-    return torch.empty(like_shape, dtype=dtype, device=device) if t is None else t
+def _out(t, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else t
+
+
+def _like(t, x):
+    return torch.empty_like(x, memory_format=torch.contiguous_format) if t is None else t
 
 
 # ---------------------------------------------------------------- short convolution
@@ -127,7 +139,7 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     N = _num_seqs(cu_seqlens, B, dev)
     state = (N, W - 1, C)
     _expect(initial_state, "initial_state", x.dtype, state, dev)
-    out = _out(out, x.shape, x.dtype, dev)
+    out = _like(out, x)
     os = _rows(out, "out", x.dtype, x.shape, dev, 2)
     if final_state is None and output_final_state:
         final_state = torch.empty(state, dtype=x.dtype, device=dev)
@@ -171,7 +183,7 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, d_out: torch.Tensor,
     _expect(initial_state, "initial_state", x.dtype, state, dev)
     _expect(d_final_state, "d_final_state", x.dtype, state, dev)
     g = dict(grads or {})
-    g["dx"] = _out(g.get("dx"), x.shape, x.dtype, dev)
+    g["dx"] = _like(g.get("dx"), x)
     dxs = _rows(g["dx"], "dx", x.dtype, x.shape, dev, 2)
     g["dweight"] = _out(g.get("dweight"), (C, W), torch.float32, dev)
     _expect(g["dweight"], "dweight", torch.float32, (C, W), dev)
@@ -204,7 +216,7 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor,
     if state is None:
         raise TypeError("state must be a tensor")
     _expect(state, "state", x.dtype, (B, W - 1, C), dev)
-    out = _out(out, x.shape, x.dtype, dev)
+    out = _like(out, x)
     os = _rows(out, "out", x.dtype, x.shape, dev, 1)
     _call("kda_short_conv_step", dev, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(out),
           B, C, W, xs, os, act, dt)
@@ -258,8 +270,8 @@ def qk_norm(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] =
     dt = _dtype(q, "q")
     n, hq, hk, d, rot, rows, (qs, ks), lead = _qk_common(q, k, q_weight, k_weight, table,
                                                          positions, kind)
-    out_q = _out(out_q, q.shape, q.dtype, q.device)
-    out_k = _out(out_k, k.shape, q.dtype, q.device)
+    out_q = _like(out_q, q)
+    out_k = _like(out_k, k)
     oqs = _rows(out_q, "out_q", q.dtype, q.shape, q.device, lead)
     oks = _rows(out_k, "out_k", q.dtype, k.shape, q.device, lead)
     _call("kda_qk_norm_fwd", q.device, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
@@ -293,7 +305,7 @@ def qk_norm_bwd(q: torch.Tensor, k: torch.Tensor, d_out_q: torch.Tensor, d_out_k
     gks = _rows(d_out_k, "d_out_k", q.dtype, k.shape, dev, lead)
     g = dict(grads or {})
     for name, like in (("dq", q), ("dk", k)):
-        g[name] = _out(g.get(name), like.shape, q.dtype, dev)
+        g[name] = _like(g.get(name), like)
     dqs = _rows(g["dq"], "dq", q.dtype, q.shape, dev, lead)
     dks = _rows(g["dk"], "dk", q.dtype, k.shape, dev, lead)
     for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
@@ -366,7 +378,7 @@ def ssm_chunk_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.T
     n = _num_seqs(cu_seqlens, b, dev)
     state = (n, H, P, N)
     _expect(initial_state, "initial_state", torch.float32, state, dev)
-    out = _out(out, x.shape, x.dtype, dev)
+    out = _like(out, x)
     os = _rows(out, "out", x.dtype, x.shape, dev, 2)
     if final_state is None and output_final_state:
         final_state = torch.empty(state, dtype=torch.float32, device=dev)
@@ -419,7 +431,7 @@ def ssm_chunk_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.T
     g = dict(grads or {})
     rows = []
     for name, like in (("dx", x), ("dB", B), ("dC", C)):
-        g[name] = _out(g.get(name), like.shape, x.dtype, dev)
+        g[name] = _like(g.get(name), like)
         rows.append(_rows(g[name], name, x.dtype, like.shape, dev, 2))
     for name, shape in (("ddt", (b, T, H)), ("dA", (H,))):
         g[name] = _out(g.get(name), shape, torch.float32, dev)
@@ -455,7 +467,7 @@ def ssm_decode_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch
     if state is None:
         raise TypeError("state must be a tensor")
     _expect(state, "state", torch.float32, (b, H, P, N), dev)
-    out = _out(out, x.shape, x.dtype, dev)
+    out = _like(out, x)
     os = _rows(out, "out", x.dtype, x.shape, dev, 1)
     _call("kda_ssm_decode_step", dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
           _ptr(state), _ptr(out), b, H, G, P, N, xs, bs, cs, os, dtc)

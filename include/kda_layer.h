@@ -162,7 +162,7 @@ int64_t kda_qk_norm_bwd_workspace_size(int32_t tokens, int32_t q_heads, int32_t 
  * decay of zero included); a token with dt = 0 leaves the state as it is.
  * NaN and infinities in x, B or C propagate, but may also turn into NaN where
  * the formula has an infinity.  Row starts of x, B, C and out are 16-byte
- * aligned.  final_state may be initial_state itself.
+ * aligned, and 64 rows of each span less than 2^31 bytes.  final_state may be initial_state itself.
  */
 int64_t kda_ssm_chunk_fwd_workspace_size(int32_t batch, int32_t seq_len, int32_t num_seqs,
                                          int32_t num_heads, int32_t head_dim, int32_t state_dim);
