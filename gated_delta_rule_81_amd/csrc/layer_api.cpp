@@ -393,7 +393,7 @@ struct SsmSpace {
 SsmSpace ssm_space(const kda::Seqs &s, int32_t heads, int32_t p, int32_t n) {
     const PiecePlan plan = piece_plan(s, heads);
     if (!plan.split || s.num == 0) return {0, 0};
-    const int64_t count = ((int64_t)s.total / plan.len + s.num + 1) * heads;
+    const int64_t count = kda::piece_count(s, plan.len) * heads;
     return {count * p * n, count};
 }
 
@@ -472,21 +472,21 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
         a.seg_decay = static_cast<double *>(workspace);
         a.seg_states = reinterpret_cast<float *>(a.seg_decay + (space.decay + 1) / 2 * 2);
     }
-    return launch_status(kda::launch_ssm_scan(a, kda::kSsmOut, dtype, stream), stream, where);
+    return launch_status(kda::launch_ssm_out(a, dtype, stream), stream, where);
 }
 
 }  // extern "C"
 
 namespace {
 
-// The backward's workspace: piece decays and states (as the forward's), the
+// The backward's workspace: piece decays and states (the forward's, twice), the
 // states at every block from both sides, the parts of dA and dD, and with
 // several sets of heads the parts of dB and dC.
 struct SsmBwdSpace {
     SsmSpace pieces;
     int64_t blocks, states, params, bc;  // block numbers; floats of each part
     int32_t sets;
-    int64_t bytes() const { return pieces.bytes() + 4 * (2 * states + params + bc); }
+    int64_t bytes() const { return 2 * pieces.bytes() + 4 * (2 * states + params + bc); }
 };
 SsmBwdSpace ssm_bwd_space(const kda::Seqs &s, int32_t heads, int32_t groups, int32_t p, int32_t n,
                           int32_t dtype) {
@@ -494,7 +494,7 @@ SsmBwdSpace ssm_bwd_space(const kda::Seqs &s, int32_t heads, int32_t groups, int
     if (s.num == 0 || heads == 0) return w;
     w.pieces = ssm_space(s, heads, p, n);
     const int64_t block = dtype == kda::kDtypeBf16 ? 64 : 32;
-    w.blocks = (int64_t)s.total / block + s.num + 1;
+    w.blocks = kda::piece_count(s, block);
     w.states = w.blocks * heads * p * n;
     w.params = (2 * w.blocks * heads + 3) / 4 * 4;
     // sets: enough workgroups to fill the chip twice over
@@ -594,23 +594,25 @@ int kda_ssm_chunk_bwd(const void *x, const float *dt, const float *A, const void
         a.seqs = seqs, a.heads = num_heads, a.groups = num_groups;
         a.p = head_dim, a.n = state_dim, a.piece = piece_plan(seqs, num_heads).len;
         a.x_stride = x_stride, a.k_stride = b_stride;
+        kda::SsmScan b = a;  // from the right
+        b.x = d_out, b.k = C, b.x_stride = d_out_stride, b.k_stride = c_stride;
+        b.state0 = d_final_state, b.final_state = d_initial_state;
         char *at = static_cast<char *>(workspace);
         if (w.pieces.states > 0) {
+            const int64_t decays = (w.pieces.decay + 1) / 2 * 2;
             a.seg_decay = reinterpret_cast<double *>(at);
-            a.seg_states = reinterpret_cast<float *>(a.seg_decay + (w.pieces.decay + 1) / 2 * 2);
+            b.seg_decay = a.seg_decay + decays;
+            a.seg_states = reinterpret_cast<float *>(b.seg_decay + decays);
+            b.seg_states = a.seg_states + w.pieces.states;
         }
-        float *s_states = reinterpret_cast<float *>(at + w.pieces.bytes());
-        float *e_states = s_states + w.states;
-        a.block_states = s_states;
-        int rc = kda::launch_ssm_scan(a, kda::kSsmStates, dtype, stream);
-        a.x = d_out, a.k = C, a.x_stride = d_out_stride, a.k_stride = c_stride;
-        a.state0 = d_final_state, a.final_state = d_initial_state, a.block_states = e_states;
-        if (rc == 0) rc = kda::launch_ssm_scan(a, kda::kSsmStatesRev, dtype, stream);
+        a.block_states = reinterpret_cast<float *>(at + 2 * w.pieces.bytes());
+        b.block_states = a.block_states + w.states;
+        const int rc = kda::launch_ssm_states(a, b, dtype, stream);
         if (rc != 0) return launch_status(rc, stream, where);
         g.x = x, g.B = B, g.C = C, g.dy = d_out, g.dt = dt, g.A = A, g.D = D;
-        g.s_states = s_states, g.e_states = e_states;
+        g.s_states = a.block_states, g.e_states = b.block_states;
         g.dx = dx, g.dB = dB, g.dC = dC, g.ddt = ddt;
-        g.part_a = e_states + w.states, g.part_d = g.part_a + w.blocks * num_heads;
+        g.part_a = b.block_states + w.states, g.part_d = g.part_a + w.blocks * num_heads;
         g.part_bc = g.part_a + w.params;
         g.p = head_dim, g.n = state_dim, g.sets = w.sets, g.blocks = w.blocks;
         g.x_stride = x_stride, g.b_stride = b_stride, g.c_stride = c_stride;

@@ -5,7 +5,7 @@
 
 #include "kda_internal.h"
 
-#include <hip/hip_runtime_api.h>
+#include <hip/hip_runtime.h>
 #include <stdint.h>
 
 namespace kda {
@@ -16,6 +16,20 @@ struct Seqs {
     const int32_t *cu;
     int32_t num, seq_len, total;
 };
+
+// Pieces of `len` tokens of the sequences.  Equal rows: piece j of row n has
+// number n * per + j.  Packed: t0 / len + n + j, t0 the sequence's first token,
+// so that numbers of different sequences never meet whatever the offsets hold
+// (some belong to none).  An empty sequence has one (empty) piece.
+__host__ __device__ inline int64_t pieces_per_row(const Seqs &q, int64_t len) {
+    return q.seq_len > 0 ? (q.seq_len + len - 1) / len : 1;
+}
+__host__ __device__ inline int64_t piece_count(const Seqs &q, int64_t len) {
+    return q.cu ? q.total / len + q.num + 1 : q.num * pieces_per_row(q, len);
+}
+__host__ __device__ inline int64_t first_piece(const Seqs &q, int64_t len, int64_t t0, int n) {
+    return q.cu ? t0 / len + n : n * pieces_per_row(q, len);
+}
 
 struct ConvArgs {
     const void *x, *state0, *d_out, *d_final;
@@ -47,15 +61,10 @@ int launch_qk_norm_fwd(const QkArgs &a, hipStream_t stream);
 int launch_qk_norm_bwd(const QkArgs &a, hipStream_t stream);
 int64_t qk_norm_bwd_workspace_floats(int64_t tokens, int64_t heads, int head_dim);
 
-// The scan's walk over the sequences.  kSsmOut: y (and final states).
-// kSsmStates: the state entering every block, in block_states.  kSsmStatesRev:
-// the same from the right for the loss gradient of the state (x = d_out, k = C,
-// state0 = d_final_state, final_state = d_initial_state): what arrives at every
-// block's end.  With seg_states the sequences are cut into pieces of `piece`
-// tokens that run at once (seg_states: a state per piece number and head,
-// seg_decay: a double each); without, `piece` is at least every sequence's
-// length.
-constexpr int kSsmOut = 0, kSsmStates = 1, kSsmStatesRev = 2;
+// The scan's walk over the sequences.  With seg_states the sequences are cut into
+// pieces of `piece` tokens that run at once (seg_states: a state per piece
+// number and head, seg_decay: a double each); without, `piece` is at least every
+// sequence's length.
 struct SsmScan {
     const void *x, *k, *c;
     const float *dt, *A, *D, *state0;
@@ -66,7 +75,13 @@ struct SsmScan {
     int32_t heads, groups, p, n, piece;
     int64_t x_stride, k_stride, c_stride, out_stride;
 };
-int launch_ssm_scan(const SsmScan &a, int mode, int dtype, hipStream_t stream);
+// y and the final states.
+int launch_ssm_out(const SsmScan &a, int dtype, hipStream_t stream);
+// The state entering every block to a.block_states; and from the right, to
+// b.block_states, the loss gradient of the state behind every block (b: x =
+// d_out, k = C, state0 = d_final_state, final_state = d_initial_state; pieces of
+// its own).  a and b differ in nothing else.
+int launch_ssm_states(const SsmScan &a, const SsmScan &b, int dtype, hipStream_t stream);
 
 // The gradients from the states entering every block (s_states) and the loss
 // gradients behind every block (e_states), both [block number][head][n][p]:

@@ -54,9 +54,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     __shared__ float s_pair[TL][L], s_z[NTN][L], s_xdu[8 / TL][L], s_v[8 / TL][L];
     __shared__ float s_k[NTN], s_d[TL];
 
-    const int64_t units = a.blocks * a.groups * a.sets;
-    const int64_t unit = xcd_unit(units);
-    if (unit < 0) return;
+    const int64_t unit = blockIdx.x;
     const int set = (int)(unit % a.sets), group = (int)(unit / a.sets % a.groups);
     const int64_t number = unit / a.sets / a.groups;
     const int per_group = a.heads / a.groups, per_set = (per_group + a.sets - 1) / a.sets;
@@ -111,7 +109,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     auto weights = [&](int buf) {
         const double step = (double)rdt * ((double)A2 * kLog2eD);
         const double cum = wave_prefix(step < -400.0 ? -400.0 : step, lane);
-        const double all = __shfl(cum, 63, 64);
+        const double all = from_lane(cum, 63);
         if (lane < L) {
             s_cum[buf][lane] = cum;
             s_dt[buf][lane] = rdt;
@@ -377,13 +375,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
             }
 #pragma unroll
             for (int q = 0; q < NTN; ++q) k += s_k[q];
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const float zo = __shfl_down(z, d, 64), vo = __shfl_up(v, d, 64);
-                z += lane + d < 64 ? zo : 0.f;
-                v += lane >= d ? vo : 0.f;
-            }
-            v = __shfl_up(v, 1, 64);
+            z = wave_suffix(z, lane);
+            v = __shfl_up(wave_prefix(v, lane), 1, 64);
             dl += z + (lane > 0 ? v : 0.f) + s_all[buf] * k;
             float dd = 0.f;
 #pragma unroll
@@ -473,7 +466,7 @@ template <typename T> int grad(const SsmGrad &a, hipStream_t stream) {
         hipLaunchKernelGGL(ssm_params_kernel, dim3(a.heads), dim3(256), 0, stream, a);
         return hipGetLastError() == hipSuccess ? 0 : -1;
     }
-    const unsigned blocks = xcd_blocks(a.blocks * a.groups * a.sets);
+    const unsigned blocks = (unsigned)(a.blocks * a.groups * a.sets);
     if (a.n == 64)
         hipLaunchKernelGGL((ssm_grad_kernel<T, 64>), dim3(blocks), dim3(kGradWaves * 64), 0, stream, a);
     else

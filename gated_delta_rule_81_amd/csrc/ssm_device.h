@@ -133,10 +133,13 @@ __device__ __forceinline__ Parts<NP> read_cols(const bf16 *tile, int ks, int at)
     return p;
 }
 
+// Word 3 of a raw buffer descriptor (32-bit format, no swizzle).
+constexpr int kRsrcRaw = 0x00020000;
+
 // ROWS x COLS values of T, row r at p + r * stride, staged by NT threads:
 // global to registers in 16-byte pieces (rows at and past `valid` as zeros),
-// later registers to LDS as parts.  A thread's pieces lie RS rows apart in one
-// column: one 32-bit offset serves them all beside a uniform base (64 rows of a
+// later registers to LDS as parts.  Buffer loads whose descriptor ends behind the
+// last valid row: rows past it read as zeros without a branch (64 rows of a
 // tensor span less than 2^31 bytes).
 template <typename T, int ROWS, int COLS, int NT> struct Stage {
     static constexpr int E = 16 / sizeof(T), PER_ROW = COLS / E, COUNT = ROWS * PER_ROW / NT;
@@ -144,16 +147,13 @@ template <typename T, int ROWS, int COLS, int NT> struct Stage {
     static_assert(COUNT * NT == ROWS * PER_ROW && RS * PER_ROW == NT, "pieces over threads");
     u32x4 r[COUNT];
     __device__ __forceinline__ void load(const T *p, int64_t stride, int valid, int tid) {
-        const int row = tid / PER_ROW;
-        const unsigned off = (unsigned)(row * (int)stride + tid % PER_ROW * E) * (unsigned)sizeof(T);
-        const char *base = reinterpret_cast<const char *>(p);
+        const int row_bytes = (int)stride * (int)sizeof(T);
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)p, 0, (valid - 1) * row_bytes + COLS * (int)sizeof(T), kRsrcRaw);
+        const int off = tid / PER_ROW * row_bytes + tid % PER_ROW * 16;
 #pragma unroll
-        for (int i = 0; i < COUNT; ++i) {
-            r[i] = row + i * RS < valid
-                       ? *reinterpret_cast<const u32x4 *>(base + (int64_t)(i * RS) * stride *
-                                                                     (int)sizeof(T) + off)
-                       : u32x4{0u, 0u, 0u, 0u};
-        }
+        for (int i = 0; i < COUNT; ++i)
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + i * RS * row_bytes, 0, 0);
     }
     template <typename TL> __device__ __forceinline__ void store(bf16 *tile, int tid) const {
         const int row = tid / PER_ROW, col = tid % PER_ROW * E, first = TL::at(row, col);
@@ -200,14 +200,42 @@ __device__ __forceinline__ int here(int lane) {
     return lane;
 }
 
-// Inclusive sum over the 64 lanes in fp64.
-__device__ __forceinline__ double wave_prefix(double v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double o = __shfl_up(v, d, 64);
-        v += lane >= d ? o : 0.0;
-    }
-    return v;
+// Sums over the 64 lanes by DPP inside each 16-lane row and the rows' totals
+// read into scalars: no LDS round trips, which six shuffle steps would be (the
+// lane that forms a block's decays keeps the workgroup waiting).
+template <int CTRL> __device__ __forceinline__ float dpp_or_zero(float x) {
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL> __device__ __forceinline__ double dpp_or_zero(double x) {
+    const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(x), CTRL, 0xf, 0xf, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(x), CTRL, 0xf, 0xf, true);
+    return __hiloint2double(hi, lo);
+}
+__device__ __forceinline__ float from_lane(float x, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+__device__ __forceinline__ double from_lane(double x, int lane) {
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(x), lane),
+                            __builtin_amdgcn_readlane(__double2loint(x), lane));
+}
+// Inclusive sum over lanes 0 .. l.
+template <typename V> __device__ __forceinline__ V wave_prefix(V v, int lane) {
+    v += dpp_or_zero<0x111>(v);  // row_shr 1, 2, 4, 8
+    v += dpp_or_zero<0x112>(v);
+    v += dpp_or_zero<0x114>(v);
+    v += dpp_or_zero<0x118>(v);
+    const V r0 = from_lane(v, 15), r1 = from_lane(v, 31), r2 = from_lane(v, 47);
+    return v + (lane < 16 ? V(0) : lane < 32 ? r0 : lane < 48 ? r0 + r1 : r0 + r1 + r2);
+}
+// Inclusive sum over lanes l .. 63.
+template <typename V> __device__ __forceinline__ V wave_suffix(V v, int lane) {
+    v += dpp_or_zero<0x101>(v);  // row_shl 1, 2, 4, 8
+    v += dpp_or_zero<0x102>(v);
+    v += dpp_or_zero<0x104>(v);
+    v += dpp_or_zero<0x108>(v);
+    const V r1 = from_lane(v, 16), r2 = from_lane(v, 32), r3 = from_lane(v, 48);
+    return v + (lane < 16 ? r1 + r2 + r3 : lane < 32 ? r2 + r3 : lane < 48 ? r3 : V(0));
 }
 
 constexpr double kLog2eD = 1.4426950408889634073599;
@@ -215,12 +243,7 @@ constexpr double kLog2eD = 1.4426950408889634073599;
 // Tokens of a block of the scan (and of a checkpoint of its backward).
 template <typename T> constexpr int kSsmBlock = sizeof(T) == 2 ? 64 : 32;
 
-// Pieces of `len` tokens of the sequences: piece j of sequence n, whose first
-// token is t0, has number t0 / len + n + j, so numbers of different sequences
-// never meet, and an empty sequence has one (empty) piece.
-__host__ __device__ __forceinline__ int64_t piece_count(int64_t total, int64_t num, int64_t len) {
-    return total / len + num + 1;
-}
+// One of the pieces the sequences are cut into (piece_count).
 struct Piece {
     int seq, index, beg, end;  // sequence, number in it, tokens [beg, end)
     int seq_beg, seq_end;
@@ -228,9 +251,10 @@ struct Piece {
 };
 __device__ __forceinline__ Piece find_piece(const Seqs &q, int64_t number, int len) {
     int lo = 0, hi = q.num - 1;
-    while (lo < hi) {
+    if (!q.cu) lo = (int)(number / pieces_per_row(q, len));
+    while (q.cu && lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (seq_first_token(q.cu, q.seq_len, q.total, mid) / len + mid <= number)
+        if (first_piece(q, len, seq_first_token(q.cu, q.seq_len, q.total, mid), mid) <= number)
             lo = mid;
         else
             hi = mid - 1;
@@ -240,7 +264,7 @@ __device__ __forceinline__ Piece find_piece(const Seqs &q, int64_t number, int l
     p.seq_beg = (int)seq_first_token(q.cu, q.seq_len, q.total, lo);
     p.seq_end = seq_end_token(q, lo);
     if (p.seq_end < p.seq_beg) p.seq_end = p.seq_beg;  // malformed offsets
-    const int64_t index = number - (p.seq_beg / len + lo);
+    const int64_t index = number - first_piece(q, len, p.seq_beg, lo);
     const int64_t count = p.seq_end > p.seq_beg ? (p.seq_end - p.seq_beg + (int64_t)len - 1) / len : 1;
     p.any = index >= 0 && index < count;
     p.index = (int)index;
@@ -252,13 +276,19 @@ __device__ __forceinline__ Piece find_piece(const Seqs &q, int64_t number, int l
     return p;
 }
 
-// Workgroups of one XCD (blockIdx % 8) take consecutive units, so that the
-// heads that read the same B and C rows share an L2.  Returns -1 past the end.
-__device__ __forceinline__ int64_t xcd_unit(int64_t units) {
-    const int64_t per = (units + 7) / 8;
-    const int64_t u = (int64_t)(blockIdx.x % 8) * per + blockIdx.x / 8;
-    return blockIdx.x / 8 < per && u < units ? u : -1;
+// The heads of one (piece, group) read the same B and C rows: their workgroups
+// go to one XCD (blockIdx % 8) and share its L2, and the (piece, group) bundles
+// are dealt to the XCDs in turn, so that pieces without tokens spread evenly.
+// Returns number * heads + head, or -1 past the end.
+__device__ __forceinline__ int64_t xcd_unit(unsigned block, int64_t numbers, int heads,
+                                            int groups) {
+    const int per = heads / groups;
+    const int64_t i = block / 8, bundle = i / per * 8 + block % 8;
+    if (bundle >= numbers * groups) return -1;
+    return bundle / groups * heads + bundle % groups * per + i % per;
 }
-inline unsigned xcd_blocks(int64_t units) { return (unsigned)((units + 7) / 8 * 8); }
+inline unsigned xcd_blocks(int64_t numbers, int heads, int groups) {
+    return (unsigned)((numbers * groups + 7) / 8 * 8 * (heads / groups));
+}
 
 }  // namespace kda

@@ -21,14 +21,6 @@
 // once more and does 4 P N of the second's 4 P N + 2 L (P + N) operations a token.
 #include "ssm_device.h"
 
-#ifndef SCAN_OCC
-#define SCAN_OCC (P == 64 && sizeof(T) == 2 ? 3 : 2)
-#endif
-#ifdef SCAN_SB
-#define SB __builtin_amdgcn_sched_barrier(0)
-#else
-#define SB
-#endif
 namespace kda {
 namespace {
 
@@ -36,26 +28,39 @@ enum Mode { kLocal, kOut, kStates };
 
 // REV walks the blocks from the last to the first and the tokens' weights from
 // the right: the gradient's recurrence E_{t-1} = e^{dt_t A} (E_t + x_t k_t^T).
-template <typename T, int P, int N, int MODE, bool REV>
-__global__ __launch_bounds__(P * 4, SCAN_OCC) void ssm_scan_kernel(SsmScan a) {
-    constexpr int L = kSsmBlock<T>, NT = P * 4, NI = sizeof(T) == 2 ? 1 : 3;
+// LDS of one block's tiles.
+template <typename T, int P, int N, int MODE> struct ScanLds {
+    static constexpr int L = kSsmBlock<T>, NI = sizeof(T) == 2 ? 1 : 3;
     // Parts of y's fp32 operands, the block's weights M and the state: two for a
     // bf16 y (2^-15, nothing beside its own rounding), three for an fp32 one.
-    constexpr int KM = sizeof(T) == 2 ? 2 : 3, KP = KM;
-    constexpr bool OUT = MODE == kOut;
+    static constexpr int KP = sizeof(T) == 2 ? 2 : 3;
+    static constexpr bool OUT = MODE == kOut;
     typedef Tile<NI, L, N> TK;
     typedef Tile<NI, L, P> TX;
-    typedef Tile<KM, L, L> TM;
-    __shared__ __attribute__((aligned(16))) bf16 sk[TK::ELEMS];
-    __shared__ __attribute__((aligned(16))) bf16 sc[OUT ? TK::ELEMS : 8];
-    __shared__ __attribute__((aligned(16))) bf16 sx[TX::ELEMS];
-    __shared__ __attribute__((aligned(16))) bf16 sm[OUT ? TM::ELEMS : 8];
-    __shared__ __attribute__((aligned(16))) double s_cum[2][L];  // log2 of the decay up to t
-    __shared__ __attribute__((aligned(16))) float s_dt[2][L], s_w[2][L], s_in[2][L];
-    __shared__ double s_tot[2];
+    typedef Tile<KP, L, L> TM;
+    __attribute__((aligned(16))) bf16 k[TK::ELEMS];
+    __attribute__((aligned(16))) bf16 c[OUT ? TK::ELEMS : 8];
+    __attribute__((aligned(16))) bf16 x[TX::ELEMS];
+    __attribute__((aligned(16))) bf16 m[OUT ? TM::ELEMS : 8];
+    __attribute__((aligned(16))) double cum[2][L];  // log2 of the decay up to t
+    __attribute__((aligned(16))) float dt[2][L], w[2][L], in[2][L];
+    double tot[2];
+};
 
-    const int64_t unit = xcd_unit(piece_count(a.seqs.total, a.seqs.num, a.piece) * a.heads);
-    if (unit < 0) return;
+template <typename T, int P, int N, int MODE, bool REV>
+__device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
+                                          ScanLds<T, P, N, MODE> &lds) {
+    typedef ScanLds<T, P, N, MODE> S_;
+    constexpr int L = S_::L, NT = P * 4, NI = S_::NI, KM = S_::KP, KP = S_::KP;
+    constexpr bool OUT = S_::OUT;
+    typedef typename S_::TK TK;
+    typedef typename S_::TX TX;
+    typedef typename S_::TM TM;
+    bf16 *sk = lds.k, *sc = lds.c, *sx = lds.x, *sm = lds.m;
+    auto &s_cum = lds.cum;
+    auto &s_dt = lds.dt, &s_w = lds.w, &s_in = lds.in;
+    auto &s_tot = lds.tot;
+
     const int h = (int)(unit % a.heads);
     const int64_t number = unit / a.heads;
     const Piece pc = find_piece(a.seqs, number, a.piece);
@@ -115,7 +120,7 @@ __global__ __launch_bounds__(P * 4, SCAN_OCC) void ssm_scan_kernel(SsmScan a) {
     auto weights = [&](int buf) {  // by the last wave
         const double step = (double)rdt * A;
         const double cum = wave_prefix(step < -400.0 ? -400.0 : step, lane);
-        const double all = __shfl(cum, 63, 64);
+        const double all = from_lane(cum, 63);
         total += all;
         if (lane < L) {
             s_cum[buf][lane] = cum;
@@ -147,7 +152,7 @@ __global__ __launch_bounds__(P * 4, SCAN_OCC) void ssm_scan_kernel(SsmScan a) {
             if (weigher) load_dt(i + 1);
         }
         if constexpr (MODE == kStates) {
-            const int64_t block = pc.seq_beg / L + pc.seq + (t0 - pc.seq_beg) / L;
+            const int64_t block = first_piece(a.seqs, L, pc.seq_beg, pc.seq) + (t0 - pc.seq_beg) / L;
             float *to = a.block_states + (block * a.heads + h) * (int64_t)(P * N) +
                         (int64_t)r * P + 16 * wave + 4 * g;
 #pragma unroll
@@ -189,7 +194,6 @@ __global__ __launch_bounds__(P * 4, SCAN_OCC) void ssm_scan_kernel(SsmScan a) {
                         }
                         *reinterpret_cast<bf16x4 *>(sm + part * TM::PLANE + TM::at(t, s)) = o;
                     }
-                    SB;
                 }
             // y^T = S C^T e^{cum}: rows p, columns t
 #pragma unroll
@@ -203,7 +207,6 @@ __global__ __launch_bounds__(P * 4, SCAN_OCC) void ssm_scan_kernel(SsmScan a) {
 #pragma unroll
                 for (int it = 0; it < L / 16; ++it)
                     y[it] = mma(sp, read_rows<TK, NI>(sc, 16 * it, ks, krow), y[it]);
-                SB;
             }
 #pragma unroll
             for (int it = 0; it < L / 16; ++it) y[it] *= s_in[buf][16 * it + r];
@@ -225,7 +228,6 @@ __global__ __launch_bounds__(P * 4, SCAN_OCC) void ssm_scan_kernel(SsmScan a) {
                 f[e] = v * (e < 4 ? w0[e % 4] : w1[e % 4]);
             }
             xw[ks] = split<3>(f);
-            SB;
         }
         if constexpr (OUT) {
             const int n = pc.end - t0;
@@ -250,7 +252,6 @@ __global__ __launch_bounds__(P * 4, SCAN_OCC) void ssm_scan_kernel(SsmScan a) {
                 if (t < n)
                     store4(out + (int64_t)(t0 + t) * a.out_stride, y[it][0], y[it][1], y[it][2],
                            y[it][3]);
-                SB;
             }
         }
         const float decay = fast_exp2((float)s_tot[buf]);
@@ -284,19 +285,49 @@ __global__ __launch_bounds__(P * 4, SCAN_OCC) void ssm_scan_kernel(SsmScan a) {
         }
 }
 
+template <typename T, int P, int N>
+__global__ __launch_bounds__(P * 4, 2) void ssm_out_kernel(SsmScan a) {
+    __shared__ ScanLds<T, P, N, kOut> lds;
+    const int64_t unit = xcd_unit(blockIdx.x, piece_count(a.seqs, a.piece), a.heads, a.groups);
+    if (unit >= 0) scan_body<T, P, N, kOut, false>(a, unit, lds);
+}
+
+template <typename T, int P, int N>
+__global__ __launch_bounds__(P * 4, 2) void ssm_local_kernel(SsmScan a) {
+    __shared__ ScanLds<T, P, N, kLocal> lds;
+    const int64_t unit = xcd_unit(blockIdx.x, piece_count(a.seqs, a.piece), a.heads, a.groups);
+    if (unit >= 0) scan_body<T, P, N, kLocal, false>(a, unit, lds);
+}
+
+// Both directions of the backward's walk in one launch (half the workgroups
+// each): neither alone has enough workgroups to hide its own latencies.
+template <typename T, int P, int N, int MODE>
+__global__ __launch_bounds__(P * 4, 2) void ssm_both_kernel(SsmScan a, SsmScan b) {
+    __shared__ ScanLds<T, P, N, MODE> lds;
+    const bool rev = blockIdx.x >= gridDim.x / 2;
+    const int64_t unit = xcd_unit(rev ? blockIdx.x - gridDim.x / 2 : blockIdx.x,
+                                  piece_count(a.seqs, a.piece), a.heads, a.groups);
+    if (unit < 0) return;
+    if (!rev)
+        scan_body<T, P, N, MODE, false>(a, unit, lds);
+    else
+        scan_body<T, P, N, MODE, true>(b, unit, lds);
+}
+
 // The pieces' own final states turned in place into entering states:
 // enter[next] = e^{decay} enter + own.  One workgroup per 1024 values of a
 // (sequence, head); the pieces one after the other, the next one's load ahead.
-template <bool REV> __global__ __launch_bounds__(256) void ssm_fold_kernel(SsmScan a, int values) {
+template <bool REV>
+__device__ __forceinline__ void fold_body(const SsmScan &a, int values, int64_t block) {
     const int per = values / 1024;
-    const int64_t u = blockIdx.x / per;
+    const int64_t u = block / per;
     const int h = (int)(u % a.heads), n = (int)(u / a.heads);
-    const int64_t off = (int64_t)(blockIdx.x % per) * 1024 + threadIdx.x * 4;
+    const int64_t off = block % per * 1024 + threadIdx.x * 4;
     const int beg = (int)seq_first_token(a.seqs.cu, a.seqs.seq_len, a.seqs.total, n);
     const int end = seq_end_token(a.seqs, n);
     const int count = end > beg ? (int)(((int64_t)end - beg + a.piece - 1) / a.piece) : 1;
     if (count < 2) return;
-    const int64_t first = beg / a.piece + n;
+    const int64_t first = first_piece(a.seqs, a.piece, beg, n);
     auto at = [&](int j) {
         return a.seg_states + ((first + (REV ? count - 1 - j : j)) * a.heads + h) * (int64_t)values + off;
     };
@@ -313,47 +344,64 @@ template <bool REV> __global__ __launch_bounds__(256) void ssm_fold_kernel(SsmSc
     }
 }
 
-template <typename T, int P, int N, int MODE, bool REV>
-void launch(const SsmScan &a, hipStream_t stream) {
-    const int64_t units = piece_count(a.seqs.total, a.seqs.num, a.piece) * a.heads;
-    hipLaunchKernelGGL((ssm_scan_kernel<T, P, N, MODE, REV>), dim3(xcd_blocks(units)), dim3(P * 4),
-                       0, stream, a);
+__global__ __launch_bounds__(256) void ssm_fold_kernel(SsmScan a, int values) {
+    fold_body<false>(a, values, blockIdx.x);
 }
-
-template <typename T, int P, int N> int scan(const SsmScan &args, int mode, hipStream_t stream) {
-    SsmScan a = args;
-    if (a.seg_states) {
-        const int64_t folds = (int64_t)a.seqs.num * a.heads * (P * N / 1024);
-        if (mode == kSsmStatesRev) {
-            launch<T, P, N, kLocal, true>(a, stream);
-            hipLaunchKernelGGL((ssm_fold_kernel<true>), dim3((unsigned)folds), dim3(256), 0, stream,
-                               a, P * N);
-        } else {
-            launch<T, P, N, kLocal, false>(a, stream);
-            hipLaunchKernelGGL((ssm_fold_kernel<false>), dim3((unsigned)folds), dim3(256), 0,
-                               stream, a, P * N);
-        }
-    }
-    if (mode == kSsmOut)
-        launch<T, P, N, kOut, false>(a, stream);
-    else if (mode == kSsmStates)
-        launch<T, P, N, kStates, false>(a, stream);
+__global__ __launch_bounds__(256) void ssm_fold_both_kernel(SsmScan a, SsmScan b, int values,
+                                                            unsigned blocks) {
+    if (blockIdx.x < blocks)
+        fold_body<false>(a, values, blockIdx.x);
     else
-        launch<T, P, N, kStates, true>(a, stream);
-    return hipGetLastError() == hipSuccess ? 0 : -1;
+        fold_body<true>(b, values, blockIdx.x - blocks);
 }
 
-template <typename T> int scan_dims(const SsmScan &a, int mode, hipStream_t stream) {
-    if (a.p == 64)
-        return a.n == 64 ? scan<T, 64, 64>(a, mode, stream) : scan<T, 64, 128>(a, mode, stream);
-    return a.n == 64 ? scan<T, 128, 64>(a, mode, stream) : scan<T, 128, 128>(a, mode, stream);
+template <typename T, int P, int N> struct Scan {
+    static int out(const SsmScan &a, hipStream_t stream) {
+        const unsigned blocks = xcd_blocks(piece_count(a.seqs, a.piece), a.heads, a.groups);
+        if (a.seg_states) {
+            hipLaunchKernelGGL((ssm_local_kernel<T, P, N>), dim3(blocks), dim3(P * 4), 0,
+                               stream, a);
+            hipLaunchKernelGGL(ssm_fold_kernel, dim3((unsigned)folds(a)), dim3(256), 0, stream, a,
+                               P * N);
+        }
+        hipLaunchKernelGGL((ssm_out_kernel<T, P, N>), dim3(blocks), dim3(P * 4), 0,
+                           stream, a);
+        return hipGetLastError() == hipSuccess ? 0 : -1;
+    }
+    static int both(const SsmScan &a, const SsmScan &b, hipStream_t stream) {
+        const unsigned blocks = xcd_blocks(piece_count(a.seqs, a.piece), a.heads, a.groups);
+        if (a.seg_states) {
+            hipLaunchKernelGGL((ssm_both_kernel<T, P, N, kLocal>), dim3(2 * blocks),
+                               dim3(P * 4), 0, stream, a, b);
+            const unsigned f = (unsigned)folds(a);
+            hipLaunchKernelGGL(ssm_fold_both_kernel, dim3(2 * f), dim3(256), 0, stream, a, b, P * N,
+                               f);
+        }
+        hipLaunchKernelGGL((ssm_both_kernel<T, P, N, kStates>), dim3(2 * blocks),
+                           dim3(P * 4), 0, stream, a, b);
+        return hipGetLastError() == hipSuccess ? 0 : -1;
+    }
+    static int64_t folds(const SsmScan &a) {
+        return (int64_t)a.seqs.num * a.heads * (P * N / 1024);
+    }
+};
+
+template <typename F> int by_dims(const SsmScan &a, int dtype, F f) {
+    const bool p = a.p == 64, n = a.n == 64;
+    if (dtype == kDtypeBf16)
+        return p ? (n ? f(Scan<bf16, 64, 64>()) : f(Scan<bf16, 64, 128>()))
+                 : (n ? f(Scan<bf16, 128, 64>()) : f(Scan<bf16, 128, 128>()));
+    return p ? (n ? f(Scan<float, 64, 64>()) : f(Scan<float, 64, 128>()))
+             : (n ? f(Scan<float, 128, 64>()) : f(Scan<float, 128, 128>()));
 }
 
 }  // namespace
 
-int launch_ssm_scan(const SsmScan &a, int mode, int dtype, hipStream_t stream) {
-    return dtype == kDtypeBf16 ? scan_dims<bf16>(a, mode, stream)
-                               : scan_dims<float>(a, mode, stream);
+int launch_ssm_out(const SsmScan &a, int dtype, hipStream_t stream) {
+    return by_dims(a, dtype, [&](auto s) { return s.out(a, stream); });
+}
+int launch_ssm_states(const SsmScan &a, const SsmScan &b, int dtype, hipStream_t stream) {
+    return by_dims(a, dtype, [&](auto s) { return s.both(a, b, stream); });
 }
 
 }  // namespace kda
