@@ -17,6 +17,20 @@ namespace {
 
 constexpr int kWaves = 4;  // runs of one workgroup (one per wave)
 
+// A wave's run of tokens is the same for its 64 lanes; said so, the token, its
+// sequence and its row's address stay in scalar registers and branches.
+__device__ __forceinline__ int wave_of_block() {
+    return __builtin_amdgcn_readfirstlane(threadIdx.y);
+}
+// Channel c of a row: a scalar base and a 32-bit offset per lane.
+template <typename T> __device__ __forceinline__ const T *col(const T *row, int c) {
+    return reinterpret_cast<const T *>(reinterpret_cast<const char *>(row) +
+                                       (unsigned)c * (unsigned)sizeof(T));
+}
+template <typename T> __device__ __forceinline__ T *col(T *row, int c) {
+    return reinterpret_cast<T *>(reinterpret_cast<char *>(row) + (unsigned)c * (unsigned)sizeof(T));
+}
+
 // Row `r` of the sequence that begins at token `beg`, as floats: a token's, or
 // row r - beg + W - 1 of the sequence's state for the W - 1 rows before it.
 template <typename T, int VEC, int W>
@@ -24,9 +38,9 @@ __device__ __forceinline__ void seq_row(const T *x, int64_t xs, const T *state0,
                                         int c, int r, int beg, float (&f)[VEC]) {
     typedef Row<T, VEC> R;
     if (r >= beg) {
-        R::get(R::raw(x + (int64_t)r * xs + c), f);
+        R::get(R::raw(col(x + (int64_t)(r) * xs, c)), f);
     } else if (state0) {
-        R::get(R::raw(state0 + (n * (W - 1) + (r - beg + W - 1)) * (int64_t)C + c), f);
+        R::get(R::raw(col(state0 + (n * (W - 1) + (r - beg + W - 1)) * (int64_t)C, c)), f);
     } else {
         R::get(R::zero(), f);
     }
@@ -67,14 +81,14 @@ template <typename T, int VEC, int W>
 __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs a, int cblocks,
                                                                int run_blocks, int run) {
     typedef Row<T, VEC> R;
-    constexpr int U = 8;  // rows in flight
+    constexpr int U = 4;  // rows loaded together, the next ones' loads ahead
     const T *x = static_cast<const T *>(a.x), *state0 = static_cast<const T *>(a.state0);
-    const int C = a.channels;
+    const int C = a.channels, wave = wave_of_block();
     const int c = ((int)(blockIdx.x % cblocks) * 64 + (int)threadIdx.x) * VEC;
     if (c >= C) return;
     const int64_t blk = blockIdx.x / cblocks;
     if (blk >= run_blocks) {
-        const int64_t unit = (blk - run_blocks) * kWaves + threadIdx.y;
+        const int64_t unit = (blk - run_blocks) * kWaves + wave;
         const int64_t n = unit / (W - 1);
         const int j = (int)(unit % (W - 1));
         if (n >= a.seqs.num) return;
@@ -87,7 +101,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs a, int c
         R::put(static_cast<T *>(a.final_state) + (n * (W - 1) + j) * (int64_t)C + c, f);
         return;
     }
-    const int64_t first = (blk * kWaves + threadIdx.y) * (int64_t)run;
+    const int64_t first = (blk * kWaves + wave) * (int64_t)run;
     if (first >= a.seqs.total) return;
     const int t0 = (int)first;
     const int t1 = first + run < a.seqs.total ? (int)(first + run) : a.seqs.total;
@@ -96,11 +110,18 @@ __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs a, int c
     float w[W][VEC], b[VEC], win[W][VEC];  // win: rows t - (W-1) .. t
     load_params<VEC, W>(a, c, w, b);
     int beg = 0, end = t0, n = -1;
+    typename R::vec next[U];
+    auto load = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            next[i] = t + i < t1 ? R::raw(col(x + (int64_t)(t + i) * a.x_stride, c)) : R::zero();
+    };
+    load(t0);
     for (int t = t0; t < t1; t += U) {
         typename R::vec raw[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-            raw[i] = t + i < t1 ? R::raw(x + (int64_t)(t + i) * a.x_stride + c) : R::zero();
+        for (int i = 0; i < U; ++i) raw[i] = next[i];
+        load(t + U);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int tt = t + i;
@@ -125,7 +146,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs a, int c
                 for (int j = 0; j < W; ++j) z += w[j][e] * win[j][e];
                 y[e] = a.silu ? z * sigmoid(z) : z;
             }
-            R::put(out + (int64_t)tt * a.out_stride + c, y);
+            R::put(col(out + (int64_t)tt * a.out_stride, c), y);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
@@ -162,7 +183,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int c
     __shared__ float sum[kWaves - 1][W + 1][VEC][64];
     const T *x = static_cast<const T *>(a.x), *state0 = static_cast<const T *>(a.state0);
     const T *dy = static_cast<const T *>(a.d_out), *d_final = static_cast<const T *>(a.d_final);
-    const int C = a.channels;
+    const int C = a.channels, wave = wave_of_block();
     const int c = ((int)(blockIdx.x % cblocks) * 64 + (int)threadIdx.x) * VEC;
     const bool on = c < C;
     const int64_t blk = blockIdx.x / cblocks;
@@ -170,7 +191,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int c
     if (on) load_params<VEC, W>(a, c, w, b);
 
     if (blk >= run_blocks) {  // gradient of the initial states: kWaves sequences each
-        const int64_t n = (blk - run_blocks) * kWaves + threadIdx.y;
+        const int64_t n = (blk - run_blocks) * kWaves + wave;
         if (!on || n >= a.seqs.num) return;
         const int beg = (int)seq_first_token(a.seqs.cu, a.seqs.seq_len, a.seqs.total, (int)n);
         int end = seq_end_token(a.seqs, (int)n);
@@ -185,7 +206,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int c
                 for (int j = 0; j < W; ++j)
                     seq_row<T, VEC, W>(x, a.x_stride, state0, n, C, c, beg + t - (W - 1) + j, beg,
                                        win[j]);
-                R::get(R::raw(dy + (int64_t)(beg + t) * a.d_out_stride + c), dz[t]);
+                R::get(R::raw(col(dy + (int64_t)(beg + t) * a.d_out_stride, c)), dz[t]);
                 grad_z<VEC, W>(w, b, win, a.silu, dz[t]);
             }
         }
@@ -204,7 +225,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int c
         return;
     }
 
-    const int64_t first = (blk * kWaves + threadIdx.y) * (int64_t)run;
+    const int64_t first = (blk * kWaves + wave) * (int64_t)run;
     float dw[W][VEC], db[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -231,7 +252,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int c
             for (int i = 0; i < W; ++i)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) g[e] += w[W - 1 - i][e] * dz[i][e];
-            R::put(dx + (int64_t)s * a.dx_stride + c, g);
+            R::put(col(dx + (int64_t)s * a.dx_stride, c), g);
         };
         auto shift = [&]() {
 #pragma unroll
@@ -251,14 +272,21 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int c
         };
 
         bool done = false;
-        for (int t = t0; t < t2 && !done; t += U) {
-            typename R::vec rx[U], rg[U];
+        typename R::vec nx[U], ng[U];  // the next rows, their loads ahead
+        auto load = [&](int t) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const bool in = t + i < t2;
-                rx[i] = in ? R::raw(x + (int64_t)(t + i) * a.x_stride + c) : R::zero();
-                rg[i] = in ? R::raw(dy + (int64_t)(t + i) * a.d_out_stride + c) : R::zero();
+                nx[i] = in ? R::raw(col(x + (int64_t)(t + i) * a.x_stride, c)) : R::zero();
+                ng[i] = in ? R::raw(col(dy + (int64_t)(t + i) * a.d_out_stride, c)) : R::zero();
             }
+        };
+        load(t0);
+        for (int t = t0; t < t2 && !done; t += U) {
+            typename R::vec rx[U], rg[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) rx[i] = nx[i], rg[i] = ng[i];
+            load(t + U);
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int tt = t + i;
@@ -308,16 +336,16 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int c
         // the walk ended where its sequence does (t2 = total, or the next begins at t2)
         if (!done && n >= 0 && end <= t2) flush();
     }
-    if (threadIdx.y > 0) {
+    if (wave > 0) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            sum[threadIdx.y - 1][W][e][threadIdx.x] = db[e];
+            sum[wave - 1][W][e][threadIdx.x] = db[e];
 #pragma unroll
-            for (int j = 0; j < W; ++j) sum[threadIdx.y - 1][j][e][threadIdx.x] = dw[j][e];
+            for (int j = 0; j < W; ++j) sum[wave - 1][j][e][threadIdx.x] = dw[j][e];
         }
     }
     __syncthreads();
-    if (threadIdx.y == 0 && on) {
+    if (wave == 0 && on) {
         float *p = a.partial + blk * (W + 1) * (int64_t)C + c;
 #pragma unroll
         for (int j = 0; j <= W; ++j)
@@ -356,9 +384,9 @@ template <typename T, int VEC, int W>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, T *state, int cblocks,
                                                         int batch) {
     typedef Row<T, VEC> R;
-    const int C = a.channels;
+    const int C = a.channels, wave = wave_of_block();
     const int c = ((int)(blockIdx.x % cblocks) * 64 + (int)threadIdx.x) * VEC;
-    const int64_t n = (int64_t)(blockIdx.x / cblocks) * kWaves + threadIdx.y;
+    const int64_t n = (int64_t)(blockIdx.x / cblocks) * kWaves + wave;
     if (c >= C || n >= batch) return;
     T *st = state + n * (W - 1) * (int64_t)C + c;
     typename R::vec raw[W];

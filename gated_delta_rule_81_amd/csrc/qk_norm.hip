@@ -104,12 +104,20 @@ __device__ __forceinline__ const T *head_at(const void *const (&p)[2], const int
     return static_cast<const T *>(p[which]) + token * stride[which] + (int64_t)h * d;
 }
 
+// Eight channels of both weights (ones where there is none).
+__device__ __forceinline__ void load_weights(const QkArgs &a, int e0, float (&w)[2][8]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[k][e] = a.weight[k] ? a.weight[k][e0 + e] : 1.f;
+}
+
 // Unit: (token, group of kPasses passes).  One wave per unit.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkArgs a, int groups) {
     constexpr int LPR = D / 8, HPP = 64 / LPR;  // lanes per head, heads per pass
     const int lane = threadIdx.x & 63;
-    const int64_t unit = (int64_t)blockIdx.x * kWavesPerBlock + (threadIdx.x >> 6);
+    const int64_t unit = (int64_t)blockIdx.x * kWavesPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t token = unit / groups;
     if (token >= a.tokens) return;
     const int h0 = (int)(unit % groups) * (kPasses * HPP) + lane / LPR;
@@ -122,6 +130,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkArgs a, int gro
                                               which ? h - a.heads[0] : h, D) + e0)
                            : Vec8<T>::zero();
     }
+    float wt[2][8];
+    load_weights(a, e0, wt);
     Turn turn;
     if (a.rot) turn = load_turn<D>(a, token, lane, false);
 #pragma unroll
@@ -133,12 +143,11 @@ __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkArgs a, int gro
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
         const float inv = inv_norm(head_sum<LPR>(ss), a.rms, D, a.eps);
-        const float *w = a.weight[which];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= inv;
-        if (w) {
+        if (a.weight[0] || a.weight[1]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= w[e0 + e];
+            for (int e = 0; e < 8; ++e) x[e] *= which ? wt[1][e] : wt[0][e];
         }
         if (a.rot) rotate(turn, a.interleaved, x);
         if (h < heads)
@@ -153,12 +162,14 @@ template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkArgs a, int groups) {
     constexpr int LPR = D / 8, HPP = 64 / LPR;
     __shared__ float sum[kWavesPerBlock][2][HPP][D];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int heads = a.heads[0] + a.heads[1], e0 = 8 * (lane % LPR);
     const int64_t units = (int64_t)a.tokens * groups;
     float dw[2][8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
+    float wt[2][8];
+    load_weights(a, e0, wt);
     for (int64_t unit = (int64_t)blockIdx.x * kWavesPerBlock + wave; unit < units;
          unit += (int64_t)gridDim.x * kWavesPerBlock) {
         const int64_t token = unit / groups;
@@ -187,14 +198,13 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkArgs a, int gro
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
             const float inv = inv_norm(head_sum<LPR>(ss), a.rms, D, a.eps);
-            const float *w = a.weight[which];
-            if (w) {
+            if (a.weight[0] || a.weight[1]) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float v = h < heads ? g[e] * x[e] * inv : 0.f;
                     dw[0][e] += which ? 0.f : v;
                     dw[1][e] += which ? v : 0.f;
-                    g[e] *= w[e0 + e];
+                    g[e] *= which ? wt[1][e] : wt[0][e];
                 }
             }
             float dot = 0.f;
@@ -226,19 +236,23 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkArgs a, int gro
     }
 }
 
-// dq_weight and dk_weight: `rows` rows of [2][D], eight columns per workgroup.
-__global__ __launch_bounds__(512) void qk_reduce_kernel(const float *partial, int rows, int D,
-                                                        float *dq, float *dk) {
-    __shared__ float part[64][8];
+// dq_weight and dk_weight: `rows` rows of [2][D], eight columns per workgroup,
+// 128 rows side by side.
+__global__ __launch_bounds__(1024) void qk_reduce_kernel(const float *partial, int rows, int D,
+                                                         float *dq, float *dk) {
+    __shared__ float part[128][8];
     const int col = blockIdx.x * 8 + threadIdx.x;
     float s = 0.f;
-    for (int r = threadIdx.y; r < rows; r += 64) s += partial[(int64_t)r * 2 * D + col];
+#pragma unroll 4
+    for (int r = threadIdx.y; r < rows; r += 128) s += partial[(int64_t)r * 2 * D + col];
     part[threadIdx.y][threadIdx.x] = s;
-    __syncthreads();
+    for (int k = 64; k > 0; k >>= 1) {
+        __syncthreads();
+        if (threadIdx.y < k) part[threadIdx.y][threadIdx.x] += part[threadIdx.y + k][threadIdx.x];
+    }
     if (threadIdx.y) return;
-    for (int k = 1; k < 64; ++k) s += part[k][threadIdx.x];
     float *out = col < D ? dq : dk;
-    if (out) out[col % D] = s;
+    if (out) out[col % D] = part[0][threadIdx.x];
 }
 
 int groups_of(int heads, int d) {
@@ -247,7 +261,7 @@ int groups_of(int heads, int d) {
 }
 // Workgroups of the backward: enough to fill the chip several times over,
 // few enough that their partial sums stay small beside the data.
-constexpr int kBwdBlocks = 2048;
+constexpr int kBwdBlocks = 1024;
 int bwd_blocks(int64_t units) {
     const int64_t b = (units + kWavesPerBlock - 1) / kWavesPerBlock;
     return (int)(b < kBwdBlocks ? b : kBwdBlocks);
@@ -272,7 +286,7 @@ template <typename T, int D> int bwd(const QkArgs &args, hipStream_t stream) {
         hipLaunchKernelGGL((qk_norm_bwd_kernel<T, D>), dim3(blocks), dim3(kThreads), 0, stream, a,
                            groups);
     if (weights)
-        hipLaunchKernelGGL(qk_reduce_kernel, dim3(2 * D / 8), dim3(8, 64), 0, stream, a.partial,
+        hipLaunchKernelGGL(qk_reduce_kernel, dim3(2 * D / 8), dim3(8, 128), 0, stream, a.partial,
                            blocks, D, a.dweight[0], a.dweight[1]);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }

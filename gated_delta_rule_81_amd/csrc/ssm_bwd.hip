@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     const int h0 = group * per_group + set * per_set;
     const int h1 = set * per_set + per_set < per_group ? h0 + per_set : (group + 1) * per_group;
     const Piece pc = find_piece(a.seqs, number, L);
-    const int tid = threadIdx.x, lane0 = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane0 = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int lane = lane0, r = lane & 15, g = lane >> 4;
     const int n = pc.any ? pc.end - pc.beg : 0, t0 = pc.beg;
     if (n <= 0) {  // no token: nothing to add to dA and dD

@@ -66,7 +66,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     const Piece pc = find_piece(a.seqs, number, a.piece);
     if (!pc.any) return;
     if (MODE == kLocal && (REV ? pc.first : pc.last)) return;  // nothing enters from it
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     const RowsAt<TK> krow(lane);
     const RowsAt<TM> mrow(lane);
     int kcol[N / 16];

@@ -25,7 +25,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmStep a) {
     constexpr int LANES = N / 4, PER = 64 / LANES, STEPS = ROWS / (4 * PER);
     static_assert(STEPS * 4 * PER == ROWS, "rows over waves");
     const int64_t unit = blockIdx.x / (P / ROWS);  // session * heads + head
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = 4 * (lane % LANES);
     const int row0 = (int)(blockIdx.x % (P / ROWS)) * ROWS + wave * (ROWS / 4) + lane / LANES;
     float *S = a.state + unit * (int64_t)(P * N) + n0;
