@@ -372,14 +372,18 @@ struct PiecePlan {
     int32_t len;
 };
 PiecePlan piece_plan(const kda::Seqs &s, int32_t heads) {
-    const int64_t want = 1024;  // workgroups in flight that fill the chip
-    // equal rows: every (sequence, head) is as long as the others
+    // 1024 workgroups fill the chip (512: 3% slower on a 32K x 64-head prompt,
+    // 2048: 2%), and equal rows that come to half of that are left whole.
+    const int64_t want = 1024;
     const bool enough = !s.cu && (int64_t)s.num * heads >= want / 2;
-    int64_t len = ((int64_t)s.total * heads + want - 1) / want;
-    len = (len + 63) / 64 * 64;
-    if (len < 256) len = 256;
-    if (len > (1 << 20)) len = 1 << 20;
+    // Down to one block of 64 tokens (1,227 tokens x 8 heads fp32: 30 us, against
+    // 47 us with 256), but at most 64 pieces a sequence: the fold walks them.
     const int64_t longest = s.cu ? s.total : s.seq_len;
+    int64_t len = ((int64_t)s.total * heads + want - 1) / want;
+    if (len < longest / 64) len = longest / 64;
+    len = (len + 63) / 64 * 64;
+    if (len < 64) len = 64;
+    if (len > (1 << 20)) len = 1 << 20;
     if (enough || longest <= len) {
         int64_t whole = (longest + 63) / 64 * 64;
         return {false, (int32_t)(whole < 64 ? 64 : (whole > INT32_MAX - 63 ? INT32_MAX - 63 : whole))};

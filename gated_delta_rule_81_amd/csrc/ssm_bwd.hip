@@ -37,6 +37,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     constexpr int TL = L / 16, PT = TL / 2;      // token tiles; row tiles of du a wave owns
     constexpr int NTN = N / 16, TG = kGradWaves / NTN, TPW = TL / TG;  // tiles of dB, dC a wave owns
     constexpr int KT = L / 32;                   // 32-wide steps over tokens
+    constexpr int PG = kGradWaves / TL;          // waves of one s-tile
     typedef Tile<NI, L, N> TK;
     typedef Tile<NI, L, kPB> TX;
     typedef Tile<KQ, L, L> TQ;
@@ -47,12 +48,14 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     __shared__ __attribute__((aligned(16))) bf16 sy[TX::ELEMS];
     __shared__ __attribute__((aligned(16))) bf16 sq[TQ::ELEMS];  // Q^T: [s][t]
     __shared__ __attribute__((aligned(16))) bf16 se[TE::ELEMS];  // E: [n][p]
-    __shared__ __attribute__((aligned(16))) double s_cum[2][L];
-    __shared__ __attribute__((aligned(16))) float s_dt[2][L], s_out[2][L], s_in[2][L];
+    // of three heads: the one worked on, the next, and the one whose sums are left
+    __shared__ __attribute__((aligned(16))) double s_cum[3][L];
+    __shared__ __attribute__((aligned(16))) float s_dt[3][L], s_out[3][L], s_in[3][L];
     __shared__ __attribute__((aligned(16))) float s_g[TL * (TL + 1) / 2][64][4];  // G's tiles
-    __shared__ float s_all[2], s_D[2];
-    __shared__ float s_pair[TL][L], s_z[NTN][L], s_xdu[8 / TL][L], s_v[8 / TL][L];
-    __shared__ float s_k[NTN], s_d[TL];
+    __shared__ float s_all[3], s_D[3], s_A[3];
+    // the waves' shares of ddt, dA and dD, of two heads
+    __shared__ float s_pair[2][TL][L], s_z[2][NTN][L], s_xdu[2][PG][L], s_v[2][PG][L];
+    __shared__ float s_k[2][NTN], s_d[2][TL];
 
     const int64_t unit = blockIdx.x;
     const int set = (int)(unit % a.sets), group = (int)(unit / a.sets % a.groups);
@@ -73,9 +76,13 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     }
     const int P = a.p, halves = P / kPB;
     const int count = (h1 > h0 ? h1 - h0 : 0) * halves;  // (head, 64 of its rows) to work on
-    const int is = wave % TL, pg = wave / TL;            // s-tile and row tiles of du
-    const int nt = wave % NTN, tg = wave / NTN;          // columns and token tiles of dB, dC
-    const bool weigher = wave == kGradWaves - 1;
+    // s-tile and row tiles of du.  An early s-tile has more tiles below it: the
+    // two waves of a SIMD (w, w + 4) take one from either end.
+    const int is = wave & 4 ? TL - 1 - wave % TL : wave % TL, pg = wave / TL;
+    const int nt = wave % NTN, tg = wave / NTN;  // columns and token tiles of dB, dC
+    // of the waves with the last s-tile, one forms the next head's decays and one
+    // adds up the last head's shares
+    const bool weigher = wave == 3, summer = wave == 4;
 
     const T *x = static_cast<const T *>(a.x) + t0 * a.x_stride;
     const T *dy = static_cast<const T *>(a.dy) + t0 * a.dy_stride;
@@ -99,15 +106,15 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 for (int e = 0; e < 4; ++e) f[ks][4 * q + e] = v[e];
             }
     };
-    float rdt = 0.f, A2 = 0.f, An = 0.f, rD = 0.f;  // the weigher's head
+    float rdt = 0.f, rA = 0.f, rD = 0.f;  // the weigher's head
     auto load_dt = [&](int i) {
         const int h = h0 + i / halves;
         rdt = lane < n ? a.dt[(int64_t)(t0 + lane) * a.heads + h] : 0.f;
-        A2 = a.A[h];
+        rA = a.A[h];
         rD = a.D ? a.D[h] : 0.f;
     };
     auto weights = [&](int buf) {
-        const double step = (double)rdt * ((double)A2 * kLog2eD);
+        const double step = (double)rdt * ((double)rA * kLog2eD);
         const double cum = wave_prefix(step < -400.0 ? -400.0 : step, lane);
         const double all = from_lane(cum, 63);
         if (lane < L) {
@@ -116,7 +123,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
             s_in[buf][lane] = fast_exp2((float)cum);
             s_out[buf][lane] = fast_exp2((float)(all - cum));
         }
-        if (lane == 0) s_all[buf] = fast_exp2((float)all), s_D[buf] = rD;
+        if (lane == 0) s_all[buf] = fast_exp2((float)all), s_D[buf] = rD, s_A[buf] = rA;
     };
     float ev[kPB / 32][8], sv[kPB / 32][8];
     auto store_e = [&]() {  // E's parts to LDS
@@ -165,7 +172,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
         const RowsAt<TK> krow(lane);
 #pragma unroll
         for (int it = 0; it < TL; ++it) {
-            if (it < is || pg != it % (8 / TL)) continue;
+            if (it < is || pg != it % PG) continue;
             f32x4 v = zero4();
 #pragma unroll
             for (int ks = 0; ks < N / 32; ++ks)
@@ -179,15 +186,46 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     f32x4 dB[TPW], dC[TPW];  // rows n = 16 nt + 4 g + e, column token 16 (tg TPW + i) + r
 #pragma unroll
     for (int i = 0; i < TPW; ++i) dB[i] = dC[i] = zero4();
-    float sum_dl = 0.f, sum_xdu = 0.f, sum_d = 0.f;  // the weigher's, over a head's halves
+    // Head i's shares added up: ddt, and its parts of dA and dD (by the summer; over
+    // the head's halves in registers).
+    float sum_dl = 0.f, sum_xdu = 0.f, sum_d = 0.f;
+    auto add_up = [&](int i) {
+        const int buf = i % 3, par = i & 1, h = h0 + i / halves;
+        float dl = 0.f, xdu = 0.f, z = 0.f, v = 0.f, k = 0.f, d = 0.f;
+        if (lane < L) {
+#pragma unroll
+            for (int q = 0; q < TL; ++q) dl += q <= lane / 16 ? s_pair[par][q][lane] : 0.f;
+#pragma unroll
+            for (int q = 0; q < NTN; ++q) z += s_z[par][q][lane];
+#pragma unroll
+            for (int q = 0; q < PG; ++q) xdu += s_xdu[par][q][lane], v += s_v[par][q][lane];
+        }
+#pragma unroll
+        for (int q = 0; q < NTN; ++q) k += s_k[par][q];
+#pragma unroll
+        for (int q = 0; q < TL; ++q) d += s_d[par][q];
+        z = wave_suffix(z, lane);
+        v = __shfl_up(wave_prefix(v, lane), 1, 64);
+        dl += z + (lane > 0 ? v : 0.f) + s_all[buf] * k;
+        const bool fresh = i % halves == 0;
+        sum_dl = fresh ? dl : sum_dl + dl;
+        sum_xdu = fresh ? xdu : sum_xdu + xdu;
+        sum_d = fresh ? d : sum_d + d;
+        if (i % halves != halves - 1) return;
+        if (lane < n) a.ddt[(int64_t)(t0 + lane) * a.heads + h] = sum_xdu + s_A[buf] * sum_dl;
+        const float tot = rows4_sum(row16_total(lane < n ? s_dt[buf][lane] * sum_dl : 0.f));
+        if (lane == 0) {
+            a.part_a[number * a.heads + h] = tot;
+            a.part_d[number * a.heads + h] = sum_d;
+        }
+    };
 
     for (int i = 0; i < count; ++i) {
-        const int buf = i & 1, h = h0 + i / halves;
+        const int buf = i % 3, par = i & 1, h = h0 + i / halves;
         const bool more = i + 1 < count;
         lane = here(lane0), r = lane & 15, g = lane >> 4;
         const RowsAt<TK> krow(lane);
         const RowsAt<TX> xrow(lane);
-        if (weigher) An = A2;
         float kdot = 0.f;
         // ---- phase A: everything but the products with Q
         {   // dC_t += e^{cum_t} S0^T dy_t and z_t;  dB_s += dt_s e^{cum_L - cum_s} E^T x_s
@@ -202,7 +240,10 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                                                                  to_f32(ep[ks].v[1][e]) +
                                                                  to_f32(ep[ks].v[2][e]));
             }
-            if (more) load_rows(i + 1);
+            if (more) {
+                load_rows(i + 1);
+                if (weigher) load_dt(i + 1);
+            }
 #pragma unroll
             for (int q = 0; q < TPW; ++q) {
                 const int it = tg * TPW + q, t = 16 * it + r;
@@ -224,15 +265,13 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                     z += u[e] * cv;
                 }
                 z = rows4_sum(z);
-                if (g == 0) s_z[nt][t] = z;
+                if (g == 0) s_z[par][nt][t] = z;
                 dC[q] += u;
                 dB[q] += v * (s_out[buf][t] * s_dt[buf][t]);
-                __builtin_amdgcn_sched_barrier(0);
             }
             kdot = rows4_sum(row16_total(kdot));
-            if (tg == 0 && lane == 0) s_k[nt] = kdot;
+            if (tg == 0 && lane == 0) s_k[par][nt] = kdot;
         }
-        __builtin_amdgcn_sched_barrier(0);
         {   // this wave's s-tile: dP, M, Q, the pairs, and du
             const int s = 16 * is + r;
             const double cs = s_cum[buf][s];
@@ -257,12 +296,21 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                         const int t = 16 * it + 4 * g + e;
                         const float z = (float)(s_cum[buf][t] - cs);
                         const float d = fast_exp2(s <= t ? z : -1e30f);  // 0 above the diagonal
-                        diag += s == t ? dp[e] : 0.f;
+                        diag += s == t ? dp[e] : 0.f;  // of tile it == is
                         qv[e] = dp[e] * d * dts;
                         m[e] = G[e] * d;
                         w[e] = G[e] * qv[e];
                     }
-                    if (pg == 0) {
+                    // Q to LDS, and the pairs: the sum over t' >= t of a column, then over
+                    // the columns s < t.  The waves of an s-tile take its tiles in turn.
+#pragma unroll
+                    for (int e = 2; e >= 0; --e) w[e] += w[e + 1];
+                    float v[4];
+                    rows4_gather(w[0], v);
+                    const float below = (g < 1 ? v[1] : 0.f) + (g < 2 ? v[2] : 0.f) +
+                                        (g < 3 ? v[3] : 0.f) + tail;
+                    tail += v[0] + v[1] + v[2] + v[3];
+                    if (pg == it % PG) {
 #pragma unroll
                         for (int part = 0; part < KQ; ++part) {
                             bf16x4 o;
@@ -275,34 +323,24 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                             *reinterpret_cast<bf16x4 *>(sq + part * TQ::PLANE +
                                                         TQ::at(s, 16 * it + 4 * g)) = o;
                         }
-                        // sum over t' >= t of this column, then over the columns s < t
-#pragma unroll
-                        for (int e = 2; e >= 0; --e) w[e] += w[e + 1];
-                        float v[4];
-                        rows4_gather(w[0], v);
-                        const float below = (g < 1 ? v[1] : 0.f) + (g < 2 ? v[2] : 0.f) +
-                                            (g < 3 ? v[3] : 0.f) + tail;
-                        tail += v[0] + v[1] + v[2] + v[3];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int t = 16 * it + 4 * g + e;
                             const float sum = row16_total(s < t ? w[e] + below : 0.f);
-                            if (r == 0) s_pair[is][t] = sum;
+                            if (r == 0) s_pair[par][is][t] = sum;
                         }
                     }
                 }
                 if (it % 2 == 0) mp[it / 2] = split<3>(mf);
-                __builtin_amdgcn_sched_barrier(0);
             }
-            if (pg == 0) {
-                diag = rows4_sum(row16_total(diag));
-                if (lane == 0) s_d[is] = diag;
-            }
+            diag = rows4_sum(row16_total(diag));
+            if (pg == 0 && lane == 0) s_d[par][is] = diag;
             if (more) {  // in flight through du and phase B
                 load_state(a.e_states, i + 1, ev);
                 load_state(a.s_states, i + 1, sv);
-                if (weigher) load_dt(i + 1);
+                if (weigher) weights((i + 1) % 3);
             }
+            if (summer && i > 0) add_up(i - 1);
             float xdu = 0.f, vs = 0.f;
             const float wout = s_out[buf][s], D = s_D[buf];
             T *dx = static_cast<T *>(a.dx) + (int64_t)(t0 + s) * a.dx_stride + (int64_t)h * P +
@@ -315,7 +353,6 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 for (int ks = 0; ks < N / 32; ++ks)
                     du = mma(read_cols<TE, 3>(se, ks, cols_at<TE>(16 * pt, lane)),
                              read_rows<TK, NI>(sb, 16 * is, ks, krow), du);
-                __builtin_amdgcn_sched_barrier(0);
                 du *= wout;
                 const int at = TX::at(s, 16 * pt + 4 * g);
                 float xv[4], yv[4];
@@ -338,15 +375,13 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 if (s < n)
                     store4(dx + 16 * pt + 4 * g, dts * du[0] + D * yv[0], dts * du[1] + D * yv[1],
                            dts * du[2] + D * yv[2], dts * du[3] + D * yv[3]);
-                __builtin_amdgcn_sched_barrier(0);
             }
             xdu = rows4_sum(xdu);
             vs = rows4_sum(vs);
-            if (g == 0) s_xdu[pg][s] = xdu, s_v[pg][s] = vs * dts;
+            if (g == 0) s_xdu[par][pg][s] = xdu, s_v[par][pg][s] = vs * dts;
         }
         lds_barrier();
-        // ---- phase B: the products with Q, the sums of dt's gradient, and the
-        // next head's rows into LDS
+        // ---- phase B: the products with Q, and the next head's rows into LDS
         Parts<NI> bt[KT], ct[KT];  // B^T and C^T of this wave's columns n
 #pragma unroll
         for (int ks = 0; ks < KT; ++ks) {
@@ -361,40 +396,6 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 if (ks <= it / 2) dC[q] = mma(bt[ks], read_cols<TQ, KQ>(sq, ks, cols_at<TQ>(16 * it, lane)), dC[q]);
                 if (ks >= it / 2) dB[q] = mma(ct[ks], read_rows<TQ, KQ>(sq, 16 * it, ks, RowsAt<TQ>(lane)), dB[q]);
             }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if (weigher) {
-            float dl = 0.f, xdu = 0.f, z = 0.f, v = 0.f, k = 0.f;
-            if (lane < L) {
-#pragma unroll
-                for (int q = 0; q < TL; ++q) dl += q <= lane / 16 ? s_pair[q][lane] : 0.f;
-#pragma unroll
-                for (int q = 0; q < NTN; ++q) z += s_z[q][lane];
-#pragma unroll
-                for (int q = 0; q < 8 / TL; ++q) xdu += s_xdu[q][lane], v += s_v[q][lane];
-            }
-#pragma unroll
-            for (int q = 0; q < NTN; ++q) k += s_k[q];
-            z = wave_suffix(z, lane);
-            v = __shfl_up(wave_prefix(v, lane), 1, 64);
-            dl += z + (lane > 0 ? v : 0.f) + s_all[buf] * k;
-            float dd = 0.f;
-#pragma unroll
-            for (int q = 0; q < TL; ++q) dd += s_d[q];
-            const bool fresh = i % halves == 0;
-            sum_dl = fresh ? dl : sum_dl + dl;
-            sum_xdu = fresh ? xdu : sum_xdu + xdu;
-            sum_d = fresh ? dd : sum_d + dd;
-            if (i % halves == halves - 1) {
-                if (lane < n) a.ddt[(int64_t)(t0 + lane) * a.heads + h] = sum_xdu + An * sum_dl;
-                const float pa = lane < n ? s_dt[buf][lane] * sum_dl : 0.f;
-                const float tot = rows4_sum(row16_total(pa));
-                if (lane == 0) {
-                    a.part_a[number * a.heads + h] = tot;
-                    a.part_d[number * a.heads + h] = sum_d;
-                }
-            }
-            if (more) weights(buf ^ 1);
         }
         if (more) {
             rx.template store<TX>(sx, tid);
@@ -403,6 +404,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
         }
         lds_barrier();
     }
+    if (summer && count > 0) add_up(count - 1);
     // dB and dC of this group, or of this set of its heads
 #pragma unroll
     for (int q = 0; q < TPW; ++q) {

@@ -316,7 +316,7 @@ __global__ __launch_bounds__(P * 4, 2) void ssm_both_kernel(SsmScan a, SsmScan b
 
 // The pieces' own final states turned in place into entering states:
 // enter[next] = e^{decay} enter + own.  One workgroup per 1024 values of a
-// (sequence, head); the pieces one after the other, the next one's load ahead.
+// (sequence, head); the pieces one after the other, eight loads ahead.
 template <bool REV>
 __device__ __forceinline__ void fold_body(const SsmScan &a, int values, int64_t block) {
     const int per = values / 1024;
@@ -334,14 +334,29 @@ __device__ __forceinline__ void fold_body(const SsmScan &a, int values, int64_t 
     f32x4 S = a.state0 ? *reinterpret_cast<const f32x4 *>(
                              a.state0 + ((int64_t)n * a.heads + h) * values + off)
                        : zero4();
-    f32x4 own = *reinterpret_cast<const f32x4 *>(at(0));
-    for (int j = 1; j < count; ++j) {
-        const f32x4 now = own;
-        if (j + 1 < count) own = *reinterpret_cast<const f32x4 *>(at(j));
-        const double d = a.seg_decay[(first + (REV ? count - j : j - 1)) * a.heads + h];
-        S = S * fast_exp2((float)d) + now;
-        *reinterpret_cast<f32x4 *>(at(j)) = S;
+    constexpr int U = 8;  // pieces whose loads are in flight together
+    for (int j0 = 0; j0 < count - 1; j0 += U) {
+        f32x4 own[U];
+        float decay[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int j = j0 + i < count - 1 ? j0 + i : count - 2;
+            own[i] = *reinterpret_cast<const f32x4 *>(at(j));
+            decay[i] = fast_exp2(
+                (float)a.seg_decay[(first + (REV ? count - 1 - j : j)) * a.heads + h]);
+        }
+        f32x4 kept = S;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const f32x4 enter = kept;
+            if (j0 + i < count - 1) {
+                kept = enter * decay[i] + own[i];
+                if (j0 + i > 0) *reinterpret_cast<f32x4 *>(at(j0 + i)) = enter;
+            }
+        }
+        S = kept;
     }
+    *reinterpret_cast<f32x4 *>(at(count - 1)) = S;
 }
 
 __global__ __launch_bounds__(256) void ssm_fold_kernel(SsmScan a, int values) {
