@@ -92,16 +92,17 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
         rx.load(x + off, a.x_stride, n, tid);
         ry.load(dy + off, a.dy_stride, n, tid);
     };
-    // operand of index n (columns 16 nt ..), k = rows p, of a state stored [N][P]
+    // operand of index n (columns 16 nt ..), k = rows p (read_wide's order), of a state
+    // stored [N][P]
     auto load_state = [&](const float *states, int i, float (&f)[kPB / 32][8]) {
         const float *at = states + (number * a.heads + h0 + i / halves) * (int64_t)(P * N) +
-                          (int64_t)(16 * nt + r) * P + (i % halves) * kPB + 4 * g;
+                          (int64_t)(16 * nt + r) * P + (i % halves) * kPB + 8 * g;
 #pragma unroll
         for (int ks = 0; ks < kPB / 32; ++ks)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const f32x4 v = __builtin_nontemporal_load(
-                    reinterpret_cast<const f32x4 *>(at + 32 * ks + 16 * q));
+                    reinterpret_cast<const f32x4 *>(at + 32 * ks + 4 * q));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) f[ks][4 * q + e] = v[e];
             }
@@ -125,21 +126,19 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
         }
         if (lane == 0) s_all[buf] = fast_exp2((float)all), s_D[buf] = rD, s_A[buf] = rA;
     };
-    float ev[kPB / 32][8], sv[kPB / 32][8];
-    auto store_e = [&]() {  // E's parts to LDS
+    float ev[kPB / 32][8], sv[kPB / 32][8], kdot = 0.f;
+    auto store_e = [&]() {  // E's parts to LDS, and this wave's share of <E, S0>
+        kdot = 0.f;
 #pragma unroll
         for (int ks = 0; ks < kPB / 32; ++ks) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kdot += ev[ks][e] * sv[ks][e];
             const Parts<3> ep = split<3>(ev[ks]);
             if (tg == 0)
 #pragma unroll
-                for (int q = 0; q < 3; ++q) {
-                    bf16 *at = se + q * TE::PLANE;
-                    const bf16x8 v = ep.v[q];
-                    *reinterpret_cast<bf16x4 *>(at + TE::at(16 * nt + r, 32 * ks + 4 * g)) =
-                        __builtin_shufflevector(v, v, 0, 1, 2, 3);
-                    *reinterpret_cast<bf16x4 *>(at + TE::at(16 * nt + r, 32 * ks + 16 + 4 * g)) =
-                        __builtin_shufflevector(v, v, 4, 5, 6, 7);
-                }
+                for (int q = 0; q < 3; ++q)
+                    *reinterpret_cast<bf16x8 *>(se + q * TE::PLANE +
+                                                TE::at(16 * nt + r, 32 * ks + 8 * g)) = ep.v[q];
         }
     };
 
@@ -169,15 +168,15 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     // G's tiles it >= is (rows t = 16 it + 4 g + e, column s = 16 is + r), by lane
     auto tile_of = [](int it, int js) { return it * (it + 1) / 2 + js; };
     {
-        const RowsAt<TK> krow(lane);
+        const WideAt<TK> kwide(lane);
 #pragma unroll
         for (int it = 0; it < TL; ++it) {
             if (it < is || pg != it % PG) continue;
             f32x4 v = zero4();
 #pragma unroll
             for (int ks = 0; ks < N / 32; ++ks)
-                v = mma(read_rows<TK, NI>(sc, 16 * it, ks, krow),
-                        read_rows<TK, NI>(sb, 16 * is, ks, krow), v);
+                v = mma(read_wide<TK, NI>(sc, 16 * it, ks, kwide),
+                        read_wide<TK, NI>(sb, 16 * is, ks, kwide), v);
             *reinterpret_cast<f32x4 *>(s_g[tile_of(it, is)][lane]) = v;
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -225,20 +224,15 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
         const bool more = i + 1 < count;
         lane = here(lane0), r = lane & 15, g = lane >> 4;
         const RowsAt<TK> krow(lane);
-        const RowsAt<TX> xrow(lane);
-        float kdot = 0.f;
+        const WideAt<TX> xwide(lane);
         // ---- phase A: everything but the products with Q
         {   // dC_t += e^{cum_t} S0^T dy_t and z_t;  dB_s += dt_s e^{cum_L - cum_s} E^T x_s
             Parts<3> sp[kPB / 32], ep[kPB / 32];
-            const RowsAt<TE> erow(lane);
+            const WideAt<TE> ewide(lane);
 #pragma unroll
             for (int ks = 0; ks < kPB / 32; ++ks) {
                 sp[ks] = split<3>(sv[ks]);
-                ep[ks] = read_rows<TE, 3>(se, 16 * nt, ks, erow);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) kdot += sv[ks][e] * (to_f32(ep[ks].v[0][e]) +
-                                                                 to_f32(ep[ks].v[1][e]) +
-                                                                 to_f32(ep[ks].v[2][e]));
+                ep[ks] = read_wide<TE, 3>(se, 16 * nt, ks, ewide);
             }
             if (more) {
                 load_rows(i + 1);
@@ -250,8 +244,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 f32x4 u = zero4(), v = zero4();
 #pragma unroll
                 for (int ks = 0; ks < kPB / 32; ++ks) {
-                    u = mma(sp[ks], read_rows<TX, NI>(sy, 16 * it, ks, xrow), u);
-                    v = mma(ep[ks], read_rows<TX, NI>(sx, 16 * it, ks, xrow), v);
+                    u = mma(sp[ks], read_wide<TX, NI>(sy, 16 * it, ks, xwide), u);
+                    v = mma(ep[ks], read_wide<TX, NI>(sx, 16 * it, ks, xwide), v);
                 }
                 const float win = s_in[buf][t];
                 const bf16 *row = sc + TK::at(t, 16 * nt + 4 * g);
@@ -269,8 +263,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                 dC[q] += u;
                 dB[q] += v * (s_out[buf][t] * s_dt[buf][t]);
             }
-            kdot = rows4_sum(row16_total(kdot));
-            if (tg == 0 && lane == 0) s_k[par][nt] = kdot;
+            const float ks = rows4_sum(row16_total(kdot));
+            if (tg == 0 && lane == 0) s_k[par][nt] = ks;
         }
         {   // this wave's s-tile: dP, M, Q, the pairs, and du
             const int s = 16 * is + r;
@@ -287,8 +281,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                     f32x4 dp = zero4();
 #pragma unroll
                     for (int ks = 0; ks < kPB / 32; ++ks)
-                        dp = mma(read_rows<TX, NI>(sy, 16 * it, ks, xrow),
-                                 read_rows<TX, NI>(sx, 16 * is, ks, xrow), dp);
+                        dp = mma(read_wide<TX, NI>(sy, 16 * it, ks, xwide),
+                                 read_wide<TX, NI>(sx, 16 * is, ks, xwide), dp);
                     const f32x4 G = *reinterpret_cast<const f32x4 *>(s_g[tile_of(it, is)][lane]);
                     float qv[4], w[4];
 #pragma unroll

@@ -56,12 +56,12 @@ __device__ __forceinline__ f32x4 mma(const Parts<NA> &a, const Parts<NB> &b, f32
 }
 
 // A tile of ROWS x COLS values as NP bf16 planes in LDS, COLS 32, 64 or 128.
-// The 8-element chunks of a row change places by an XOR with `turn(row)`, which
-// takes every value once over 16 rows and runs through the even values first.
-// Sixteen rows' chunks of one column then lie in 16 different places of the 64
-// banks, and so do two neighbouring columns' chunks of eight rows: both reads
-// below are free of bank conflicts (rows padded by 32 bytes were so only along
-// columns: 157 million conflict cycles in the 32K-token scan, 0.83 ms).
+// The 8-element chunks of a row change places by an XOR with `turn(row)`, a
+// linear map that takes every value once over the rows that share the 64 banks.
+// Measured, 16 waves reading: 3.3 cycles a wave for 8 bytes a lane along rows
+// and for the transposing reads along columns, 4.1 for 16 bytes along rows; the
+// plain XOR with the row costs the transposing reads 4.1, other maps the 16-byte
+// reads 8, unswizzled rows 16 to 32.
 template <int NP, int ROWS, int COLS> struct Tile {
     static_assert(COLS == 32 || COLS == 64 || COLS == 128, "swizzle");
     static constexpr int LD = COLS;
@@ -70,7 +70,7 @@ template <int NP, int ROWS, int COLS> struct Tile {
     __device__ static int turn(int row) {
         constexpr int C = COLS / 8;       // chunks of a row
         const int q = row / (16 / C);     // rows that share the 64 banks count as one
-        return ((2 * q) & (C - 1)) | ((q / (C / 2)) & 1);
+        return ((2 * q) & (C - 1)) ^ (q & (C / 2) ? C / 2 + 1 : 0);
     }
     // Element (row, col); runs of col % 8 stay together.
     __device__ static int at(int row, int col) {
@@ -114,6 +114,29 @@ __device__ __forceinline__ Parts<NP> read_rows(const bf16 *tile, int row0, int k
         const bf16x4 v = *(lds_bf16x4 *)(b + (q * TL::PLANE + row0 * TL::LD));
         p.v[q] = __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
     }
+    return p;
+}
+
+// The same outer index with k = 32 ks + 8 (l / 16) + j, for products whose two
+// operands are both read so: one 16-byte read where the order above takes two of
+// 8 bytes at half their rate.
+template <typename TL> struct WideAt {
+    int o[TL::LD / 32];
+    __device__ __forceinline__ explicit WideAt(int lane) {
+#pragma unroll
+        for (int ks = 0; ks < TL::LD / 32; ++ks)
+            o[ks] = TL::at(lane & 15, 32 * ks + 8 * (lane >> 4));
+    }
+};
+template <typename TL, int NP>
+__device__ __forceinline__ Parts<NP> read_wide(const bf16 *tile, int row0, int ks,
+                                               const WideAt<TL> &at) {
+    typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+    Parts<NP> p;
+    lds_bf16 *a = (lds_bf16 *)tile + at.o[ks];
+#pragma unroll
+    for (int q = 0; q < NP; ++q)
+        p.v[q] = *(lds_bf16x8 *)(a + (q * TL::PLANE + row0 * TL::LD));
     return p;
 }
 

@@ -68,6 +68,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     if (MODE == kLocal && (REV ? pc.first : pc.last)) return;  // nothing enters from it
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     const RowsAt<TK> krow(lane);
+    const WideAt<TK> kwide(lane);
     const RowsAt<TM> mrow(lane);
     int kcol[N / 16];
 #pragma unroll
@@ -172,8 +173,8 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                     f32x4 m = zero4();
 #pragma unroll
                     for (int ks = 0; ks < N / 32; ++ks)
-                        m = mma(read_rows<TK, NI>(sk, 16 * is, ks, krow),
-                                read_rows<TK, NI>(sc, 16 * it, ks, krow), m);
+                        m = mma(read_wide<TK, NI>(sk, 16 * is, ks, kwide),
+                                read_wide<TK, NI>(sc, 16 * it, ks, kwide), m);
                     const int t = 16 * it + r, s = 16 * is + 4 * g;
                     const double ct = s_cum[buf][t];
                     float v[4];
