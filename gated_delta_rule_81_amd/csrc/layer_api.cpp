@@ -18,23 +18,41 @@ int elem_size(int32_t dtype) {
     return dtype == kda::kDtypeBf16 ? 2 : (dtype == kda::kDtypeF32 ? 4 : 0);
 }
 
-// Bytes from the first to the last element of `rows` rows of `len` elements.
-Range rows_range(const void *p, int64_t rows, int64_t len, int64_t stride, int esz) {
-    return {p, rows > 0 && len > 0 ? (uint64_t)((rows - 1) * stride + len) * esz : 0};
+// The bytes of a tensor: `bytes` from the first to the last; with a stride, rows
+// of `len` bytes that far apart (between them others' values may lie).
+struct Span {
+    const void *p;
+    uint64_t bytes, stride, len;
+    Span(const void *p_ = nullptr, uint64_t bytes_ = 0, uint64_t stride_ = 0, uint64_t len_ = 0)
+        : p(p_), bytes(bytes_), stride(stride_), len(len_) {}
+};
+Span rows_range(const void *p, int64_t rows, int64_t len, int64_t stride, int esz) {
+    if (rows <= 0 || len <= 0) return {p};
+    return {p, (uint64_t)((rows - 1) * stride + len) * esz, (uint64_t)stride * esz,
+            (uint64_t)len * esz};
+}
+
+// Rows the same distance apart whose columns lie beside each other (slices of
+// one wider row) share no byte; everything else goes by first and last byte.
+bool overlap(const Span &a, const Span &b) {
+    if (!overlap(Range{a.p, a.bytes}, Range{b.p, b.bytes})) return false;
+    if (a.stride == 0 || a.stride != b.stride) return true;
+    const int64_t s = (int64_t)a.stride;
+    const int64_t apart = (int64_t)reinterpret_cast<uintptr_t>(b.p) -
+                          (int64_t)reinterpret_cast<uintptr_t>(a.p);
+    const uint64_t d = (uint64_t)((apart % s + s) % s);  // b's column in a's row
+    return d < a.len || d + b.len > a.stride;
 }
 
 // No output may overlap another output or an input.
-int check_alias(const Range *outs, int n_out, const Range *ins, int n_in) {
-    for (int i = 0; i < n_out; ++i) {
-        for (int j = i + 1; j < n_out; ++j)
+template <int NO, int NI> int check_alias(const Span (&outs)[NO], const Span (&ins)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = i + 1; j < NO; ++j)
             if (overlap(outs[i], outs[j])) return KDA_ERR_ALIAS;
-        for (int j = 0; j < n_in; ++j)
+        for (int j = 0; j < NI; ++j)
             if (overlap(outs[i], ins[j])) return KDA_ERR_ALIAS;
     }
     return KDA_OK;
-}
-template <int NO, int NI> int check_alias(const Range (&outs)[NO], const Range (&ins)[NI]) {
-    return check_alias(outs, NO, ins, NI);
 }
 
 // Sizes of a call over sequences; *seqs receives them.
@@ -74,9 +92,9 @@ int kda_short_conv_fwd(const void *x, const float *weight, const float *bias,
         !aligned4(cu_seqlens))
         return KDA_ERR_ALIGN;
     const uint64_t state = (uint64_t)seqs.num * (width - 1) * channels * esz;
-    const Range outs[] = {rows_range(out, seqs.total, channels, out_stride, esz),
+    const Span outs[] = {rows_range(out, seqs.total, channels, out_stride, esz),
                           {final_state, state}};
-    const Range ins[] = {rows_range(x, seqs.total, channels, x_stride, esz),
+    const Span ins[] = {rows_range(x, seqs.total, channels, x_stride, esz),
                          {weight, (uint64_t)channels * width * 4},
                          {bias, (uint64_t)channels * 4},
                          {initial_state, state},
@@ -134,12 +152,12 @@ int kda_short_conv_bwd(const void *x, const float *weight, const float *bias,
         return KDA_ERR_ALIGN;
     const uint64_t state = (uint64_t)seqs.num * (width - 1) * channels * esz;
     const uint64_t wb = (uint64_t)channels * width * 4, bb = (uint64_t)channels * 4;
-    const Range outs[] = {rows_range(dx, seqs.total, channels, dx_stride, esz),
+    const Span outs[] = {rows_range(dx, seqs.total, channels, dx_stride, esz),
                           {dweight, wb},
                           {dbias, bb},
                           {d_initial_state, state},
                           {workspace, (uint64_t)need}};
-    const Range ins[] = {rows_range(x, seqs.total, channels, x_stride, esz),
+    const Span ins[] = {rows_range(x, seqs.total, channels, x_stride, esz),
                          rows_range(d_out, seqs.total, channels, d_out_stride, esz),
                          {weight, wb},
                          {bias, bb},
@@ -179,9 +197,9 @@ int kda_short_conv_step(const void *x, const float *weight, const float *bias, v
     if (!aligned_to(x, esz) || !aligned_to(out, esz) || !aligned_to(state, esz) ||
         !aligned4(weight) || !aligned4(bias))
         return KDA_ERR_ALIGN;
-    const Range outs[] = {rows_range(out, batch, channels, out_stride, esz),
+    const Span outs[] = {rows_range(out, batch, channels, out_stride, esz),
                           {state, (uint64_t)batch * (width - 1) * channels * esz}};
-    const Range ins[] = {rows_range(x, batch, channels, x_stride, esz),
+    const Span ins[] = {rows_range(x, batch, channels, x_stride, esz),
                          {weight, (uint64_t)channels * width * 4},
                          {bias, (uint64_t)channels * 4}};
     int st = check_alias(outs, ins);
@@ -201,13 +219,13 @@ int kda_short_conv_step(const void *x, const float *weight, const float *bias, v
 // ------------------------------------------------------------ norm and rotation
 namespace {
 
-// Checks shared by both directions; the ranges of q, k, weights, table and
+// Checks shared by both directions; the spans of q, k, weights, table and
 // positions go to `ins` (six of them).
 int check_qk(const void *q, const void *k, const float *q_weight, const float *k_weight,
              const float *table, const int32_t *positions, int32_t tokens, int32_t q_heads,
              int32_t k_heads, int32_t head_dim, int32_t rotary_dim, int32_t table_rows,
              int64_t q_stride, int64_t k_stride, float eps, int32_t norm, int32_t dtype,
-             Range (&ins)[6]) {
+             Span (&ins)[6]) {
     if (tokens < 0 || q_heads < 0 || k_heads < 0 || head_dim <= 0 || rotary_dim < 0)
         return KDA_ERR_SHAPE;
     if ((int64_t)q_heads + k_heads > INT32_MAX) return KDA_ERR_SHAPE;
@@ -241,7 +259,7 @@ int check_qk(const void *q, const void *k, const float *q_weight, const float *k
 
 // One more pair of tensors laid out like q and k.
 int check_qk_rows(const void *q, const void *k, int32_t tokens, int32_t q_heads, int32_t k_heads,
-                  int32_t head_dim, int64_t q_stride, int64_t k_stride, int32_t dtype, Range *r) {
+                  int32_t head_dim, int64_t q_stride, int64_t k_stride, int32_t dtype, Span *r) {
     const int esz = elem_size(dtype);
     const int64_t ql = (int64_t)q_heads * head_dim, kl = (int64_t)k_heads * head_dim;
     const bool any_q = tokens > 0 && q_heads > 0, any_k = tokens > 0 && k_heads > 0;
@@ -265,7 +283,7 @@ int kda_qk_norm_fwd(const void *q, const void *k, const float *q_weight, const f
                     int32_t rotary_dim, int32_t table_rows, int64_t q_stride, int64_t k_stride,
                     int64_t out_q_stride, int64_t out_k_stride, float eps, int32_t norm,
                     int32_t interleaved, int32_t dtype, hipStream_t stream) {
-    Range ins[6], outs[2];
+    Span ins[6], outs[2];
     int st = check_qk(q, k, q_weight, k_weight, table, positions, tokens, q_heads, k_heads,
                       head_dim, rotary_dim, table_rows, q_stride, k_stride, eps, norm, dtype, ins);
     if (st != KDA_OK) return st;
@@ -301,7 +319,7 @@ int kda_qk_norm_bwd(const void *q, const void *k, const float *q_weight, const f
                     int64_t d_out_q_stride, int64_t d_out_k_stride, int64_t dq_stride,
                     int64_t dk_stride, float eps, int32_t norm, int32_t interleaved,
                     int32_t dtype, void *workspace, int64_t workspace_bytes, hipStream_t stream) {
-    Range ins[8], outs[5], base[6];
+    Span ins[8], outs[5], base[6];
     int st = check_qk(q, k, q_weight, k_weight, table, positions, tokens, q_heads, k_heads,
                       head_dim, rotary_dim, table_rows, q_stride, k_stride, eps, norm, dtype,
                       base);
@@ -444,10 +462,10 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
         !aligned16(final_state) || !aligned4(cu_seqlens) || !aligned16(workspace))
         return KDA_ERR_ALIGN;
     const uint64_t state = (uint64_t)seqs.num * xl * state_dim * 4;
-    const Range outs[] = {rows_range(out, seqs.total, xl, out_stride, esz),
+    const Span outs[] = {rows_range(out, seqs.total, xl, out_stride, esz),
                           {workspace, (uint64_t)space.bytes()},
                           {final_state, state}};
-    const Range ins[] = {rows_range(x, seqs.total, xl, x_stride, esz),
+    const Span ins[] = {rows_range(x, seqs.total, xl, x_stride, esz),
                          rows_range(B, seqs.total, bl, b_stride, esz),
                          rows_range(C, seqs.total, bl, c_stride, esz),
                          {dt, (uint64_t)th * 4},
@@ -457,7 +475,7 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
                          {final_state == initial_state ? nullptr : initial_state, state}};
     if ((st = check_alias(outs, ins)) != KDA_OK) return st;
     if (final_state == initial_state &&  // in place: still apart from the other outputs
-        (overlap(outs[0], {initial_state, state}) || overlap(outs[1], {initial_state, state})))
+        (overlap(outs[0], Span{initial_state, state}) || overlap(outs[1], Span{initial_state, state})))
         return KDA_ERR_ALIAS;
     if (seqs.num == 0 || num_heads == 0) return KDA_OK;
     if ((st = check_device()) != KDA_OK) return st;
@@ -565,7 +583,7 @@ int kda_ssm_chunk_bwd(const void *x, const float *dt, const float *A, const void
         !aligned4(ddt) || !aligned4(dA) || !aligned4(dD) || !aligned16(workspace))
         return KDA_ERR_ALIGN;
     const uint64_t state = (uint64_t)seqs.num * xl * state_dim * 4, hb = (uint64_t)num_heads * 4;
-    const Range outs[] = {rows_range(dx, seqs.total, xl, dx_stride, esz),
+    const Span outs[] = {rows_range(dx, seqs.total, xl, dx_stride, esz),
                           rows_range(dB, seqs.total, bl, db_stride, esz),
                           rows_range(dC, seqs.total, bl, dc_stride, esz),
                           {ddt, (uint64_t)th * 4},
@@ -573,7 +591,7 @@ int kda_ssm_chunk_bwd(const void *x, const float *dt, const float *A, const void
                           {dD, hb},
                           {d_initial_state, state},
                           {workspace, (uint64_t)w.bytes()}};
-    const Range ins[] = {rows_range(x, seqs.total, xl, x_stride, esz),
+    const Span ins[] = {rows_range(x, seqs.total, xl, x_stride, esz),
                          rows_range(B, seqs.total, bl, b_stride, esz),
                          rows_range(C, seqs.total, bl, c_stride, esz),
                          rows_range(d_out, seqs.total, xl, d_out_stride, esz),
@@ -646,9 +664,9 @@ int kda_ssm_decode_step(const void *x, const float *dt, const float *A, const vo
         (st = check_ssm_rows(out, batch, xl, out_stride, esz)) != KDA_OK)
         return st;
     if (!aligned4(dt) || !aligned4(A) || !aligned4(D) || !aligned16(state)) return KDA_ERR_ALIGN;
-    const Range outs[] = {rows_range(out, batch, xl, out_stride, esz),
+    const Span outs[] = {rows_range(out, batch, xl, out_stride, esz),
                           {state, units * head_dim * state_dim * 4}};
-    const Range ins[] = {rows_range(x, batch, xl, x_stride, esz),
+    const Span ins[] = {rows_range(x, batch, xl, x_stride, esz),
                          rows_range(B, batch, bl, b_stride, esz),
                          rows_range(C, batch, bl, c_stride, esz),
                          {dt, units * 4},

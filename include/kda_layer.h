@@ -29,8 +29,9 @@
  *   - Nothing is allocated and no host memory is read after the call returns:
  *     every call may be captured into a graph.  Results do not depend on the
  *     order in which workgroups run.
- *   - An output must not overlap an input or another output
- *     (KDA_ERR_ALIAS) except where said.
+ *   - An output must not overlap an input or another output (KDA_ERR_ALIAS)
+ *     except where said.  Slices of one wider row (the same distance between
+ *     tokens, columns beside each other) do not overlap.
  */
 #ifndef KDA_LAYER_H_
 #define KDA_LAYER_H_
