@@ -81,7 +81,7 @@ template <typename T, int VEC, int W>
 __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs a, int cblocks,
                                                                int run_blocks, int run) {
     typedef Row<T, VEC> R;
-    constexpr int U = 4;  // rows loaded together, the next ones' loads ahead
+    constexpr int U = 2;  // rows loaded together, the next ones' loads ahead (4: 3% slower, 8: 6%)
     const T *x = static_cast<const T *>(a.x), *state0 = static_cast<const T *>(a.state0);
     const int C = a.channels, wave = wave_of_block();
     const int c = ((int)(blockIdx.x % cblocks) * 64 + (int)threadIdx.x) * VEC;
@@ -109,48 +109,57 @@ __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs a, int c
 
     float w[W][VEC], b[VEC], win[W][VEC];  // win: rows t - (W-1) .. t
     load_params<VEC, W>(a, c, w, b);
-    int beg = 0, end = t0, n = -1;
+    int beg = 0, end = 0, n = -1;
     typename R::vec next[U];
     auto load = [&](int t) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
             next[i] = t + i < t1 ? R::raw(col(x + (int64_t)(t + i) * a.x_stride, c)) : R::zero();
     };
+    auto token = [&](int t, const typename R::vec &raw) {
+        R::get(raw, win[W - 1]);
+        float y[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            float z = b[e];
+#pragma unroll
+            for (int j = 0; j < W; ++j) z += w[j][e] * win[j][e];
+            y[e] = a.silu ? z * sigmoid(z) : z;
+        }
+        R::put(col(out + (int64_t)t * a.out_stride, c), y);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+    };
+    // Token t's sequence and the rows before t; n < 0 where none holds it.
+    auto enter = [&](int t) {
+        n = seq_of_token(a.seqs, t, &beg, &end);
+        if (n < 0) {
+            end = t + 1;
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            seq_row<T, VEC, W>(x, a.x_stride, state0, n, C, c, t - (W - 1) + j, beg, win[j]);
+    };
     load(t0);
+    enter(t0);
     for (int t = t0; t < t1; t += U) {
         typename R::vec raw[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) raw[i] = next[i];
         load(t + U);
+        if (t + U <= t1 && t + U <= end && n >= 0) {  // inside one sequence
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int tt = t + i;
-            if (tt >= t1) break;
-            if (tt >= end) {  // a sequence begins here, or the run does
-                n = seq_of_token(a.seqs, tt, &beg, &end);
-                if (n < 0) {
-                    end = tt + 1;
-                    continue;
-                }
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-                    seq_row<T, VEC, W>(x, a.x_stride, state0, n, C, c, tt - (W - 1) + j, beg,
-                                       win[j]);
-            }
-            R::get(raw[i], win[W - 1]);
-            float y[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float z = b[e];
-#pragma unroll
-                for (int j = 0; j < W; ++j) z += w[j][e] * win[j][e];
-                y[e] = a.silu ? z * sigmoid(z) : z;
-            }
-            R::put(col(out + (int64_t)tt * a.out_stride, c), y);
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+            for (int i = 0; i < U; ++i) token(t + i, raw[i]);
+            continue;
+        }
+#pragma unroll 1
+        for (int tt = t; tt < t + U && tt < t1; ++tt) {
+            if (tt >= end) enter(tt);
+            if (n < 0) continue;
+            token(tt, R::raw(col(x + (int64_t)tt * a.x_stride, c)));
         }
     }
 }
@@ -281,16 +290,54 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int c
                 ng[i] = in ? R::raw(col(dy + (int64_t)(t + i) * a.d_out_stride, c)) : R::zero();
             }
         };
+        auto token = [&](int t, const typename R::vec &rx, const typename R::vec &rg, bool own) {
+            R::get(rx, win[W - 1]);
+            shift();
+            R::get(rg, dz[W - 1]);
+            grad_z<VEC, W>(w, b, win, a.silu, dz[W - 1]);
+            if (own) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    db[e] += dz[W - 1][e];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j][e] += dz[W - 1][e] * win[j][e];
+                }
+            }
+            const int s = t - (W - 1);
+            if (s >= beg && s >= t0) emit(s, -1);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+        };
+        auto enter = [&](int t) {
+            n = seq_of_token(a.seqs, t, &beg, &end);
+            if (n < 0) {
+                end = t + 1;
+                return;
+            }
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+                seq_row<T, VEC, W>(x, a.x_stride, state0, n, C, c, t - (W - 1) + j, beg, win[j]);
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) dz[j][e] = 0.f;
+        };
         load(t0);
+        enter(t0);
         for (int t = t0; t < t2 && !done; t += U) {
             typename R::vec rx[U], rg[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) rx[i] = nx[i], rg[i] = ng[i];
             load(t + U);
+            if (t + U <= t1 && t + U <= end && n >= 0) {  // inside one sequence
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int tt = t + i;
-                if (tt >= t2 || done) break;
+                for (int i = 0; i < U; ++i) token(t + i, rx[i], rg[i], true);
+                continue;
+            }
+#pragma unroll 1
+            for (int tt = t; tt < t + U && tt < t2; ++tt) {
                 if (tt >= end) {
                     if (n >= 0) flush();
                     if (tt >= t1) {  // what follows is another sequence's
@@ -298,39 +345,11 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int c
                         done = true;
                         break;
                     }
-                    n = seq_of_token(a.seqs, tt, &beg, &end);
-                    if (n < 0) {
-                        end = tt + 1;
-                        continue;
-                    }
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j)
-                        seq_row<T, VEC, W>(x, a.x_stride, state0, n, C, c, tt - (W - 1) + j, beg,
-                                           win[j]);
-#pragma unroll
-                    for (int j = 0; j < W; ++j)
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) dz[j][e] = 0.f;
+                    enter(tt);
                 }
                 if (n < 0) continue;
-                R::get(rx[i], win[W - 1]);
-                shift();
-                R::get(rg[i], dz[W - 1]);
-                grad_z<VEC, W>(w, b, win, a.silu, dz[W - 1]);
-                if (tt < t1) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        db[e] += dz[W - 1][e];
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][e] += dz[W - 1][e] * win[j][e];
-                    }
-                }
-                const int s = tt - (W - 1);
-                if (s >= beg && s >= t0) emit(s, -1);
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) win[j][e] = win[j + 1][e];
+                token(tt, R::raw(col(x + (int64_t)tt * a.x_stride, c)),
+                      R::raw(col(dy + (int64_t)tt * a.d_out_stride, c)), tt < t1);
             }
         }
         // the walk ended where its sequence does (t2 = total, or the next begins at t2)
@@ -419,10 +438,13 @@ int run_tokens(int64_t total, int cblocks) {
     run = (run + 7) / 8 * 8;
     return (int)(run < 8 ? 8 : (run > 128 ? 128 : run));
 }
-constexpr int kBwdRun = 64;  // at most; the workspace is sized without cblocks
+// The backward's runs read 2 (W - 1) rows twice and are worth more length: 16 to
+// 64 tokens, for 2048 waves (8K x 4096 channels bf16: 53 us with 64, 60 with
+// 32, 61 with 16).
 int bwd_run_tokens(int64_t total, int cblocks) {
-    const int run = run_tokens(total, cblocks);
-    return run < 16 ? 16 : (run > kBwdRun ? kBwdRun : run);
+    int64_t run = total * cblocks / 2048;
+    run = (run + 7) / 8 * 8;
+    return (int)(run < 16 ? 16 : (run > 64 ? 64 : run));
 }
 
 template <typename T, int VEC, int W> int fwd(const ConvArgs &a, hipStream_t stream) {

@@ -228,7 +228,8 @@ int check_qk(const void *q, const void *k, const float *q_weight, const float *k
              Span (&ins)[6]) {
     if (tokens < 0 || q_heads < 0 || k_heads < 0 || head_dim <= 0 || rotary_dim < 0)
         return KDA_ERR_SHAPE;
-    if ((int64_t)q_heads + k_heads > INT32_MAX) return KDA_ERR_SHAPE;
+    // the kernels address a token's heads with 32-bit byte offsets
+    if (((int64_t)q_heads + k_heads) * head_dim > INT32_MAX / 4) return KDA_ERR_UNSUPPORTED;
     if (rotary_dim > head_dim || !(eps >= 0.f)) return KDA_ERR_SHAPE;
     const int esz = elem_size(dtype);
     if (!esz) return KDA_ERR_UNSUPPORTED;
@@ -306,9 +307,9 @@ int kda_qk_norm_fwd(const void *q, const void *k, const float *q_weight, const f
 int64_t kda_qk_norm_bwd_workspace_size(int32_t tokens, int32_t q_heads, int32_t k_heads,
                                        int32_t head_dim) {
     if (tokens < 0 || q_heads < 0 || k_heads < 0 || (head_dim != 64 && head_dim != 128) ||
-        (int64_t)q_heads + k_heads > INT32_MAX)
+        ((int64_t)q_heads + k_heads) * head_dim > INT32_MAX / 4)
         return -1;
-    return 4 * kda::qk_norm_bwd_workspace_floats(tokens, (int64_t)q_heads + k_heads, head_dim);
+    return 4 * kda::qk_norm_bwd_workspace_floats(tokens, q_heads, k_heads, head_dim);
 }
 
 int kda_qk_norm_bwd(const void *q, const void *k, const float *q_weight, const float *k_weight,

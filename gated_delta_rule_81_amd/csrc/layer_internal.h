@@ -59,7 +59,8 @@ struct QkArgs {
 };
 int launch_qk_norm_fwd(const QkArgs &a, hipStream_t stream);
 int launch_qk_norm_bwd(const QkArgs &a, hipStream_t stream);
-int64_t qk_norm_bwd_workspace_floats(int64_t tokens, int64_t heads, int head_dim);
+int64_t qk_norm_bwd_workspace_floats(int64_t tokens, int64_t q_heads, int64_t k_heads,
+                                     int head_dim);
 
 // The scan's walk over the sequences.  With seg_states the sequences are cut into
 // pieces of `piece` tokens that run at once (seg_states: a state per piece

@@ -98,12 +98,6 @@ __device__ __forceinline__ float inv_norm(float ss, bool rms, int d, float eps) 
     return __builtin_amdgcn_rsqf((rms ? ss * (1.f / d) : ss) + eps);
 }
 
-template <typename T>
-__device__ __forceinline__ const T *head_at(const void *const (&p)[2], const int64_t (&stride)[2],
-                                            int which, int64_t token, int h, int d) {
-    return static_cast<const T *>(p[which]) + token * stride[which] + (int64_t)h * d;
-}
-
 // Eight channels of both weights (ones where there is none).
 __device__ __forceinline__ void load_weights(const QkArgs &a, int e0, float (&w)[2][8]) {
 #pragma unroll
@@ -112,31 +106,58 @@ __device__ __forceinline__ void load_weights(const QkArgs &a, int e0, float (&w)
         for (int e = 0; e < 8; ++e) w[k][e] = a.weight[k] ? a.weight[k][e0 + e] : 1.f;
 }
 
+// The heads of one token in passes of HPP heads, q's first, then k's: a pass is
+// never of both, so which of the two it is is the same for the whole wave.
+struct Pass {
+    int which, head;  // tensor, this lane's head in it
+    bool on, any;     // whether there is such a head; whether there is such a pass
+};
+template <int HPP>
+__device__ __forceinline__ Pass pass_of(const QkArgs &a, int pass, int sub) {
+    const int pq = (a.heads[0] + HPP - 1) / HPP, pk = (a.heads[1] + HPP - 1) / HPP;
+    Pass p;
+    p.which = pass >= pq;
+    p.any = pass < pq + pk;
+    p.head = (p.which ? pass - pq : pass) * HPP + sub;
+    p.on = p.any && p.head < (p.which ? a.heads[1] : a.heads[0]);
+    return p;
+}
+
+// Row of this lane's eight channels in a tensor of the pass: scalar base, 32-bit
+// offset (a token's heads span less than 2^31 bytes).
+template <typename T>
+__device__ __forceinline__ T *row_of(const void *q, const void *k, const int64_t (&stride)[2],
+                                     const Pass &p, int64_t token, int d, int e0) {
+    const char *base = static_cast<const char *>(p.which ? k : q) +
+                       token * (p.which ? stride[1] : stride[0]) * (int64_t)sizeof(T);
+    return (T *)(base + (unsigned)(p.head * d + e0) * (unsigned)sizeof(T));
+}
+
 // Unit: (token, group of kPasses passes).  One wave per unit.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkArgs a, int groups) {
     constexpr int LPR = D / 8, HPP = 64 / LPR;  // lanes per head, heads per pass
     const int lane = threadIdx.x & 63;
-    const int64_t unit = (int64_t)blockIdx.x * kWavesPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t unit = (int64_t)blockIdx.x * kWavesPerBlock +
+                         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t token = unit / groups;
     if (token >= a.tokens) return;
-    const int h0 = (int)(unit % groups) * (kPasses * HPP) + lane / LPR;
-    const int heads = a.heads[0] + a.heads[1], e0 = 8 * (lane % LPR);
+    const int pass0 = (int)(unit % groups) * kPasses, e0 = 8 * (lane % LPR);
     typename Vec8<T>::raw raw[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        const int h = h0 + i * HPP, which = h >= a.heads[0];
-        raw[i] = h < heads ? load8(head_at<T>(a.x, a.x_stride, which, token,
-                                              which ? h - a.heads[0] : h, D) + e0)
-                           : Vec8<T>::zero();
+        const Pass p = pass_of<HPP>(a, pass0 + i, lane / LPR);
+        raw[i] = p.on ? load8(row_of<T>(a.x[0], a.x[1], a.x_stride, p, token, D, e0))
+                      : Vec8<T>::zero();
     }
+    const bool weights = a.weight[0] || a.weight[1];
     float wt[2][8];
-    load_weights(a, e0, wt);
+    if (weights) load_weights(a, e0, wt);
     Turn turn;
     if (a.rot) turn = load_turn<D>(a, token, lane, false);
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-        const int h = h0 + i * HPP, which = h >= a.heads[0];
+        const Pass p = pass_of<HPP>(a, pass0 + i, lane / LPR);
         float x[8];
         Vec8<T>::to_float(raw[i], x);
         float ss = 0.f;
@@ -145,51 +166,48 @@ __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkArgs a, int gro
         const float inv = inv_norm(head_sum<LPR>(ss), a.rms, D, a.eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= inv;
-        if (a.weight[0] || a.weight[1]) {
+        if (weights) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= which ? wt[1][e] : wt[0][e];
+            for (int e = 0; e < 8; ++e) x[e] *= p.which ? wt[1][e] : wt[0][e];
         }
         if (a.rot) rotate(turn, a.interleaved, x);
-        if (h < heads)
-            store8(const_cast<T *>(head_at<T>({a.y[0], a.y[1]}, a.y_stride, which, token,
-                                              which ? h - a.heads[0] : h, D)) + e0, x);
+        if (p.on) store8(row_of<T>(a.y[0], a.y[1], a.y_stride, p, token, D, e0), x);
     }
 }
 
 // The same walk; the gradients of the two weights of all of a workgroup's heads go
 // to its row of `partial` ([row][2][D]), summed afterwards in row order.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkArgs a, int groups) {
+__global__ __launch_bounds__(kThreads, 4) void qk_norm_bwd_kernel(QkArgs a, int groups) {
     constexpr int LPR = D / 8, HPP = 64 / LPR;
     __shared__ float sum[kWavesPerBlock][2][HPP][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int heads = a.heads[0] + a.heads[1], e0 = 8 * (lane % LPR);
+    const int e0 = 8 * (lane % LPR);
     const int64_t units = (int64_t)a.tokens * groups;
-    float dw[2][8];
+    const bool weights = a.weight[0] || a.weight[1];
+    float dw[2][8], wt[2][8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
-    float wt[2][8];
-    load_weights(a, e0, wt);
+    if (weights) load_weights(a, e0, wt);
     for (int64_t unit = (int64_t)blockIdx.x * kWavesPerBlock + wave; unit < units;
          unit += (int64_t)gridDim.x * kWavesPerBlock) {
         const int64_t token = unit / groups;
-        const int h0 = (int)(unit % groups) * (kPasses * HPP) + lane / LPR;
+        const int pass0 = (int)(unit % groups) * kPasses;
         typename Vec8<T>::raw rx[kPasses], rg[kPasses];
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            const int h = h0 + i * HPP, which = h >= a.heads[0];
-            const int hh = which ? h - a.heads[0] : h;
-            const bool in = h < heads;
-            rx[i] = in ? load8(head_at<T>(a.x, a.x_stride, which, token, hh, D) + e0)
-                       : Vec8<T>::zero();
-            rg[i] = in ? load8(head_at<T>(a.dy, a.dy_stride, which, token, hh, D) + e0)
-                       : Vec8<T>::zero();
+            const Pass p = pass_of<HPP>(a, pass0 + i, lane / LPR);
+            rx[i] = p.on ? load8(row_of<T>(a.x[0], a.x[1], a.x_stride, p, token, D, e0))
+                         : Vec8<T>::zero();
+            rg[i] = p.on ? load8(row_of<T>(a.dy[0], a.dy[1], a.dy_stride, p, token, D, e0))
+                         : Vec8<T>::zero();
         }
         Turn turn;
         if (a.rot) turn = load_turn<D>(a, token, lane, true);
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            const int h = h0 + i * HPP, which = h >= a.heads[0];
+            const Pass p = pass_of<HPP>(a, pass0 + i, lane / LPR);
+            if (!p.any) break;
             float x[8], g[8];
             Vec8<T>::to_float(rx[i], x);
             Vec8<T>::to_float(rg[i], g);
@@ -198,13 +216,15 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkArgs a, int gro
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
             const float inv = inv_norm(head_sum<LPR>(ss), a.rms, D, a.eps);
-            if (a.weight[0] || a.weight[1]) {
+            if (weights) {
+                // a lane without a head adds nothing (0 * inf where eps is 0)
+                const float k = p.on ? inv : 0.f;
+                if (p.which) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = h < heads ? g[e] * x[e] * inv : 0.f;
-                    dw[0][e] += which ? 0.f : v;
-                    dw[1][e] += which ? v : 0.f;
-                    g[e] *= which ? wt[1][e] : wt[0][e];
+                    for (int e = 0; e < 8; ++e) dw[1][e] += g[e] * (x[e] * k), g[e] *= wt[1][e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dw[0][e] += g[e] * (x[e] * k), g[e] *= wt[0][e];
                 }
             }
             float dot = 0.f;
@@ -214,9 +234,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_bwd_kernel(QkArgs a, int gro
             const float k = head_sum<LPR>(dot) * inv * (a.rms ? 1.f / D : 1.f) * inv;
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = inv * (g[e] - x[e] * k);
-            if (h < heads)
-                store8(const_cast<T *>(head_at<T>({a.y[0], a.y[1]}, a.y_stride, which, token,
-                                                  which ? h - a.heads[0] : h, D)) + e0, x);
+            if (p.on) store8(row_of<T>(a.y[0], a.y[1], a.y_stride, p, token, D, e0), x);
         }
     }
     if (!a.partial) return;
@@ -255,9 +273,10 @@ __global__ __launch_bounds__(1024) void qk_reduce_kernel(const float *partial, i
     if (out) out[col % D] = part[0][threadIdx.x];
 }
 
-int groups_of(int heads, int d) {
+int groups_of(int64_t q_heads, int64_t k_heads, int d) {
     const int hpp = 512 / d;  // heads per pass
-    return (heads + kPasses * hpp - 1) / (kPasses * hpp);
+    const int64_t passes = (q_heads + hpp - 1) / hpp + (k_heads + hpp - 1) / hpp;
+    return (int)((passes + kPasses - 1) / kPasses);
 }
 // Workgroups of the backward: enough to fill the chip several times over,
 // few enough that their partial sums stay small beside the data.
@@ -268,7 +287,7 @@ int bwd_blocks(int64_t units) {
 }
 
 template <typename T, int D> int fwd(const QkArgs &a, hipStream_t stream) {
-    const int groups = groups_of(a.heads[0] + a.heads[1], D);
+    const int groups = groups_of(a.heads[0], a.heads[1], D);
     const int64_t units = (int64_t)a.tokens * groups;
     hipLaunchKernelGGL((qk_norm_fwd_kernel<T, D>),
                        dim3((unsigned)((units + kWavesPerBlock - 1) / kWavesPerBlock)),
@@ -280,7 +299,7 @@ template <typename T, int D> int bwd(const QkArgs &args, hipStream_t stream) {
     QkArgs a = args;
     const bool weights = a.dweight[0] || a.dweight[1];
     if (!weights) a.partial = nullptr;
-    const int groups = groups_of(a.heads[0] + a.heads[1], D);
+    const int groups = groups_of(a.heads[0], a.heads[1], D);
     const int blocks = bwd_blocks((int64_t)a.tokens * groups);
     if (blocks > 0)
         hipLaunchKernelGGL((qk_norm_bwd_kernel<T, D>), dim3(blocks), dim3(kThreads), 0, stream, a,
@@ -301,8 +320,9 @@ template <typename T, int D> int bwd(const QkArgs &args, hipStream_t stream) {
 int launch_qk_norm_fwd(const QkArgs &a, hipStream_t stream) { return KDA_QK_DISPATCH(fwd); }
 int launch_qk_norm_bwd(const QkArgs &a, hipStream_t stream) { return KDA_QK_DISPATCH(bwd); }
 
-int64_t qk_norm_bwd_workspace_floats(int64_t tokens, int64_t heads, int head_dim) {
-    return (int64_t)bwd_blocks(tokens * groups_of((int)heads, head_dim)) * 2 * head_dim;
+int64_t qk_norm_bwd_workspace_floats(int64_t tokens, int64_t q_heads, int64_t k_heads,
+                                     int head_dim) {
+    return (int64_t)bwd_blocks(tokens * groups_of(q_heads, k_heads, head_dim)) * 2 * head_dim;
 }
 
 }  // namespace kda
