@@ -16,8 +16,12 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256, kWavesPerBlock = 4;
-constexpr int kPasses = 4;  // passes (of 4 or 8 heads each) whose loads are in flight together
+// Passes (of 4 or 8 heads each) of one unit, whose loads are in flight together,
+// and waves of a workgroup.  Measured, us: forward 32K x 192 heads x 128 bf16 with
+// 4 passes and 1, 4, 8 waves 571, 581, 586, with 2 and 8 passes 584, 586; backward
+// 8K x 40 heads (4 waves) with 2, 4, 8 passes 55, 58, 132, with 1 and 8 waves 105, 68.
+constexpr int kFwdPasses = 4, kFwdWaves = 1;
+constexpr int kBwdPasses = 2, kBwdWaves = 4;
 
 // Sum over aligned groups of LPR (8 or 16) lanes, in every lane of the group.
 template <int LPR> __device__ __forceinline__ float head_sum(float x) {
@@ -133,19 +137,20 @@ __device__ __forceinline__ T *row_of(const void *q, const void *k, const int64_t
     return (T *)(base + (unsigned)(p.head * d + e0) * (unsigned)sizeof(T));
 }
 
-// Unit: (token, group of kPasses passes).  One wave per unit.
+// Unit: (token, group of kFwdPasses passes).  One wave per unit.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkArgs a, int groups) {
+__global__ __launch_bounds__(64 * kFwdWaves) void qk_norm_fwd_kernel(QkArgs a, int groups,
+                                                                     int64_t unit0) {
     constexpr int LPR = D / 8, HPP = 64 / LPR;  // lanes per head, heads per pass
     const int lane = threadIdx.x & 63;
-    const int64_t unit = (int64_t)blockIdx.x * kWavesPerBlock +
+    const int64_t unit = unit0 + (int64_t)blockIdx.x * kFwdWaves +
                          __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t token = unit / groups;
     if (token >= a.tokens) return;
-    const int pass0 = (int)(unit % groups) * kPasses, e0 = 8 * (lane % LPR);
-    typename Vec8<T>::raw raw[kPasses];
+    const int pass0 = (int)(unit % groups) * kFwdPasses, e0 = 8 * (lane % LPR);
+    typename Vec8<T>::raw raw[kFwdPasses];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
+    for (int i = 0; i < kFwdPasses; ++i) {
         const Pass p = pass_of<HPP>(a, pass0 + i, lane / LPR);
         raw[i] = p.on ? load8(row_of<T>(a.x[0], a.x[1], a.x_stride, p, token, D, e0))
                       : Vec8<T>::zero();
@@ -156,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkArgs a, int gro
     Turn turn;
     if (a.rot) turn = load_turn<D>(a, token, lane, false);
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
+    for (int i = 0; i < kFwdPasses; ++i) {
         const Pass p = pass_of<HPP>(a, pass0 + i, lane / LPR);
         float x[8];
         Vec8<T>::to_float(raw[i], x);
@@ -178,9 +183,9 @@ __global__ __launch_bounds__(kThreads) void qk_norm_fwd_kernel(QkArgs a, int gro
 // The same walk; the gradients of the two weights of all of a workgroup's heads go
 // to its row of `partial` ([row][2][D]), summed afterwards in row order.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads, 4) void qk_norm_bwd_kernel(QkArgs a, int groups) {
+__global__ __launch_bounds__(64 * kBwdWaves, 4) void qk_norm_bwd_kernel(QkArgs a, int groups) {
     constexpr int LPR = D / 8, HPP = 64 / LPR;
-    __shared__ float sum[kWavesPerBlock][2][HPP][D];
+    __shared__ float sum[kBwdWaves][2][HPP][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int e0 = 8 * (lane % LPR);
     const int64_t units = (int64_t)a.tokens * groups;
@@ -189,13 +194,13 @@ __global__ __launch_bounds__(kThreads, 4) void qk_norm_bwd_kernel(QkArgs a, int 
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.f;
     if (weights) load_weights(a, e0, wt);
-    for (int64_t unit = (int64_t)blockIdx.x * kWavesPerBlock + wave; unit < units;
-         unit += (int64_t)gridDim.x * kWavesPerBlock) {
+    for (int64_t unit = (int64_t)blockIdx.x * kBwdWaves + wave; unit < units;
+         unit += (int64_t)gridDim.x * kBwdWaves) {
         const int64_t token = unit / groups;
-        const int pass0 = (int)(unit % groups) * kPasses;
-        typename Vec8<T>::raw rx[kPasses], rg[kPasses];
+        const int pass0 = (int)(unit % groups) * kBwdPasses;
+        typename Vec8<T>::raw rx[kBwdPasses], rg[kBwdPasses];
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
+        for (int i = 0; i < kBwdPasses; ++i) {
             const Pass p = pass_of<HPP>(a, pass0 + i, lane / LPR);
             rx[i] = p.on ? load8(row_of<T>(a.x[0], a.x[1], a.x_stride, p, token, D, e0))
                          : Vec8<T>::zero();
@@ -205,7 +210,7 @@ __global__ __launch_bounds__(kThreads, 4) void qk_norm_bwd_kernel(QkArgs a, int 
         Turn turn;
         if (a.rot) turn = load_turn<D>(a, token, lane, true);
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
+        for (int i = 0; i < kBwdPasses; ++i) {
             const Pass p = pass_of<HPP>(a, pass0 + i, lane / LPR);
             if (!p.any) break;
             float x[8], g[8];
@@ -244,10 +249,10 @@ __global__ __launch_bounds__(kThreads, 4) void qk_norm_bwd_kernel(QkArgs a, int 
         sum[wave][1][lane / LPR][e0 + e] = dw[1][e];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    for (int i = threadIdx.x; i < 2 * D; i += 64 * kBwdWaves) {
         float s = 0.f;
 #pragma unroll
-        for (int wv = 0; wv < kWavesPerBlock; ++wv)
+        for (int wv = 0; wv < kBwdWaves; ++wv)
 #pragma unroll
             for (int r = 0; r < HPP; ++r) s += sum[wv][i / D][r][i % D];
         a.partial[(int64_t)blockIdx.x * 2 * D + i] = s;
@@ -273,25 +278,29 @@ __global__ __launch_bounds__(1024) void qk_reduce_kernel(const float *partial, i
     if (out) out[col % D] = part[0][threadIdx.x];
 }
 
-int groups_of(int64_t q_heads, int64_t k_heads, int d) {
+int groups_of(int64_t q_heads, int64_t k_heads, int d, int per_unit) {
     const int hpp = 512 / d;  // heads per pass
     const int64_t passes = (q_heads + hpp - 1) / hpp + (k_heads + hpp - 1) / hpp;
-    return (int)((passes + kPasses - 1) / kPasses);
+    return (int)((passes + per_unit - 1) / per_unit);
 }
 // Workgroups of the backward: enough to fill the chip several times over,
 // few enough that their partial sums stay small beside the data.
 constexpr int kBwdBlocks = 1024;
 int bwd_blocks(int64_t units) {
-    const int64_t b = (units + kWavesPerBlock - 1) / kWavesPerBlock;
+    const int64_t b = (units + kBwdWaves - 1) / kBwdWaves;
     return (int)(b < kBwdBlocks ? b : kBwdBlocks);
 }
 
 template <typename T, int D> int fwd(const QkArgs &a, hipStream_t stream) {
-    const int groups = groups_of(a.heads[0], a.heads[1], D);
+    const int groups = groups_of(a.heads[0], a.heads[1], D, kFwdPasses);
     const int64_t units = (int64_t)a.tokens * groups;
-    hipLaunchKernelGGL((qk_norm_fwd_kernel<T, D>),
-                       dim3((unsigned)((units + kWavesPerBlock - 1) / kWavesPerBlock)),
-                       dim3(kThreads), 0, stream, a, groups);
+    constexpr int64_t kMost = (int64_t)1 << 25;  // a launch holds less than 2^32 threads
+    for (int64_t u = 0; u < units; u += kMost) {
+        const int64_t now = units - u < kMost ? units - u : kMost;
+        hipLaunchKernelGGL((qk_norm_fwd_kernel<T, D>),
+                           dim3((unsigned)((now + kFwdWaves - 1) / kFwdWaves)), dim3(64 * kFwdWaves),
+                           0, stream, a, groups, u);
+    }
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
@@ -299,10 +308,10 @@ template <typename T, int D> int bwd(const QkArgs &args, hipStream_t stream) {
     QkArgs a = args;
     const bool weights = a.dweight[0] || a.dweight[1];
     if (!weights) a.partial = nullptr;
-    const int groups = groups_of(a.heads[0], a.heads[1], D);
+    const int groups = groups_of(a.heads[0], a.heads[1], D, kBwdPasses);
     const int blocks = bwd_blocks((int64_t)a.tokens * groups);
     if (blocks > 0)
-        hipLaunchKernelGGL((qk_norm_bwd_kernel<T, D>), dim3(blocks), dim3(kThreads), 0, stream, a,
+        hipLaunchKernelGGL((qk_norm_bwd_kernel<T, D>), dim3(blocks), dim3(64 * kBwdWaves), 0, stream, a,
                            groups);
     if (weights)
         hipLaunchKernelGGL(qk_reduce_kernel, dim3(2 * D / 8), dim3(8, 128), 0, stream, a.partial,
@@ -322,7 +331,7 @@ int launch_qk_norm_bwd(const QkArgs &a, hipStream_t stream) { return KDA_QK_DISP
 
 int64_t qk_norm_bwd_workspace_floats(int64_t tokens, int64_t q_heads, int64_t k_heads,
                                      int head_dim) {
-    return (int64_t)bwd_blocks(tokens * groups_of(q_heads, k_heads, head_dim)) * 2 * head_dim;
+    return (int64_t)bwd_blocks(tokens * groups_of(q_heads, k_heads, head_dim, kBwdPasses)) * 2 * head_dim;
 }
 
 }  // namespace kda
