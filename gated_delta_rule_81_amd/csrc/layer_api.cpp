@@ -55,13 +55,18 @@ template <int NO, int NI> int check_alias(const Span (&outs)[NO], const Span (&i
     return KDA_OK;
 }
 
+// Token numbers a little past the last one still fit 32 bits; a row of the
+// convolution is addressed with 32-bit byte offsets.
+constexpr int64_t kMostTokens = INT32_MAX - 4095;
+constexpr int32_t kMostChannels = INT32_MAX / 4;
+
 // Sizes of a call over sequences; *seqs receives them.
 int check_seqs(const int32_t *cu, int32_t batch, int32_t seq_len, int32_t num_seqs,
                kda::Seqs *seqs) {
     if (batch < 0 || seq_len < 0) return KDA_ERR_SHAPE;
     if (cu && (batch != 1 || num_seqs < 0)) return KDA_ERR_SHAPE;
     const int64_t tokens = (int64_t)batch * seq_len;
-    if (tokens > INT32_MAX) return KDA_ERR_SHAPE;
+    if (tokens > kMostTokens) return KDA_ERR_SHAPE;
     *seqs = {cu, cu ? num_seqs : batch, seq_len, (int32_t)tokens};
     return KDA_OK;
 }
@@ -85,7 +90,7 @@ int kda_short_conv_fwd(const void *x, const float *weight, const float *bias,
     const bool work = seqs.total > 0 && channels > 0;
     if (work && (x_stride < channels || out_stride < channels)) return KDA_ERR_SHAPE;
     if (work && (!x || !weight || !out)) return KDA_ERR_NULL;
-    if (width < 2 || width > 4) return KDA_ERR_UNSUPPORTED;
+    if (width < 2 || width > 4 || channels > kMostChannels) return KDA_ERR_UNSUPPORTED;
     if (activation != KDA_ACT_NONE && activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
     if (!aligned_to(x, esz) || !aligned_to(out, esz) || !aligned_to(initial_state, esz) ||
         !aligned_to(final_state, esz) || !aligned4(weight) || !aligned4(bias) ||
@@ -118,7 +123,7 @@ int64_t kda_short_conv_bwd_workspace_size(int32_t batch, int32_t seq_len, int32_
                                           int32_t width) {
     if (batch < 0 || seq_len < 0 || channels < 0 || width < 2 || width > 4) return -1;
     const int64_t tokens = (int64_t)batch * seq_len;
-    if (tokens > INT32_MAX) return -1;
+    if (tokens > kMostTokens || channels > kMostChannels) return -1;
     return 4 * kda::conv_bwd_workspace_floats(tokens, channels, width);
 }
 
@@ -140,7 +145,7 @@ int kda_short_conv_bwd(const void *x, const float *weight, const float *bias,
         return KDA_ERR_SHAPE;
     if (work && (!x || !d_out || !dx)) return KDA_ERR_NULL;
     if (channels > 0 && (!weight || !dweight)) return KDA_ERR_NULL;
-    if (width < 2 || width > 4) return KDA_ERR_UNSUPPORTED;
+    if (width < 2 || width > 4 || channels > kMostChannels) return KDA_ERR_UNSUPPORTED;
     if (activation != KDA_ACT_NONE && activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
     const int64_t need = 4 * kda::conv_bwd_workspace_floats(seqs.total, channels, width);
     if (need > 0 && !workspace) return KDA_ERR_NULL;
@@ -192,7 +197,7 @@ int kda_short_conv_step(const void *x, const float *weight, const float *bias, v
     const bool work = batch > 0 && channels > 0;
     if (work && (x_stride < channels || out_stride < channels)) return KDA_ERR_SHAPE;
     if (work && (!x || !weight || !state || !out)) return KDA_ERR_NULL;
-    if (width < 2 || width > 4) return KDA_ERR_UNSUPPORTED;
+    if (width < 2 || width > 4 || channels > kMostChannels) return KDA_ERR_UNSUPPORTED;
     if (activation != KDA_ACT_NONE && activation != KDA_ACT_SILU) return KDA_ERR_UNSUPPORTED;
     if (!aligned_to(x, esz) || !aligned_to(out, esz) || !aligned_to(state, esz) ||
         !aligned4(weight) || !aligned4(bias))

@@ -90,8 +90,9 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                                 : (int64_t)(16 * wave + r) * N + 4 * g;
     const float *enter = nullptr;
     if (MODE != kLocal) {
-        const bool edge = REV ? pc.last : pc.first;
-        enter = a.seg_states && !edge
+        // Of a sequence in several pieces the fold has written every entering state,
+        // the first too: final_state may be state0, and another workgroup writes it.
+        enter = a.seg_states && !(pc.first && pc.last)
                     ? a.seg_states + (number * a.heads + h) * (int64_t)(P * N)
                     : (a.state0 ? a.state0 + ((int64_t)pc.seq * a.heads + h) * (P * N) : nullptr);
     }
@@ -211,6 +212,8 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
             }
 #pragma unroll
             for (int it = 0; it < L / 16; ++it) y[it] *= s_in[buf][16 * it + r];
+            // the next block's decays, by a wave that had a tile of M less to form
+            if (weigher && i + 1 < blocks) weights(buf ^ 1);
             lds_barrier();
         }
         // x^T operands of this wave's rows p, and x^T weighted for the state
@@ -264,7 +267,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                 S[t] = TR ? mma(xw[ks], read_cols<TK, NI>(sk, ks, kcol[t]), S[t])
                           : mma(read_cols<TK, NI>(sk, ks, kcol[t]), xw[ks], S[t]);
         }
-        if (weigher && i + 1 < blocks) weights(buf ^ 1);
+        if (!OUT && weigher && i + 1 < blocks) weights(buf ^ 1);
         lds_barrier();  // the tiles are read: the next block's may be written
     }
     float *to = nullptr;
@@ -352,7 +355,7 @@ __device__ __forceinline__ void fold_body(const SsmScan &a, int values, int64_t 
             const f32x4 enter = kept;
             if (j0 + i < count - 1) {
                 kept = enter * decay[i] + own[i];
-                if (j0 + i > 0) *reinterpret_cast<f32x4 *>(at(j0 + i)) = enter;
+                *reinterpret_cast<f32x4 *>(at(j0 + i)) = enter;
             }
         }
         S = kept;

@@ -13,7 +13,8 @@ from typing import Optional, Tuple
 import torch
 
 from ._lib import check, lib
-from .ops import _DTYPES, _expect, _ptr
+from .ops import _DTYPES, _ptr
+from .ops import _expect as _expect_dense
 
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 _NORMS = {"l2": 0, "rms": 1}
@@ -28,11 +29,12 @@ def _rows(t, name, dtype, shape, device, lead: int) -> int:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
+    sizes = t.shape
+    if sizes != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_contiguous():
-        return t.shape[lead:].numel()
-    sizes, strides, width = t.shape, t.stride(), 1
+        return sizes[lead:].numel()
+    strides, width = t.stride(), 1
     for i in range(len(sizes) - 1, lead - 1, -1):
         if strides[i] != width and sizes[i] != 1:
             raise ValueError(f"{name}: the values of a token must be contiguous")
@@ -49,6 +51,14 @@ def _rows(t, name, dtype, shape, device, lead: int) -> int:
     if row < width:
         raise ValueError(f"{name}: the rows of two tokens overlap")
     return row
+
+
+def _expect(t, name, dtype, shape, device):
+    """``ops._expect`` with the common case first."""
+    if t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                     and t.device == device and t.is_contiguous()):
+        return
+    _expect_dense(t, name, dtype, shape, device)
 
 
 def _dtype(t, name):

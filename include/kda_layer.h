@@ -19,7 +19,8 @@
  *   - Tensors with one row per token may be slices of wider rows: `*_stride`
  *     is the distance in elements between consecutive tokens (token t of batch
  *     row b is row b * seq_len + t), at least the row's own length.  Everything
- *     else is dense.  Offsets are 64-bit.
+ *     else is dense.  Offsets are 64-bit; tokens are counted in 32 bits (batch *
+ *     seq_len at most 2^31 - 4096).
  *   - Parameters (weights, biases, A, D), dt and scan states are fp32; sums,
  *     norms and states are held in fp32; outputs are rounded once.
  *   - A workspace is the caller's, 16-byte aligned, of at least the size its

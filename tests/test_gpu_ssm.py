@@ -257,6 +257,22 @@ def test_prompt_then_tokens(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", [CASES[9], CASES[11], CASES[3]], ids=str)
+def test_state_updated_in_place(case):
+    """final_state = initial_state, in one piece and in several (whose first and
+    last workgroups both use the state): the bits of the call with two buffers."""
+    say("ssm_chunk_fwd in place", case)
+    dev, _ = make(case, 4)
+    args = (dev["x"], dev["dt"], dev["A"], dev["B"], dev["C"], dev["D"])
+    want, fin = kda.ssm_chunk_fwd(*args, dev["state"], dev["cu"])
+    st = dev["state"].clone()
+    out, got = kda.ssm_chunk_fwd(*args, st, dev["cu"], final_state=st)
+    torch.cuda.synchronize()
+    assert got.data_ptr() == st.data_ptr()
+    assert torch.equal(out, want) and torch.equal(st, fin)
+
+
+@pytest.mark.gpu
 def test_tokens_behind_the_last_sequence_stay():
     say("ssm_chunk_fwd: tokens behind the last offset")
     dev, _ = make((1, 0, [100, 30], 2, 1, 64, 64, True, True, 0, "bf16", 1.0))

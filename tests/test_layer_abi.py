@@ -136,6 +136,8 @@ def test_types_and_configurations(name):
     if "width" in DECLARED[name]:
         assert call(name, width=1) == UNSUP and call(name, width=5) == UNSUP
         assert call(name, width=0) == SHAPE
+        rows = {a: 1 << 30 for a in DECLARED[name] if a.endswith("_stride")}
+        assert call(name, channels=(1 << 29) + 1, **rows) == UNSUP  # a row passes 2^31 bytes
         assert call(name, activation=2) == UNSUP
     if "head_dim" in DECLARED[name]:
         assert call(name, head_dim=96) == UNSUP
@@ -225,6 +227,7 @@ def test_packed_needs_one_row(name):
     assert call(name, batch=1, cu_seqlens=1 << 50, num_seqs=-1) == SHAPE
     assert call(name, batch=1, cu_seqlens=1 << 50, num_seqs=3) == DEVICE
     assert call(name, batch=1 << 16, seq_len=1 << 16) == SHAPE  # tokens pass int32
+    assert call(name, batch=1, seq_len=2 ** 31 - 4095) == SHAPE
 
 
 @pytest.mark.parametrize("name", [n for n in CALLS if "workspace" in DECLARED[n]])
