@@ -92,7 +92,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs a, int c
         const int64_t n = unit / (W - 1);
         const int j = (int)(unit % (W - 1));
         if (n >= a.seqs.num) return;
-        const int beg = (int)seq_first_token(a.seqs.cu, a.seqs.seq_len, a.seqs.total, (int)n);
+        const int beg = seq_first(a.seqs, (int)n);
         int end = seq_end_token(a.seqs, (int)n);
         end = end < beg ? beg : end;
         float f[VEC];
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs a, int c
     if (blk >= run_blocks) {  // gradient of the initial states: kWaves sequences each
         const int64_t n = (blk - run_blocks) * kWaves + wave;
         if (!on || n >= a.seqs.num) return;
-        const int beg = (int)seq_first_token(a.seqs.cu, a.seqs.seq_len, a.seqs.total, (int)n);
+        const int beg = seq_first(a.seqs, (int)n);
         int end = seq_end_token(a.seqs, (int)n);
         const int len = end < beg ? 0 : end - beg;
         float dz[W - 1][VEC];  // of the first W - 1 tokens

@@ -4,7 +4,6 @@
 #pragma once
 
 #include "kda_device.h"
-#include "kda_slots.h"
 #include "layer_internal.h"
 
 namespace kda {
@@ -34,34 +33,38 @@ template <typename T> struct Row<T, 1> {
     __device__ static vec zero() { return T(0.f); }
 };
 
-// End of sequence m, clamped into [0, total].
-__device__ __forceinline__ int seq_end_token(const Seqs &q, int m) {
-    if (!q.cu) return (m + 1) * q.seq_len;
-    const int a = q.cu[m + 1];
+// Packed offset i, clamped into [0, total].  Offsets are not written while a kernel
+// runs: read as constants, at an index that is the same for the whole wave they
+// come through scalar loads, which do not queue behind the wave's row loads.
+__device__ __forceinline__ int offset_at(const Seqs &q, int i) {
+    typedef const __attribute__((address_space(4))) int32_t constant_i32;
+    const int a = ((constant_i32 *)(uintptr_t)q.cu)[i];
     return a < 0 ? 0 : (a > q.total ? q.total : a);
+}
+// First token of sequence m and the one behind its last.
+__device__ __forceinline__ int seq_first(const Seqs &q, int m) {
+    return q.cu ? offset_at(q, m) : m * q.seq_len;
+}
+__device__ __forceinline__ int seq_end_token(const Seqs &q, int m) {
+    return q.cu ? offset_at(q, m + 1) : (m + 1) * q.seq_len;
 }
 
 // The sequence that holds token t (its tokens are [beg, end)): the last one
 // that begins at or before t.  Returns -1 where none holds it (t behind the
 // last offset, or malformed offsets).  q.num >= 1.
 __device__ __forceinline__ int seq_of_token(const Seqs &q, int t, int *beg, int *end) {
-    int m;
-    if (!q.cu) {
-        m = t / q.seq_len;
-    } else {
-        int lo = 0, hi = q.num - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (seq_first_token(q.cu, q.seq_len, q.total, mid) <= t)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        m = lo;
+    int lo = 0, hi = q.num - 1;
+    if (!q.cu) lo = hi = t / q.seq_len;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (offset_at(q, mid) <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
     }
-    *beg = (int)seq_first_token(q.cu, q.seq_len, q.total, m);
-    *end = seq_end_token(q, m);
-    return t >= *beg && t < *end ? m : -1;
+    *beg = seq_first(q, lo);
+    *end = seq_end_token(q, lo);
+    return t >= *beg && t < *end ? lo : -1;
 }
 
 // 1 / (1 + e^-z) in fp32 (exp2 and reciprocal to one step of their result; e^-z

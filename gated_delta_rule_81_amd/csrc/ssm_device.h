@@ -277,14 +277,14 @@ __device__ __forceinline__ Piece find_piece(const Seqs &q, int64_t number, int l
     if (!q.cu) lo = (int)(number / pieces_per_row(q, len));
     while (q.cu && lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (first_piece(q, len, seq_first_token(q.cu, q.seq_len, q.total, mid), mid) <= number)
+        if (first_piece(q, len, seq_first(q, mid), mid) <= number)
             lo = mid;
         else
             hi = mid - 1;
     }
     Piece p;
     p.seq = lo;
-    p.seq_beg = (int)seq_first_token(q.cu, q.seq_len, q.total, lo);
+    p.seq_beg = seq_first(q, lo);
     p.seq_end = seq_end_token(q, lo);
     if (p.seq_end < p.seq_beg) p.seq_end = p.seq_beg;  // malformed offsets
     const int64_t index = number - first_piece(q, len, p.seq_beg, lo);

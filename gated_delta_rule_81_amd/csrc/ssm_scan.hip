@@ -327,7 +327,7 @@ __device__ __forceinline__ void fold_body(const SsmScan &a, int values, int64_t 
     const int64_t u = block / per;
     const int h = (int)(u % a.heads), n = (int)(u / a.heads);
     const int64_t off = block % per * 1024 + threadIdx.x * 4;
-    const int beg = (int)seq_first_token(a.seqs.cu, a.seqs.seq_len, a.seqs.total, n);
+    const int beg = seq_first(a.seqs, n);
     const int end = seq_end_token(a.seqs, n);
     const int count = end > beg ? (int)(((int64_t)end - beg + a.piece - 1) / a.piece) : 1;
     if (count < 2) return;
