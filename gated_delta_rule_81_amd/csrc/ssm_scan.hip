@@ -29,29 +29,33 @@ enum Mode { kLocal, kOut, kStates };
 // REV walks the blocks from the last to the first and the tokens' weights from
 // the right: the gradient's recurrence E_{t-1} = e^{dt_t A} (E_t + x_t k_t^T).
 // LDS of one block's tiles.
-template <typename T, int P, int N, int MODE> struct ScanLds {
+template <typename T, int P, int N, int HEADS, int MODE> struct ScanLds {
     static constexpr int L = kSsmBlock<T>, NI = sizeof(T) == 2 ? 1 : 3;
     // Parts of y's fp32 operands, the block's weights M and the state: two for a
     // bf16 y (2^-15, nothing beside its own rounding), three for an fp32 one.
     static constexpr int KP = sizeof(T) == 2 ? 2 : 3;
     static constexpr bool OUT = MODE == kOut;
     typedef Tile<NI, L, N> TK;
-    typedef Tile<NI, L, P> TX;
-    typedef Tile<KP, L, L> TM;
+    typedef Tile<NI, L, HEADS * P> TX;
+    // Row tiles 0 and 1 have nothing right of column 32: of 64 rows, 1 lies beside 0.
+    static constexpr bool PACK = L == 64;
+    typedef Tile<KP, PACK ? 48 : L, L> TM;
+    __device__ static constexpr int m_row(int it) { return PACK && it > 0 ? it - 1 : it; }
+    __device__ static constexpr int m_step(int it) { return PACK && it == 1; }  // 32 columns each
     __attribute__((aligned(16))) bf16 k[TK::ELEMS];
     __attribute__((aligned(16))) bf16 c[OUT ? TK::ELEMS : 8];
     __attribute__((aligned(16))) bf16 x[TX::ELEMS];
-    __attribute__((aligned(16))) bf16 m[OUT ? TM::ELEMS : 8];
-    __attribute__((aligned(16))) double cum[2][L];  // log2 of the decay up to t
-    __attribute__((aligned(16))) float dt[2][L], w[2][L], in[2][L];
-    double tot[2];
+    __attribute__((aligned(16))) bf16 m[OUT ? HEADS * TM::ELEMS : 8];
+    __attribute__((aligned(16))) double cum[2][HEADS][L];  // log2 of the decay up to t
+    __attribute__((aligned(16))) float dt[2][HEADS][L], w[2][HEADS][L], in[2][HEADS][L];
+    double tot[2][HEADS];
 };
 
-template <typename T, int P, int N, int MODE, bool REV>
+template <typename T, int P, int N, int HEADS, int RT, int MODE, bool REV>
 __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
-                                          ScanLds<T, P, N, MODE> &lds) {
-    typedef ScanLds<T, P, N, MODE> S_;
-    constexpr int L = S_::L, NT = P * 4, NI = S_::NI, KM = S_::KP, KP = S_::KP;
+                                          ScanLds<T, P, N, HEADS, MODE> &lds) {
+    typedef ScanLds<T, P, N, HEADS, MODE> S_;
+    constexpr int L = S_::L, NT = HEADS * P * 4 / RT, NW = NT / 64, WPH = NW / HEADS, NI = S_::NI, KM = S_::KP, KP = S_::KP;
     constexpr bool OUT = S_::OUT;
     typedef typename S_::TK TK;
     typedef typename S_::TX TX;
@@ -61,8 +65,8 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     auto &s_dt = lds.dt, &s_w = lds.w, &s_in = lds.in;
     auto &s_tot = lds.tot;
 
-    const int h = (int)(unit % a.heads);
-    const int64_t number = unit / a.heads;
+    const int h0 = (int)(unit % (a.heads / HEADS)) * HEADS;
+    const int64_t number = unit / (a.heads / HEADS);
     const Piece pc = find_piece(a.seqs, number, a.piece);
     if (!pc.any) return;
     if (MODE == kLocal && (REV ? pc.first : pc.last)) return;  // nothing enters from it
@@ -73,39 +77,47 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     int kcol[N / 16];
 #pragma unroll
     for (int t = 0; t < N / 16; ++t) kcol[t] = cols_at<TK>(16 * t, lane);
-    const int xcol = cols_at<TX>(16 * wave, lane);
-    const int group = h / (a.heads / a.groups);
-    const T *x = static_cast<const T *>(a.x) + (int64_t)h * P;
+    // this wave's rows, counted over the workgroup's heads, and their head
+    const int row0 = 16 * RT * wave, mine = wave / WPH;
+    int xcol[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) xcol[rt] = cols_at<TX>(row0 + 16 * rt, lane);
+    const int group = h0 / (a.heads / a.groups);
+    const T *x = static_cast<const T *>(a.x) + (int64_t)h0 * P;
     const T *k = static_cast<const T *>(a.k) + (int64_t)group * N;
     const T *c = static_cast<const T *>(a.c) + (int64_t)group * N;
-    const double A = (double)a.A[h] * kLog2eD;
+    // the last waves, one for each head, form the decays (the first ones have a tile
+    // of M more)
+    const bool weigher = wave >= NW - HEADS;
+    const int wh = weigher ? wave - (NW - HEADS) : 0;
+    const double A = (double)a.A[h0 + wh] * kLog2eD;
     const int blocks = (pc.end - pc.beg + L - 1) / L;
 
-    // S^T tiles: rows n = 16 t + 4 g + e, column p = 16 wave + r.  kStates, which
+    // S^T tiles: rows n = 16 t + 4 g + e, column p = row0 + 16 rt + r.  kStates, which
     // forms no outputs, keeps S tiles (rows p, column n = 16 t + r) instead: its
     // states are stored [N][P], four rows p a lane.
-    f32x4 S[N / 16];
+    f32x4 S[RT][N / 16];
     constexpr bool TR = MODE == kStates;
-    const int64_t lane_off = TR ? (int64_t)(16 * wave + 4 * g) * N + r
-                                : (int64_t)(16 * wave + r) * N + 4 * g;
+    const int lane_off = TR ? (row0 + 4 * g) * N + r : (row0 + r) * N + 4 * g;
     const float *enter = nullptr;
     if (MODE != kLocal) {
         // Of a sequence in several pieces the fold has written every entering state,
         // the first too: final_state may be state0, and another workgroup writes it.
         enter = a.seg_states && !(pc.first && pc.last)
-                    ? a.seg_states + (number * a.heads + h) * (int64_t)(P * N)
-                    : (a.state0 ? a.state0 + ((int64_t)pc.seq * a.heads + h) * (P * N) : nullptr);
+                    ? a.seg_states + (number * a.heads + h0) * (int64_t)(P * N)
+                    : (a.state0 ? a.state0 + ((int64_t)pc.seq * a.heads + h0) * (P * N) : nullptr);
     }
 #pragma unroll
-    for (int t = 0; t < N / 16; ++t) {
-        const float *at = enter + lane_off + 16 * t;
-        S[t] = !enter ? zero4()
+    for (int i = 0; i < RT * (N / 16); ++i) {
+        const int rt = i / (N / 16), t = i % (N / 16);
+        const float *at = enter + lane_off + 16 * rt * N + 16 * t;
+        S[rt][t] = !enter ? zero4()
                : TR   ? f32x4{at[0], at[N], at[2 * N], at[3 * N]}
                       : *reinterpret_cast<const f32x4 *>(at);
     }
 
     Stage<T, L, N, NT> rk, rc;
-    Stage<T, L, P, NT> rx;
+    Stage<T, L, HEADS * P, NT> rx;
     float rdt = 0.f;
     auto first_token = [&](int i) { return pc.beg + (REV ? blocks - 1 - i : i) * L; };
     auto load_rows = [&](int i) {
@@ -116,23 +128,22 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     };
     auto load_dt = [&](int i) {  // lane = token; tokens past the end do nothing (dt = 0)
         const int t = first_token(i) + lane;
-        rdt = lane < L && t < pc.end ? a.dt[(int64_t)t * a.heads + h] : 0.f;
+        rdt = lane < L && t < pc.end ? a.dt[(int64_t)t * a.heads + h0 + wh] : 0.f;
     };
     double total = 0.0;
-    auto weights = [&](int buf) {  // by the last wave
+    auto weights = [&](int buf) {
         const double step = (double)rdt * A;
         const double cum = wave_prefix(step < -400.0 ? -400.0 : step, lane);
         const double all = from_lane(cum, 63);
         total += all;
         if (lane < L) {
-            s_cum[buf][lane] = cum;
-            s_dt[buf][lane] = rdt;
-            s_in[buf][lane] = fast_exp2((float)cum);
-            s_w[buf][lane] = REV ? fast_exp2((float)cum) : rdt * fast_exp2((float)(all - cum));
+            s_cum[buf][wh][lane] = cum;
+            s_dt[buf][wh][lane] = rdt;
+            s_in[buf][wh][lane] = fast_exp2((float)cum);
+            s_w[buf][wh][lane] = REV ? fast_exp2((float)cum) : rdt * fast_exp2((float)(all - cum));
         }
-        if (lane == 0) s_tot[buf] = all;
+        if (lane == 0) s_tot[buf][wh] = all;
     };
-    const bool weigher = wave == NT / 64 - 1;
     if (blocks > 0) {
         load_rows(0);
         if (weigher) {
@@ -141,7 +152,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         }
     }
     if constexpr (OUT) {  // tiles above the diagonal that a 32-wide step reads: zero for good
-        for (int i = tid; i < TM::ELEMS; i += NT) sm[i] = static_cast<bf16>(0.f);
+        for (int i = tid; i < HEADS * TM::ELEMS; i += NT) sm[i] = static_cast<bf16>(0.f);
     }
     for (int i = 0; i < blocks; ++i) {
         const int buf = i & 1, t0 = first_token(i);
@@ -155,13 +166,15 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         }
         if constexpr (MODE == kStates) {
             const int64_t block = first_piece(a.seqs, L, pc.seq_beg, pc.seq) + (t0 - pc.seq_beg) / L;
-            float *to = a.block_states + (block * a.heads + h) * (int64_t)(P * N) +
-                        (int64_t)r * P + 16 * wave + 4 * g;
+            float *to = a.block_states + (block * a.heads + h0 + mine) * (int64_t)(P * N) +
+                        (int64_t)r * P + row0 % P + 4 * g;
 #pragma unroll
-            for (int t = 0; t < N / 16; ++t)
-                *reinterpret_cast<f32x4 *>(to + (int64_t)16 * t * P) = S[t];
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int t = 0; t < N / 16; ++t)
+                    *reinterpret_cast<f32x4 *>(to + (int64_t)16 * t * P + 16 * rt) = S[rt][t];
         }
-        f32x4 y[L / 16];
+        f32x4 y[RT][L / 16];
         const int ln = here(lane), r = ln & 15, g = ln >> 4;
         if constexpr (OUT) {
             // M[t][s] = e^{cum_t - cum_s} (C_t . B_s) dt_s, s <= t, formed as tiles of M^T
@@ -170,152 +183,183 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
             for (int it = 0; it < L / 16; ++it)
 #pragma unroll
                 for (int is = 0; is <= it; ++is, ++q) {
-                    if (q % (NT / 64) != wave) continue;
+                    if (q % NW != wave) continue;
                     f32x4 m = zero4();
 #pragma unroll
                     for (int ks = 0; ks < N / 32; ++ks)
                         m = mma(read_wide<TK, NI>(sk, 16 * is, ks, kwide),
                                 read_wide<TK, NI>(sc, 16 * it, ks, kwide), m);
                     const int t = 16 * it + r, s = 16 * is + 4 * g;
-                    const double ct = s_cum[buf][t];
-                    float v[4];
+                    const int to = TM::at(16 * S_::m_row(it) + r, s + 32 * S_::m_step(it));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                    {
-                        const float z = (float)(ct - s_cum[buf][s + e]);  // 0 above the diagonal
-                        v[e] = m[e] * fast_exp2(s + e <= t ? z : -1e30f) * s_dt[buf][s + e];
-                    }
-#pragma unroll
-                    for (int part = 0; part < KM; ++part) {
-                        bf16x4 o;
+                    for (int hh = 0; hh < HEADS; ++hh) {
+                        const double ct = s_cum[buf][hh][t];
+                        float v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float f = part < KM - 1 ? top_bits(v[e]) : v[e];
-                            o[e] = static_cast<bf16>(f);
-                            v[e] -= f;
+                            const float z = (float)(ct - s_cum[buf][hh][s + e]);  // 0 above the diagonal
+                            v[e] = m[e] * fast_exp2(s + e <= t ? z : -1e30f) * s_dt[buf][hh][s + e];
                         }
-                        *reinterpret_cast<bf16x4 *>(sm + part * TM::PLANE + TM::at(t, s)) = o;
+#pragma unroll
+                        for (int part = 0; part < KM; ++part) {
+                            bf16x4 o;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float f = part < KM - 1 ? top_bits(v[e]) : v[e];
+                                o[e] = static_cast<bf16>(f);
+                                v[e] -= f;
+                            }
+                            *reinterpret_cast<bf16x4 *>(sm + hh * TM::ELEMS + part * TM::PLANE + to) = o;
+                        }
                     }
                 }
             // y^T = S C^T e^{cum}: rows p, columns t
 #pragma unroll
-            for (int it = 0; it < L / 16; ++it) y[it] = zero4();
+            for (int i = 0; i < RT * (L / 16); ++i) y[i % RT][i / RT] = zero4();
 #pragma unroll
             for (int ks = 0; ks < N / 32; ++ks) {
-                float f[8];
+                Parts<KP> sp[RT];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = S[2 * ks][e], f[4 + e] = S[2 * ks + 1][e];
-                const Parts<KP> sp = split<KP>(f);
+                for (int rt = 0; rt < RT; ++rt) {
+                    float f[8];
 #pragma unroll
-                for (int it = 0; it < L / 16; ++it)
-                    y[it] = mma(sp, read_rows<TK, NI>(sc, 16 * it, ks, krow), y[it]);
+                    for (int e = 0; e < 4; ++e) f[e] = S[rt][2 * ks][e], f[4 + e] = S[rt][2 * ks + 1][e];
+                    sp[rt] = split<KP>(f);
+                }
+#pragma unroll
+                for (int it = 0; it < L / 16; ++it) {
+                    const Parts<NI> ct = read_rows<TK, NI>(sc, 16 * it, ks, krow);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) y[rt][it] = mma(sp[rt], ct, y[rt][it]);
+                }
             }
 #pragma unroll
-            for (int it = 0; it < L / 16; ++it) y[it] *= s_in[buf][16 * it + r];
+            for (int it = 0; it < L / 16; ++it)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) y[rt][it] *= s_in[buf][mine][16 * it + r];
             // the next block's decays, by a wave that had a tile of M less to form
             if (weigher && i + 1 < blocks) weights(buf ^ 1);
             lds_barrier();
         }
         // x^T operands of this wave's rows p, and x^T weighted for the state
-        Parts<NI> xt[L / 32];
-        Parts<3> xw[L / 32];
+        Parts<NI> xt[RT][L / 32];
+        Parts<3> xw[RT][L / 32];
 #pragma unroll
         for (int ks = 0; ks < L / 32; ++ks) {
-            xt[ks] = read_cols<TX, NI>(sx, ks, xcol);
-            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&s_w[buf][32 * ks + 4 * g]);
-            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&s_w[buf][32 * ks + 16 + 4 * g]);
-            float f[8];
+            const f32x4 w0 = *reinterpret_cast<const f32x4 *>(&s_w[buf][mine][32 * ks + 4 * g]);
+            const f32x4 w1 = *reinterpret_cast<const f32x4 *>(&s_w[buf][mine][32 * ks + 16 + 4 * g]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float v = to_f32(xt[ks].v[0][e]);
-                if constexpr (NI == 3) v += to_f32(xt[ks].v[1][e]) + to_f32(xt[ks].v[2][e]);
-                f[e] = v * (e < 4 ? w0[e % 4] : w1[e % 4]);
+            for (int rt = 0; rt < RT; ++rt) {
+                const Parts<NI> &xv = xt[rt][ks] = read_cols<TX, NI>(sx, ks, xcol[rt]);
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float v = to_f32(xv.v[0][e]);
+                    if constexpr (NI == 3) v += to_f32(xv.v[1][e]) + to_f32(xv.v[2][e]);
+                    f[e] = v * (e < 4 ? w0[e % 4] : w1[e % 4]);
+                }
+                xw[rt][ks] = split<3>(f);
             }
-            xw[ks] = split<3>(f);
         }
         if constexpr (OUT) {
             const int n = pc.end - t0;
-            T *out = static_cast<T *>(a.out) + (int64_t)h * P + 16 * wave + 4 * g;
-            const float D = a.D ? a.D[h] : 0.f;
+            T *out = static_cast<T *>(a.out) + (int64_t)h0 * P + row0 + 4 * g;
+            const float D = a.D ? a.D[h0 + mine] : 0.f;
+            const bf16 *weights_of = sm + mine * TM::ELEMS;
 #pragma unroll
             for (int it = 0; it < L / 16; ++it) {
 #pragma unroll
-                for (int ks = 0; ks <= it / 2; ++ks)
-                    y[it] = mma(xt[ks], read_rows<TM, KM>(sm, 16 * it, ks, mrow), y[it]);
-                const int t = 16 * it + r;
-                if (a.D) {
-                    const bf16 *row = sx + TX::at(t, 16 * wave + 4 * g);
+                for (int ks = 0; ks <= it / 2; ++ks) {
+                    const Parts<KM> mt = read_rows<TM, KM>(weights_of, 16 * S_::m_row(it),
+                                                           ks + S_::m_step(it), mrow);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v = to_f32(row[e]);
-                        if constexpr (NI == 3)
-                            v += to_f32(row[TX::PLANE + e]) + to_f32(row[2 * TX::PLANE + e]);
-                        y[it][e] += D * v;
-                    }
+                    for (int rt = 0; rt < RT; ++rt) y[rt][it] = mma(xt[rt][ks], mt, y[rt][it]);
                 }
-                if (t < n)
-                    store4(out + (int64_t)(t0 + t) * a.out_stride, y[it][0], y[it][1], y[it][2],
-                           y[it][3]);
+                const int t = 16 * it + r;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    f32x4 &o = y[rt][it];
+                    if (a.D) {
+                        const bf16 *row = sx + TX::at(t, row0 + 16 * rt + 4 * g);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float v = to_f32(row[e]);
+                            if constexpr (NI == 3)
+                                v += to_f32(row[TX::PLANE + e]) + to_f32(row[2 * TX::PLANE + e]);
+                            o[e] += D * v;
+                        }
+                    }
+                    if (t < n)
+                        store4(out + (int64_t)(t0 + t) * a.out_stride + 16 * rt, o[0], o[1], o[2],
+                               o[3]);
+                }
             }
         }
-        const float decay = fast_exp2((float)s_tot[buf]);
+        const float decay = fast_exp2((float)s_tot[buf][mine]);
 #pragma unroll
         for (int t = 0; t < N / 16; ++t) {
-            S[t] *= decay;
 #pragma unroll
-            for (int ks = 0; ks < L / 32; ++ks)
-                S[t] = TR ? mma(xw[ks], read_cols<TK, NI>(sk, ks, kcol[t]), S[t])
-                          : mma(read_cols<TK, NI>(sk, ks, kcol[t]), xw[ks], S[t]);
+            for (int rt = 0; rt < RT; ++rt) S[rt][t] *= decay;
+#pragma unroll
+            for (int ks = 0; ks < L / 32; ++ks) {
+                const Parts<NI> kt = read_cols<TK, NI>(sk, ks, kcol[t]);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    S[rt][t] = TR ? mma(xw[rt][ks], kt, S[rt][t]) : mma(kt, xw[rt][ks], S[rt][t]);
+            }
         }
         if (!OUT && weigher && i + 1 < blocks) weights(buf ^ 1);
         lds_barrier();  // the tiles are read: the next block's may be written
     }
     float *to = nullptr;
     if (MODE == kLocal) {
-        to = a.seg_states + (number * a.heads + h) * (int64_t)(P * N);
-        if (weigher && lane == 0) a.seg_decay[number * a.heads + h] = total;
+        to = a.seg_states + (number * a.heads + h0) * (int64_t)(P * N);
+        if (weigher && lane == 0) a.seg_decay[number * a.heads + h0 + wh] = total;
     } else if (a.final_state && (REV ? pc.first : pc.last)) {
-        to = a.final_state + ((int64_t)pc.seq * a.heads + h) * (P * N);
+        to = a.final_state + ((int64_t)pc.seq * a.heads + h0) * (P * N);
     }
     if (to)
 #pragma unroll
-        for (int t = 0; t < N / 16; ++t) {
-            float *at = to + lane_off + 16 * t;
+        for (int i = 0; i < RT * (N / 16); ++i) {
+            const int rt = i / (N / 16), t = i % (N / 16);
+            float *at = to + lane_off + 16 * rt * N + 16 * t;
             if constexpr (TR)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) at[e * N] = S[t][e];
+                for (int e = 0; e < 4; ++e) at[e * N] = S[rt][t][e];
             else
-                *reinterpret_cast<f32x4 *>(at) = S[t];
+                *reinterpret_cast<f32x4 *>(at) = S[rt][t];
         }
 }
 
-template <typename T, int P, int N>
-__global__ __launch_bounds__(P * 4, 2) void ssm_out_kernel(SsmScan a) {
-    __shared__ ScanLds<T, P, N, kOut> lds;
-    const int64_t unit = xcd_unit(blockIdx.x, piece_count(a.seqs, a.piece), a.heads, a.groups);
-    if (unit >= 0) scan_body<T, P, N, kOut, false>(a, unit, lds);
+template <typename T, int P, int N, int HEADS, int RT>
+__global__ __launch_bounds__(HEADS * P * 4 / RT, 2) void ssm_out_kernel(SsmScan a) {
+    __shared__ ScanLds<T, P, N, HEADS, kOut> lds;
+    const int64_t unit =
+        xcd_unit(blockIdx.x, piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
+    if (unit >= 0) scan_body<T, P, N, HEADS, RT, kOut, false>(a, unit, lds);
 }
 
-template <typename T, int P, int N>
-__global__ __launch_bounds__(P * 4, 2) void ssm_local_kernel(SsmScan a) {
-    __shared__ ScanLds<T, P, N, kLocal> lds;
-    const int64_t unit = xcd_unit(blockIdx.x, piece_count(a.seqs, a.piece), a.heads, a.groups);
-    if (unit >= 0) scan_body<T, P, N, kLocal, false>(a, unit, lds);
+template <typename T, int P, int N, int HEADS, int RT>
+__global__ __launch_bounds__(HEADS * P * 4 / RT, 2) void ssm_local_kernel(SsmScan a) {
+    __shared__ ScanLds<T, P, N, HEADS, kLocal> lds;
+    const int64_t unit =
+        xcd_unit(blockIdx.x, piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
+    if (unit >= 0) scan_body<T, P, N, HEADS, RT, kLocal, false>(a, unit, lds);
 }
 
 // Both directions of the backward's walk in one launch (half the workgroups
 // each): neither alone has enough workgroups to hide its own latencies.
-template <typename T, int P, int N, int MODE>
-__global__ __launch_bounds__(P * 4, 2) void ssm_both_kernel(SsmScan a, SsmScan b) {
-    __shared__ ScanLds<T, P, N, MODE> lds;
+template <typename T, int P, int N, int HEADS, int RT, int MODE>
+__global__ __launch_bounds__(HEADS * P * 4 / RT, 2) void ssm_both_kernel(SsmScan a, SsmScan b) {
+    __shared__ ScanLds<T, P, N, HEADS, MODE> lds;
     const bool rev = blockIdx.x >= gridDim.x / 2;
     const int64_t unit = xcd_unit(rev ? blockIdx.x - gridDim.x / 2 : blockIdx.x,
-                                  piece_count(a.seqs, a.piece), a.heads, a.groups);
+                                  piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
     if (unit < 0) return;
     if (!rev)
-        scan_body<T, P, N, MODE, false>(a, unit, lds);
+        scan_body<T, P, N, HEADS, RT, MODE, false>(a, unit, lds);
     else
-        scan_body<T, P, N, MODE, true>(b, unit, lds);
+        scan_body<T, P, N, HEADS, RT, MODE, true>(b, unit, lds);
 }
 
 // The pieces' own final states turned in place into entering states:
@@ -374,30 +418,31 @@ __global__ __launch_bounds__(256) void ssm_fold_both_kernel(SsmScan a, SsmScan b
         fold_body<true>(b, values, blockIdx.x - blocks);
 }
 
-template <typename T, int P, int N> struct Scan {
+template <typename T, int P, int N, int HEADS, int RT> struct Scan {
+    static constexpr int NT = HEADS * P * 4 / RT;
     static int out(const SsmScan &a, hipStream_t stream) {
-        const unsigned blocks = xcd_blocks(piece_count(a.seqs, a.piece), a.heads, a.groups);
+        const unsigned blocks = xcd_blocks(piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
         if (a.seg_states) {
-            hipLaunchKernelGGL((ssm_local_kernel<T, P, N>), dim3(blocks), dim3(P * 4), 0,
+            hipLaunchKernelGGL((ssm_local_kernel<T, P, N, HEADS, RT>), dim3(blocks), dim3(NT), 0,
                                stream, a);
             hipLaunchKernelGGL(ssm_fold_kernel, dim3((unsigned)folds(a)), dim3(256), 0, stream, a,
                                P * N);
         }
-        hipLaunchKernelGGL((ssm_out_kernel<T, P, N>), dim3(blocks), dim3(P * 4), 0,
-                           stream, a);
+        hipLaunchKernelGGL((ssm_out_kernel<T, P, N, HEADS, RT>), dim3(blocks), dim3(NT), 0, stream,
+                           a);
         return hipGetLastError() == hipSuccess ? 0 : -1;
     }
     static int both(const SsmScan &a, const SsmScan &b, hipStream_t stream) {
-        const unsigned blocks = xcd_blocks(piece_count(a.seqs, a.piece), a.heads, a.groups);
+        const unsigned blocks = xcd_blocks(piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
         if (a.seg_states) {
-            hipLaunchKernelGGL((ssm_both_kernel<T, P, N, kLocal>), dim3(2 * blocks),
-                               dim3(P * 4), 0, stream, a, b);
+            hipLaunchKernelGGL((ssm_both_kernel<T, P, N, HEADS, RT, kLocal>), dim3(2 * blocks),
+                               dim3(NT), 0, stream, a, b);
             const unsigned f = (unsigned)folds(a);
             hipLaunchKernelGGL(ssm_fold_both_kernel, dim3(2 * f), dim3(256), 0, stream, a, b, P * N,
                                f);
         }
-        hipLaunchKernelGGL((ssm_both_kernel<T, P, N, kStates>), dim3(2 * blocks),
-                           dim3(P * 4), 0, stream, a, b);
+        hipLaunchKernelGGL((ssm_both_kernel<T, P, N, HEADS, RT, kStates>), dim3(2 * blocks),
+                           dim3(NT), 0, stream, a, b);
         return hipGetLastError() == hipSuccess ? 0 : -1;
     }
     static int64_t folds(const SsmScan &a) {
@@ -405,13 +450,21 @@ template <typename T, int P, int N> struct Scan {
     }
 };
 
+#ifndef VAR
+#define VAR 1
+#endif
+template <typename T, int P, typename F> int by_state(const SsmScan &a, F f) {
+    if constexpr (sizeof(T) == 2) {
+        constexpr int HEADS = 128 / P;
+        const bool pairs = a.heads / a.groups % HEADS == 0 && VAR;
+        if (pairs)
+            return a.n == 64 ? f(Scan<T, P, 64, HEADS, 2>()) : f(Scan<T, P, 128, HEADS, 2>());
+    }
+    return a.n == 64 ? f(Scan<T, P, 64, 1, 1>()) : f(Scan<T, P, 128, 1, 1>());
+}
 template <typename F> int by_dims(const SsmScan &a, int dtype, F f) {
-    const bool p = a.p == 64, n = a.n == 64;
-    if (dtype == kDtypeBf16)
-        return p ? (n ? f(Scan<bf16, 64, 64>()) : f(Scan<bf16, 64, 128>()))
-                 : (n ? f(Scan<bf16, 128, 64>()) : f(Scan<bf16, 128, 128>()));
-    return p ? (n ? f(Scan<float, 64, 64>()) : f(Scan<float, 64, 128>()))
-             : (n ? f(Scan<float, 128, 64>()) : f(Scan<float, 128, 128>()));
+    if (dtype == kDtypeBf16) return a.p == 64 ? by_state<bf16, 64>(a, f) : by_state<bf16, 128>(a, f);
+    return a.p == 64 ? by_state<float, 64>(a, f) : by_state<float, 128>(a, f);
 }
 
 }  // namespace
