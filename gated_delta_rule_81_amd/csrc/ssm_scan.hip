@@ -48,6 +48,12 @@ template <typename T, int P, int N, int HEADS, int MODE> struct ScanLds {
     __attribute__((aligned(16))) bf16 m[OUT ? HEADS * TM::ELEMS : 8];
     __attribute__((aligned(16))) double cum[2][HEADS][L];  // log2 of the decay up to t
     __attribute__((aligned(16))) float dt[2][HEADS][L], w[2][HEADS][L], in[2][HEADS][L];
+    // Weights of M's tiles below the diagonal as products, from the last token before
+    // the tile's rows: row[t] = e^{cum_t - cum_ref}, col[at(it) + s] = dt_s e^{cum_ref - cum_s}.
+    static constexpr int TL = L / 16;
+    __device__ static constexpr int col_at(int it) { return 8 * it * (it - 1); }
+    __attribute__((aligned(16))) float row[OUT ? 2 : 1][HEADS][OUT ? L : 1];
+    __attribute__((aligned(16))) float col[OUT ? 2 : 1][HEADS][OUT ? col_at(TL) : 4];
     double tot[2][HEADS];
 };
 
@@ -130,6 +136,9 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         const int t = first_token(i) + lane;
         rdt = lane < L && t < pc.end ? a.dt[(int64_t)t * a.heads + h0 + wh] : 0.f;
     };
+    float D[HEADS];
+#pragma unroll
+    for (int hh = 0; hh < HEADS; ++hh) D[hh] = OUT && a.D ? a.D[h0 + hh] : 0.f;
     double total = 0.0;
     auto weights = [&](int buf) {
         const double step = (double)rdt * A;
@@ -141,6 +150,16 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
             s_dt[buf][wh][lane] = rdt;
             s_in[buf][wh][lane] = fast_exp2((float)cum);
             s_w[buf][wh][lane] = REV ? fast_exp2((float)cum) : rdt * fast_exp2((float)(all - cum));
+        }
+        if constexpr (OUT) {
+            double ref = 0.0;
+#pragma unroll
+            for (int it = 1; it < S_::TL; ++it) {
+                const double before = from_lane(cum, 16 * it - 1);
+                if (lane >= 16 * it) ref = before;
+                else lds.col[buf][wh][S_::col_at(it) + lane] = rdt * fast_exp2((float)(before - cum));
+            }
+            if (lane < L) lds.row[buf][wh][lane] = fast_exp2((float)(cum - ref));
         }
         if (lane == 0) s_tot[buf][wh] = all;
     };
@@ -193,12 +212,21 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                     const int to = TM::at(16 * S_::m_row(it) + r, s + 32 * S_::m_step(it));
 #pragma unroll
                     for (int hh = 0; hh < HEADS; ++hh) {
-                        const double ct = s_cum[buf][hh][t];
                         float v[4];
+                        if (is < it) {
+                            const float row = lds.row[buf][hh][t];
+                            const f32x4 col =
+                                *reinterpret_cast<const f32x4 *>(&lds.col[buf][hh][S_::col_at(it) + s]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float z = (float)(ct - s_cum[buf][hh][s + e]);  // 0 above the diagonal
-                            v[e] = m[e] * fast_exp2(s + e <= t ? z : -1e30f) * s_dt[buf][hh][s + e];
+                            for (int e = 0; e < 4; ++e) v[e] = m[e] * row * col[e];
+                        } else {  // 0 above the diagonal, D's term on it
+                            const double ct = s_cum[buf][hh][t];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float z = (float)(ct - s_cum[buf][hh][s + e]);
+                                v[e] = m[e] * fast_exp2(s + e <= t ? z : -1e30f) * s_dt[buf][hh][s + e] +
+                                       (s + e == t ? D[hh] : 0.f);
+                            }
                         }
 #pragma unroll
                         for (int part = 0; part < KM; ++part) {
@@ -264,7 +292,6 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         if constexpr (OUT) {
             const int n = pc.end - t0;
             T *out = static_cast<T *>(a.out) + (int64_t)h0 * P + row0 + 4 * g;
-            const float D = a.D ? a.D[h0 + mine] : 0.f;
             const bf16 *weights_of = sm + mine * TM::ELEMS;
 #pragma unroll
             for (int it = 0; it < L / 16; ++it) {
@@ -279,16 +306,6 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     f32x4 &o = y[rt][it];
-                    if (a.D) {
-                        const bf16 *row = sx + TX::at(t, row0 + 16 * rt + 4 * g);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float v = to_f32(row[e]);
-                            if constexpr (NI == 3)
-                                v += to_f32(row[TX::PLANE + e]) + to_f32(row[2 * TX::PLANE + e]);
-                            o[e] += D * v;
-                        }
-                    }
                     if (t < n)
                         store4(out + (int64_t)(t0 + t) * a.out_stride + 16 * rt, o[0], o[1], o[2],
                                o[3]);
