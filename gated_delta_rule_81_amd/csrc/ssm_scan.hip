@@ -125,7 +125,11 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     Stage<T, L, N, NT> rk, rc;
     Stage<T, L, HEADS * P, NT> rx;
     float rdt = 0.f;
-    auto first_token = [&](int i) { return pc.beg + (REV ? blocks - 1 - i : i) * L; };
+    // kLocal walks against the recurrence: a token's weight in the state behind the
+    // piece is known from the blocks before it in that order, and the sums need no
+    // decay from block to block.
+    constexpr bool FROM_END = REV != (MODE == kLocal);
+    auto first_token = [&](int i) { return pc.beg + (FROM_END ? blocks - 1 - i : i) * L; };
     auto load_rows = [&](int i) {
         const int t0 = first_token(i), n = pc.end - t0 < L ? pc.end - t0 : L;
         rk.load(k + t0 * a.k_stride, a.k_stride, n, tid);
@@ -143,13 +147,14 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     auto weights = [&](int buf) {
         const double step = (double)rdt * A;
         const double cum = wave_prefix(step < -400.0 ? -400.0 : step, lane);
-        const double all = from_lane(cum, 63);
+        const double all = from_lane(cum, 63), behind = MODE == kLocal ? total : 0.0;
         total += all;
         if (lane < L) {
             s_cum[buf][wh][lane] = cum;
             s_dt[buf][wh][lane] = rdt;
             s_in[buf][wh][lane] = fast_exp2((float)cum);
-            s_w[buf][wh][lane] = REV ? fast_exp2((float)cum) : rdt * fast_exp2((float)(all - cum));
+            s_w[buf][wh][lane] = REV ? fast_exp2((float)(behind + cum))
+                                     : rdt * fast_exp2((float)(behind + (all - cum)));
         }
         if constexpr (OUT) {
             double ref = 0.0;
@@ -316,7 +321,8 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
 #pragma unroll
         for (int t = 0; t < N / 16; ++t) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) S[rt][t] *= decay;
+            for (int rt = 0; rt < RT; ++rt)
+                if (MODE != kLocal) S[rt][t] *= decay;
 #pragma unroll
             for (int ks = 0; ks < L / 32; ++ks) {
                 const Parts<NI> kt = read_cols<TK, NI>(sk, ks, kcol[t]);
