@@ -395,15 +395,18 @@ struct PiecePlan {
     bool split;
     int32_t len;
 };
-PiecePlan piece_plan(const kda::Seqs &s, int32_t heads) {
-    // 1024 workgroups fill the chip (512: 3% slower on a 32K x 64-head prompt,
-    // 2048: 2%), and equal rows that come to half of that are left whole.
-    const int64_t want = 1024;
-    const bool enough = !s.cu && (int64_t)s.num * heads >= want / 2;
+PiecePlan piece_plan(const kda::Seqs &s, int32_t heads, int32_t p, int directions) {
+    // 512 workgroups of 128 state rows, two a CU, in one round (both directions of
+    // the backward are one launch).  32K x 64 heads of 64 rows 384 us, with 256
+    // workgroups 477, with 1024 409; of 128 rows 690, with 1024 723.  8K backward 549
+    // us, with 256 613, with 1024 567.  Equal rows that come to half of that are
+    // left whole.
+    const int64_t want = 512 / directions, units = ((int64_t)heads * p + 127) / 128;
+    const bool enough = !s.cu && s.num * units >= want / 2;
     // Down to one block of 64 tokens (1,227 tokens x 8 heads fp32: 30 us, against
     // 47 us with 256), but at most 64 pieces a sequence: the fold walks them.
     const int64_t longest = s.cu ? s.total : s.seq_len;
-    int64_t len = ((int64_t)s.total * heads + want - 1) / want;
+    int64_t len = (s.total * units + want - 1) / want;
     if (len < longest / 64) len = longest / 64;
     len = (len + 63) / 64 * 64;
     if (len < 64) len = 64;
@@ -418,8 +421,8 @@ struct SsmSpace {
     int64_t states, decay;  // floats of the piece states, doubles of their decays
     int64_t bytes() const { return 8 * ((decay + 1) / 2 * 2) + 4 * states; }
 };
-SsmSpace ssm_space(const kda::Seqs &s, int32_t heads, int32_t p, int32_t n) {
-    const PiecePlan plan = piece_plan(s, heads);
+SsmSpace ssm_space(const kda::Seqs &s, int32_t heads, int32_t p, int32_t n, int directions = 1) {
+    const PiecePlan plan = piece_plan(s, heads, p, directions);
     if (!plan.split || s.num == 0) return {0, 0};
     const int64_t count = kda::piece_count(s, plan.len) * heads;
     return {count * p * n, count};
@@ -493,7 +496,7 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
     a.x = x, a.k = B, a.c = C, a.dt = dt, a.A = A, a.D = D, a.state0 = initial_state;
     a.out = out, a.final_state = final_state, a.seqs = seqs;
     a.heads = num_heads, a.groups = num_groups, a.p = head_dim, a.n = state_dim;
-    a.piece = piece_plan(seqs, num_heads).len;
+    a.piece = piece_plan(seqs, num_heads, head_dim, 1).len;
     a.x_stride = x_stride, a.k_stride = b_stride, a.c_stride = c_stride;
     a.out_stride = out_stride;
     if (space.states > 0) {
@@ -520,7 +523,7 @@ SsmBwdSpace ssm_bwd_space(const kda::Seqs &s, int32_t heads, int32_t groups, int
                           int32_t dtype) {
     SsmBwdSpace w = {};
     if (s.num == 0 || heads == 0) return w;
-    w.pieces = ssm_space(s, heads, p, n);
+    w.pieces = ssm_space(s, heads, p, n, 2);
     const int64_t block = dtype == kda::kDtypeBf16 ? 64 : 32;
     w.blocks = kda::piece_count(s, block);
     w.states = w.blocks * heads * p * n;
@@ -620,7 +623,7 @@ int kda_ssm_chunk_bwd(const void *x, const float *dt, const float *A, const void
         kda::SsmScan a = {};
         a.x = x, a.k = B, a.dt = dt, a.A = A, a.state0 = initial_state;
         a.seqs = seqs, a.heads = num_heads, a.groups = num_groups;
-        a.p = head_dim, a.n = state_dim, a.piece = piece_plan(seqs, num_heads).len;
+        a.p = head_dim, a.n = state_dim, a.piece = piece_plan(seqs, num_heads, head_dim, 2).len;
         a.x_stride = x_stride, a.k_stride = b_stride;
         kda::SsmScan b = a;  // from the right
         b.x = d_out, b.k = C, b.x_stride = d_out_stride, b.k_stride = c_stride;

@@ -473,17 +473,19 @@ template <typename T, int P, int N, int HEADS, int RT> struct Scan {
     }
 };
 
-#ifndef VAR
-#define VAR 1
-#endif
+// bf16: 128 rows a workgroup and 32 a wave, two heads of 64 that share B and C
+// together.  32K x 64 heads of 64 x 128: 384 us, with one head a workgroup and 16
+// rows a wave 452; heads of 128 rows 723 and 814; 1,227 tokens x 8 heads of 64 x 64,
+// where the launches count, 28 and 29.  An odd number of heads a group leaves one
+// head a workgroup; fp32 has no LDS for two (three parts of every tile).
 template <typename T, int P, typename F> int by_state(const SsmScan &a, F f) {
     if constexpr (sizeof(T) == 2) {
         constexpr int HEADS = 128 / P;
-        const bool pairs = a.heads / a.groups % HEADS == 0 && VAR;
-        if (pairs)
+        if (a.heads / a.groups % HEADS == 0)
             return a.n == 64 ? f(Scan<T, P, 64, HEADS, 2>()) : f(Scan<T, P, 128, HEADS, 2>());
     }
-    return a.n == 64 ? f(Scan<T, P, 64, 1, 1>()) : f(Scan<T, P, 128, 1, 1>());
+    if constexpr (sizeof(T) == 2 && P == 128) return -1;  // HEADS = 1 divides any number
+    else return a.n == 64 ? f(Scan<T, P, 64, 1, 1>()) : f(Scan<T, P, 128, 1, 1>());
 }
 template <typename F> int by_dims(const SsmScan &a, int dtype, F f) {
     if (dtype == kDtypeBf16) return a.p == 64 ? by_state<bf16, 64>(a, f) : by_state<bf16, 128>(a, f);
