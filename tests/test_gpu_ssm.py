@@ -39,6 +39,10 @@ CASES = [  # batch, seq_len, lens, H, G, P, N, state, skip, pad, dtype, decay
     (2, 513, None, 1, 1, 128, 128, False, True, 0, "f32", 1.0),
     (1, 0, [300, 0, 257, 2, 511, 256, 0], 2, 2, 64, 128, True, True, 0, "bf16", 1.0),
     (1, 0, [700, 1, 300], 1, 1, 64, 64, True, False, 0, "f32", 0.1),
+    # heads of 64 rows, two a workgroup: three pairs a group, and no pairs in a group of three
+    (1, 0, [130, 0, 1, 260, 15], 12, 2, 64, 128, True, True, 8, "bf16", 1.0),
+    (1, 300, None, 6, 2, 64, 64, True, True, 0, "bf16", 8.0),
+    (1, 449, None, 3, 1, 128, 128, True, False, 0, "bf16", 0.1),
 ]
 
 
@@ -257,7 +261,7 @@ def test_prompt_then_tokens(dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("case", [CASES[9], CASES[11], CASES[3]], ids=str)
+@pytest.mark.parametrize("case", [CASES[9], CASES[11], CASES[3], CASES[13], CASES[14]], ids=str)
 def test_state_updated_in_place(case):
     """final_state = initial_state, in one piece and in several (whose first and
     last workgroups both use the state): the bits of the call with two buffers."""
