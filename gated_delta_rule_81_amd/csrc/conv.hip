@@ -10,6 +10,13 @@
 // and writes whole 1 KiB pieces of a row, and the only rows read twice are the
 // W - 1 before each run.  Sequence boundaries inside a run are a wave-uniform
 // branch per token that reloads the window from the next sequence's state.
+//
+// Measured, bf16: 32K x 12288 channels (1.6 GB) 334 us, 4.8 TB/s; backward of 2 x
+// 4096 x 4096 (0.2 GB) 54 us with the sum of its parts (4), 3.7 TB/s; a token of 256
+// sessions (0.15 GB) 28 to 33 us, 4.6 to 5.4 TB/s.  Few tokens (3,923 x 2184 channels
+// in 7 sequences, 34 MB: 15 to 17 us) are one round of waves and hardly more than
+// the call: there runs of 4, 8 or 16 tokens and 2, 4 or 8 rows loaded together
+// measure 16.7 to 19.3 us.
 #include "layer_device.h"
 
 namespace kda {
@@ -81,7 +88,7 @@ template <typename T, int VEC, int W>
 __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs a, int cblocks,
                                                                int run_blocks, int run) {
     typedef Row<T, VEC> R;
-    constexpr int U = 2;  // rows loaded together, the next ones' loads ahead (4: 3% slower, 8: 6%)
+    constexpr int U = 2;  // rows loaded together, the next ones' loads ahead (32K: 334 us, with 8 346)
     const T *x = static_cast<const T *>(a.x), *state0 = static_cast<const T *>(a.state0);
     const int C = a.channels, wave = wave_of_block();
     const int c = ((int)(blockIdx.x % cblocks) * 64 + (int)threadIdx.x) * VEC;

@@ -18,10 +18,19 @@
 // right, E of every block, both fp32 and transposed ([N][P]).  Then one
 // workgroup per (block, group, set of heads) loops over its heads with dB and dC
 // in registers: 8 waves, each the owner of 16 columns n of dB and dC and of a
-// 16-token s-tile of du, where G, dP, M and Q never leave registers except Q
-// (to dB's and dC's waves) and E (read by columns n, needed by rows too), as
-// bf16 parts in LDS.  A head of 128 rows is two of 64 that share dt and A: every
-// sum above is linear in the rows.
+// 16-token s-tile of du.  dP and M stay in its registers; in LDS lie G (fp32, the
+// same for all heads of the group), and, as bf16 parts, Q (for dB's and dC's
+// waves) and E (read by columns n, needed by rows too).  A head of 128 rows is
+// two of 64 that share dt and A: every sum above is linear in the rows.
+//
+// 2 x 4096 tokens x 64 heads of 64 x 128 bf16, 0.29 GB of inputs and gradients:
+// 534 us = pieces 65, fold 17, states 168 (writes 0.54 GB of block states and
+// reads the inputs twice: 4.4 TB/s), gradients 330, dA and dD 4.5.  HBM bounds the
+// states pass.  In the gradient kernel VALU issues in 45% of the cycles, LDS works
+// in 27% and the matrix unit in 15%; its waves wait half of their time, at two
+// barriers a head and for LDS, with one workgroup of 8 waves a CU, the most that
+// 137 KB of LDS and 230 registers leave.  Fewer VALU instructions do not help it
+// (weights below the diagonal as products, as the scan has them: 538 us).
 #include "ssm_device.h"
 
 namespace kda {
@@ -219,6 +228,14 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
         }
     };
 
+    // The waves with more tiles below their s-tile issue first: the barriers wait for
+    // them (539 us without, 534 with).
+    if (is == 0)
+        __builtin_amdgcn_s_setprio(3);
+    else if (is == 1)
+        __builtin_amdgcn_s_setprio(2);
+    else if (is == 2)
+        __builtin_amdgcn_s_setprio(1);
     for (int i = 0; i < count; ++i) {
         const int buf = i % 3, par = i & 1, h = h0 + i / halves;
         const bool more = i + 1 < count;
@@ -265,6 +282,8 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
             }
             const float ks = rows4_sum(row16_total(kdot));
             if (tg == 0 && lane == 0) s_k[par][nt] = ks;
+            // E's loads here and S0's after the pairs: both there 547 us, both here 566
+            if (more) load_state(a.e_states, i + 1, ev);
         }
         {   // this wave's s-tile: dP, M, Q, the pairs, and du
             const int s = 16 * is + r;
@@ -329,8 +348,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
             }
             diag = rows4_sum(row16_total(diag));
             if (pg == 0 && lane == 0) s_d[par][is] = diag;
-            if (more) {  // in flight through du and phase B
-                load_state(a.e_states, i + 1, ev);
+            if (more) {
                 load_state(a.s_states, i + 1, sv);
                 if (weigher) weights((i + 1) % 3);
             }

@@ -12,13 +12,23 @@
 // leaves nothing of any fp32 value): its differences are then exact to 2^-37
 // whatever lies before them, so any dt A <= 0 is accepted.
 //
-// One workgroup walks the blocks of one (piece, head); wave w keeps the 16 state
-// rows p = 16 w .. as fp32 accumulators of S^T tiles (N / 16 of them), which are
-// the next block's operand as they stand.  A long sequence is cut into pieces
-// that run at once: a first pass leaves each piece's own final state, a fold
-// turns these into entering states (the transition of a piece is one number per
-// head), and the second pass is the scan proper.  The first pass reads x and B
-// once more and does 4 P N of the second's 4 P N + 2 L (P + N) operations a token.
+// One workgroup walks the blocks of a piece for 128 state rows (fp32: one head);
+// a wave keeps 32 of them (fp32: 16) as fp32 accumulators of S^T tiles, which are
+// the next block's operand as they stand.  D x is a term on the diagonal of the
+// block's weights.  A long sequence is cut into pieces that run at once: a first
+// pass leaves each piece's own final state, a fold turns these into entering
+// states (the transition of a piece is one number per head), and the second pass
+// is the scan proper.  The first pass reads x and B once more and does 4 P N of
+// the second's 4 P N + 2 L (P + N) operations a token.
+//
+// Bound by issue, not by HBM: fp32 operands enter the matrix unit as two or three
+// bf16 parts, so a token costs 2 to 3 times the products above, and the parts
+// (3 VALU instructions a value for two, 7 for three) and decays take as many
+// cycles again.  32K tokens x 64 heads of 64 x 128 bf16, 0.68 GB: 384 us = pieces
+// 118, fold 14 (67 MB, 4.8 TB/s), scan 290; the scan's SIMDs issue VALU half and
+// the matrix unit works a third of the time, LDS a third.  Wave rows: a 32-row
+// wave reads every row of B, C and M from LDS once for two tiles of products
+// (16 rows: 452 us).
 #include "ssm_device.h"
 
 namespace kda {
