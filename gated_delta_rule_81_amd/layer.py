@@ -108,8 +108,13 @@ def _out(t, shape, dtype, device):
     return torch.empty(shape, dtype=dtype, device=device) if t is None else t
 
 
-def _like(t, x):
-    return torch.empty_like(x, memory_format=torch.contiguous_format) if t is None else t
+def _out_rows(t, name, like, device, lead: int):
+    """An output with ``like``'s dtype and shape, new if ``t`` is None, and the
+    distance between its tokens."""
+    if t is None:
+        return (torch.empty_like(like, memory_format=torch.contiguous_format),
+                like.shape[lead:].numel())
+    return t, _rows(t, name, like.dtype, like.shape, device, lead)
 
 
 # ---------------------------------------------------------------- short convolution
@@ -149,8 +154,7 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     N = _num_seqs(cu_seqlens, B, dev)
     state = (N, W - 1, C)
     _expect(initial_state, "initial_state", x.dtype, state, dev)
-    out = _like(out, x)
-    os = _rows(out, "out", x.dtype, x.shape, dev, 2)
+    out, os = _out_rows(out, "out", x, dev, 2)
     if final_state is None and output_final_state:
         final_state = torch.empty(state, dtype=x.dtype, device=dev)
     _expect(final_state, "final_state", x.dtype, state, dev)
@@ -193,8 +197,7 @@ def short_conv_bwd(x: torch.Tensor, weight: torch.Tensor, d_out: torch.Tensor,
     _expect(initial_state, "initial_state", x.dtype, state, dev)
     _expect(d_final_state, "d_final_state", x.dtype, state, dev)
     g = dict(grads or {})
-    g["dx"] = _like(g.get("dx"), x)
-    dxs = _rows(g["dx"], "dx", x.dtype, x.shape, dev, 2)
+    g["dx"], dxs = _out_rows(g.get("dx"), "dx", x, dev, 2)
     g["dweight"] = _out(g.get("dweight"), (C, W), torch.float32, dev)
     _expect(g["dweight"], "dweight", torch.float32, (C, W), dev)
     g["dbias"] = None if bias is None else _out(g.get("dbias"), (C,), torch.float32, dev)
@@ -226,8 +229,7 @@ def short_conv_step(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor,
     if state is None:
         raise TypeError("state must be a tensor")
     _expect(state, "state", x.dtype, (B, W - 1, C), dev)
-    out = _like(out, x)
-    os = _rows(out, "out", x.dtype, x.shape, dev, 1)
+    out, os = _out_rows(out, "out", x, dev, 1)
     _call("kda_short_conv_step", dev, _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(out),
           B, C, W, xs, os, act, dt)
     return out
@@ -280,10 +282,8 @@ def qk_norm(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] =
     dt = _dtype(q, "q")
     n, hq, hk, d, rot, rows, (qs, ks), lead = _qk_common(q, k, q_weight, k_weight, table,
                                                          positions, kind)
-    out_q = _like(out_q, q)
-    out_k = _like(out_k, k)
-    oqs = _rows(out_q, "out_q", q.dtype, q.shape, q.device, lead)
-    oks = _rows(out_k, "out_k", q.dtype, k.shape, q.device, lead)
+    out_q, oqs = _out_rows(out_q, "out_q", q, q.device, lead)
+    out_k, oks = _out_rows(out_k, "out_k", k, q.device, lead)
     _call("kda_qk_norm_fwd", q.device, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
           _ptr(table), _ptr(positions), _ptr(out_q), _ptr(out_k), n, hq, hk, d, rot, rows, qs, ks,
           oqs, oks, eps, _NORMS[kind], int(bool(interleaved)), dt)
@@ -314,10 +314,8 @@ def qk_norm_bwd(q: torch.Tensor, k: torch.Tensor, d_out_q: torch.Tensor, d_out_k
     gqs = _rows(d_out_q, "d_out_q", q.dtype, q.shape, dev, lead)
     gks = _rows(d_out_k, "d_out_k", q.dtype, k.shape, dev, lead)
     g = dict(grads or {})
-    for name, like in (("dq", q), ("dk", k)):
-        g[name] = _like(g.get(name), like)
-    dqs = _rows(g["dq"], "dq", q.dtype, q.shape, dev, lead)
-    dks = _rows(g["dk"], "dk", q.dtype, k.shape, dev, lead)
+    g["dq"], dqs = _out_rows(g.get("dq"), "dq", q, dev, lead)
+    g["dk"], dks = _out_rows(g.get("dk"), "dk", k, dev, lead)
     for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
         g[name] = None if w is None else _out(g.get(name), (d,), torch.float32, dev)
         _expect(g[name], name, torch.float32, (d,), dev)
@@ -388,8 +386,7 @@ def ssm_chunk_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.T
     n = _num_seqs(cu_seqlens, b, dev)
     state = (n, H, P, N)
     _expect(initial_state, "initial_state", torch.float32, state, dev)
-    out = _like(out, x)
-    os = _rows(out, "out", x.dtype, x.shape, dev, 2)
+    out, os = _out_rows(out, "out", x, dev, 2)
     if final_state is None and output_final_state:
         final_state = torch.empty(state, dtype=torch.float32, device=dev)
     _expect(final_state, "final_state", torch.float32, state, dev)
@@ -441,8 +438,8 @@ def ssm_chunk_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.T
     g = dict(grads or {})
     rows = []
     for name, like in (("dx", x), ("dB", B), ("dC", C)):
-        g[name] = _like(g.get(name), like)
-        rows.append(_rows(g[name], name, x.dtype, like.shape, dev, 2))
+        g[name], row = _out_rows(g.get(name), name, like, dev, 2)
+        rows.append(row)
     for name, shape in (("ddt", (b, T, H)), ("dA", (H,))):
         g[name] = _out(g.get(name), shape, torch.float32, dev)
         _expect(g[name], name, torch.float32, shape, dev)
@@ -477,8 +474,7 @@ def ssm_decode_step(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch
     if state is None:
         raise TypeError("state must be a tensor")
     _expect(state, "state", torch.float32, (b, H, P, N), dev)
-    out = _like(out, x)
-    os = _rows(out, "out", x.dtype, x.shape, dev, 1)
+    out, os = _out_rows(out, "out", x, dev, 1)
     _call("kda_ssm_decode_step", dev, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
           _ptr(state), _ptr(out), b, H, G, P, N, xs, bs, cs, os, dtc)
     return out
