@@ -29,7 +29,7 @@
 // states pass.  In the gradient kernel VALU issues in 45% of the cycles, LDS works
 // in 27% and the matrix unit in 15%; its waves wait half of their time, at two
 // barriers a head and for LDS, with one workgroup of 8 waves a CU, the most that
-// 137 KB of LDS and 230 registers leave.  Fewer VALU instructions do not help it
+// 145 KB of LDS and 230 registers leave.  Fewer VALU instructions do not help it
 // (weights below the diagonal as products, as the scan has them: 538 us).
 #include "ssm_device.h"
 
@@ -42,7 +42,7 @@ constexpr int kGradWaves = 8;
 template <typename T, int N>
 __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
     constexpr int L = kSsmBlock<T>, NT = kGradWaves * 64, NI = sizeof(T) == 2 ? 1 : 3;
-    constexpr int KQ = sizeof(T) == 2 ? 2 : 3;   // parts of Q (dB and dC only)
+    constexpr int KQ = 3;                        // parts of Q (2: 535 us where 3 take 549)
     constexpr int TL = L / 16, PT = TL / 2;      // token tiles; row tiles of du a wave owns
     constexpr int NTN = N / 16, TG = kGradWaves / NTN, TPW = TL / TG;  // tiles of dB, dC a wave owns
     constexpr int KT = L / 32;                   // 32-wide steps over tokens

@@ -117,6 +117,28 @@ __device__ __forceinline__ Parts<NP> read_rows(const bf16 *tile, int row0, int k
     return p;
 }
 
+// The rows of a tile of fp32 values (TL in elements: two a value), in that k order,
+// split into their three parts here.
+template <typename TL> struct FloatRowsAt {
+    int o[TL::LD / 64][2];
+    __device__ __forceinline__ explicit FloatRowsAt(int lane) {
+#pragma unroll
+        for (int ks = 0; ks < TL::LD / 64; ++ks)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                o[ks][q] = TL::at(lane & 15, 2 * (32 * ks + 16 * q + 4 * (lane >> 4))) / 2;
+    }
+};
+template <typename TL>
+__device__ __forceinline__ Parts<3> read_float_rows(const float *tile, int row0, int ks,
+                                                    const FloatRowsAt<TL> &at) {
+    const float *a = tile + row0 * (TL::LD / 2);
+    const f32x4 u = *reinterpret_cast<const f32x4 *>(a + at.o[ks][0]);
+    const f32x4 v = *reinterpret_cast<const f32x4 *>(a + at.o[ks][1]);
+    const float f[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+    return split<3>(f);
+}
+
 // The same outer index with k = 32 ks + 8 (l / 16) + j, for products whose two
 // operands are both read so: one 16-byte read where the order above takes two of
 // 8 bytes at half their rate.

@@ -21,14 +21,15 @@
 // is the scan proper.  The first pass reads x and B once more and does 4 P N of
 // the second's 4 P N + 2 L (P + N) operations a token.
 //
-// Bound by issue, not by HBM: fp32 operands enter the matrix unit as two or three
-// bf16 parts, so a token costs 2 to 3 times the products above, and the parts
-// (3 VALU instructions a value for two, 7 for three) and decays take as many
-// cycles again.  32K tokens x 64 heads of 64 x 128 bf16, 0.68 GB: 384 us = pieces
-// 118, fold 14 (67 MB, 4.8 TB/s), scan 290; the scan's SIMDs issue VALU half and
-// the matrix unit works a third of the time, LDS a third.  Wave rows: a 32-row
-// wave reads every row of B, C and M from LDS once for two tiles of products
-// (16 rows: 452 us).
+// Bound by issue, not by HBM: fp32 operands (the state, its updates, the block's
+// weights) enter the matrix unit as three bf16 parts, so a token costs 3 times the
+// products above, and the parts (7 VALU instructions a value) and decays take as many
+// cycles again.  Two parts of the state and the weights where they enter y would
+// take 402 us where three take 438, but then sums that cancel to less than 2^-8 of
+// their terms lose more to the parts than to a bf16 output's own rounding.
+// 32K tokens x 64 heads of 64 x 128 bf16, 0.68 GB: 438 us a call.  Wave rows: a
+// 32-row wave reads every row of B, C and M from LDS once for two tiles of products
+// (with two parts: 16 rows 452 us, 32 rows 384).
 #include "ssm_device.h"
 
 namespace kda {
@@ -41,21 +42,20 @@ enum Mode { kLocal, kOut, kStates };
 // LDS of one block's tiles.
 template <typename T, int P, int N, int HEADS, int MODE> struct ScanLds {
     static constexpr int L = kSsmBlock<T>, NI = sizeof(T) == 2 ? 1 : 3;
-    // Parts of y's fp32 operands, the block's weights M and the state: two for a
-    // bf16 y (2^-15, nothing beside its own rounding), three for an fp32 one.
-    static constexpr int KP = sizeof(T) == 2 ? 2 : 3;
     static constexpr bool OUT = MODE == kOut;
     typedef Tile<NI, L, N> TK;
     typedef Tile<NI, L, HEADS * P> TX;
     // Row tiles 0 and 1 have nothing right of column 32: of 64 rows, 1 lies beside 0.
     static constexpr bool PACK = L == 64;
-    typedef Tile<KP, PACK ? 48 : L, L> TM;
+    // The weights M as fp32 (a value takes two elements), split where they are read:
+    // three parts of each in LDS would leave one workgroup a CU.
+    typedef Tile<1, PACK ? 48 : L, 2 * L> TM;
     __device__ static constexpr int m_row(int it) { return PACK && it > 0 ? it - 1 : it; }
     __device__ static constexpr int m_step(int it) { return PACK && it == 1; }  // 32 columns each
     __attribute__((aligned(16))) bf16 k[TK::ELEMS];
     __attribute__((aligned(16))) bf16 c[OUT ? TK::ELEMS : 8];
     __attribute__((aligned(16))) bf16 x[TX::ELEMS];
-    __attribute__((aligned(16))) bf16 m[OUT ? HEADS * TM::ELEMS : 8];
+    __attribute__((aligned(16))) float m[OUT ? HEADS * (TM::ELEMS / 2) : 4];
     __attribute__((aligned(16))) double cum[2][HEADS][L];  // log2 of the decay up to t
     __attribute__((aligned(16))) float dt[2][HEADS][L], w[2][HEADS][L], in[2][HEADS][L];
     // Weights of M's tiles below the diagonal as products, from the last token before
@@ -71,12 +71,13 @@ template <typename T, int P, int N, int HEADS, int RT, int MODE, bool REV>
 __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                                           ScanLds<T, P, N, HEADS, MODE> &lds) {
     typedef ScanLds<T, P, N, HEADS, MODE> S_;
-    constexpr int L = S_::L, NT = HEADS * P * 4 / RT, NW = NT / 64, WPH = NW / HEADS, NI = S_::NI, KM = S_::KP, KP = S_::KP;
+    constexpr int L = S_::L, NT = HEADS * P * 4 / RT, NW = NT / 64, WPH = NW / HEADS, NI = S_::NI;
     constexpr bool OUT = S_::OUT;
     typedef typename S_::TK TK;
     typedef typename S_::TX TX;
     typedef typename S_::TM TM;
-    bf16 *sk = lds.k, *sc = lds.c, *sx = lds.x, *sm = lds.m;
+    bf16 *sk = lds.k, *sc = lds.c, *sx = lds.x;
+    float *sm = lds.m;
     auto &s_cum = lds.cum;
     auto &s_dt = lds.dt, &s_w = lds.w, &s_in = lds.in;
     auto &s_tot = lds.tot;
@@ -89,7 +90,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     const RowsAt<TK> krow(lane);
     const WideAt<TK> kwide(lane);
-    const RowsAt<TM> mrow(lane);
+    const FloatRowsAt<TM> mrow(lane);
     int kcol[N / 16];
 #pragma unroll
     for (int t = 0; t < N / 16; ++t) kcol[t] = cols_at<TK>(16 * t, lane);
@@ -186,7 +187,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         }
     }
     if constexpr (OUT) {  // tiles above the diagonal that a 32-wide step reads: zero for good
-        for (int i = tid; i < HEADS * TM::ELEMS; i += NT) sm[i] = static_cast<bf16>(0.f);
+        for (int i = tid; i < HEADS * (TM::ELEMS / 2); i += NT) sm[i] = 0.f;
     }
     for (int i = 0; i < blocks; ++i) {
         const int buf = i & 1, t0 = first_token(i);
@@ -224,7 +225,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                         m = mma(read_wide<TK, NI>(sk, 16 * is, ks, kwide),
                                 read_wide<TK, NI>(sc, 16 * it, ks, kwide), m);
                     const int t = 16 * it + r, s = 16 * is + 4 * g;
-                    const int to = TM::at(16 * S_::m_row(it) + r, s + 32 * S_::m_step(it));
+                    const int to = TM::at(16 * S_::m_row(it) + r, 2 * (s + 32 * S_::m_step(it))) / 2;
 #pragma unroll
                     for (int hh = 0; hh < HEADS; ++hh) {
                         float v[4];
@@ -243,17 +244,8 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                                        (s + e == t ? D[hh] : 0.f);
                             }
                         }
-#pragma unroll
-                        for (int part = 0; part < KM; ++part) {
-                            bf16x4 o;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float f = part < KM - 1 ? top_bits(v[e]) : v[e];
-                                o[e] = static_cast<bf16>(f);
-                                v[e] -= f;
-                            }
-                            *reinterpret_cast<bf16x4 *>(sm + hh * TM::ELEMS + part * TM::PLANE + to) = o;
-                        }
+                        *reinterpret_cast<f32x4 *>(sm + hh * (TM::ELEMS / 2) + to) =
+                            f32x4{v[0], v[1], v[2], v[3]};
                     }
                 }
             // y^T = S C^T e^{cum}: rows p, columns t
@@ -261,13 +253,13 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
             for (int i = 0; i < RT * (L / 16); ++i) y[i % RT][i / RT] = zero4();
 #pragma unroll
             for (int ks = 0; ks < N / 32; ++ks) {
-                Parts<KP> sp[RT];
+                Parts<3> sp[RT];
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     float f[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) f[e] = S[rt][2 * ks][e], f[4 + e] = S[rt][2 * ks + 1][e];
-                    sp[rt] = split<KP>(f);
+                    sp[rt] = split<3>(f);
                 }
 #pragma unroll
                 for (int it = 0; it < L / 16; ++it) {
@@ -307,13 +299,13 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         if constexpr (OUT) {
             const int n = pc.end - t0;
             T *out = static_cast<T *>(a.out) + (int64_t)h0 * P + row0 + 4 * g;
-            const bf16 *weights_of = sm + mine * TM::ELEMS;
+            const float *weights_of = sm + mine * (TM::ELEMS / 2);
 #pragma unroll
             for (int it = 0; it < L / 16; ++it) {
 #pragma unroll
                 for (int ks = 0; ks <= it / 2; ++ks) {
-                    const Parts<KM> mt = read_rows<TM, KM>(weights_of, 16 * S_::m_row(it),
-                                                           ks + S_::m_step(it), mrow);
+                    const Parts<3> mt = read_float_rows<TM>(weights_of, 16 * S_::m_row(it),
+                                                            ks + S_::m_step(it), mrow);
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) y[rt][it] = mma(xt[rt][ks], mt, y[rt][it]);
                 }
@@ -484,8 +476,8 @@ template <typename T, int P, int N, int HEADS, int RT> struct Scan {
 };
 
 // bf16: 128 rows a workgroup and 32 a wave, two heads of 64 that share B and C
-// together.  32K x 64 heads of 64 x 128: 384 us, with one head a workgroup and 16
-// rows a wave 452; heads of 128 rows 723 and 814; 1,227 tokens x 8 heads of 64 x 64,
+// together.  Measured with two parts of y's operands: 32K x 64 heads of 64 x 128 384
+// us, with one head a workgroup and 16 rows a wave 452; heads of 128 rows 690 and 814; 1,227 tokens x 8 heads of 64 x 64,
 // where the launches count, 28 and 29.  An odd number of heads a group leaves one
 // head a workgroup; fp32 has no LDS for two (three parts of every tile).
 template <typename T, int P, typename F> int by_state(const SsmScan &a, F f) {
