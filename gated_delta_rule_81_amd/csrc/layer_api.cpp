@@ -458,7 +458,8 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
     const int64_t xl = (int64_t)num_heads * head_dim;
     const int64_t bl = num_heads > 0 ? (int64_t)num_groups * state_dim : 0;
     const int64_t th = (int64_t)seqs.total * num_heads;
-    if (th > 0 && (!dt || !A)) return KDA_ERR_NULL;
+    if (th > 0 && !dt) return KDA_ERR_NULL;
+    if (seqs.num > 0 && num_heads > 0 && !A) return KDA_ERR_NULL;  // read without tokens too
     if ((st = check_ssm_rows(x, seqs.total, xl, x_stride, esz)) != KDA_OK ||
         (st = check_ssm_rows(B, seqs.total, bl, b_stride, esz)) != KDA_OK ||
         (st = check_ssm_rows(C, seqs.total, bl, c_stride, esz)) != KDA_OK ||
