@@ -424,7 +424,7 @@ struct SsmSpace {
 SsmSpace ssm_space(const kda::Seqs &s, int32_t heads, int32_t p, int32_t n, int directions = 1) {
     const PiecePlan plan = piece_plan(s, heads, p, directions);
     if (!plan.split || s.num == 0) return {0, 0};
-    const int64_t count = kda::piece_count(s, plan.len) * heads;
+    const int64_t count = kda::slot_count(s, plan.len) * heads;
     return {count * p * n, count};
 }
 

@@ -31,6 +31,17 @@ __host__ __device__ inline int64_t first_piece(const Seqs &q, int64_t len, int64
     return q.cu ? t0 / len + n : n * pieces_per_row(q, len);
 }
 
+// Places for the states of pieces, for sequences of two and more only.  Equal rows:
+// the piece's number.  Packed: floor(2 t0 / len) + j.  A sequence of T > len tokens
+// takes ceil(T / len) <= floor(2 T / len) places, so the next one's begin behind them
+// and all are under 2 total / len, however many short sequences there are.
+__host__ __device__ inline int64_t slot_count(const Seqs &q, int64_t len) {
+    return q.cu ? 2 * (int64_t)q.total / len : q.num * pieces_per_row(q, len);
+}
+__host__ __device__ inline int64_t first_slot(const Seqs &q, int64_t len, int64_t t0, int n) {
+    return q.cu ? 2 * t0 / len : n * pieces_per_row(q, len);
+}
+
 struct ConvArgs {
     const void *x, *state0, *d_out, *d_final;
     const float *weight, *bias;
@@ -63,9 +74,9 @@ int64_t qk_norm_bwd_workspace_floats(int64_t tokens, int64_t q_heads, int64_t k_
                                      int head_dim);
 
 // The scan's walk over the sequences.  With seg_states the sequences are cut into
-// pieces of `piece` tokens that run at once (seg_states: a state per piece
-// number and head, seg_decay: a double each); without, `piece` is at least every
-// sequence's length.
+// pieces of `piece` tokens that run at once (seg_states: a state per slot and
+// head, seg_decay: a double each); without, `piece` is at least every sequence's
+// length.
 struct SsmScan {
     const void *x, *k, *c;
     const float *dt, *A, *D, *state0;

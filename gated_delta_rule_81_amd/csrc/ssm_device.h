@@ -293,13 +293,20 @@ struct Piece {
     int seq, index, beg, end;  // sequence, number in it, tokens [beg, end)
     int seq_beg, seq_end;
     bool first, last, any;     // any: the number belongs to a sequence
+    int64_t slot;              // of a sequence in several pieces
 };
+// By the piece's number, or by its slot (which sequences in one piece have none of;
+// a sequence's slots all lie before those where the next one would have its own).
+template <bool BY_SLOT = false>
 __device__ __forceinline__ Piece find_piece(const Seqs &q, int64_t number, int len) {
+    auto first_of = [&](int64_t t0, int n) {
+        return BY_SLOT ? first_slot(q, len, t0, n) : first_piece(q, len, t0, n);
+    };
     int lo = 0, hi = q.num - 1;
     if (!q.cu) lo = (int)(number / pieces_per_row(q, len));
     while (q.cu && lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (first_piece(q, len, seq_first(q, mid), mid) <= number)
+        if (first_of(seq_first(q, mid), mid) <= number)
             lo = mid;
         else
             hi = mid - 1;
@@ -309,9 +316,10 @@ __device__ __forceinline__ Piece find_piece(const Seqs &q, int64_t number, int l
     p.seq_beg = seq_first(q, lo);
     p.seq_end = seq_end_token(q, lo);
     if (p.seq_end < p.seq_beg) p.seq_end = p.seq_beg;  // malformed offsets
-    const int64_t index = number - first_piece(q, len, p.seq_beg, lo);
+    const int64_t index = number - first_of(p.seq_beg, lo);
     const int64_t count = p.seq_end > p.seq_beg ? (p.seq_end - p.seq_beg + (int64_t)len - 1) / len : 1;
-    p.any = index >= 0 && index < count;
+    p.any = index >= 0 && index < count && (count > 1 || !BY_SLOT);
+    p.slot = first_slot(q, len, p.seq_beg, lo) + index;
     p.index = (int)index;
     p.first = index == 0;
     p.last = index == count - 1;

@@ -84,7 +84,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
 
     const int h0 = (int)(unit % (a.heads / HEADS)) * HEADS;
     const int64_t number = unit / (a.heads / HEADS);
-    const Piece pc = find_piece(a.seqs, number, a.piece);
+    const Piece pc = find_piece<MODE == kLocal>(a.seqs, number, a.piece);
     if (!pc.any) return;
     if (MODE == kLocal && (REV ? pc.first : pc.last)) return;  // nothing enters from it
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
@@ -121,7 +121,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         // Of a sequence in several pieces the fold has written every entering state,
         // the first too: final_state may be state0, and another workgroup writes it.
         enter = a.seg_states && !(pc.first && pc.last)
-                    ? a.seg_states + (number * a.heads + h0) * (int64_t)(P * N)
+                    ? a.seg_states + (pc.slot * a.heads + h0) * (int64_t)(P * N)
                     : (a.state0 ? a.state0 + ((int64_t)pc.seq * a.heads + h0) * (P * N) : nullptr);
     }
 #pragma unroll
@@ -338,8 +338,8 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     }
     float *to = nullptr;
     if (MODE == kLocal) {
-        to = a.seg_states + (number * a.heads + h0) * (int64_t)(P * N);
-        if (weigher && lane == 0) a.seg_decay[number * a.heads + h0 + wh] = total;
+        to = a.seg_states + (pc.slot * a.heads + h0) * (int64_t)(P * N);
+        if (weigher && lane == 0) a.seg_decay[pc.slot * a.heads + h0 + wh] = total;
     } else if (a.final_state && (REV ? pc.first : pc.last)) {
         to = a.final_state + ((int64_t)pc.seq * a.heads + h0) * (P * N);
     }
@@ -368,7 +368,7 @@ template <typename T, int P, int N, int HEADS, int RT>
 __global__ __launch_bounds__(HEADS * P * 4 / RT, 2) void ssm_local_kernel(SsmScan a) {
     __shared__ ScanLds<T, P, N, HEADS, kLocal> lds;
     const int64_t unit =
-        xcd_unit(blockIdx.x, piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
+        xcd_unit(blockIdx.x, slot_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
     if (unit >= 0) scan_body<T, P, N, HEADS, RT, kLocal, false>(a, unit, lds);
 }
 
@@ -378,8 +378,10 @@ template <typename T, int P, int N, int HEADS, int RT, int MODE>
 __global__ __launch_bounds__(HEADS * P * 4 / RT, 2) void ssm_both_kernel(SsmScan a, SsmScan b) {
     __shared__ ScanLds<T, P, N, HEADS, MODE> lds;
     const bool rev = blockIdx.x >= gridDim.x / 2;
-    const int64_t unit = xcd_unit(rev ? blockIdx.x - gridDim.x / 2 : blockIdx.x,
-                                  piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
+    const int64_t numbers =
+        MODE == kLocal ? slot_count(a.seqs, a.piece) : piece_count(a.seqs, a.piece);
+    const int64_t unit = xcd_unit(rev ? blockIdx.x - gridDim.x / 2 : blockIdx.x, numbers,
+                                  a.heads / HEADS, a.groups);
     if (unit < 0) return;
     if (!rev)
         scan_body<T, P, N, HEADS, RT, MODE, false>(a, unit, lds);
@@ -389,18 +391,27 @@ __global__ __launch_bounds__(HEADS * P * 4 / RT, 2) void ssm_both_kernel(SsmScan
 
 // The pieces' own final states turned in place into entering states:
 // enter[next] = e^{decay} enter + own.  One workgroup per 1024 values of a
-// (sequence, head); the pieces one after the other, eight loads ahead.
+// (sequence, head); the pieces one after the other, eight loads ahead.  Packed
+// sequences in several pieces are found by the tokens i * piece: each holds one at
+// least, its first is its own, and there are few beside many short sequences.
 template <bool REV>
 __device__ __forceinline__ void fold_body(const SsmScan &a, int values, int64_t block) {
     const int per = values / 1024;
     const int64_t u = block / per;
-    const int h = (int)(u % a.heads), n = (int)(u / a.heads);
+    const int h = (int)(u % a.heads);
+    int n = (int)(u / a.heads), beg, end;
     const int64_t off = block % per * 1024 + threadIdx.x * 4;
-    const int beg = seq_first(a.seqs, n);
-    const int end = seq_end_token(a.seqs, n);
+    if (a.seqs.cu) {
+        const int i = n;
+        n = seq_of_token(a.seqs, i * a.piece, &beg, &end);
+        if (n < 0 || ((int64_t)beg + a.piece - 1) / a.piece != i) return;
+    } else {
+        beg = seq_first(a.seqs, n);
+        end = seq_end_token(a.seqs, n);
+    }
     const int count = end > beg ? (int)(((int64_t)end - beg + a.piece - 1) / a.piece) : 1;
     if (count < 2) return;
-    const int64_t first = first_piece(a.seqs, a.piece, beg, n);
+    const int64_t first = first_slot(a.seqs, a.piece, beg, n);
     auto at = [&](int j) {
         return a.seg_states + ((first + (REV ? count - 1 - j : j)) * a.heads + h) * (int64_t)values + off;
     };
@@ -448,7 +459,7 @@ template <typename T, int P, int N, int HEADS, int RT> struct Scan {
     static int out(const SsmScan &a, hipStream_t stream) {
         const unsigned blocks = xcd_blocks(piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
         if (a.seg_states) {
-            hipLaunchKernelGGL((ssm_local_kernel<T, P, N, HEADS, RT>), dim3(blocks), dim3(NT), 0,
+            hipLaunchKernelGGL((ssm_local_kernel<T, P, N, HEADS, RT>), dim3(slots(a)), dim3(NT), 0,
                                stream, a);
             hipLaunchKernelGGL(ssm_fold_kernel, dim3((unsigned)folds(a)), dim3(256), 0, stream, a,
                                P * N);
@@ -460,7 +471,7 @@ template <typename T, int P, int N, int HEADS, int RT> struct Scan {
     static int both(const SsmScan &a, const SsmScan &b, hipStream_t stream) {
         const unsigned blocks = xcd_blocks(piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
         if (a.seg_states) {
-            hipLaunchKernelGGL((ssm_both_kernel<T, P, N, HEADS, RT, kLocal>), dim3(2 * blocks),
+            hipLaunchKernelGGL((ssm_both_kernel<T, P, N, HEADS, RT, kLocal>), dim3(2 * slots(a)),
                                dim3(NT), 0, stream, a, b);
             const unsigned f = (unsigned)folds(a);
             hipLaunchKernelGGL(ssm_fold_both_kernel, dim3(2 * f), dim3(256), 0, stream, a, b, P * N,
@@ -470,8 +481,13 @@ template <typename T, int P, int N, int HEADS, int RT> struct Scan {
                            dim3(NT), 0, stream, a, b);
         return hipGetLastError() == hipSuccess ? 0 : -1;
     }
+    static unsigned slots(const SsmScan &a) {
+        return xcd_blocks(slot_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
+    }
     static int64_t folds(const SsmScan &a) {
-        return (int64_t)a.seqs.num * a.heads * (P * N / 1024);
+        const int64_t seqs =
+            a.seqs.cu ? ((int64_t)a.seqs.total + a.piece - 1) / a.piece : a.seqs.num;
+        return seqs * a.heads * (P * N / 1024);
     }
 };
 
