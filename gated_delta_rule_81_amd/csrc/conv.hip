@@ -435,7 +435,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, T *state, in
     R::put(static_cast<T *>(a.out) + n * a.out_stride + c, y);
 }
 
-int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tokens of one wave's run.  Long runs read fewer rows twice, short ones fill
 // the chip when there is little to do: about 8 waves per SIMD's worth of runs,
@@ -454,36 +454,54 @@ int bwd_run_tokens(int64_t total, int cblocks) {
     return (int)(run < 16 ? 16 : (run > 64 ? 64 : run));
 }
 
+// Workgroups: channel blocks x (runs of tokens + rows of states).
+struct Grid {
+    int64_t cb, rb, sb;
+    int run;
+    int64_t blocks() const { return cb * (rb + sb); }
+};
+Grid fwd_grid(const ConvArgs &a, int vec) {
+    Grid g = {div_up(a.channels, 64 * vec), 0, 0, 0};
+    g.run = run_tokens(a.seqs.total, (int)g.cb);
+    g.rb = div_up(a.seqs.total, (int64_t)g.run * kWaves);
+    g.sb = a.final_state ? div_up((int64_t)a.seqs.num * (a.width - 1), kWaves) : 0;
+    return g;
+}
+Grid bwd_grid(const ConvArgs &a, int vec) {
+    Grid g = {div_up(a.channels, 64 * vec), 0, 0, 0};
+    g.run = bwd_run_tokens(a.seqs.total, (int)g.cb);
+    g.rb = div_up(a.seqs.total, (int64_t)g.run * kWaves);
+    g.sb = a.d_state0 ? div_up(a.seqs.num, kWaves) : 0;
+    return g;
+}
+Grid step_grid(const ConvArgs &a, int32_t batch, int vec) {
+    return {div_up(a.channels, 64 * vec), div_up(batch, kWaves), 0, 0};
+}
+int64_t reduce_blocks(const ConvArgs &a) { return div_up((int64_t)a.channels * (a.width + 1), 64); }
+
 template <typename T, int VEC, int W> int fwd(const ConvArgs &a, hipStream_t stream) {
-    const int cb = div_up(a.channels, 64 * VEC);
-    const int run = run_tokens(a.seqs.total, cb);
-    const int rb = div_up(a.seqs.total, (int64_t)run * kWaves);
-    const int sb = a.final_state ? div_up((int64_t)a.seqs.num * (W - 1), kWaves) : 0;
-    if (rb + sb == 0) return 0;
-    hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, W>), dim3((unsigned)cb * (unsigned)(rb + sb)),
-                       dim3(64, kWaves), 0, stream, a, cb, rb, run);
+    const Grid g = fwd_grid(a, VEC);
+    if (g.blocks() == 0) return 0;
+    hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, W>), dim3((unsigned)g.blocks()), dim3(64, kWaves), 0,
+                       stream, a, (int)g.cb, (int)g.rb, g.run);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 template <typename T, int VEC, int W> int bwd(const ConvArgs &a, hipStream_t stream) {
-    const int cb = div_up(a.channels, 64 * VEC);
-    const int run = bwd_run_tokens(a.seqs.total, cb);
-    const int rb = div_up(a.seqs.total, (int64_t)run * kWaves);
-    const int sb = a.d_state0 ? div_up(a.seqs.num, kWaves) : 0;
-    if (rb + sb > 0)
-        hipLaunchKernelGGL((conv_bwd_kernel<T, VEC, W>), dim3((unsigned)cb * (unsigned)(rb + sb)),
-                           dim3(64, kWaves), 0, stream, a, cb, rb, run);
-    hipLaunchKernelGGL(conv_reduce_kernel, dim3(div_up((int64_t)a.channels * (W + 1), 64)),
-                       dim3(64, 16), 0, stream, a.partial, rb, a.channels, W, a.dweight, a.dbias);
+    const Grid g = bwd_grid(a, VEC);
+    if (g.blocks() > 0)
+        hipLaunchKernelGGL((conv_bwd_kernel<T, VEC, W>), dim3((unsigned)g.blocks()),
+                           dim3(64, kWaves), 0, stream, a, (int)g.cb, (int)g.rb, g.run);
+    hipLaunchKernelGGL(conv_reduce_kernel, dim3((unsigned)reduce_blocks(a)), dim3(64, 16), 0, stream,
+                       a.partial, (int)g.rb, a.channels, W, a.dweight, a.dbias);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 template <typename T, int VEC, int W>
 int step(const ConvArgs &a, void *state, int batch, hipStream_t stream) {
-    const int cb = div_up(a.channels, 64 * VEC);
-    hipLaunchKernelGGL((conv_step_kernel<T, VEC, W>),
-                       dim3((unsigned)cb * (unsigned)div_up(batch, kWaves)), dim3(64, kWaves), 0,
-                       stream, a, static_cast<T *>(state), cb, batch);
+    const Grid g = step_grid(a, batch, VEC);
+    hipLaunchKernelGGL((conv_step_kernel<T, VEC, W>), dim3((unsigned)g.blocks()), dim3(64, kWaves), 0,
+                       stream, a, static_cast<T *>(state), (int)g.cb, batch);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
@@ -501,6 +519,12 @@ bool wide(const ConvArgs &a, const void *state, int vec) {
            a.d_out_stride % vec == 0 && a.dx_stride % vec == 0;
 }
 
+// Channels of a lane: 16-byte pieces, 8 in the bf16 backward, or one channel.
+int vec_of(const ConvArgs &a, const void *state, bool backward) {
+    const int vec = a.dtype == kDtypeBf16 && !backward ? 8 : 4;
+    return wide(a, state, vec) ? vec : 1;
+}
+
 #define KDA_CONV_WIDTHS(fn, T, VEC, ...)                       \
     (a.width == 4   ? fn<T, VEC, 4>(__VA_ARGS__)               \
      : a.width == 3 ? fn<T, VEC, 3>(__VA_ARGS__)               \
@@ -508,19 +532,31 @@ bool wide(const ConvArgs &a, const void *state, int vec) {
 
 }  // namespace
 
+int64_t conv_fwd_threads(const ConvArgs &a) {
+    return fwd_grid(a, vec_of(a, nullptr, false)).blocks() * 64 * kWaves;
+}
+int64_t conv_bwd_threads(const ConvArgs &a) {
+    const int64_t runs = bwd_grid(a, vec_of(a, nullptr, true)).blocks() * 64 * kWaves;
+    const int64_t sums = reduce_blocks(a) * 1024;
+    return runs > sums ? runs : sums;
+}
+int64_t conv_step_threads(const ConvArgs &a, const void *state, int32_t batch) {
+    return step_grid(a, batch, vec_of(a, state, false)).blocks() * 64 * kWaves;
+}
+
 int launch_conv_fwd(const ConvArgs &a, hipStream_t stream) {
     if (a.dtype == kDtypeBf16)
-        return wide(a, nullptr, 8) ? KDA_CONV_WIDTHS(fwd, bf16, 8, a, stream)
+        return vec_of(a, nullptr, false) == 8 ? KDA_CONV_WIDTHS(fwd, bf16, 8, a, stream)
                                    : KDA_CONV_WIDTHS(fwd, bf16, 1, a, stream);
-    return wide(a, nullptr, 4) ? KDA_CONV_WIDTHS(fwd, float, 4, a, stream)
+    return vec_of(a, nullptr, false) == 4 ? KDA_CONV_WIDTHS(fwd, float, 4, a, stream)
                                : KDA_CONV_WIDTHS(fwd, float, 1, a, stream);
 }
 
 int launch_conv_bwd(const ConvArgs &a, hipStream_t stream) {
     if (a.dtype == kDtypeBf16)
-        return wide(a, nullptr, 4) ? KDA_CONV_WIDTHS(bwd, bf16, 4, a, stream)
+        return vec_of(a, nullptr, true) == 4 ? KDA_CONV_WIDTHS(bwd, bf16, 4, a, stream)
                                    : KDA_CONV_WIDTHS(bwd, bf16, 1, a, stream);
-    return wide(a, nullptr, 4) ? KDA_CONV_WIDTHS(bwd, float, 4, a, stream)
+    return vec_of(a, nullptr, true) == 4 ? KDA_CONV_WIDTHS(bwd, float, 4, a, stream)
                                : KDA_CONV_WIDTHS(bwd, float, 1, a, stream);
 }
 
@@ -532,9 +568,9 @@ int64_t conv_bwd_workspace_floats(int64_t total, int64_t channels, int width) {
 
 int launch_conv_step(const ConvArgs &a, void *state, int32_t batch, hipStream_t stream) {
     if (a.dtype == kDtypeBf16)
-        return wide(a, state, 8) ? KDA_CONV_WIDTHS(step, bf16, 8, a, state, batch, stream)
+        return vec_of(a, state, false) == 8 ? KDA_CONV_WIDTHS(step, bf16, 8, a, state, batch, stream)
                                  : KDA_CONV_WIDTHS(step, bf16, 1, a, state, batch, stream);
-    return wide(a, state, 4) ? KDA_CONV_WIDTHS(step, float, 4, a, state, batch, stream)
+    return vec_of(a, state, false) == 4 ? KDA_CONV_WIDTHS(step, float, 4, a, state, batch, stream)
                              : KDA_CONV_WIDTHS(step, float, 1, a, state, batch, stream);
 }
 

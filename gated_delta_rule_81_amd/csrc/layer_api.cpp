@@ -106,16 +106,17 @@ int kda_short_conv_fwd(const void *x, const float *weight, const float *bias,
                          {cu_seqlens, (uint64_t)(seqs.num + 1) * 4}};
     if ((st = check_alias(outs, ins)) != KDA_OK) return st;
     if (seqs.num == 0 || channels == 0) return KDA_OK;
-    if ((st = check_device()) != KDA_OK) return st;
-    const char *where = "kda_short_conv_fwd";
-    if (debug_mode() &&
-        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
-        return st;
     kda::ConvArgs a = {};
     a.x = x, a.state0 = initial_state, a.weight = weight, a.bias = bias, a.out = out;
     a.final_state = final_state, a.seqs = seqs, a.channels = channels, a.width = width;
     a.silu = activation == KDA_ACT_SILU, a.dtype = dtype;
     a.x_stride = x_stride, a.out_stride = out_stride;
+    if (kda::conv_fwd_threads(a) > kda::kMostThreads) return KDA_ERR_UNSUPPORTED;
+    if ((st = check_device()) != KDA_OK) return st;
+    const char *where = "kda_short_conv_fwd";
+    if (debug_mode() &&
+        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
+        return st;
     return launch_status(kda::launch_conv_fwd(a, stream), stream, where);
 }
 
@@ -171,11 +172,7 @@ int kda_short_conv_bwd(const void *x, const float *weight, const float *bias,
                          {cu_seqlens, (uint64_t)(seqs.num + 1) * 4}};
     if ((st = check_alias(outs, ins)) != KDA_OK) return st;
     if (channels == 0) return KDA_OK;
-    if ((st = check_device()) != KDA_OK) return st;
-    const char *where = "kda_short_conv_bwd";
-    if (debug_mode() &&
-        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
-        return st;
+    const int32_t tokens = seqs.total;
     if (seqs.num == 0) seqs.total = 0;  // no sequence holds a token
     kda::ConvArgs a = {};
     a.x = x, a.state0 = initial_state, a.d_out = d_out, a.d_final = d_final_state;
@@ -184,6 +181,12 @@ int kda_short_conv_bwd(const void *x, const float *weight, const float *bias,
     a.seqs = seqs, a.channels = channels, a.width = width;
     a.silu = activation == KDA_ACT_SILU, a.dtype = dtype;
     a.x_stride = x_stride, a.d_out_stride = d_out_stride, a.dx_stride = dx_stride;
+    if (kda::conv_bwd_threads(a) > kda::kMostThreads) return KDA_ERR_UNSUPPORTED;
+    if ((st = check_device()) != KDA_OK) return st;
+    const char *where = "kda_short_conv_bwd";
+    if (debug_mode() &&
+        (st = debug_check_offsets(cu_seqlens, seqs.num, tokens, stream, where)) != KDA_OK)
+        return st;
     return launch_status(kda::launch_conv_bwd(a, stream), stream, where);
 }
 
@@ -210,11 +213,12 @@ int kda_short_conv_step(const void *x, const float *weight, const float *bias, v
     int st = check_alias(outs, ins);
     if (st != KDA_OK) return st;
     if (!work) return KDA_OK;
-    if ((st = check_device()) != KDA_OK) return st;
     kda::ConvArgs a = {};
     a.x = x, a.weight = weight, a.bias = bias, a.out = out;
     a.channels = channels, a.width = width, a.silu = activation == KDA_ACT_SILU, a.dtype = dtype;
     a.x_stride = x_stride, a.out_stride = out_stride;
+    if (kda::conv_step_threads(a, state, batch) > kda::kMostThreads) return KDA_ERR_UNSUPPORTED;
+    if ((st = check_device()) != KDA_OK) return st;
     return launch_status(kda::launch_conv_step(a, state, batch, stream), stream,
                          "kda_short_conv_step");
 }
@@ -488,11 +492,6 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
         (overlap(outs[0], Span{initial_state, state}) || overlap(outs[1], Span{initial_state, state})))
         return KDA_ERR_ALIAS;
     if (seqs.num == 0 || num_heads == 0) return KDA_OK;
-    if ((st = check_device()) != KDA_OK) return st;
-    const char *where = "kda_ssm_chunk_fwd";
-    if (debug_mode() &&
-        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
-        return st;
     kda::SsmScan a = {};
     a.x = x, a.k = B, a.c = C, a.dt = dt, a.A = A, a.D = D, a.state0 = initial_state;
     a.out = out, a.final_state = final_state, a.seqs = seqs;
@@ -504,6 +503,12 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
         a.seg_decay = static_cast<double *>(workspace);
         a.seg_states = reinterpret_cast<float *>(a.seg_decay + (space.decay + 1) / 2 * 2);
     }
+    if (kda::ssm_scan_threads(a, dtype, 1) > kda::kMostThreads) return KDA_ERR_UNSUPPORTED;
+    if ((st = check_device()) != KDA_OK) return st;
+    const char *where = "kda_ssm_chunk_fwd";
+    if (debug_mode() &&
+        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
+        return st;
     return launch_status(kda::launch_ssm_out(a, dtype, stream), stream, where);
 }
 
@@ -613,20 +618,15 @@ int kda_ssm_chunk_bwd(const void *x, const float *dt, const float *A, const void
                          {d_final_state, state}};
     if ((st = check_alias(outs, ins)) != KDA_OK) return st;
     if (num_heads == 0) return KDA_OK;
-    if ((st = check_device()) != KDA_OK) return st;
-    const char *where = "kda_ssm_chunk_bwd";
-    if (debug_mode() &&
-        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
-        return st;
     kda::SsmGrad g = {};
     g.dA = dA, g.dD = dD, g.seqs = seqs, g.heads = num_heads, g.groups = num_groups;
+    kda::SsmScan a = {}, b = {};  // from the left, from the right
     if (seqs.num > 0) {
-        kda::SsmScan a = {};
         a.x = x, a.k = B, a.dt = dt, a.A = A, a.state0 = initial_state;
         a.seqs = seqs, a.heads = num_heads, a.groups = num_groups;
         a.p = head_dim, a.n = state_dim, a.piece = piece_plan(seqs, num_heads, head_dim, 2).len;
         a.x_stride = x_stride, a.k_stride = b_stride;
-        kda::SsmScan b = a;  // from the right
+        b = a;
         b.x = d_out, b.k = C, b.x_stride = d_out_stride, b.k_stride = c_stride;
         b.state0 = d_final_state, b.final_state = d_initial_state;
         char *at = static_cast<char *>(workspace);
@@ -639,8 +639,6 @@ int kda_ssm_chunk_bwd(const void *x, const float *dt, const float *A, const void
         }
         a.block_states = reinterpret_cast<float *>(at + 2 * w.pieces.bytes());
         b.block_states = a.block_states + w.states;
-        const int rc = kda::launch_ssm_states(a, b, dtype, stream);
-        if (rc != 0) return launch_status(rc, stream, where);
         g.x = x, g.B = B, g.C = C, g.dy = d_out, g.dt = dt, g.A = A, g.D = D;
         g.s_states = a.block_states, g.e_states = b.block_states;
         g.dx = dx, g.dB = dB, g.dC = dC, g.ddt = ddt;
@@ -650,6 +648,18 @@ int kda_ssm_chunk_bwd(const void *x, const float *dt, const float *A, const void
         g.x_stride = x_stride, g.b_stride = b_stride, g.c_stride = c_stride;
         g.dy_stride = d_out_stride, g.dx_stride = dx_stride;
         g.db_stride = db_stride, g.dc_stride = dc_stride;
+        if (kda::ssm_scan_threads(a, dtype, 2) > kda::kMostThreads ||
+            kda::ssm_grad_threads(g) > kda::kMostThreads)
+            return KDA_ERR_UNSUPPORTED;
+    }
+    if ((st = check_device()) != KDA_OK) return st;
+    const char *where = "kda_ssm_chunk_bwd";
+    if (debug_mode() &&
+        (st = debug_check_offsets(cu_seqlens, seqs.num, seqs.total, stream, where)) != KDA_OK)
+        return st;
+    if (seqs.num > 0) {
+        const int rc = kda::launch_ssm_states(a, b, dtype, stream);
+        if (rc != 0) return launch_status(rc, stream, where);
     }
     return launch_status(kda::launch_ssm_grad(g, dtype, stream), stream, where);
 }
@@ -666,7 +676,7 @@ int kda_ssm_decode_step(const void *x, const float *dt, const float *A, const vo
     const int64_t xl = (int64_t)num_heads * head_dim;
     const int64_t bl = num_heads > 0 ? (int64_t)num_groups * state_dim : 0;
     const uint64_t units = (uint64_t)batch * num_heads;
-    if (units > INT32_MAX / 4) return KDA_ERR_UNSUPPORTED;
+    if (units * kda::kSsmStepThreads > (uint64_t)kda::kMostThreads) return KDA_ERR_UNSUPPORTED;
     if (units > 0 && (!dt || !A || !state)) return KDA_ERR_NULL;
     if ((st = check_ssm_rows(x, batch, xl, x_stride, esz)) != KDA_OK ||
         (st = check_ssm_rows(B, batch, bl, b_stride, esz)) != KDA_OK ||

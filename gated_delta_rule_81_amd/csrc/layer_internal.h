@@ -51,6 +51,11 @@ struct ConvArgs {
     int32_t channels, width, silu, dtype;
     int64_t x_stride, out_stride, d_out_stride, dx_stride;
 };
+// Threads of a call's largest launch, which holds kMostThreads at most.
+constexpr int64_t kMostThreads = UINT32_MAX;
+int64_t conv_fwd_threads(const ConvArgs &a);
+int64_t conv_bwd_threads(const ConvArgs &a);
+int64_t conv_step_threads(const ConvArgs &a, const void *state, int32_t batch);
 int launch_conv_fwd(const ConvArgs &a, hipStream_t stream);
 int launch_conv_bwd(const ConvArgs &a, hipStream_t stream);
 int64_t conv_bwd_workspace_floats(int64_t total, int64_t channels, int width);
@@ -87,6 +92,9 @@ struct SsmScan {
     int32_t heads, groups, p, n, piece;
     int64_t x_stride, k_stride, c_stride, out_stride;
 };
+// Threads of the largest launch of launch_ssm_out (directions = 1) or
+// launch_ssm_states (2).
+int64_t ssm_scan_threads(const SsmScan &a, int dtype, int directions);
 // y and the final states.
 int launch_ssm_out(const SsmScan &a, int dtype, hipStream_t stream);
 // The state entering every block to a.block_states; and from the right, to
@@ -109,6 +117,7 @@ struct SsmGrad {
     int32_t heads, groups, p, n, sets;
     int64_t blocks, x_stride, b_stride, c_stride, dy_stride, dx_stride, db_stride, dc_stride;
 };
+int64_t ssm_grad_threads(const SsmGrad &a);
 int launch_ssm_grad(const SsmGrad &a, int dtype, hipStream_t stream);
 
 struct SsmStep {
@@ -119,6 +128,7 @@ struct SsmStep {
     int32_t batch, heads, groups, p, n;
     int64_t x_stride, b_stride, c_stride, out_stride;
 };
+constexpr int kSsmStepThreads = 256;  // of a workgroup; one per session and head
 int launch_ssm_step(const SsmStep &a, int dtype, hipStream_t stream);
 
 }  // namespace kda

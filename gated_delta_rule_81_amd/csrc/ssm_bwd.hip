@@ -497,6 +497,7 @@ template <typename T> int grad(const SsmGrad &a, hipStream_t stream) {
 
 }  // namespace
 
+int64_t ssm_grad_threads(const SsmGrad &a) { return a.blocks * a.groups * a.sets * kGradWaves * 64; }
 int launch_ssm_grad(const SsmGrad &a, int dtype, hipStream_t stream) {
     return dtype == kDtypeBf16 ? grad<bf16>(a, stream) : grad<float>(a, stream);
 }

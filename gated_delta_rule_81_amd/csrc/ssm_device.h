@@ -340,8 +340,8 @@ __device__ __forceinline__ int64_t xcd_unit(unsigned block, int64_t numbers, int
     if (bundle >= numbers * groups) return -1;
     return bundle / groups * heads + bundle % groups * per + i % per;
 }
-inline unsigned xcd_blocks(int64_t numbers, int heads, int groups) {
-    return (unsigned)((numbers * groups + 7) / 8 * 8 * (heads / groups));
+inline int64_t xcd_blocks(int64_t numbers, int heads, int groups) {
+    return (numbers * groups + 7) / 8 * 8 * (heads / groups);
 }
 
 }  // namespace kda

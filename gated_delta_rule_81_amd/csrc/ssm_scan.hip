@@ -32,6 +32,8 @@
 // (with two parts: 16 rows 452 us, 32 rows 384).
 #include "ssm_device.h"
 
+#include <algorithm>
+
 namespace kda {
 namespace {
 
@@ -456,38 +458,45 @@ __global__ __launch_bounds__(256) void ssm_fold_both_kernel(SsmScan a, SsmScan b
 
 template <typename T, int P, int N, int HEADS, int RT> struct Scan {
     static constexpr int NT = HEADS * P * 4 / RT;
-    static int out(const SsmScan &a, hipStream_t stream) {
-        const unsigned blocks = xcd_blocks(piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
-        if (a.seg_states) {
-            hipLaunchKernelGGL((ssm_local_kernel<T, P, N, HEADS, RT>), dim3(slots(a)), dim3(NT), 0,
-                               stream, a);
-            hipLaunchKernelGGL(ssm_fold_kernel, dim3((unsigned)folds(a)), dim3(256), 0, stream, a,
-                               P * N);
-        }
-        hipLaunchKernelGGL((ssm_out_kernel<T, P, N, HEADS, RT>), dim3(blocks), dim3(NT), 0, stream,
-                           a);
-        return hipGetLastError() == hipSuccess ? 0 : -1;
+    static int64_t pieces(const SsmScan &a) {
+        return xcd_blocks(piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
     }
-    static int both(const SsmScan &a, const SsmScan &b, hipStream_t stream) {
-        const unsigned blocks = xcd_blocks(piece_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
-        if (a.seg_states) {
-            hipLaunchKernelGGL((ssm_both_kernel<T, P, N, HEADS, RT, kLocal>), dim3(2 * slots(a)),
-                               dim3(NT), 0, stream, a, b);
-            const unsigned f = (unsigned)folds(a);
-            hipLaunchKernelGGL(ssm_fold_both_kernel, dim3(2 * f), dim3(256), 0, stream, a, b, P * N,
-                               f);
-        }
-        hipLaunchKernelGGL((ssm_both_kernel<T, P, N, HEADS, RT, kStates>), dim3(2 * blocks),
-                           dim3(NT), 0, stream, a, b);
-        return hipGetLastError() == hipSuccess ? 0 : -1;
-    }
-    static unsigned slots(const SsmScan &a) {
+    static int64_t slots(const SsmScan &a) {
         return xcd_blocks(slot_count(a.seqs, a.piece), a.heads / HEADS, a.groups);
     }
     static int64_t folds(const SsmScan &a) {
         const int64_t seqs =
             a.seqs.cu ? ((int64_t)a.seqs.total + a.piece - 1) / a.piece : a.seqs.num;
         return seqs * a.heads * (P * N / 1024);
+    }
+    static int64_t threads(const SsmScan &a, int directions) {
+        const int64_t walk = pieces(a) * NT;
+        if (!a.seg_states) return directions * walk;
+        const int64_t local = slots(a) * NT, fold = folds(a) * 256;
+        return directions * std::max(walk, std::max(local, fold));
+    }
+    static int out(const SsmScan &a, hipStream_t stream) {
+        if (a.seg_states) {
+            hipLaunchKernelGGL((ssm_local_kernel<T, P, N, HEADS, RT>), dim3((unsigned)slots(a)),
+                               dim3(NT), 0, stream, a);
+            hipLaunchKernelGGL(ssm_fold_kernel, dim3((unsigned)folds(a)), dim3(256), 0, stream, a,
+                               P * N);
+        }
+        hipLaunchKernelGGL((ssm_out_kernel<T, P, N, HEADS, RT>), dim3((unsigned)pieces(a)), dim3(NT),
+                           0, stream, a);
+        return hipGetLastError() == hipSuccess ? 0 : -1;
+    }
+    static int both(const SsmScan &a, const SsmScan &b, hipStream_t stream) {
+        if (a.seg_states) {
+            hipLaunchKernelGGL((ssm_both_kernel<T, P, N, HEADS, RT, kLocal>),
+                               dim3((unsigned)(2 * slots(a))), dim3(NT), 0, stream, a, b);
+            const unsigned f = (unsigned)folds(a);
+            hipLaunchKernelGGL(ssm_fold_both_kernel, dim3(2 * f), dim3(256), 0, stream, a, b, P * N,
+                               f);
+        }
+        hipLaunchKernelGGL((ssm_both_kernel<T, P, N, HEADS, RT, kStates>),
+                           dim3((unsigned)(2 * pieces(a))), dim3(NT), 0, stream, a, b);
+        return hipGetLastError() == hipSuccess ? 0 : -1;
     }
 };
 
@@ -496,22 +505,26 @@ template <typename T, int P, int N, int HEADS, int RT> struct Scan {
 // us, with one head a workgroup and 16 rows a wave 452; heads of 128 rows 690 and 814; 1,227 tokens x 8 heads of 64 x 64,
 // where the launches count, 28 and 29.  An odd number of heads a group leaves one
 // head a workgroup; fp32 has no LDS for two (three parts of every tile).
-template <typename T, int P, typename F> int by_state(const SsmScan &a, F f) {
+template <typename T, int P, typename F> auto by_state(const SsmScan &a, F f) {
+    typedef decltype(f(Scan<T, 64, 64, 1, 1>())) R;
     if constexpr (sizeof(T) == 2) {
         constexpr int HEADS = 128 / P;
         if (a.heads / a.groups % HEADS == 0)
             return a.n == 64 ? f(Scan<T, P, 64, HEADS, 2>()) : f(Scan<T, P, 128, HEADS, 2>());
     }
-    if constexpr (sizeof(T) == 2 && P == 128) return -1;  // HEADS = 1 divides any number
+    if constexpr (sizeof(T) == 2 && P == 128) return R(-1);  // HEADS = 1 divides any number
     else return a.n == 64 ? f(Scan<T, P, 64, 1, 1>()) : f(Scan<T, P, 128, 1, 1>());
 }
-template <typename F> int by_dims(const SsmScan &a, int dtype, F f) {
+template <typename F> auto by_dims(const SsmScan &a, int dtype, F f) {
     if (dtype == kDtypeBf16) return a.p == 64 ? by_state<bf16, 64>(a, f) : by_state<bf16, 128>(a, f);
     return a.p == 64 ? by_state<float, 64>(a, f) : by_state<float, 128>(a, f);
 }
 
 }  // namespace
 
+int64_t ssm_scan_threads(const SsmScan &a, int dtype, int directions) {
+    return by_dims(a, dtype, [&](auto s) { return s.threads(a, directions); });
+}
 int launch_ssm_out(const SsmScan &a, int dtype, hipStream_t stream) {
     return by_dims(a, dtype, [&](auto s) { return s.out(a, stream); });
 }

@@ -23,7 +23,7 @@ template <int LANES> __device__ __forceinline__ float row_sum(float x) {
 
 // One workgroup (4 waves) per (session, head, ROWS state rows).
 template <typename T, int P, int N, int ROWS>
-__global__ __launch_bounds__(256) void ssm_step_kernel(SsmStep a) {
+__global__ __launch_bounds__(kSsmStepThreads) void ssm_step_kernel(SsmStep a) {
     constexpr int LANES = N / 4, PER = 64 / LANES, STEPS = ROWS / (4 * PER);
     static_assert(STEPS * 4 * PER == ROWS, "rows over waves");
     const int64_t unit = blockIdx.x / (P / ROWS);  // session * heads + head
@@ -66,9 +66,9 @@ template <typename T, int P, int N> int step(const SsmStep &a, hipStream_t strea
     // few units: a quarter of the rows each, so that four times the CUs take part
     if (units * 4 <= 1024)
         hipLaunchKernelGGL((ssm_step_kernel<T, P, N, P / 4>), dim3((unsigned)(units * 4)),
-                           dim3(256), 0, stream, a);
+                           dim3(kSsmStepThreads), 0, stream, a);
     else
-        hipLaunchKernelGGL((ssm_step_kernel<T, P, N, P>), dim3((unsigned)units), dim3(256), 0,
+        hipLaunchKernelGGL((ssm_step_kernel<T, P, N, P>), dim3((unsigned)units), dim3(kSsmStepThreads), 0,
                            stream, a);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }

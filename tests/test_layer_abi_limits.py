@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from gated_delta_rule_81_amd._lib import lib
-from test_layer_abi import DEVICE, NULL, OK, call
+from test_layer_abi import DECLARED, DEVICE, NULL, OK, UNSUP, call
 
 pytestmark = pytest.mark.skipif(torch.cuda.device_count() > 0, reason="runs on a host without a GPU")
 
@@ -46,3 +46,41 @@ def test_workspace_of_many_short_sequences():
         assert bwd < 2 * blocks * H * (P * N * 4 + 8) + 4 * one + 64
     # many more sequences than tokens
     assert scan_space(1, 100, 1 << 20, H, 1, P, N)[0] < 128 << 20
+
+
+def packed(num):
+    return dict(batch=1, cu_seqlens=1 << 59, num_seqs=num)
+
+
+WIDE = {s: 1 << 28 for s in ("x_stride", "d_out_stride", "dx_stride")}
+PAST_A_LAUNCH = [  # entry point, the most that fits (or close to it), the least that does not
+    # a workgroup of 256 threads copies four rows of states
+    ("kda_short_conv_fwd", packed((1 << 24) // 3 * 4 - 64), packed((1 << 24) // 3 * 4 + 64)),
+    # ... forms the gradient of four states
+    ("kda_short_conv_bwd", packed((1 << 26) - 64), packed(1 << 26)),
+    # the sum of five gradients a channel, 64 of them in 1024 threads
+    ("kda_short_conv_bwd", dict(batch=1, seq_len=1, channels=(1 << 28) // 5 - 64, **WIDE),
+     dict(batch=1, seq_len=1, channels=(1 << 28) // 5 + 64, **WIDE)),
+    ("kda_short_conv_step", dict(batch=(1 << 26) - 4), dict(batch=1 << 26)),
+    # a pair of heads in 256 threads, and one head where a group has one
+    ("kda_ssm_chunk_fwd", dict(batch=(1 << 23) - 8, seq_len=1), dict(batch=1 << 23, seq_len=1)),
+    ("kda_ssm_chunk_fwd", dict(batch=(1 << 22) - 8, seq_len=1, num_groups=4),
+     dict(batch=1 << 22, seq_len=1, num_groups=4)),
+    ("kda_ssm_chunk_fwd", packed((1 << 23) - 16), packed(1 << 23)),
+    ("kda_ssm_chunk_fwd", packed(1), packed(1 << 30)),  # 2^32 workgroups
+    # both directions of the walk at once; 512 threads a block and group
+    ("kda_ssm_chunk_bwd", dict(batch=(1 << 22) - 8, seq_len=1), dict(batch=1 << 22, seq_len=1)),
+    ("kda_ssm_decode_step", dict(batch=(1 << 22) - 1), dict(batch=1 << 22)),
+]
+
+
+@pytest.mark.parametrize("name,fits,past", PAST_A_LAUNCH)
+def test_calls_past_a_launch(name, fits, past):
+    """A launch holds less than 2^32 threads: more work is refused before any of it
+    is done."""
+    kw = dict(workspace=1 << 60, workspace_bytes=1 << 62, state=1 << 60)
+    if name.startswith("kda_ssm"):
+        kw.update(initial_state=None, final_state=None, d_initial_state=None, d_final_state=None)
+    kw = {k: v for k, v in kw.items() if k in DECLARED[name]}
+    assert call(name, **kw, **fits) == DEVICE
+    assert call(name, **kw, **past) == UNSUP
