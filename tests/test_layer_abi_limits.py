@@ -5,6 +5,7 @@ test_layer_abi.py: fake addresses, a host without a GPU.
 import pytest
 import torch
 
+import gated_delta_rule_81_amd as kda
 from gated_delta_rule_81_amd._lib import lib
 from test_layer_abi import DECLARED, DEVICE, NULL, OK, UNSUP, call
 
@@ -84,3 +85,35 @@ def test_calls_past_a_launch(name, fits, past):
     kw = {k: v for k, v in kw.items() if k in DECLARED[name]}
     assert call(name, **kw, **fits) == DEVICE
     assert call(name, **kw, **past) == UNSUP
+
+
+def test_sizes_past_32_bits():
+    """The C calls count in 32 bits; a size past them is refused and not cut off
+    (a T of 2^32 + 8 would run as 8 tokens)."""
+    n = (1 << 32) + 8
+    m = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="meta")
+    f = lambda *s: m(*s, dtype=torch.float32)
+    for run in [
+        lambda: kda.short_conv(m(1, n, 1), f(1, 4)),
+        lambda: kda.short_conv(m(n, 0, 1), f(1, 4), output_final_state=False),
+        lambda: kda.short_conv(m(1, 2, n), f(n, 4)),
+        lambda: kda.short_conv(m(1, 8, 1), f(1, n)),
+        lambda: kda.short_conv(m(1, 8, 1), f(1, 4), cu_seqlens=m(n + 1, dtype=torch.int32)),
+        lambda: kda.short_conv_bwd(m(1, n, 1), f(1, 4), m(1, n, 1)),
+        lambda: kda.short_conv_step(m(n, 1), f(1, 4), m(n, 3, 1)),
+        lambda: kda.qk_norm(m(1 << 20, 1 << 13, 1, 64), m(1 << 20, 1 << 13, 0, 64)),
+        lambda: kda.qk_norm(m(2, 1, 64), m(2, 1, 64), table=f(n, 16),
+                            positions=m(2, dtype=torch.int32)),
+        lambda: kda.qk_norm(m(1, n, 64), m(1, 1, 64)),
+        lambda: kda.ssm_chunk_fwd(m(1, n, 1, 64), f(1, n, 1), f(1), m(1, n, 1, 64), m(1, n, 1, 64)),
+        lambda: kda.ssm_chunk_bwd(m(1, n, 1, 64), f(1, n, 1), f(1), m(1, n, 1, 64), m(1, n, 1, 64),
+                                  m(1, n, 1, 64)),
+        lambda: kda.ssm_decode_step(m(n, 1, 64), f(n, 1), f(1), m(n, 1, 64), m(n, 1, 64),
+                                    f(n, 1, 64, 64)),
+        lambda: kda.short_conv_bwd_workspace_size(1, n, 1, 4),
+        lambda: kda.qk_norm_bwd_workspace_size(n, 1, 1, 64),
+        lambda: kda.ssm_workspace_size(1, n, 1, 64, 64),
+        lambda: kda.ssm_bwd_workspace_size(1, n, 1, 1, 64, 64, torch.bfloat16),
+    ]:
+        with pytest.raises(ValueError, match="32 bits"):
+            run()
