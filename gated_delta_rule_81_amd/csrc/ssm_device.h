@@ -26,6 +26,10 @@ __device__ __forceinline__ float top_bits(float x) {
     return __uint_as_float(__float_as_uint(x) & 0xffff0000u);
 }
 
+__device__ __forceinline__ bool finite(float x) {
+    return __builtin_fabsf(x) < __builtin_inff();
+}
+
 // Eight floats as NP parts; NP = 1 rounds to nearest.
 template <int NP> __device__ __forceinline__ Parts<NP> split(const float (&f)[8]) {
     Parts<NP> p;
@@ -199,6 +203,28 @@ template <typename T, int ROWS, int COLS, int NT> struct Stage {
 #pragma unroll
         for (int i = 0; i < COUNT; ++i)
             r[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + i * RS * row_bytes, 0, 0);
+    }
+    // A sum of this thread's values: finite if all of them are (and none is huge).
+    __device__ __forceinline__ float sum() const {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        unsigned ones = 0x3f803f80u;  // in a register: as a constant it would be one value
+        asm("" : "+s"(ones));
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            float p = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const unsigned v = r[i][e];
+                if constexpr (sizeof(T) == 2)
+                    p = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v),
+                                                        __builtin_bit_cast(bf16x2, ones), p, false);
+                else
+                    p += __uint_as_float(v);
+            }
+            s += p;
+        }
+        return s;
     }
     template <typename TL> __device__ __forceinline__ void store(bf16 *tile, int tid) const {
         const int row = tid / PER_ROW, col = tid % PER_ROW * E, first = TL::at(row, col);

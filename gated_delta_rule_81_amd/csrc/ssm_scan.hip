@@ -67,6 +67,8 @@ template <typename T, int P, int N, int HEADS, int MODE> struct ScanLds {
     __attribute__((aligned(16))) float row[OUT ? 2 : 1][HEADS][OUT ? L : 1];
     __attribute__((aligned(16))) float col[OUT ? 2 : 1][HEADS][OUT ? col_at(TL) : 4];
     double tot[2][HEADS];
+    // whether a wave staged a NaN or an infinity of x; a row's first such token, or L
+    __attribute__((aligned(4))) unsigned char odd[8], from[OUT ? HEADS * P : 4];
 };
 
 template <typename T, int P, int N, int HEADS, int RT, int MODE, bool REV>
@@ -195,7 +197,11 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         const int buf = i & 1, t0 = first_token(i);
         rk.template store<TK>(sk, tid);
         rx.template store<TX>(sx, tid);
-        if constexpr (OUT) rc.template store<TK>(sc, tid);
+        if constexpr (OUT) {
+            rc.template store<TK>(sc, tid);
+            const bool any = __builtin_amdgcn_ballot_w64(!finite(rx.sum())) != 0;
+            if (lane == 0) lds.odd[wave] = any;
+        }
         lds_barrier();
         if (i + 1 < blocks) {
             load_rows(i + 1);
@@ -213,6 +219,30 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         }
         f32x4 y[RT][L / 16];
         const int ln = here(lane), r = ln & 15, g = ln >> 4;
+        // A product with a zero weight still passes on a NaN or an infinity of x, so a
+        // token's would reach earlier ones.  They enter the products as zeros; y of the
+        // row is NaN from that token on, and the row of the state behind the block.
+        bool odd = false;
+        if constexpr (OUT) {
+            static_assert(NW == 4 || NW == 8, "flags of the waves as words");
+            const unsigned *f = reinterpret_cast<const unsigned *>(lds.odd);
+            odd = __builtin_amdgcn_readfirstlane(NW == 4 ? f[0] : f[0] | f[1]) != 0;
+            if (__builtin_expect(odd, 0)) {  // every wave its own rows
+                constexpr int ROWS = 16 * RT, SPAN = L * ROWS / 64;  // tokens of a lane
+                const int col = row0 + ln % ROWS, begin = ln / ROWS * SPAN;
+                int first = L;
+#pragma unroll 1
+                for (int t = begin + SPAN - 1; t >= begin; --t) {
+                    bf16 *at = sx + TX::at(t, col);
+                    if (finite(to_f32(*at))) continue;
+                    first = t;
+                    for (int q = 0; q < NI; ++q) at[q * TX::PLANE] = static_cast<bf16>(0.f);
+                }
+                if (RT == 1) first = min(first, __shfl_xor(first, 16, 64));
+                first = min(first, __shfl_xor(first, 32, 64));
+                lds.from[col] = (unsigned char)first;
+            }
+        }
         if constexpr (OUT) {
             // M[t][s] = e^{cum_t - cum_s} (C_t . B_s) dt_s, s <= t, formed as tiles of M^T
             int q = 0;
@@ -242,8 +272,8 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const float z = (float)(ct - s_cum[buf][hh][s + e]);
-                                v[e] = m[e] * fast_exp2(s + e <= t ? z : -1e30f) * s_dt[buf][hh][s + e] +
-                                       (s + e == t ? D[hh] : 0.f);
+                                const float on = m[e] * fast_exp2(z) * s_dt[buf][hh][s + e];
+                                v[e] = s + e > t ? 0.f : s + e == t ? on + D[hh] : on;
                             }
                         }
                         *reinterpret_cast<f32x4 *>(sm + hh * (TM::ELEMS / 2) + to) =
@@ -315,6 +345,10 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     f32x4 &o = y[rt][it];
+                    if (__builtin_expect(odd, 0))
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = t < lds.from[row0 + 16 * rt + 4 * g + e] ? o[e] : __builtin_nanf("");
                     if (t < n)
                         store4(out + (int64_t)(t0 + t) * a.out_stride + 16 * rt, o[0], o[1], o[2],
                                o[3]);
@@ -334,6 +368,13 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                 for (int rt = 0; rt < RT; ++rt)
                     S[rt][t] = TR ? mma(xw[rt][ks], kt, S[rt][t]) : mma(kt, xw[rt][ks], S[rt][t]);
             }
+        }
+        if (OUT && __builtin_expect(odd, 0)) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                if (lds.from[row0 + 16 * rt + r] < L)
+#pragma unroll
+                    for (int t = 0; t < N / 16; ++t) S[rt][t] = zero4() + __builtin_nanf("");
         }
         if (!OUT && weigher && i + 1 < blocks) weights(buf ^ 1);
         lds_barrier();  // the tiles are read: the next block's may be written

@@ -164,9 +164,11 @@ int64_t kda_qk_norm_bwd_workspace_size(int32_t tokens, int32_t q_heads, int32_t 
  * Heads num_heads / num_groups * j .. share row j of B and C.  head_dim and
  * state_dim are 64 or 128 each.  dt and A are finite, dt * A <= 0 (any size: a
  * decay of zero included); a token with dt = 0 leaves the state as it is.
- * NaN and infinities in x, B or C propagate, but may also turn into NaN where
- * the formula has an infinity.  Row starts of x, B, C and out are 16-byte
- * aligned, and 64 rows of each span less than 2^31 bytes.  final_state may be initial_state itself.
+ * NaN and infinities in x, B or C reach what the formula says they reach (never
+ * an earlier token, another sequence or, from x, another row of a head), but may
+ * turn into NaN where it has an infinity.  Row starts of x, B, C and out are
+ * 16-byte aligned, and 64 rows of each span less than 2^31 bytes.  final_state
+ * may be initial_state itself.
  */
 int64_t kda_ssm_chunk_fwd_workspace_size(int32_t batch, int32_t seq_len, int32_t num_seqs,
                                          int32_t num_heads, int32_t head_dim, int32_t state_dim);
@@ -184,7 +186,8 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
  *   dx  like x;  dB, dC  like B and C (summed over the heads that share a row)
  *   ddt [batch, seq_len, num_heads], dA [num_heads], dD [num_heads] or NULL  fp32
  *   d_initial_state like initial_state, or NULL
- * The workspace holds the state at every block of 64 (fp32: 32) tokens twice:
+ * With a NaN or an infinity in an input, any gradient of its sequence and dA and
+ * dD may be NaN.  The workspace holds the state at every block of 64 (fp32: 32) tokens twice:
  * about seq_len / 32 states per head.
  */
 int64_t kda_ssm_chunk_bwd_workspace_size(int32_t batch, int32_t seq_len, int32_t num_seqs,
