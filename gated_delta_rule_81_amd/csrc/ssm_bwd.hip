@@ -324,18 +324,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void ssm_grad_kernel(SsmGrad a) {
                                         (g < 3 ? v[3] : 0.f) + tail;
                     tail += v[0] + v[1] + v[2] + v[3];
                     if (pg == it % PG) {
-#pragma unroll
-                        for (int part = 0; part < KQ; ++part) {
-                            bf16x4 o;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float f = part < KQ - 1 ? top_bits(qv[e]) : qv[e];
-                                o[e] = static_cast<bf16>(f);
-                                qv[e] -= f;
-                            }
-                            *reinterpret_cast<bf16x4 *>(sq + part * TQ::PLANE +
-                                                        TQ::at(s, 16 * it + 4 * g)) = o;
-                        }
+                        store_parts<TQ::PLANE>(sq + TQ::at(s, 16 * it + 4 * g), qv);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int t = 16 * it + 4 * g + e;

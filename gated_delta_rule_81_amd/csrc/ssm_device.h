@@ -47,6 +47,21 @@ template <int NP> __device__ __forceinline__ Parts<NP> split(const float (&f)[8]
     return p;
 }
 
+// Four floats as three parts, a plane each.
+template <int PLANE> __device__ __forceinline__ void store_parts(bf16 *at, float (&v)[4]) {
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+        bf16x4 h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float t = q < 2 ? top_bits(v[e]) : v[e];
+            h[e] = static_cast<bf16>(t);
+            v[e] -= t;
+        }
+        *reinterpret_cast<bf16x4 *>(at + q * PLANE) = h;
+    }
+}
+
 // acc += A B, smallest products first.
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mma(const Parts<NA> &a, const Parts<NB> &b, f32x4 acc) {
@@ -130,17 +145,17 @@ template <typename TL> struct FloatRowsAt {
         for (int ks = 0; ks < TL::LD / 64; ++ks)
 #pragma unroll
             for (int q = 0; q < 2; ++q)
-                o[ks][q] = TL::at(lane & 15, 2 * (32 * ks + 16 * q + 4 * (lane >> 4))) / 2;
+                o[ks][q] = TL::at(lane & 15, 2 * (32 * ks + 16 * q + 4 * (lane >> 4)));
     }
 };
-template <typename TL>
-__device__ __forceinline__ Parts<3> read_float_rows(const float *tile, int row0, int ks,
-                                                    const FloatRowsAt<TL> &at) {
-    const float *a = tile + row0 * (TL::LD / 2);
+template <typename TL, int NP>
+__device__ __forceinline__ Parts<NP> read_rows(const bf16 *tile, int row0, int ks,
+                                               const FloatRowsAt<TL> &at) {
+    const bf16 *a = tile + row0 * TL::LD;
     const f32x4 u = *reinterpret_cast<const f32x4 *>(a + at.o[ks][0]);
     const f32x4 v = *reinterpret_cast<const f32x4 *>(a + at.o[ks][1]);
     const float f[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
-    return split<3>(f);
+    return split<NP>(f);
 }
 
 // The same outer index with k = 32 ks + 8 (l / 16) + j, for products whose two
@@ -237,17 +252,7 @@ template <typename T, int ROWS, int COLS, int NT> struct Stage {
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(r[i][e]);
-#pragma unroll
-                for (int q = 0; q < 3; ++q) {
-                    bf16x4 h;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float t = q < 2 ? top_bits(v[e]) : v[e];
-                        h[e] = static_cast<bf16>(t);
-                        v[e] -= t;
-                    }
-                    *reinterpret_cast<bf16x4 *>(at + q * TL::PLANE) = h;
-                }
+                store_parts<TL::PLANE>(at, v);
             }
         }
     }

@@ -33,6 +33,7 @@
 #include "ssm_device.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace kda {
 namespace {
@@ -49,15 +50,16 @@ template <typename T, int P, int N, int HEADS, int MODE> struct ScanLds {
     typedef Tile<NI, L, HEADS * P> TX;
     // Row tiles 0 and 1 have nothing right of column 32: of 64 rows, 1 lies beside 0.
     static constexpr bool PACK = L == 64;
-    // The weights M as fp32 (a value takes two elements), split where they are read:
-    // three parts of each in LDS would leave one workgroup a CU.
-    typedef Tile<1, PACK ? 48 : L, 2 * L> TM;
+    // The weights M in three parts; of 64 rows as fp32 (a value takes two elements),
+    // split where they are read: three parts of each would leave one workgroup a CU.
+    typedef std::conditional_t<PACK, Tile<1, 48, 2 * L>, Tile<3, L, L>> TM;
+    typedef std::conditional_t<PACK, FloatRowsAt<TM>, RowsAt<TM>> MRows;
     __device__ static constexpr int m_row(int it) { return PACK && it > 0 ? it - 1 : it; }
     __device__ static constexpr int m_step(int it) { return PACK && it == 1; }  // 32 columns each
     __attribute__((aligned(16))) bf16 k[TK::ELEMS];
     __attribute__((aligned(16))) bf16 c[OUT ? TK::ELEMS : 8];
     __attribute__((aligned(16))) bf16 x[TX::ELEMS];
-    __attribute__((aligned(16))) float m[OUT ? HEADS * (TM::ELEMS / 2) : 4];
+    __attribute__((aligned(16))) bf16 m[OUT ? HEADS * TM::ELEMS : 8];
     __attribute__((aligned(16))) double cum[2][HEADS][L];  // log2 of the decay up to t
     __attribute__((aligned(16))) float dt[2][HEADS][L], w[2][HEADS][L], in[2][HEADS][L];
     // Weights of M's tiles below the diagonal as products, from the last token before
@@ -80,8 +82,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     typedef typename S_::TK TK;
     typedef typename S_::TX TX;
     typedef typename S_::TM TM;
-    bf16 *sk = lds.k, *sc = lds.c, *sx = lds.x;
-    float *sm = lds.m;
+    bf16 *sk = lds.k, *sc = lds.c, *sx = lds.x, *sm = lds.m;
     auto &s_cum = lds.cum;
     auto &s_dt = lds.dt, &s_w = lds.w, &s_in = lds.in;
     auto &s_tot = lds.tot;
@@ -94,7 +95,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     const RowsAt<TK> krow(lane);
     const WideAt<TK> kwide(lane);
-    const FloatRowsAt<TM> mrow(lane);
+    const typename S_::MRows mrow(lane);
     int kcol[N / 16];
 #pragma unroll
     for (int t = 0; t < N / 16; ++t) kcol[t] = cols_at<TK>(16 * t, lane);
@@ -191,7 +192,7 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         }
     }
     if constexpr (OUT) {  // tiles above the diagonal that a 32-wide step reads: zero for good
-        for (int i = tid; i < HEADS * (TM::ELEMS / 2); i += NT) sm[i] = 0.f;
+        for (int i = tid; i < HEADS * TM::ELEMS; i += NT) sm[i] = static_cast<bf16>(0.f);
     }
     for (int i = 0; i < blocks; ++i) {
         const int buf = i & 1, t0 = first_token(i);
@@ -257,7 +258,8 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                         m = mma(read_wide<TK, NI>(sk, 16 * is, ks, kwide),
                                 read_wide<TK, NI>(sc, 16 * it, ks, kwide), m);
                     const int t = 16 * it + r, s = 16 * is + 4 * g;
-                    const int to = TM::at(16 * S_::m_row(it) + r, 2 * (s + 32 * S_::m_step(it))) / 2;
+                    const int to = TM::at(16 * S_::m_row(it) + r,
+                                          (S_::PACK ? 2 : 1) * (s + 32 * S_::m_step(it)));
 #pragma unroll
                     for (int hh = 0; hh < HEADS; ++hh) {
                         float v[4];
@@ -276,8 +278,11 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                                 v[e] = s + e > t ? 0.f : s + e == t ? on + D[hh] : on;
                             }
                         }
-                        *reinterpret_cast<f32x4 *>(sm + hh * (TM::ELEMS / 2) + to) =
-                            f32x4{v[0], v[1], v[2], v[3]};
+                        bf16 *at = sm + hh * TM::ELEMS + to;
+                        if constexpr (S_::PACK)
+                            *reinterpret_cast<f32x4 *>(at) = f32x4{v[0], v[1], v[2], v[3]};
+                        else
+                            store_parts<TM::PLANE>(at, v);
                     }
                 }
             // y^T = S C^T e^{cum}: rows p, columns t
@@ -331,13 +336,13 @@ __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
         if constexpr (OUT) {
             const int n = pc.end - t0;
             T *out = static_cast<T *>(a.out) + (int64_t)h0 * P + row0 + 4 * g;
-            const float *weights_of = sm + mine * (TM::ELEMS / 2);
+            const bf16 *weights_of = sm + mine * TM::ELEMS;
 #pragma unroll
             for (int it = 0; it < L / 16; ++it) {
 #pragma unroll
                 for (int ks = 0; ks <= it / 2; ++ks) {
-                    const Parts<3> mt = read_float_rows<TM>(weights_of, 16 * S_::m_row(it),
-                                                            ks + S_::m_step(it), mrow);
+                    const Parts<3> mt = read_rows<TM, 3>(weights_of, 16 * S_::m_row(it),
+                                                         ks + S_::m_step(it), mrow);
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) y[rt][it] = mma(xt[rt][ks], mt, y[rt][it]);
                 }
