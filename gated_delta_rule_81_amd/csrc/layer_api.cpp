@@ -401,10 +401,10 @@ struct PiecePlan {
 };
 PiecePlan piece_plan(const kda::Seqs &s, int32_t heads, int32_t p, int directions) {
     // 512 workgroups of 128 state rows, two a CU, in one round (both directions of
-    // the backward are one launch).  32K x 64 heads of 64 rows 384 us, with 256
-    // workgroups 477, with 1024 409; of 128 rows 690, with 1024 723.  8K backward 549
-    // us, with 256 613, with 1024 567.  Equal rows that come to half of that are
-    // left whole.
+    // the backward are one launch).  Measured with two bf16 parts where y, dB and dC
+    // take three now: 32K x 64 heads of 64 rows 384 us, with 256 workgroups 477, with
+    // 1024 409; of 128 rows 690, with 1024 723.  8K backward 549 us, with 256 613, with
+    // 1024 567.  Equal rows that come to half of that are left whole.
     const int64_t want = 512 / directions, units = ((int64_t)heads * p + 127) / 128;
     const bool enough = !s.cu && s.num * units >= want / 2;
     // Down to one block of 64 tokens (1,227 tokens x 8 heads fp32: 30 us, against

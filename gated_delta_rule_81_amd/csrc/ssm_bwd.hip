@@ -24,13 +24,14 @@
 // two of 64 that share dt and A: every sum above is linear in the rows.
 //
 // 2 x 4096 tokens x 64 heads of 64 x 128 bf16, 0.29 GB of inputs and gradients:
-// 534 us = pieces 65, fold 17, states 168 (writes 0.54 GB of block states and
-// reads the inputs twice: 4.4 TB/s), gradients 330, dA and dD 4.5.  HBM bounds the
-// states pass.  In the gradient kernel VALU issues in 45% of the cycles, LDS works
-// in 27% and the matrix unit in 15%; its waves wait half of their time, at two
-// barriers a head and for LDS, with one workgroup of 8 waves a CU, the most that
+// 550 us a call; in a trace of warm calls pieces 60, fold 17, states 161 (writes
+// 1.07 GB of block states and reads the inputs once), gradients 308, dA and dD 4.6.
+// HBM bounds the states pass.  In the gradient kernel VALU issues in 45% of the
+// cycles, LDS works in 29% and the matrix unit in 17%; its waves wait 45% of their
+// time, at two barriers a head and for LDS, with one workgroup of 8 waves a CU, the most that
 // 145 KB of LDS and 230 registers leave.  Fewer VALU instructions do not help it
-// (weights below the diagonal as products, as the scan has them: 538 us).
+// (weights below the diagonal as products, as the scan has them: 538 us where 534
+// stood).  fp32: 992 us.
 #include "ssm_device.h"
 
 namespace kda {

@@ -80,7 +80,11 @@ __device__ __forceinline__ f32x4 mma(const Parts<NA> &a, const Parts<NB> &b, f32
 // Measured, 16 waves reading: 3.3 cycles a wave for 8 bytes a lane along rows
 // and for the transposing reads along columns, 4.1 for 16 bytes along rows; the
 // plain XOR with the row costs the transposing reads 4.1, other maps the 16-byte
-// reads 8, unswizzled rows 16 to 32.
+// reads 8, unswizzled rows 16 to 32.  By the counters, each kind of access in a loop
+// of its own: 16-byte row reads, transposing reads, reads of fp32 rows and the staged
+// 16-byte stores have no conflict cycles; two 8-byte row reads that the compiler joins
+// into one instruction, and stores of accumulators (M, Q, E: 16 rows x 4 pieces a
+// wave) have 8 in 16.
 template <int NP, int ROWS, int COLS> struct Tile {
     static_assert(COLS == 32 || COLS == 64 || COLS == 128, "swizzle");
     static constexpr int LD = COLS;

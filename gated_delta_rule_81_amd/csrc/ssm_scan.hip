@@ -23,13 +23,15 @@
 //
 // Bound by issue, not by HBM: fp32 operands (the state, its updates, the block's
 // weights) enter the matrix unit as three bf16 parts, so a token costs 3 times the
-// products above, and the parts (7 VALU instructions a value) and decays take as many
-// cycles again.  Two parts of the state and the weights where they enter y would
-// take 402 us where three take 438, but then sums that cancel to less than 2^-8 of
-// their terms lose more to the parts than to a bf16 output's own rounding.
-// 32K tokens x 64 heads of 64 x 128 bf16, 0.68 GB: 438 us a call.  Wave rows: a
-// 32-row wave reads every row of B, C and M from LDS once for two tiles of products
-// (with two parts: 16 rows 452 us, 32 rows 384).
+// products above, and the parts (5.5 VALU instructions a value) and decays take as
+// many cycles again.  Two parts of the state and the weights where they enter y
+// would take 383 us where three take 432, but then sums that cancel to less than
+// 2^-8 of their terms lose more to the parts than to a bf16 output's own rounding.
+// 32K tokens x 64 heads of 64 x 128 bf16, 0.68 GB: 427 to 439 us a call; in a trace
+// of warm calls pieces 109, fold 13 (67 MB, 5 TB/s), scan 319.  The scan's SIMDs
+// issue VALU in 55% of the cycles and the matrix unit works in 34%.  fp32: 990 us.
+// Wave rows: a 32-row wave reads every row of B, C and M from LDS once for two tiles
+// of products (with two parts: 16 rows 452 us, 32 rows 384).
 #include "ssm_device.h"
 
 #include <algorithm>
@@ -40,8 +42,6 @@ namespace {
 
 enum Mode { kLocal, kOut, kStates };
 
-// REV walks the blocks from the last to the first and the tokens' weights from
-// the right: the gradient's recurrence E_{t-1} = e^{dt_t A} (E_t + x_t k_t^T).
 // LDS of one block's tiles.
 template <typename T, int P, int N, int HEADS, int MODE> struct ScanLds {
     static constexpr int L = kSsmBlock<T>, NI = sizeof(T) == 2 ? 1 : 3;
@@ -73,6 +73,8 @@ template <typename T, int P, int N, int HEADS, int MODE> struct ScanLds {
     __attribute__((aligned(4))) unsigned char odd[8], from[OUT ? HEADS * P : 4];
 };
 
+// REV walks the blocks from the last to the first and the tokens' weights from
+// the right: the gradient's recurrence E_{t-1} = e^{dt_t A} (E_t + x_t k_t^T).
 template <typename T, int P, int N, int HEADS, int RT, int MODE, bool REV>
 __device__ __forceinline__ void scan_body(const SsmScan &a, int64_t unit,
                                           ScanLds<T, P, N, HEADS, MODE> &lds) {
@@ -548,7 +550,8 @@ template <typename T, int P, int N, int HEADS, int RT> struct Scan {
 
 // bf16: 128 rows a workgroup and 32 a wave, two heads of 64 that share B and C
 // together.  Measured with two parts of y's operands: 32K x 64 heads of 64 x 128 384
-// us, with one head a workgroup and 16 rows a wave 452; heads of 128 rows 690 and 814; 1,227 tokens x 8 heads of 64 x 64,
+// us, with one head a workgroup and 16 rows a wave 452; heads of 128 rows 690 and 814
+// (with three parts 806); 1,227 tokens x 8 heads of 64 x 64,
 // where the launches count, 28 and 29.  An odd number of heads a group leaves one
 // head a workgroup; fp32 has no LDS for two (three parts of every tile).
 template <typename T, int P, typename F> auto by_state(const SsmScan &a, F f) {

@@ -119,6 +119,8 @@ int kda_short_conv_step(const void *x, const float *weight, const float *bias, v
  *   q_weight, k_weight  [head_dim] or NULL (ones)                fp32
  *   table      [table_rows, rotary_dim]: cos, then sin           fp32
  *   positions  [tokens]  int32; values outside the table are moved into it
+ * Squares are summed in fp32 as they are: heads whose ss + eps is no normal fp32
+ * number (a norm over 1.8e19, or under 1.1e-19 with eps = 0) are not divided right.
  * head_dim is 64 or 128; rotary_dim a multiple of 16, at most head_dim, 0 = no
  * rotation (table and positions are then not read).  Row starts of q, k and
  * the outputs and the table are 16-byte aligned.
@@ -187,8 +189,11 @@ int kda_ssm_chunk_fwd(const void *x, const float *dt, const float *A, const void
  *   ddt [batch, seq_len, num_heads], dA [num_heads], dD [num_heads] or NULL  fp32
  *   d_initial_state like initial_state, or NULL
  * With a NaN or an infinity in an input, any gradient of its sequence and dA and
- * dD may be NaN.  The workspace holds the state at every block of 64 (fp32: 32) tokens twice:
- * about seq_len / 32 states per head.
+ * dD may be NaN.  The workspace holds the state at every block of 64 (fp32: 32)
+ * tokens from both sides: about seq_len / 32 (fp32: seq_len / 16) states per head,
+ * and one or two a sequence more when packed; beside them twice the forward's
+ * workspace and, where a group's heads are split into sets, dB and dC in fp32 of
+ * each set.
  */
 int64_t kda_ssm_chunk_bwd_workspace_size(int32_t batch, int32_t seq_len, int32_t num_seqs,
                                          int32_t num_heads, int32_t num_groups, int32_t head_dim,
