@@ -22,9 +22,14 @@ _NORMS = {"l2": 0, "rms": 1}
 _MOST = (1 << 31) - 1  # sizes go to the library in 32 bits, which ctypes would cut off
 
 
-def _fits(name, *sizes):
+def _sizes_fit(name, *sizes):
     if max(sizes, default=0) > _MOST:
         raise ValueError(f"{name}: a size of {max(sizes)} does not fit 32 bits")
+
+
+def _fits(t, name):
+    if not 0 < t.numel() <= _MOST:  # else no size is larger
+        _sizes_fit(name, *t.shape)
 
 
 def _rows(t, name, dtype, shape, device, lead: int) -> int:
@@ -73,7 +78,7 @@ def _dtype(t, name):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    _fits(name, *t.shape)
+    _fits(t, name)
     return _DTYPES[t.dtype]
 
 
@@ -85,7 +90,7 @@ def _num_seqs(cu_seqlens, batch, device):
     _expect(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, device)
     if batch != 1:
         raise ValueError("packed sequences need a batch of 1")
-    _fits("cu_seqlens", cu_seqlens.shape[0])
+    _fits(cu_seqlens, "cu_seqlens")
     return cu_seqlens.shape[0] - 1
 
 
@@ -134,7 +139,7 @@ def _conv_common(x, weight, bias, activation):
         raise ValueError(f"activation must be 'silu' or 'none', got {activation!r}")
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [C, width]")
-    _fits("weight", weight.shape[1])
+    _fits(weight, "weight")
     C = x.shape[2]
     _expect(weight, "weight", torch.float32, (C, weight.shape[1]), x.device)
     _expect(bias, "bias", torch.float32, (C,), x.device)
@@ -176,7 +181,7 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
 
 def short_conv_bwd_workspace_size(batch: int, seq_len: int, channels: int, width: int) -> int:
     """Bytes of workspace ``short_conv_bwd`` needs."""
-    _fits("short_conv_bwd", batch, seq_len, channels, width)
+    _sizes_fit("short_conv_bwd", batch, seq_len, channels, width)
     n = lib().kda_short_conv_bwd_workspace_size(batch, seq_len, channels, width)
     if n < 0:
         raise ValueError("invalid sizes")
@@ -264,13 +269,15 @@ def _qk_common(q, k, q_weight, k_weight, table, positions, kind):
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError("table must be [rows, rotary_dim]")
         rows, rot = table.shape
-        _fits("table", rows, rot)
+        _fits(table, "table")
         _expect(table, "table", torch.float32, (rows, rot), dev)
         _expect(positions, "positions", torch.int32, q.shape[:-2], dev)
     tokens = 1
     for n in q.shape[:-2]:
         tokens *= n
-    _fits("q and k", tokens, k.shape[-2])
+    _fits(k, "k")
+    if tokens > _MOST:
+        _sizes_fit("q and k", tokens)
     return tokens, q.shape[-2], k.shape[-2], d, rot, rows, strides, lead
 
 
@@ -305,7 +312,7 @@ def qk_norm(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor] =
 
 def qk_norm_bwd_workspace_size(tokens: int, q_heads: int, k_heads: int, head_dim: int) -> int:
     """Bytes of workspace ``qk_norm_bwd`` needs when it returns weights' gradients."""
-    _fits("qk_norm_bwd", tokens, q_heads, k_heads, head_dim)
+    _sizes_fit("qk_norm_bwd", tokens, q_heads, k_heads, head_dim)
     n = lib().kda_qk_norm_bwd_workspace_size(tokens, q_heads, k_heads, head_dim)
     if n < 0:
         raise ValueError("invalid sizes")
@@ -349,7 +356,7 @@ def _ssm_common(x, dt, A, B, C, D, lead):
     if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
         raise ValueError("B must be [..., G, N] with the leading axes of x")
     G, N = B.shape[lead:]
-    _fits("B", G, N)
+    _fits(B, "B")
     dev, dtype = x.device, x.dtype
     if H % max(G, 1) or (H and not G):
         raise ValueError(f"{H} heads cannot share {G} groups of B and C")
@@ -368,7 +375,7 @@ def ssm_workspace_size(batch: int, seq_len: int, num_heads: int, head_dim: int, 
                        num_seqs: int = 0) -> int:
     """Bytes of workspace ``ssm_chunk_fwd`` needs (``num_seqs``: packed sequences,
     0 for a batch of equal rows)."""
-    _fits("ssm_chunk_fwd", batch, seq_len, num_seqs, num_heads, head_dim, state_dim)
+    _sizes_fit("ssm_chunk_fwd", batch, seq_len, num_seqs, num_heads, head_dim, state_dim)
     n = lib().kda_ssm_chunk_fwd_workspace_size(batch, seq_len, num_seqs, num_heads, head_dim,
                                                state_dim)
     if n < 0:
@@ -420,7 +427,7 @@ def ssm_bwd_workspace_size(batch: int, seq_len: int, num_heads: int, num_groups:
                            num_seqs: int = 0) -> int:
     """Bytes of workspace ``ssm_chunk_bwd`` needs (``num_seqs``: packed sequences,
     0 for a batch of equal rows)."""
-    _fits("ssm_chunk_bwd", batch, seq_len, num_seqs, num_heads, num_groups, head_dim, state_dim)
+    _sizes_fit("ssm_chunk_bwd", batch, seq_len, num_seqs, num_heads, num_groups, head_dim, state_dim)
     n = lib().kda_ssm_chunk_bwd_workspace_size(batch, seq_len, num_seqs, num_heads, num_groups,
                                                head_dim, state_dim, _DTYPES[dtype])
     if n < 0:
