@@ -27,7 +27,7 @@
 // many cycles again.  Two parts of the state and the weights where they enter y
 // would take 383 us where three take 432, but then sums that cancel to less than
 // 2^-8 of their terms lose more to the parts than to a bf16 output's own rounding.
-// 32K tokens x 64 heads of 64 x 128 bf16, 0.68 GB: 427 to 439 us a call; in a trace
+// 32K tokens x 64 heads of 64 x 128 bf16, 0.68 GB: 427 to 451 us a call; in a trace
 // of warm calls pieces 109, fold 13 (67 MB, 5 TB/s), scan 319.  The scan's SIMDs
 // issue VALU in 55% of the cycles and the matrix unit works in 34%.  fp32: 990 us.
 // Wave rows: a 32-row wave reads every row of B, C and M from LDS once for two tiles

@@ -21,7 +21,7 @@
  *     row b is row b * seq_len + t), at least the row's own length.  Everything
  *     else is dense.  Offsets are 64-bit; tokens are counted in 32 bits (batch *
  *     seq_len at most 2^31 - 4096).  A launch holds less than 2^32 threads: where
- *     tens of millions of sequences, sessions or channels need more, the call is
+ *     millions of sequences, sessions or channels need more, the call is
  *     refused (KDA_ERR_UNSUPPORTED) before any work.
  *   - Parameters (weights, biases, A, D), dt and scan states are fp32; sums,
  *     norms and states are held in fp32; outputs are rounded once.
