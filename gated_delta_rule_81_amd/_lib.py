@@ -1,5 +1,5 @@
-"""ctypes loader for ``libkda.so`` (the C ABI of include/kda.h and
-include/kda_layer.h).
+"""ctypes loader for ``libkda.so`` (the C ABI of include/kda.h, include/kda_layer.h
+and include/kda_cache.h).
 
 The library is built in-tree by ``python -m gated_delta_rule_81_amd.build``.
 There is no fallback: if the library is missing, every call raises.
@@ -81,6 +81,17 @@ LAYER_SIGNATURES = {
                              _i64, _i64, _i64, _i64, _i32, _vp], ctypes.c_int),
 }
 
+# The operators on a paged cache: include/kda_cache.h, in its order.
+CACHE_SIGNATURES = {
+    "kda_cache_append": ([_vp, _vp, _vp, _fp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
+                          _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i64, _i64, _i64, _i64,
+                          _i64, _i64, _i64, _i32, _i32, _vp], ctypes.c_int),
+    "kda_prefix_attn_workspace_size": ([_i32] * 10, _i64),
+    "kda_prefix_attn_fwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _fp, _i32, _i32, _i32,
+                             _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i64, _i64, _i64, _i64,
+                             _i64, _f32, _i32, _vp, _i64, _vp], ctypes.c_int),
+}
+
 _lib = None
 
 
@@ -102,7 +113,8 @@ def lib():
                 f"{LIB_PATH} is not built; run `python -m gated_delta_rule_81_amd.build`")
         import torch  # noqa: F401
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in {**SIGNATURES, **LAYER_SIGNATURES}.items():
+        for name, (args, res) in {**SIGNATURES, **LAYER_SIGNATURES,
+                                  **CACHE_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = res

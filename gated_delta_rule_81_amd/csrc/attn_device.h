@@ -1,0 +1,322 @@
+// attn_device.h -- building blocks of the attention kernels over a paged cache:
+// tiles of the cache in LDS, the products of a tile with 32 query rows, and the
+// running maximum and sum of their softmax.
+//
+// Orientation.  Scores are formed as S^T = K Q^T in 32 x 32 tiles: lane l holds
+// query row l % 32 and the sixteen tokens 8 (i / 4) + 4 (l / 32) + i % 4.  A
+// row's maximum and sum are then in-lane operations and one exchange of the two
+// halves, and the probabilities already lie as the second operand of
+// O^T = V^T P^T, whose k order they set: for the 16 tokens of a step, slots
+// 0..3 and 4..7 of a lane are tokens 4 (l / 32) + {0..3} and 8 on.
+//
+// Tiles.  The rows of K and V go from the cache to LDS without registers
+// (global_load_lds, 16 bytes a lane), in the cache's order except that the
+// 16-byte chunks of a row change places by an XOR with turn(row), done by the
+// choice of each lane's source.  Rows 0..15 at one chunk (the reads of K) and
+// four rows of four neighbouring chunks (the transposing reads of V) then fall
+// on different banks.
+#pragma once
+
+#include "cache_device.h"
+
+#include <type_traits>
+
+namespace kda {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+
+// A tile of rows of C 16-byte chunks in LDS.
+template <int C> __device__ __forceinline__ int tile_turn(int row) {
+    return C % 16 == 0 ? ((row & 3) << 2) | ((row >> 2) & 3)
+                       : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+}
+template <int C> __device__ __forceinline__ int tile_at(int row, int chunk) {
+    return (row * C + (chunk ^ tile_turn<C>(row))) * 16;
+}
+
+// Read in place of a token that is not there: its product with a probability of
+// zero has to be zero.
+__device__ const u32x4 kNoRow[80] = {};
+
+__device__ __forceinline__ float half_max(float x) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                    false);
+    return __builtin_fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                    false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// Products of one type of element.  chunk(): acc += over the channels of one
+// 16-byte chunk per half wave.  values(): the operand of V^T for 16 tokens from
+// `row0` and 32 channels from `d0` (CH chunks a row), and its product.
+template <typename T> struct AttnMma;
+
+template <> struct AttnMma<bf16> {
+    static constexpr int kOps = 1;  // products that use one Value
+    struct Value { bf16x8 a; };
+    typedef bf16x8 Prob;
+    __device__ static f32x16 chunk(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+    // Lane's place in a tile for the transposing reads, channels 0..31, tokens 0..3 of
+    // each half; others are reached by the offset of `step`.
+    template <int CH> __device__ static int value_at(int row0, int d0, int lane, int second) {
+        const int row = row0 + 8 * second + 4 * (lane >> 5) + ((lane & 15) >> 2);
+        const int col = d0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+        return tile_at<CH>(row, col >> 3) + (col & 7) * 2;
+    }
+    template <int CH> __device__ static Value value(lds_char *tile, int row0, int d0, int lane) {
+        typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+        const bf16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+            (lds_bf16x4 *)(tile + value_at<CH>(row0, d0, lane, 0)));
+        const bf16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+            (lds_bf16x4 *)(tile + value_at<CH>(row0, d0, lane, 1)));
+        return {__builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7)};
+    }
+    __device__ static Prob prob(const f32x16 &s, int step) {
+        Prob p;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = static_cast<bf16>(s[8 * step + j]);
+        return p;
+    }
+    __device__ static f32x16 mma(const Value &v, const Prob &p, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.a, p, c, 0, 0, 0);
+    }
+    // The operand with every token but `j` of the 16 left out.
+    __device__ static Value only(const Value &v, int j, int lane) {
+        Value o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            o.a[e] = 8 * (e / 4) + 4 * (lane >> 5) + e % 4 == j ? v.a[e] : static_cast<bf16>(0.f);
+        return o;
+    }
+};
+
+template <> struct AttnMma<float> {
+    struct Value { float a[8]; };
+    struct Prob { float p[8]; };
+    __device__ static f32x16 chunk(u32x4 a, u32x4 b, f32x16 c) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c,
+                                                     0, 0, 0);
+        return c;
+    }
+    template <int CH> __device__ static Value value(lds_char *tile, int row0, int d0, int lane) {
+        typedef __attribute__((address_space(3))) float lds_float;
+        Value v;
+        const int col = d0 + (lane & 31);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int row = row0 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
+            v.a[e] = *(lds_float *)(tile + tile_at<CH>(row, col >> 2) + (col & 3) * 4);
+        }
+        return v;
+    }
+    __device__ static Prob prob(const f32x16 &s, int step) {
+        Prob p;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p.p[j] = s[8 * step + j];
+        return p;
+    }
+    __device__ static f32x16 mma(const Value &v, const Prob &p, f32x16 c) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(v.a[e], p.p[e], c, 0, 0, 0);
+        return c;
+    }
+    __device__ static Value only(const Value &v, int j, int lane) {
+        Value o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            o.a[e] = 8 * (e / 4) + 4 * (lane >> 5) + e % 4 == j ? v.a[e] : 0.f;
+        return o;
+    }
+};
+
+// Splits.  A length of `units` (of kSplitTokens tokens) in at most `splits` parts
+// of `per` units each, the last one shorter.
+__device__ __forceinline__ int split_units(int units, int splits) {
+    return splits > 0 ? (units + splits - 1) / splits : 0;
+}
+__device__ __forceinline__ int units_of(int tokens) {
+    return (tokens + kSplitTokens - 1) / kSplitTokens;
+}
+
+__device__ __forceinline__ int prefix_tokens(const AttnArgs &a) {
+    if (!a.prefix_width) return 0;
+    const int64_t most = (int64_t)a.prefix_width * a.pages.size;
+    const int n = word_at(a.prefix_len, 0);
+    return n < 0 ? 0 : (n > most ? (int)most : n);
+}
+
+// Where the tokens of a tile lie: lane l looks after token base + l.
+struct Places {
+    const int32_t *table;
+    int base, end;  // tokens [base, end) of the tile at hand
+};
+__device__ __forceinline__ int page_entry(const AttnArgs &a, const int32_t *table, int tok, int end) {
+    return tok < end ? table[a.pages.by_size(tok)] : -1;
+}
+// Byte offset of the token behind the start of its head, -1 where it is not to be read.
+__device__ __forceinline__ int64_t token_offset(const AttnArgs &a, int entry, int tok) {
+    if (entry < 0 || entry >= a.pages.count) return -1;
+    const int in = tok - (int)a.pages.by_size(tok) * a.pages.size;
+    return (int64_t)entry * a.pages.page + (int64_t)in * a.pages.token;
+}
+__device__ __forceinline__ int64_t shfl64(int64_t x, int lane) {
+    const int lo = __builtin_amdgcn_ds_bpermute(4 * lane, (int)x);
+    const int hi = __builtin_amdgcn_ds_bpermute(4 * lane, (int)(x >> 32));
+    return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+
+// 16 bytes a lane from memory to LDS at `to` + 16 * lane.  In assembly, so that the compiler
+// does not wait for all loads on their way before each read of LDS; what is read is
+// waited for by wait_loads().  m0 is read one wait state after it is written.
+__device__ __forceinline__ void load_lds16(const char *from, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :
+                 : "v"(from), "s"(to)
+                 : "memory");
+}
+// Until at most N of this wave's loads are on their way.
+template <int N> __device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Rows of C chunks of `rows` tokens into a tile, 64 chunks a load, wave `wave` of NW taking
+// every NW-th load; off: each token's offset, at its lane.
+template <int C, int ROWS, int NW>
+__device__ __forceinline__ void load_tile(const char *base, int64_t off, lds_char *tile, int wave,
+                                          int lane) {
+    constexpr int LOADS = ROWS * C / 64;
+#pragma unroll
+    for (int i = 0; i < (LOADS + NW - 1) / NW; ++i) {
+        const int load = NW * i + wave;
+        if (LOADS % NW != 0 && load >= LOADS) break;
+        const int p = 64 * load + lane, row = p / C;
+        const int chunk = (p % C) ^ tile_turn<C>(row);
+        const int64_t o = shfl64(off, row);
+        const char *src = o < 0 ? reinterpret_cast<const char *>(kNoRow) : base + o;
+        load_lds16(src + chunk * 16, (uint32_t)(uintptr_t)tile + 1024 * load);
+    }
+}
+
+// Whether one of the 16-byte chunks lane, lane + 64, .. under `chunks` of a tile holds a NaN
+// or an infinity, of any lane.
+template <typename T>
+__device__ __forceinline__ bool any_odd(lds_char *tile, int chunks, int lane) {
+    bool odd = false;
+    for (int i = lane; i < chunks; i += 64) {
+        const u32x4 w = *(lds_u32x4 *)(tile + 16 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            odd |= (w[e] & 0x7f800000u) == 0x7f800000u ||
+                   (sizeof(T) == 2 && (w[e] & 0x7f80u) == 0x7f80u);
+    }
+    return __ballot(odd) != 0;
+}
+
+// The lane number as a value the compiler cannot trace: what is formed from it in a rare
+// path is formed there and does not fill the registers as a constant of the loop around.
+__device__ __forceinline__ int here(int lane) {
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+// Workgroup barrier that waits for this wave's LDS operations only: loads stay on their way.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// A maximum that may stand in an exponent's difference.
+__device__ __forceinline__ float usable(float m) { return m == -__builtin_inff() ? 0.f : m; }
+
+// Scores of tokens that are not there (valid) or lie at or behind the row's `ahead`-th of
+// the tile's become -inf.
+template <int TT>
+__device__ __forceinline__ void hide_scores(f32x16 (&s)[TT], uint64_t valid, int ahead, int lane) {
+    // bit 8 (e / 4) + e % 4 of word j: whether this lane's row sees its token e
+    uint64_t see = ahead <= 0 ? 0 : (ahead < 32 * TT ? valid & ~(~0ull << ahead) : valid);
+    see >>= 4 * (here(lane) >> 5);
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+        const uint32_t word = (uint32_t)(see >> (32 * j));
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            s[j][e] = word & (1u << (8 * (e / 4) + e % 4)) ? s[j][e] : -__builtin_inff();
+    }
+}
+
+// Scores to probabilities relative to the running maximum m, their sum into l.
+template <int TT, int DT>
+__device__ __forceinline__ void soften(f32x16 (&s)[TT], float &m, float &l, f32x16 (&o)[DT],
+                                       float sl) {
+    float top = s[0][0];
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, s[j][e]);
+    top = half_max(top);
+    // The maximum moves on only where a score passes it by 2^8 (at first by any): exponents
+    // up to 8 lose nothing in fp32, and the steps of their bf16 values are relative.
+    if (__ballot((top - m) * sl > 8.f)) {
+        const float to = __builtin_fmaxf(m, top), f = fast_exp2((m - usable(to)) * sl);
+        m = to, l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= f;
+    }
+    const float ms = usable(m) * sl;
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            s[j][e] = fast_exp2(s[j][e] * sl - ms);
+            l += s[j][e];
+        }
+}
+
+// o += V^T P^T over a tile's tokens, channels 32 d0 .. 32 (d0 + DT).
+template <typename T, int TT, int DT, int CH>
+__device__ __forceinline__ void add_values(const f32x16 (&s)[TT], lds_char *tile, int d0, int lane,
+                                           f32x16 (&o)[DT]) {
+    typedef AttnMma<T> M;
+#pragma unroll
+    for (int j = 0; j < 2 * TT; ++j) {
+        const typename M::Prob p = M::prob(s[j / 2], j % 2);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+            o[d] = M::mma(M::template value<CH>(tile, 16 * j, 32 * (d0 + d), lane), p, o[d]);
+    }
+}
+// The same with the tokens one by one, each for the rows that see it (those under ahead).
+template <typename T, int TT, int DT, int CH>
+__device__ __forceinline__ void add_values_apart(const f32x16 (&s)[TT], lds_char *tile, int d0,
+                                                 int ahead, int lane, f32x16 (&o)[DT]) {
+    typedef AttnMma<T> M;
+#pragma unroll
+    for (int j = 0; j < 2 * TT; ++j) {
+        const typename M::Prob p = M::prob(s[j / 2], j % 2);
+        const int ln = here(lane);
+#pragma unroll 1
+        for (int e = 0; e < 16; ++e) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const typename M::Value v =
+                    M::only(M::template value<CH>(tile, 16 * j, 32 * (d0 + d), ln), e, ln);
+                const f32x16 with = M::mma(v, p, o[d]);
+                o[d] = 16 * j + e < ahead ? with : o[d];
+                __builtin_amdgcn_sched_barrier(0);  // one at a time: few registers
+            }
+        }
+    }
+}
+
+}  // namespace kda

@@ -1,0 +1,287 @@
+// attn_few.hip -- attention of few query rows (at most 32: one token's heads of a group, or a
+// few tokens') over a long cache, and the join of the parts of every row.
+#include "attn_device.h"
+
+namespace kda {
+namespace {
+
+constexpr int kTile = 32;  // tokens of a wave's tile
+
+template <typename T, int D, int NW, int ST> struct FewShape {
+    static constexpr int C = D * (int)sizeof(T) / 16;   // 16-byte chunks of a row
+    static constexpr int HALF = kTile * C * 16, BUF = 2 * HALF;
+    static constexpr int LOADS = 2 * kTile * C / 64;    // of a tile, keys and values
+    static constexpr int LD = D + 4;                    // floats between rows of the joined output
+    static constexpr int RING = NW * ST * BUF, JOIN = NW * 32 * LD * 4;
+    static constexpr int LDS = (RING > JOIN ? RING : JOIN) + NW * 32 * 8;
+    static_assert((ST - 1) * LOADS < 64, "the counter of loads on their way");
+};
+
+// One workgroup per (session, kv head, split), or per (kv head, split) of the prefix.
+template <typename T, int D, int NW, int ST>
+__global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, int own_blocks) {
+    typedef FewShape<T, D, NW, ST> S;
+    typedef AttnMma<T> M;
+    constexpr int DT = D / 32, KS = S::C / 2;
+    __shared__ __attribute__((aligned(1024))) char smem[S::LDS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5, G = a.group;
+    const bool pre = (int)blockIdx.x >= own_blocks;
+    const int b = pre ? blockIdx.x - own_blocks : blockIdx.x;
+    const int splits = pre ? a.plan.prefix_splits : a.plan.own_splits;
+    const int split = b % splits, hk = b / splits % a.kv_heads, session = b / splits / a.kv_heads;
+    int tok0 = 0, n = a.seqs.tokens, len;
+    if (pre) {
+        len = prefix_tokens(a);
+    } else {
+        tok0 = session_first(a.seqs, session);
+        n = session_first(a.seqs, session + 1) - tok0;
+        len = own_tokens(a.seqs, a.pages, session);
+    }
+    if (n <= 0 || (int64_t)n * G > 32) return;
+    const int rows = n * G;
+    const int units = units_of(len), per = split_units(units, splits);
+    if (split * per >= units && (split > 0 || a.part)) return;
+    auto seen = [&](int row) { return pre ? len : len - n + row / G + 1; };
+    const int64_t to = (int64_t)(split + 1) * per * kSplitTokens;
+    const int beg = split * per * kSplitTokens, end = to < len ? (int)to : len;
+    const int32_t *table = pre ? a.prefix_pages : a.seqs.table + (int64_t)session * a.seqs.width;
+
+    const int row = (lane & 31) < rows ? lane & 31 : rows - 1;
+    const int lim = seen(row), lim_min = seen(0);
+    u32x4 q[KS];
+    {
+        const T *src = static_cast<const T *>(a.q) + (int64_t)(tok0 + row / G) * a.q_stride +
+                       ((int64_t)hk * G + row % G) * D;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            q[s] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(src) +
+                                                    16 * (2 * s + half));
+    }
+    const char *kc = static_cast<const char *>(a.k_cache) + (int64_t)hk * a.pages.head;
+    const char *vc = static_cast<const char *>(a.v_cache) + (int64_t)hk * a.pages.head;
+    lds_char *ring = (lds_char *)smem + wave * (ST * S::BUF);
+
+    // This wave's tiles are its own: every NW-th, in a ring of ST places that no other wave
+    // reads, so that only its own loads are waited for.  A window of 64 entries of the page
+    // table is held in the lanes.
+    const int tiles = (end - beg + kTile - 1) / kTile;
+    const int count = tiles > wave ? (tiles - wave + NW - 1) / NW : 0;
+    int first = 0, entries = -1;
+    bool held = false;
+    auto base_of = [&](int k) { return beg + (k * NW + wave) * kTile; };
+    auto issue = [&](int k, int place) -> uint32_t {
+        const int base = base_of(k), tok = base + lane;
+        const int stop = base + kTile < end ? base + kTile : end;
+        const int lo = a.pages.by_size(base), hi = a.pages.by_size(stop - 1);
+        if (!held || hi - first >= 64) {
+            const int most = a.pages.by_size(end - 1);
+            held = true, first = lo;
+            entries = table[lo + lane < most ? lo + lane : most];
+        }
+        const int idx = a.pages.by_size(tok < stop ? tok : base);
+        int entry = __builtin_amdgcn_ds_bpermute(4 * (idx - first), entries);
+        entry = tok < stop ? entry : -1;
+        const int64_t off = token_offset(a, entry, tok);
+        lds_char *buf = ring + place * S::BUF;
+        load_tile<S::C, kTile, 1>(kc, off, buf, 0, lane);
+        load_tile<S::C, kTile, 1>(vc, off, buf + S::HALF, 0, lane);
+        return (uint32_t)__ballot(off >= 0);
+    };
+
+    f32x16 o[DT];
+    float m = -__builtin_inff(), l = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = f32x16(0.f);
+    const float sl = a.scale * kLog2e;
+    uint32_t valid[ST];
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) valid[i] = i < count ? issue(i, i) : 0;
+    int place = 0, ahead = ST - 1;
+    for (int k = 0; k < count; ++k) {
+        if (k + ST - 1 < count) {
+            valid[ST - 1] = issue(k + ST - 1, ahead);
+            wait_loads<(ST - 1) * S::LOADS>();
+        } else {
+            wait_loads<0>();
+        }
+        const int base = base_of(k);
+        lds_char *kt = ring + place * S::BUF, *vt = kt + S::HALF;
+        f32x16 s[1] = {f32x16(0.f)};
+#pragma unroll
+        for (int c = 0; c < KS; ++c)
+            s[0] = M::chunk(*(lds_u32x4 *)(kt + tile_at<S::C>(lane & 31, 2 * c + half)), q[c], s[0]);
+        const bool later = base + kTile > lim_min;
+        if (later || valid[0] != ~0u) hide_scores<1>(s, valid[0], lim - base, lane);
+        soften<1, DT>(s, m, l, o, sl);
+        if (later && any_odd<T>(vt, kTile * S::C, lane))
+            add_values_apart<T, 1, DT, S::C>(s, vt, 0, lim - base, lane, o);
+        else
+            add_values<T, 1, DT, S::C>(s, vt, 0, lane, o);
+        // the tile is read before its place is filled again
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) valid[i] = valid[i + 1];
+        place = place + 1 == ST ? 0 : place + 1;
+        ahead = ahead + 1 == ST ? 0 : ahead + 1;
+    }
+
+    // the waves' parts are joined through LDS, in wave order
+    l = half_sum(l);
+    __syncthreads();
+    float *join = reinterpret_cast<float *>(smem);
+    float2 *stat = reinterpret_cast<float2 *>(smem + (S::RING > S::JOIN ? S::RING : S::JOIN));
+    if ((lane & 31) < rows) {
+        float *dst = join + (wave * 32 + (lane & 31)) * S::LD + 4 * half;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                store4(dst + 32 * d + 8 * e, o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2],
+                       o[d][4 * e + 3]);
+        if (half == 0) stat[wave * 32 + lane] = float2{m, l};
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * NW) {
+        const int r = i / (D / 4), c = 4 * (i % (D / 4));
+        float top = -__builtin_inff(), sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) top = __builtin_fmaxf(top, stat[w * 32 + r].x);
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float2 v = stat[w * 32 + r];
+            if (v.x == -__builtin_inff()) continue;  // nothing of it was seen
+            const float f = fast_exp2((v.x - top) * sl);
+            sum += v.y * f;
+            y += *reinterpret_cast<const f32x4 *>(join + (w * 32 + r) * S::LD + c) * f;
+        }
+        const int64_t token = tok0 + r / G, h = (int64_t)hk * G + r % G;
+        const int64_t at = token * a.heads + h;
+        if (a.part) {
+            const int64_t slot = (pre ? 0 : a.plan.prefix_splits) + split;
+            const int64_t to = slot * a.seqs.tokens * a.heads + at;
+            *reinterpret_cast<f32x4 *>(a.part + to * D + c) = y;
+            if (c == 0) a.stat[to] = float2{top * sl, sum};
+        } else {
+            const bool any = seen(r) > 0;
+            const float inv = any ? 1.f / sum : 0.f;
+            T *out = static_cast<T *>(a.out) + token * a.out_stride + h * D + c;
+            store4(out, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+            if (a.lse && c == 0)
+                a.lse[at] = any ? (usable(top) * sl + __builtin_log2f(sum)) * kLn2
+                                : -__builtin_inff();
+        }
+    }
+}
+
+int64_t few_blocks(const AttnArgs &a, int64_t *own) {
+    const AttnPlan &p = a.plan;
+    *own = p.few_rows > 0 && !p.joint ? (int64_t)a.seqs.num * a.kv_heads * p.own_splits : 0;
+    return *own + (p.prefix_few ? (int64_t)a.kv_heads * p.prefix_splits : 0);
+}
+
+template <typename T, int D, int NW, int ST> int few(const AttnArgs &a, hipStream_t stream) {
+    int64_t own;
+    const int64_t n = few_blocks(a, &own);
+    if (n > 0)
+        hipLaunchKernelGGL((attn_few_kernel<T, D, NW, ST>), dim3((unsigned)n), dim3(64 * NW),
+                           0, stream, a, (int)own);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+// Row (token, head): the parts of its splits, in their order.  DV / 4 lanes a row.
+template <typename T, int DV>
+__global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
+    constexpr int LANES = DV / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, at = i / LANES;
+    const int c = 4 * (int)(i % LANES);
+    const int64_t rows = (int64_t)a.seqs.tokens * a.heads;
+    if (at >= rows) return;
+    const int token = (int)(at / a.heads), h = (int)(at % a.heads);
+    // the session (the last that begins at or before the token)
+    int lo = 0;
+    if (a.seqs.cu) {
+        int hi = a.seqs.num - 1;
+        while (lo < hi) {
+            const int mid = (int)(((int64_t)lo + hi + 1) >> 1);
+            if (a.seqs.cu[mid] <= token)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+    } else {
+        lo = token / a.seqs.each;
+    }
+    int first = lo * a.seqs.each, last = first + a.seqs.each;
+    if (a.seqs.cu) first = a.seqs.cu[lo], last = a.seqs.cu[lo + 1];
+    first = first < 0 ? 0 : first;
+    last = last > a.seqs.tokens ? a.seqs.tokens : last;
+    if (token < first || token >= last) return;  // in no session
+    const int64_t most = (int64_t)a.seqs.width * a.pages.size;
+    int L = a.seqs.lens[lo];
+    L = L < 0 ? 0 : (L > most ? (int)most : L);
+    const int P = prefix_tokens(a);
+    const bool any = P > 0 || L - (last - token) + 1 > 0;
+
+    // which slots hold a part
+    const AttnPlan &p = a.plan;
+    const int pu = units_of(P), lu = units_of(L);
+    const int u0 = p.joint ? pu + lu : pu, per0 = split_units(u0, p.prefix_splits);
+    const int n0 = per0 > 0 ? (u0 + per0 - 1) / per0 : 0;
+    const int per1 = p.joint ? 0 : split_units(lu, p.own_splits);
+    const int n1 = per1 > 0 ? (lu + per1 - 1) / per1 : 0;
+    float top = -__builtin_inff(), sum = 0.f;
+    for (int k = 0; k < n0 + n1; ++k) {
+        const int64_t slot = k < n0 ? k : p.prefix_splits + k - n0;
+        top = __builtin_fmaxf(top, a.stat[slot * rows + at].x);
+    }
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < n0 + n1; ++k) {
+        const int64_t slot = k < n0 ? k : p.prefix_splits + k - n0;
+        const float2 v = a.stat[slot * rows + at];
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(a.part + (slot * rows + at) * DV + c);
+        if (v.x == -__builtin_inff()) continue;  // nothing of it was seen
+        const float f = fast_exp2(v.x - top);
+        sum += v.y * f;
+        y += w * f;
+    }
+    const float inv = any ? 1.f / sum : 0.f;
+    T *out = static_cast<T *>(a.out) + token * a.out_stride + (int64_t)h * DV + c;
+    store4(out, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    if (a.lse && c == 0)
+        a.lse[at] = any ? (usable(top) + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
+}
+
+}  // namespace
+
+int64_t attn_few_threads(const AttnArgs &a) {
+    int64_t own;
+    return few_blocks(a, &own) * 256;
+}
+int64_t attn_merge_threads(const AttnArgs &a) {
+    return ((int64_t)a.seqs.tokens * a.heads * (a.dv / 4) + 255) / 256 * 256;
+}
+
+int launch_attn_few(const AttnArgs &a, hipStream_t stream) {
+    if (a.dtype == kDtypeF32)
+        return a.d == 64 ? few<float, 64, 4, 2>(a, stream) : few<float, 128, 2, 2>(a, stream);
+    return a.d == 64 ? few<bf16, 64, 4, 2>(a, stream) : few<bf16, 128, 4, 2>(a, stream);
+}
+
+int launch_attn_merge(const AttnArgs &a, hipStream_t stream) {
+    const dim3 grid((unsigned)(attn_merge_threads(a) / 256));
+    if (a.dv == 512)
+        hipLaunchKernelGGL((attn_merge_kernel<bf16, 512>), grid, dim3(256), 0, stream, a);
+    else if (a.dtype == kDtypeF32 && a.dv == 64)
+        hipLaunchKernelGGL((attn_merge_kernel<float, 64>), grid, dim3(256), 0, stream, a);
+    else if (a.dtype == kDtypeF32)
+        hipLaunchKernelGGL((attn_merge_kernel<float, 128>), grid, dim3(256), 0, stream, a);
+    else if (a.dv == 64)
+        hipLaunchKernelGGL((attn_merge_kernel<bf16, 64>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((attn_merge_kernel<bf16, 128>), grid, dim3(256), 0, stream, a);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+}  // namespace kda

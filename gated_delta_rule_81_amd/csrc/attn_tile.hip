@@ -1,0 +1,272 @@
+// attn_tile.hip -- attention of many query rows over a shared prefix, over a
+// session's own tokens, or over both: matrix products fed from LDS.
+#include "attn_device.h"
+
+namespace kda {
+namespace {
+
+template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK> struct TileShape {
+    static constexpr int E = sizeof(T), C = D * E / 16, CV = DV * E / 16;
+    static constexpr int BM = 32 * NW / SPLIT;          // rows of a workgroup
+    static constexpr int KB = TK * C * 16, VB = LATENT ? 0 : TK * CV * 16, BUF = KB + VB;
+    static constexpr int LDS = 2 * BUF + (SPLIT == 2 ? 4096 * NW : 0);
+    static constexpr int CHV = LATENT ? C : CV;         // chunks of a row that holds values
+    static_assert(TK * C % 64 == 0 && TK * CV % 64 == 0, "whole loads");
+};
+
+// Ranges (kv heads x splits) and row tiles of the prefix and of the sessions' own tokens (or
+// both), and the blocks of each, a multiple of the 8 XCDs.
+struct TileGrid {
+    int prefix_ranges, prefix_tiles, prefix_blocks;
+    int own_ranges, own_tiles, own_blocks;
+};
+
+template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK>
+__global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileGrid g) {
+    typedef TileShape<T, D, DV, LATENT, SPLIT, NW, TK> S;
+    typedef AttnMma<T> M;
+    // A wave's share: 32 rows, KS chunk pairs of their channels, DT * 32 of their values.
+    constexpr int TT = TK / 32, DT = DV / 32 / SPLIT, KS = S::C / 2 / SPLIT;
+    constexpr uint64_t kAll = ~0ull >> (64 - TK);
+    __shared__ __attribute__((aligned(1024))) char smem[S::LDS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5, group = wave / SPLIT, part = wave % SPLIT;
+
+    // Blocks in the order of their ranges (kv head, split), an eighth of them on each XCD:
+    // those that read the same tokens share an L2.
+    const bool pre = (int)blockIdx.x < g.prefix_blocks;
+    const int b = pre ? blockIdx.x : blockIdx.x - g.prefix_blocks;
+    const int tiles = pre ? g.prefix_tiles : g.own_tiles;
+    const int unit = b % 8 * (pre ? g.prefix_blocks / 8 : g.own_blocks / 8) + b / 8;
+    const int range = unit / tiles;
+    int tile = unit % tiles;
+    if (range >= (pre ? g.prefix_ranges : g.own_ranges)) return;
+    const bool joint = a.plan.joint;
+    const int splits = pre || joint ? a.plan.prefix_splits : a.plan.own_splits;
+    const int hk = range / splits, split = range % splits, G = a.group;
+
+    // rows [row0, row0 + rows) of the tokens from tok0 on, G rows a token
+    const int P = pre || joint ? prefix_tokens(a) : 0;
+    int tok0 = 0, n = a.seqs.tokens, L = 0, session = 0;
+    if (!pre) {
+        const int64_t bm = S::BM;
+        session = session_search(a.seqs, tile, lane,
+                                 [&](int first, int s) { return (int64_t)first * G / bm + s; });
+        tok0 = session_first(a.seqs, session);
+        n = session_first(a.seqs, session + 1) - tok0;
+        tile -= (int)((int64_t)tok0 * G / bm) + session;
+        L = own_tokens(a.seqs, a.pages, session);
+        if (tile < 0 || (int64_t)n * G <= a.plan.few_rows) return;
+    }
+    const int64_t rows = (int64_t)n * G - (int64_t)tile * S::BM;
+    if (rows <= 0) return;
+    const int64_t row0 = (int64_t)tile * S::BM;
+    const int last = (int)(rows < S::BM ? rows : S::BM) - 1;
+
+    // the tokens of this split: of the prefix, then of the session's own
+    const int pu = units_of(P), units = pu + units_of(L), per = split_units(units, splits);
+    const int u0 = split * per, u1 = u0 + per < units ? u0 + per : units;
+    if (u0 >= units && (split > 0 || a.part)) return;
+    auto seen = [&](int64_t row) { return L - n + (int)((row0 + row) / G) + 1; };  // own tokens
+    int base0 = 0, end0 = 0, base1 = 0, end1 = 0;
+    if (u0 < pu) {
+        base0 = u0 * kSplitTokens;
+        end0 = u1 < pu ? u1 * kSplitTokens : P;
+    }
+    if (u1 > pu) {
+        const int64_t to = (int64_t)(u1 - pu) * kSplitTokens;
+        base1 = u0 > pu ? (u0 - pu) * kSplitTokens : 0;
+        end1 = to < L ? (int)to : L;
+        const int most = seen(last);
+        end1 = end1 < most ? end1 : most;
+        end1 = end1 > base1 ? end1 : base1;
+    }
+    const int n0 = (end0 - base0 + TK - 1) / TK, nt = n0 + (end1 - base1 + TK - 1) / TK;
+    const int32_t *own_table = pre ? nullptr : a.seqs.table + (int64_t)session * a.seqs.width;
+
+    // this wave's queries; rows behind the last one are computed as the last one's
+    u32x4 q[KS];
+    const bool active = 32 * group <= last;
+    int lim = 0, wave_min = 0, wave_max = 0;  // own tokens that a row sees
+    {
+        int r = 32 * group + (lane & 31);
+        r = r < last ? r : last;
+        const int64_t row = row0 + r;
+        const T *src = static_cast<const T *>(a.q) + (tok0 + row / G) * a.q_stride +
+                       ((int64_t)hk * G + row % G) * D;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            q[s] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(src) +
+                                                    16 * (2 * (part * KS + s) + half));
+        if (!pre) {
+            const int r0 = 32 * group, r1 = r0 + 31;
+            lim = seen(r);
+            wave_min = seen(r0 < last ? r0 : last), wave_max = seen(r1 < last ? r1 : last);
+        }
+    }
+
+    const int64_t head = (int64_t)hk * a.pages.head;
+    const char *kc = static_cast<const char *>(a.k_cache) + head;
+    const char *vc = LATENT ? nullptr : static_cast<const char *>(a.v_cache) + head;
+    lds_char *lds = (lds_char *)smem;
+    auto base_of = [&](int t) { return t < n0 ? base0 + t * TK : base1 + (t - n0) * TK; };
+    auto entry_of = [&](int t) {
+        if (t >= nt || lane >= TK) return -1;
+        const int tok = base_of(t) + lane;
+        return page_entry(a, t < n0 ? a.prefix_pages : own_table, tok, t < n0 ? end0 : end1);
+    };
+    auto issue = [&](int t, int entry) -> uint64_t {
+        const int64_t off = token_offset(a, entry, base_of(t) + lane);
+        lds_char *buf = lds + (t & 1) * S::BUF;
+        load_tile<S::C, TK, NW>(kc, off, buf, wave, lane);
+        if constexpr (!LATENT) load_tile<S::CV, TK, NW>(vc, off, buf + S::KB, wave, lane);
+        return __ballot(off >= 0);
+    };
+
+    f32x16 o[DT];
+    float m = -__builtin_inff(), l = 0.f;  // running maximum of q k; this lane's half of the sum
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = f32x16(0.f);
+    const float sl = a.scale * kLog2e;  // scores in units of log 2
+
+    uint64_t valid = 0, next_valid = 0;
+    int entry = -1;
+    if (nt > 0) {
+        valid = issue(0, entry_of(0));
+        entry = entry_of(1);
+    }
+    for (int t = 0; t < nt; ++t) {
+        wait_loads<0>();
+        __syncthreads();
+        if (t + 1 < nt) {
+            next_valid = issue(t + 1, entry);
+            entry = entry_of(t + 2);
+        }
+        const int base = base_of(t);
+        const bool own = t >= n0, look = active && !(own && base >= wave_max);
+        lds_char *kt = lds + (t & 1) * S::BUF, *vt = LATENT ? kt : kt + S::KB;
+        f32x16 s[TT];
+#pragma unroll
+        for (int j = 0; j < TT; ++j) s[j] = f32x16(0.f);
+        if (look) {
+#pragma unroll
+            for (int j = 0; j < TT; ++j)
+#pragma unroll
+                for (int c = 0; c < KS; ++c) {
+                    const u32x4 k = *(lds_u32x4 *)(
+                        kt + tile_at<S::C>(32 * j + (lane & 31), 2 * (part * KS + c) + half));
+                    s[j] = M::chunk(k, q[c], s[j]);
+                }
+        }
+        if constexpr (SPLIT == 2) {  // the sum over the other half of the channels
+            lds_char *mine = lds + 2 * S::BUF + wave * 4096 + lane * 16;
+            lds_char *other = lds + 2 * S::BUF + (wave ^ 1) * 4096 + lane * 16;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *(lds_f32x4 *)(mine + 1024 * e) =
+                    f32x4{s[0][4 * e], s[0][4 * e + 1], s[0][4 * e + 2], s[0][4 * e + 3]};
+            lds_barrier();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f32x4 w = *(lds_f32x4 *)(other + 1024 * e);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[0][4 * e + i] += w[i];
+            }
+        }
+        if (look) {
+            const bool later = own && base + TK > wave_min;  // some row does not see some token
+            if (later || valid != kAll)
+                hide_scores<TT>(s, valid, own ? lim - base : TK, lane);
+            soften<TT, DT>(s, m, l, o, sl);
+            // A value that is no number must not reach rows that do not see its token (0 * inf).
+            if (later && any_odd<T>(vt, TK * S::CHV, lane))
+                add_values_apart<T, TT, DT, S::CHV>(s, vt, part * DT, lim - base, lane, o);
+            else
+                add_values<T, TT, DT, S::CHV>(s, vt, part * DT, lane, o);
+        }
+        valid = next_valid;
+    }
+
+    if (!active) return;
+    const int r = 32 * group + (lane & 31);
+    if (r > last) return;
+    l = half_sum(l);
+    const int64_t row = row0 + r, token = tok0 + row / G, h = (int64_t)hk * G + row % G;
+    const int64_t at = token * a.heads + h;
+    const int c0 = 32 * part * DT + 4 * half;  // first channel of this lane
+    const bool first = half == 0 && part == 0;
+    if (a.part) {
+        const int64_t slot = (pre || joint ? 0 : a.plan.prefix_splits) + split;
+        const int64_t place = slot * a.seqs.tokens * a.heads + at;
+        if (first) a.stat[place] = float2{m * sl, l};
+        float *dst = a.part + place * DV + c0;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                store4(dst + 32 * d + 8 * e, o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2],
+                       o[d][4 * e + 3]);
+    } else {
+        const bool any = P > 0 || lim > 0;
+        const float inv = any ? 1.f / l : 0.f;
+        T *dst = static_cast<T *>(a.out) + token * a.out_stride + h * DV + c0;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                store4(dst + 32 * d + 8 * e, o[d][4 * e] * inv, o[d][4 * e + 1] * inv,
+                       o[d][4 * e + 2] * inv, o[d][4 * e + 3] * inv);
+        if (a.lse && first)
+            a.lse[at] = any ? (usable(m) * sl + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
+    }
+}
+
+template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK>
+int launch(const AttnArgs &a, const TileGrid &g, int64_t blocks, hipStream_t stream) {
+    auto kernel = attn_tile_kernel<T, D, DV, LATENT, SPLIT, NW, TK>;
+    if (blocks > 0)
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * NW), 0, stream, a, g);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+// Blocks of the launch; -1 where they are too many for one.
+int64_t grid_of(const AttnArgs &a, TileGrid *g) {
+    const AttnPlan &p = a.plan;
+    const int64_t rows = (int64_t)a.seqs.tokens * a.group;
+    int64_t r0 = 0, t0 = 0, r1 = 0, t1 = 0;
+    if (p.prefix_splits > 0 && !p.joint && !p.prefix_few) {
+        r0 = (int64_t)a.kv_heads * p.prefix_splits;
+        t0 = (rows + p.tile_rows - 1) / p.tile_rows;
+    }
+    if (p.joint || (p.own_splits > 0 && p.own_tiles)) {
+        r1 = (int64_t)a.kv_heads * (p.joint ? p.prefix_splits : p.own_splits);
+        t1 = rows / p.tile_rows + a.seqs.num;  // a session's first one: its first row's / tile_rows + its number
+    }
+    constexpr int64_t kMost = (int64_t)1 << 22;  // 512 threads each
+    if (r0 > kMost || t0 > kMost || r1 > kMost || t1 > kMost) return -1;
+    const int64_t b0 = (r0 * t0 + 7) / 8 * 8, b1 = (r1 * t1 + 7) / 8 * 8;
+    if (b0 + b1 > kMost) return -1;
+    *g = {(int)r0, (int)t0, (int)b0, (int)r1, (int)t1, (int)b1};
+    return b0 + b1;
+}
+
+}  // namespace
+
+int64_t attn_tile_threads(const AttnArgs &a) {
+    TileGrid g;
+    const int64_t n = grid_of(a, &g);
+    return n < 0 ? kMostThreads + 1 : n * 512;
+}
+
+int launch_attn_tiles(const AttnArgs &a, hipStream_t stream) {
+    TileGrid g;
+    const int64_t n = grid_of(a, &g);
+    if (a.d == 576) return launch<bf16, 576, 512, true, 2, 8, 32>(a, g, n, stream);
+    if (a.dtype == kDtypeF32)
+        return a.d == 64 ? launch<float, 64, 64, false, 1, 4, 32>(a, g, n, stream)
+                         : launch<float, 128, 128, false, 1, 4, 32>(a, g, n, stream);
+    return a.d == 64 ? launch<bf16, 64, 64, false, 1, 4, 64>(a, g, n, stream)
+                     : launch<bf16, 128, 128, false, 1, 4, 64>(a, g, n, stream);
+}
+
+}  // namespace kda
