@@ -37,10 +37,6 @@ template <int C> __device__ __forceinline__ int tile_at(int row, int chunk) {
     return (row * C + (chunk ^ tile_turn<C>(row))) * 16;
 }
 
-// Read in place of a token that is not there: its product with a probability of
-// zero has to be zero.
-__device__ const u32x4 kNoRow[80] = {};
-
 __device__ __forceinline__ float half_max(float x) {
     const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
                                                     false);
@@ -157,24 +153,19 @@ __device__ __forceinline__ int prefix_tokens(const AttnArgs &a) {
     return n < 0 ? 0 : (n > most ? (int)most : n);
 }
 
-// Where the tokens of a tile lie: lane l looks after token base + l.
-struct Places {
-    const int32_t *table;
-    int base, end;  // tokens [base, end) of the tile at hand
-};
-__device__ __forceinline__ int page_entry(const AttnArgs &a, const int32_t *table, int tok, int end) {
-    return tok < end ? table[a.pages.by_size(tok)] : -1;
+// The lane number as a value the compiler cannot trace: what is formed from it in a rare
+// path is formed there and does not fill the registers as a constant of the loop around.
+__device__ __forceinline__ int here(int lane) {
+    asm volatile("" : "+v"(lane));
+    return lane;
 }
-// Byte offset of the token behind the start of its head, -1 where it is not to be read.
-__device__ __forceinline__ int64_t token_offset(const AttnArgs &a, int entry, int tok) {
-    if (entry < 0 || entry >= a.pages.count) return -1;
-    const int in = tok - (int)a.pages.by_size(tok) * a.pages.size;
-    return (int64_t)entry * a.pages.page + (int64_t)in * a.pages.token;
-}
-__device__ __forceinline__ int64_t shfl64(int64_t x, int lane) {
-    const int lo = __builtin_amdgcn_ds_bpermute(4 * lane, (int)x);
-    const int hi = __builtin_amdgcn_ds_bpermute(4 * lane, (int)(x >> 32));
-    return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+
+// Place of token `tok` in the page `entry`, in units of 2^shift bytes behind the start of its
+// head; 0 (the first page's first token, which is there) for an entry that is no page.
+__device__ __forceinline__ uint32_t token_place(const Pages &p, int entry, int tok, bool *there) {
+    *there = entry >= 0 && entry < p.count;
+    const uint32_t in = tok - p.by_size(tok) * (uint32_t)p.size;
+    return *there ? (uint32_t)entry * p.page_units + in * p.token_units : 0;
 }
 
 // 16 bytes a lane from memory to LDS at `to` + 16 * lane.  In assembly, so that the compiler
@@ -186,16 +177,20 @@ __device__ __forceinline__ void load_lds16(const char *from, uint32_t to) {
                  : "v"(from), "s"(to)
                  : "memory");
 }
-// Until at most N of this wave's loads are on their way.
+// Until at most N of this wave's loads are on their way.  The compiler knows this instruction:
+// it does not wait again for its own loads from before.
 template <int N> __device__ __forceinline__ void wait_loads() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | 7 << 4 | 15 << 8 | (N >> 4) << 14);
+    asm volatile("" ::: "memory");
 }
 
-// Rows of C chunks of `rows` tokens into a tile, 64 chunks a load, wave `wave` of NW taking
-// every NW-th load; off: each token's offset, at its lane.
-template <int C, int ROWS, int NW>
-__device__ __forceinline__ void load_tile(const char *base, int64_t off, lds_char *tile, int wave,
-                                          int lane) {
+// Rows of C chunks of ROWS tokens into a tile, 64 chunks a load, wave `wave` of NW taking
+// every NW-th load; place: each token's, at its lane.  TWO: the same rows of another cache
+// into the tile behind.
+template <int C, int ROWS, int NW, bool TWO>
+__device__ __forceinline__ void load_tile(const char *base, const char *second, uint32_t place,
+                                          int shift, lds_char *tile, int wave, int lane) {
     constexpr int LOADS = ROWS * C / 64;
 #pragma unroll
     for (int i = 0; i < (LOADS + NW - 1) / NW; ++i) {
@@ -203,9 +198,22 @@ __device__ __forceinline__ void load_tile(const char *base, int64_t off, lds_cha
         if (LOADS % NW != 0 && load >= LOADS) break;
         const int p = 64 * load + lane, row = p / C;
         const int chunk = (p % C) ^ tile_turn<C>(row);
-        const int64_t o = shfl64(off, row);
-        const char *src = o < 0 ? reinterpret_cast<const char *>(kNoRow) : base + o;
-        load_lds16(src + chunk * 16, (uint32_t)(uintptr_t)tile + 1024 * load);
+        const uint64_t at =
+            (uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(4 * row, (int)place) << shift;
+        const uint32_t to = (uint32_t)(uintptr_t)tile + 1024 * load;
+        load_lds16(base + chunk * 16 + at, to);
+        if (TWO) load_lds16(second + chunk * 16 + at, to + ROWS * C * 16);
+    }
+}
+// Rows of tokens that are not there (valid) to zeros: their product with a probability of zero
+// has to be zero.  Each wave clears what it has loaded, once that has come.
+template <int C, int ROWS, int NW>
+__device__ __forceinline__ void clear_rows(lds_char *tile, uint64_t valid, int wave, int lane) {
+    constexpr int LOADS = ROWS * C / 64;
+#pragma unroll 1
+    for (int load = wave; load < LOADS; load += NW) {
+        const int p = 64 * load + here(lane), row = p / C;
+        if (!((valid >> row) & 1)) *(lds_u32x4 *)(tile + 16 * p) = u32x4{0u, 0u, 0u, 0u};
     }
 }
 
@@ -222,13 +230,6 @@ __device__ __forceinline__ bool any_odd(lds_char *tile, int chunks, int lane) {
                    (sizeof(T) == 2 && (w[e] & 0x7f80u) == 0x7f80u);
     }
     return __ballot(odd) != 0;
-}
-
-// The lane number as a value the compiler cannot trace: what is formed from it in a rare
-// path is formed there and does not fill the registers as a constant of the loop around.
-__device__ __forceinline__ int here(int lane) {
-    asm volatile("" : "+v"(lane));
-    return lane;
 }
 
 // Workgroup barrier that waits for this wave's LDS operations only: loads stay on their way.
@@ -280,6 +281,20 @@ __device__ __forceinline__ void soften(f32x16 (&s)[TT], float &m, float &l, f32x
         for (int e = 0; e < 16; ++e) {
             s[j][e] = fast_exp2(s[j][e] * sl - ms);
             l += s[j][e];
+        }
+}
+
+// S^T of 32 * TT tokens: KS chunk pairs of their rows from pair c0 on, with those of q.
+template <typename T, int C, int TT, int KS>
+__device__ __forceinline__ void scores(lds_char *tile, const u32x4 (&q)[KS], int c0, int lane,
+                                       f32x16 (&s)[TT]) {
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+            const u32x4 k = *(lds_u32x4 *)(
+                tile + tile_at<C>(32 * j + (lane & 31), 2 * (c0 + c) + (lane >> 5)));
+            s[j] = AttnMma<T>::chunk(k, q[c], c ? s[j] : f32x16(0.f));
         }
 }
 

@@ -21,7 +21,6 @@ template <typename T, int D, int NW, int ST> struct FewShape {
 template <typename T, int D, int NW, int ST>
 __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, int own_blocks) {
     typedef FewShape<T, D, NW, ST> S;
-    typedef AttnMma<T> M;
     constexpr int DT = D / 32, KS = S::C / 2;
     __shared__ __attribute__((aligned(1024))) char smem[S::LDS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -65,7 +64,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, int own_b
     // This wave's tiles are its own: every NW-th, in a ring of ST places that no other wave
     // reads, so that only its own loads are waited for.  A window of 64 entries of the page
     // table is held in the lanes.
-    const int tiles = (end - beg + kTile - 1) / kTile;
+    const int tiles = a.pages.count > 0 ? (end - beg + kTile - 1) / kTile : 0;
     const int count = tiles > wave ? (tiles - wave + NW - 1) / NW : 0;
     int first = 0, entries = -1;
     bool held = false;
@@ -82,11 +81,10 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, int own_b
         const int idx = a.pages.by_size(tok < stop ? tok : base);
         int entry = __builtin_amdgcn_ds_bpermute(4 * (idx - first), entries);
         entry = tok < stop ? entry : -1;
-        const int64_t off = token_offset(a, entry, tok);
-        lds_char *buf = ring + place * S::BUF;
-        load_tile<S::C, kTile, 1>(kc, off, buf, 0, lane);
-        load_tile<S::C, kTile, 1>(vc, off, buf + S::HALF, 0, lane);
-        return (uint32_t)__ballot(off >= 0);
+        bool there;
+        const uint32_t at = token_place(a.pages, entry, tok, &there);
+        load_tile<S::C, kTile, 1, true>(kc, vc, at, a.pages.shift, ring + place * S::BUF, 0, lane);
+        return (uint32_t)__ballot(there);
     };
 
     f32x16 o[DT];
@@ -107,10 +105,12 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, int own_b
         }
         const int base = base_of(k);
         lds_char *kt = ring + place * S::BUF, *vt = kt + S::HALF;
-        f32x16 s[1] = {f32x16(0.f)};
-#pragma unroll
-        for (int c = 0; c < KS; ++c)
-            s[0] = M::chunk(*(lds_u32x4 *)(kt + tile_at<S::C>(lane & 31, 2 * c + half)), q[c], s[0]);
+        if (valid[0] != ~0u) {
+            clear_rows<S::C, kTile, 1>(vt, valid[0], 0, lane);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        f32x16 s[1];
+        scores<T, S::C, 1, KS>(kt, q, 0, lane, s);
         const bool later = base + kTile > lim_min;
         if (later || valid[0] != ~0u) hide_scores<1>(s, valid[0], lim - base, lane);
         soften<1, DT>(s, m, l, o, sl);

@@ -24,7 +24,6 @@ struct TileGrid {
 template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK>
 __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileGrid g) {
     typedef TileShape<T, D, DV, LATENT, SPLIT, NW, TK> S;
-    typedef AttnMma<T> M;
     // A wave's share: 32 rows, KS chunk pairs of their channels, DT * 32 of their values.
     constexpr int TT = TK / 32, DT = DV / 32 / SPLIT, KS = S::C / 2 / SPLIT;
     constexpr uint64_t kAll = ~0ull >> (64 - TK);
@@ -81,6 +80,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
         end1 = end1 < most ? end1 : most;
         end1 = end1 > base1 ? end1 : base1;
     }
+    if (a.pages.count == 0) end0 = base0, end1 = base1;  // no page to read in place of one
     const int n0 = (end0 - base0 + TK - 1) / TK, nt = n0 + (end1 - base1 + TK - 1) / TK;
     const int32_t *own_table = pre ? nullptr : a.seqs.table + (int64_t)session * a.seqs.width;
 
@@ -110,17 +110,17 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
     const char *vc = LATENT ? nullptr : static_cast<const char *>(a.v_cache) + head;
     lds_char *lds = (lds_char *)smem;
     auto base_of = [&](int t) { return t < n0 ? base0 + t * TK : base1 + (t - n0) * TK; };
+    // This lane's token of tile t: the entry of its page, -1 where there is none.
     auto entry_of = [&](int t) {
-        if (t >= nt || lane >= TK) return -1;
         const int tok = base_of(t) + lane;
-        return page_entry(a, t < n0 ? a.prefix_pages : own_table, tok, t < n0 ? end0 : end1);
+        if (t >= nt || lane >= TK || tok >= (t < n0 ? end0 : end1)) return -1;
+        return (t < n0 ? a.prefix_pages : own_table)[a.pages.by_size(tok)];
     };
     auto issue = [&](int t, int entry) -> uint64_t {
-        const int64_t off = token_offset(a, entry, base_of(t) + lane);
-        lds_char *buf = lds + (t & 1) * S::BUF;
-        load_tile<S::C, TK, NW>(kc, off, buf, wave, lane);
-        if constexpr (!LATENT) load_tile<S::CV, TK, NW>(vc, off, buf + S::KB, wave, lane);
-        return __ballot(off >= 0);
+        bool there;
+        const uint32_t place = token_place(a.pages, entry, base_of(t) + lane, &there);
+        load_tile<S::C, TK, NW, !LATENT>(kc, vc, place, a.pages.shift, lds + (t & 1) * S::BUF, wave, lane);
+        return __ballot(there);
     };
 
     f32x16 o[DT];
@@ -135,29 +135,21 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
         valid = issue(0, entry_of(0));
         entry = entry_of(1);
     }
-    for (int t = 0; t < nt; ++t) {
+    // One tile; LATER: some row may not see some token of it.
+    auto step = [&](int t, auto LATER) {
+        constexpr bool later_tiles = decltype(LATER)::value;
+        lds_char *kt = lds + (t & 1) * S::BUF, *vt = LATENT ? kt : kt + S::KB;
         wait_loads<0>();
+        if (valid != kAll) clear_rows<S::CHV, TK, NW>(vt, valid, wave, lane);
         __syncthreads();
         if (t + 1 < nt) {
             next_valid = issue(t + 1, entry);
             entry = entry_of(t + 2);
         }
         const int base = base_of(t);
-        const bool own = t >= n0, look = active && !(own && base >= wave_max);
-        lds_char *kt = lds + (t & 1) * S::BUF, *vt = LATENT ? kt : kt + S::KB;
+        const bool look = active && !(later_tiles && base >= wave_max);
         f32x16 s[TT];
-#pragma unroll
-        for (int j = 0; j < TT; ++j) s[j] = f32x16(0.f);
-        if (look) {
-#pragma unroll
-            for (int j = 0; j < TT; ++j)
-#pragma unroll
-                for (int c = 0; c < KS; ++c) {
-                    const u32x4 k = *(lds_u32x4 *)(
-                        kt + tile_at<S::C>(32 * j + (lane & 31), 2 * (part * KS + c) + half));
-                    s[j] = M::chunk(k, q[c], s[j]);
-                }
-        }
+        if (SPLIT == 2 || look) scores<T, S::C, TT, KS>(kt, q, part * KS, lane, s);
         if constexpr (SPLIT == 2) {  // the sum over the other half of the channels
             lds_char *mine = lds + 2 * S::BUF + wave * 4096 + lane * 16;
             lds_char *other = lds + 2 * S::BUF + (wave ^ 1) * 4096 + lane * 16;
@@ -174,9 +166,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
             }
         }
         if (look) {
-            const bool later = own && base + TK > wave_min;  // some row does not see some token
-            if (later || valid != kAll)
-                hide_scores<TT>(s, valid, own ? lim - base : TK, lane);
+            const bool later = later_tiles && base + TK > wave_min;
+            if (later || valid != kAll) hide_scores<TT>(s, valid, later_tiles ? lim - base : TK, lane);
             soften<TT, DT>(s, m, l, o, sl);
             // A value that is no number must not reach rows that do not see its token (0 * inf).
             if (later && any_odd<T>(vt, TK * S::CHV, lane))
@@ -185,7 +176,16 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
                 add_values<T, TT, DT, S::CHV>(s, vt, part * DT, lane, o);
         }
         valid = next_valid;
+    };
+    wait_loads<0>();  // the queries among them
+    // tiles that all rows see whole first: of the prefix, and of own tokens up to the first row's
+    int t = 0, plain = nt;
+    if (!pre && end1 > base1) {
+        const int whole = seen(0) > base1 ? (seen(0) - base1) / TK : 0;
+        plain = n0 + whole < nt ? n0 + whole : nt;
     }
+    for (; t < plain; ++t) step(t, std::false_type{});
+    for (; t < nt; ++t) step(t, std::true_type{});
 
     if (!active) return;
     const int r = 32 * group + (lane & 31);

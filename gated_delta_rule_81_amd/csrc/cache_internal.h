@@ -39,6 +39,9 @@ struct Pages {
     int32_t count, size;
     Divisor by_size;
     int64_t page, token, head;  // distance between pages, tokens, heads
+    // the first two in units of 2^shift bytes: every token's place of a head fits 32 bits
+    uint32_t page_units, token_units;
+    int32_t shift;
 };
 
 struct AppendArgs {
