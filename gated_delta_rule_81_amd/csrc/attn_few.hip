@@ -7,6 +7,12 @@ namespace {
 
 constexpr int kTile = 32;  // tokens of a wave's tile
 
+// What a part (its maximum in units of log 2, its sum) counts beside others: nothing where its
+// maximum is -inf, unless its scores were no numbers, which its sum then is not either.
+__device__ __forceinline__ float part_weight(const float2 &part, float top) {
+    return part.x > -__builtin_inff() ? fast_exp2(part.x - top) : (part.y == 0.f ? 0.f : part.y);
+}
+
 template <typename T, int D, int NW, int ST> struct FewShape {
     static constexpr int C = D * (int)sizeof(T) / 16;   // 16-byte chunks of a row
     static constexpr int HALF = kTile * C * 16, BUF = 2 * HALF;
@@ -139,7 +145,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, int own_b
             for (int e = 0; e < 4; ++e)
                 store4(dst + 32 * d + 8 * e, o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2],
                        o[d][4 * e + 3]);
-        if (half == 0) stat[wave * 32 + lane] = float2{m, l};
+        if (half == 0) stat[wave * 32 + lane] = float2{m * sl, l};
     }
     __syncthreads();
     for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * NW) {
@@ -151,8 +157,7 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, int own_b
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             const float2 v = stat[w * 32 + r];
-            if (v.x == -__builtin_inff()) continue;  // nothing of it was seen
-            const float f = fast_exp2((v.x - top) * sl);
+            const float f = part_weight(v, top);
             sum += v.y * f;
             y += *reinterpret_cast<const f32x4 *>(join + (w * 32 + r) * S::LD + c) * f;
         }
@@ -162,15 +167,14 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, int own_b
             const int64_t slot = (pre ? 0 : a.plan.prefix_splits) + split;
             const int64_t to = slot * a.seqs.tokens * a.heads + at;
             *reinterpret_cast<f32x4 *>(a.part + to * D + c) = y;
-            if (c == 0) a.stat[to] = float2{top * sl, sum};
+            if (c == 0) a.stat[to] = float2{top, sum};
         } else {
             const bool any = seen(r) > 0;
             const float inv = any ? 1.f / sum : 0.f;
             T *out = static_cast<T *>(a.out) + token * a.out_stride + h * D + c;
             store4(out, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
             if (a.lse && c == 0)
-                a.lse[at] = any ? (usable(top) * sl + __builtin_log2f(sum)) * kLn2
-                                : -__builtin_inff();
+                a.lse[at] = any ? (usable(top) + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
         }
     }
 }
@@ -190,62 +194,55 @@ template <typename T, int D, int NW, int ST> int few(const AttnArgs &a, hipStrea
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
-// Row (token, head): the parts of its splits, in their order.  DV / 4 lanes a row.
-template <typename T, int DV>
-__global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
-    constexpr int LANES = DV / 4;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, at = i / LANES;
-    const int c = 4 * (int)(i % LANES);
-    const int64_t rows = (int64_t)a.seqs.tokens * a.heads;
-    if (at >= rows) return;
+// One workgroup per row (token, head): DV / 4 lanes hold a row's values, the 1024 / DV groups
+// of them take every so many-th part, and are added up in their order.  Its time is one chain
+// of loads (lengths, statistics, parts), so everything that does not depend on another load is
+// read at once.
+template <typename T, int DV> __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
+    constexpr int LANES = DV / 4, GROUPS = 256 / LANES, SLOTS = 128;
+    __shared__ float2 stat[SLOTS];
+    __shared__ f32x4 sums[GROUPS][LANES];
+    const int64_t at = blockIdx.x, rows = (int64_t)a.seqs.tokens * a.heads;
     const int token = (int)(at / a.heads), h = (int)(at % a.heads);
-    // the session (the last that begins at or before the token)
-    int lo = 0;
-    if (a.seqs.cu) {
-        int hi = a.seqs.num - 1;
-        while (lo < hi) {
-            const int mid = (int)(((int64_t)lo + hi + 1) >> 1);
-            if (a.seqs.cu[mid] <= token)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-    } else {
-        lo = token / a.seqs.each;
-    }
-    int first = lo * a.seqs.each, last = first + a.seqs.each;
-    if (a.seqs.cu) first = a.seqs.cu[lo], last = a.seqs.cu[lo + 1];
-    first = first < 0 ? 0 : first;
-    last = last > a.seqs.tokens ? a.seqs.tokens : last;
+    const int tid = threadIdx.x, lane = tid & 63, group = tid / LANES, c = 4 * (tid % LANES);
+    const AttnPlan &p = a.plan;
+    // statistics of every slot, whether a part was written or not
+    const int slots = p.prefix_splits + p.own_splits;
+    float2 mine = {0.f, 0.f};
+    if (tid < slots) mine = a.stat[tid * rows + at];
+    const int s = a.seqs.cu ? session_search(a.seqs, token, lane, [](int first, int) { return first; })
+                            : token / a.seqs.each;
+    const int first = session_first(a.seqs, s), last = session_first(a.seqs, s + 1);
     if (token < first || token >= last) return;  // in no session
-    const int64_t most = (int64_t)a.seqs.width * a.pages.size;
-    int L = a.seqs.lens[lo];
-    L = L < 0 ? 0 : (L > most ? (int)most : L);
-    const int P = prefix_tokens(a);
+    const int L = own_tokens(a.seqs, a.pages, s), P = prefix_tokens(a);
     const bool any = P > 0 || L - (last - token) + 1 > 0;
 
-    // which slots hold a part
-    const AttnPlan &p = a.plan;
+    // which slots hold a part: the first n0 of the prefix's, the first n1 of the own ones
     const int pu = units_of(P), lu = units_of(L);
     const int u0 = p.joint ? pu + lu : pu, per0 = split_units(u0, p.prefix_splits);
     const int n0 = per0 > 0 ? (u0 + per0 - 1) / per0 : 0;
     const int per1 = p.joint ? 0 : split_units(lu, p.own_splits);
-    const int n1 = per1 > 0 ? (lu + per1 - 1) / per1 : 0;
-    float top = -__builtin_inff(), sum = 0.f;
-    for (int k = 0; k < n0 + n1; ++k) {
-        const int64_t slot = k < n0 ? k : p.prefix_splits + k - n0;
-        top = __builtin_fmaxf(top, a.stat[slot * rows + at].x);
-    }
+    const int n1 = per1 > 0 ? (lu + per1 - 1) / per1 : 0, n = n0 + n1;
+    const int slot = tid < p.prefix_splits ? tid : tid - p.prefix_splits + n0;
+    if (tid < slots && (tid < p.prefix_splits ? tid < n0 : slot < n)) stat[slot] = mine;
+    __syncthreads();
+    float top = -__builtin_inff();
+    for (int k = 0; k < n; ++k) top = __builtin_fmaxf(top, stat[k].x);
+    float sum = 0.f;
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < n0 + n1; ++k) {
-        const int64_t slot = k < n0 ? k : p.prefix_splits + k - n0;
-        const float2 v = a.stat[slot * rows + at];
-        const f32x4 w = *reinterpret_cast<const f32x4 *>(a.part + (slot * rows + at) * DV + c);
-        if (v.x == -__builtin_inff()) continue;  // nothing of it was seen
-        const float f = fast_exp2(v.x - top);
-        sum += v.y * f;
-        y += w * f;
+    for (int k = 0; k < n; ++k) sum += stat[k].y * part_weight(stat[k], top);
+#pragma unroll 4
+    for (int k = group; k < n; k += GROUPS) {
+        const int64_t from = k < n0 ? k : p.prefix_splits + k - n0;
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(a.part + (from * rows + at) * DV + c);
+        const float f = part_weight(stat[k], top);
+        if (f != 0.f) y += w * f;  // a part of which nothing was seen holds anything
     }
+    sums[group][tid % LANES] = y;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) y += sums[g][tid];
     const float inv = any ? 1.f / sum : 0.f;
     T *out = static_cast<T *>(a.out) + token * a.out_stride + (int64_t)h * DV + c;
     store4(out, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
@@ -260,7 +257,7 @@ int64_t attn_few_threads(const AttnArgs &a) {
     return few_blocks(a, &own) * 256;
 }
 int64_t attn_merge_threads(const AttnArgs &a) {
-    return ((int64_t)a.seqs.tokens * a.heads * (a.dv / 4) + 255) / 256 * 256;
+    return (int64_t)a.seqs.tokens * a.heads * 256;
 }
 
 int launch_attn_few(const AttnArgs &a, hipStream_t stream) {
