@@ -48,9 +48,24 @@ __device__ __forceinline__ float half_sum(float x) {
     return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
+// Where the 16-byte chunks of a lane's row (token l % 32 of a tile) lie: pairs of them from
+// pair c0 on, a half wave each; classes by the period of turn(), as for values.
+template <int C> struct Keys {
+    static constexpr int NK = C % 16 == 0 ? 8 : 4;
+    int at[NK];
+    __device__ __forceinline__ Keys(int c0, int lane) {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) at[k] = tile_at<C>(lane & 31, 2 * (c0 + k) + (lane >> 5));
+    }
+    // Pair c0 + c of token 32 j + l % 32.
+    __device__ __forceinline__ u32x4 read(lds_char *tile, int j, int c) const {
+        return *(lds_u32x4 *)(tile + at[c % NK] + 32 * j * C * 16 + c / NK * NK * 32);
+    }
+};
+
 // Products of one type of element.  chunk(): acc += over the channels of one
-// 16-byte chunk per half wave.  values(): the operand of V^T for 16 tokens from
-// `row0` and 32 channels from `d0` (CH chunks a row), and its product.
+// 16-byte chunk per half wave.  Values: the operand of V^T for 16 tokens and 32
+// channels of a tile of CH chunks a row; mma(): its product.
 template <typename T> struct AttnMma;
 
 template <> struct AttnMma<bf16> {
@@ -61,21 +76,33 @@ template <> struct AttnMma<bf16> {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                        __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     }
-    // Lane's place in a tile for the transposing reads, channels 0..31, tokens 0..3 of
-    // each half; others are reached by the offset of `step`.
-    template <int CH> __device__ static int value_at(int row0, int d0, int lane, int second) {
-        const int row = row0 + 8 * second + 4 * (lane >> 5) + ((lane & 15) >> 2);
-        const int col = d0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-        return tile_at<CH>(row, col >> 3) + (col & 7) * 2;
-    }
-    template <int CH> __device__ static Value value(lds_char *tile, int row0, int d0, int lane) {
-        typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-        const bf16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-            (lds_bf16x4 *)(tile + value_at<CH>(row0, d0, lane, 0)));
-        const bf16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-            (lds_bf16x4 *)(tile + value_at<CH>(row0, d0, lane, 1)));
-        return {__builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7)};
-    }
+    // Where the transposing reads of 32 channels from 32 d0 on, tokens 0..3 and 8..11 of each
+    // half, lie for this lane.  turn() repeats after 16 rows and 8 or 16 chunks: NV classes of
+    // d, the others by immediate offsets.
+    template <int CH> struct Values {
+        static constexpr int NV = CH % 16 == 0 ? 4 : 2;
+        int at[NV][2];
+        __device__ __forceinline__ Values(int d0, int lane) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int second = 0; second < 2; ++second) {
+                    const int row = 8 * second + 4 * (lane >> 5) + ((lane & 15) >> 2);
+                    const int col = 32 * (d0 + k) + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+                    at[k][second] = tile_at<CH>(row, col >> 3) + (col & 7) * 2;
+                }
+        }
+        // Tokens 16 j .. 16 j + 15, channels 32 (d0 + d) on (d0 a multiple of NV).
+        __device__ __forceinline__ Value read(lds_char *tile, int j, int d) const {
+            typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+            const int off = 16 * j * CH * 16 + d / NV * NV * 64;
+            const bf16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                (lds_bf16x4 *)(tile + at[d % NV][0] + off));
+            const bf16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                (lds_bf16x4 *)(tile + at[d % NV][1] + off));
+            return {__builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7)};
+        }
+    };
     __device__ static Prob prob(const f32x16 &s, int step) {
         Prob p;
 #pragma unroll
@@ -85,13 +112,15 @@ template <> struct AttnMma<bf16> {
     __device__ static f32x16 mma(const Value &v, const Prob &p, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(v.a, p, c, 0, 0, 0);
     }
-    // The operand with every token but `j` of the 16 left out.
-    __device__ static Value only(const Value &v, int j, int lane) {
-        Value o;
+    // The operand with zeros where it is no number.
+    __device__ static Value numbers(const Value &v) {
+        u32x4 w = __builtin_bit_cast(u32x4, v.a);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            o.a[e] = 8 * (e / 4) + 4 * (lane >> 5) + e % 4 == j ? v.a[e] : static_cast<bf16>(0.f);
-        return o;
+        for (int e = 0; e < 4; ++e) {
+            w[e] = (w[e] & 0x7f80u) == 0x7f80u ? w[e] & 0xffff0000u : w[e];
+            w[e] = (w[e] & 0x7f800000u) == 0x7f800000u ? w[e] & 0xffffu : w[e];
+        }
+        return {__builtin_bit_cast(bf16x8, w)};
     }
 };
 
@@ -105,17 +134,22 @@ template <> struct AttnMma<float> {
                                                      0, 0, 0);
         return c;
     }
-    template <int CH> __device__ static Value value(lds_char *tile, int row0, int d0, int lane) {
-        typedef __attribute__((address_space(3))) float lds_float;
-        Value v;
-        const int col = d0 + (lane & 31);
+    template <int CH> struct Values {
+        int d0, lane;
+        __device__ __forceinline__ Values(int d0_, int lane_) : d0(d0_), lane(lane_) {}
+        __device__ __forceinline__ Value read(lds_char *tile, int j, int d) const {
+            typedef __attribute__((address_space(3))) float lds_float;
+            Value v;
+            const int col = 32 * (d0 + d) + (lane & 31);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int row = row0 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
-            v.a[e] = *(lds_float *)(tile + tile_at<CH>(row, col >> 2) + (col & 3) * 4);
+            for (int e = 0; e < 8; ++e) {
+                const int row = 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
+                v.a[e] = *(lds_float *)(tile + 16 * j * CH * 16 + tile_at<CH>(row, col >> 2) +
+                                        (col & 3) * 4);
+            }
+            return v;
         }
-        return v;
-    }
+    };
     __device__ static Prob prob(const f32x16 &s, int step) {
         Prob p;
 #pragma unroll
@@ -128,11 +162,11 @@ template <> struct AttnMma<float> {
             c = __builtin_amdgcn_mfma_f32_32x32x2f32(v.a[e], p.p[e], c, 0, 0, 0);
         return c;
     }
-    __device__ static Value only(const Value &v, int j, int lane) {
+    __device__ static Value numbers(const Value &v) {
         Value o;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            o.a[e] = 8 * (e / 4) + 4 * (lane >> 5) + e % 4 == j ? v.a[e] : 0.f;
+            o.a[e] = __builtin_fabsf(v.a[e]) < __builtin_inff() ? v.a[e] : 0.f;
         return o;
     }
 };
@@ -196,7 +230,8 @@ __device__ __forceinline__ void load_tile(const char *base, const char *second, 
     for (int i = 0; i < (LOADS + NW - 1) / NW; ++i) {
         const int load = NW * i + wave;
         if (LOADS % NW != 0 && load >= LOADS) break;
-        const int p = 64 * load + lane, row = p / C;
+        // (rows that are no power of two: formed again each time, to keep registers free)
+        const int p = 64 * load + ((C & (C - 1)) != 0 ? here(lane) : lane), row = p / C;
         const int chunk = (p % C) ^ tile_turn<C>(row);
         const uint64_t at =
             (uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(4 * row, (int)place) << shift;
@@ -284,53 +319,57 @@ __device__ __forceinline__ void soften(f32x16 (&s)[TT], float &m, float &l, f32x
         }
 }
 
-// S^T of 32 * TT tokens: KS chunk pairs of their rows from pair c0 on, with those of q.
+// S^T of 32 * TT tokens: KS chunk pairs of their rows with those of q.
 template <typename T, int C, int TT, int KS>
-__device__ __forceinline__ void scores(lds_char *tile, const u32x4 (&q)[KS], int c0, int lane,
+__device__ __forceinline__ void scores(lds_char *tile, const Keys<C> &keys, const u32x4 (&q)[KS],
                                        f32x16 (&s)[TT]) {
 #pragma unroll
     for (int j = 0; j < TT; ++j)
 #pragma unroll
-        for (int c = 0; c < KS; ++c) {
-            const u32x4 k = *(lds_u32x4 *)(
-                tile + tile_at<C>(32 * j + (lane & 31), 2 * (c0 + c) + (lane >> 5)));
-            s[j] = AttnMma<T>::chunk(k, q[c], c ? s[j] : f32x16(0.f));
-        }
+        for (int c = 0; c < KS; ++c)
+            s[j] = AttnMma<T>::chunk(keys.read(tile, j, c), q[c], c ? s[j] : f32x16(0.f));
 }
 
-// o += V^T P^T over a tile's tokens, channels 32 d0 .. 32 (d0 + DT).
-template <typename T, int TT, int DT, int CH>
-__device__ __forceinline__ void add_values(const f32x16 (&s)[TT], lds_char *tile, int d0, int lane,
+// o += V^T P^T over a tile's tokens, DT * 32 channels.  NUMBERS: what is no number (an infinity
+// or a NaN) is left out: a product would carry it to rows that do not see its token (0 * inf).
+template <typename T, bool NUMBERS, int TT, int DT, typename V>
+__device__ __forceinline__ void add_values(const f32x16 (&s)[TT], lds_char *tile, const V &values,
                                            f32x16 (&o)[DT]) {
     typedef AttnMma<T> M;
 #pragma unroll
     for (int j = 0; j < 2 * TT; ++j) {
         const typename M::Prob p = M::prob(s[j / 2], j % 2);
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-            o[d] = M::mma(M::template value<CH>(tile, 16 * j, 32 * (d0 + d), lane), p, o[d]);
+        for (int d = 0; d < DT; ++d) {
+            const typename M::Value v = values.read(tile, j, d);
+            o[d] = M::mma(NUMBERS ? M::numbers(v) : v, p, o[d]);
+        }
     }
 }
-// The same with the tokens one by one, each for the rows that see it (those under ahead).
-template <typename T, int TT, int DT, int CH>
-__device__ __forceinline__ void add_values_apart(const f32x16 (&s)[TT], lds_char *tile, int d0,
-                                                 int ahead, int lane, f32x16 (&o)[DT]) {
-    typedef AttnMma<T> M;
-#pragma unroll
-    for (int j = 0; j < 2 * TT; ++j) {
-        const typename M::Prob p = M::prob(s[j / 2], j % 2);
-        const int ln = here(lane);
+
+// What add_values has left out of tokens [from, to) of one session, added for the rows that
+// see it: row l % 32 of this wave sees the tokens under lim.  Values from the cache itself.
+template <typename T, int DT>
+__device__ __forceinline__ void add_others(const Pages &pages, const int32_t *table, const char *vc,
+                                           int from, int to, int d0, int lim, int lane,
+                                           f32x16 (&o)[DT]) {
+    const int half = lane >> 5;
 #pragma unroll 1
-        for (int e = 0; e < 16; ++e) {
+    for (int tok = from; tok < to; ++tok) {
+        bool there;
+        const uint32_t place = token_place(pages, table[pages.by_size(tok)], tok, &there);
+        if (!there) continue;
+        const T *row = reinterpret_cast<const T *>(vc + ((uint64_t)place << pages.shift));
+        const bool see = tok < lim;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const typename M::Value v =
-                    M::only(M::template value<CH>(tile, 16 * j, 32 * (d0 + d), ln), e, ln);
-                const f32x16 with = M::mma(v, p, o[d]);
-                o[d] = 16 * j + e < ahead ? with : o[d];
-                __builtin_amdgcn_sched_barrier(0);  // one at a time: few registers
-            }
-        }
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float x = to_f32(row[32 * (d0 + d) + 8 * k + 4 * half + i]);
+                    o[d][4 * k + i] += see && !(__builtin_fabsf(x) < __builtin_inff()) ? x : 0.f;
+                }
     }
 }
 

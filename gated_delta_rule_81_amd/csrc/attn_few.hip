@@ -98,11 +98,16 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, int own_b
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16(0.f);
     const float sl = a.scale * kLog2e;
+    const Keys<S::C> keys(0, lane);
+    const typename AttnMma<T>::template Values<S::C> values(0, lane);
     uint32_t valid[ST];
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) valid[i] = i < count ? issue(i, i) : 0;
     int place = 0, ahead = ST - 1;
-    for (int k = 0; k < count; ++k) {
+    bool odd = false;  // a value that is no number in a tile that not all rows see whole
+    // One tile; LATER: some row may not see some token of it.
+    auto step = [&](int k, auto LATER) {
+        constexpr bool later = decltype(LATER)::value;
         if (k + ST - 1 < count) {
             valid[ST - 1] = issue(k + ST - 1, ahead);
             wait_loads<(ST - 1) * S::LOADS>();
@@ -116,21 +121,25 @@ __global__ __launch_bounds__(64 * NW) void attn_few_kernel(AttnArgs a, int own_b
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
         f32x16 s[1];
-        scores<T, S::C, 1, KS>(kt, q, 0, lane, s);
-        const bool later = base + kTile > lim_min;
-        if (later || valid[0] != ~0u) hide_scores<1>(s, valid[0], lim - base, lane);
+        scores<T, S::C, 1, KS>(kt, keys, q, s);
+        if (later || valid[0] != ~0u) hide_scores<1>(s, valid[0], later ? lim - base : kTile, lane);
         soften<1, DT>(s, m, l, o, sl);
-        if (later && any_odd<T>(vt, kTile * S::C, lane))
-            add_values_apart<T, 1, DT, S::C>(s, vt, 0, lim - base, lane, o);
-        else
-            add_values<T, 1, DT, S::C>(s, vt, 0, lane, o);
+        if (later && any_odd<T>(vt, kTile * S::C, lane)) odd = true;
+        add_values<T, later>(s, vt, values, o);
         // the tile is read before its place is filled again
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
         for (int i = 0; i < ST - 1; ++i) valid[i] = valid[i + 1];
         place = place + 1 == ST ? 0 : place + 1;
         ahead = ahead + 1 == ST ? 0 : ahead + 1;
-    }
+    };
+    // tiles that all rows see whole first: those that end at the first row's last token or before
+    const int whole = lim_min >= end ? tiles : (lim_min > beg ? (lim_min - beg) / kTile : 0);
+    const int plain = whole > wave ? (whole - wave + NW - 1) / NW : 0;
+    int k = 0;
+    for (; k < plain; ++k) step(k, std::false_type{});
+    for (; k < count; ++k) step(k, std::true_type{});
+    if (odd) add_others<T>(a.pages, table, vc, beg + whole * kTile, end, 0, lim, lane, o);
 
     // the waves' parts are joined through LDS, in wave order
     l = half_sum(l);

@@ -87,7 +87,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
     // this wave's queries; rows behind the last one are computed as the last one's
     u32x4 q[KS];
     const bool active = 32 * group <= last;
-    int lim = 0, wave_min = 0, wave_max = 0;  // own tokens that a row sees
+    int lim = 0, wave_max = 0;  // own tokens that a row sees, and the wave's last
     {
         int r = 32 * group + (lane & 31);
         r = r < last ? r : last;
@@ -99,9 +99,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
             q[s] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(src) +
                                                     16 * (2 * (part * KS + s) + half));
         if (!pre) {
-            const int r0 = 32 * group, r1 = r0 + 31;
             lim = seen(r);
-            wave_min = seen(r0 < last ? r0 : last), wave_max = seen(r1 < last ? r1 : last);
+            wave_max = seen(32 * group + 31 < last ? 32 * group + 31 : last);
         }
     }
 
@@ -129,6 +128,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
     for (int d = 0; d < DT; ++d) o[d] = f32x16(0.f);
     const float sl = a.scale * kLog2e;  // scores in units of log 2
 
+    const Keys<S::C> keys(part * KS, lane);
+    const typename AttnMma<T>::template Values<S::CHV> values(part * DT, lane);
+
+    bool odd = false;  // a value that is no number in a tile that not all rows see whole
     uint64_t valid = 0, next_valid = 0;
     int entry = -1;
     if (nt > 0) {
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
         const int base = base_of(t);
         const bool look = active && !(later_tiles && base >= wave_max);
         f32x16 s[TT];
-        if (SPLIT == 2 || look) scores<T, S::C, TT, KS>(kt, q, part * KS, lane, s);
+        if (SPLIT == 2 || look) scores<T, S::C, TT, KS>(kt, keys, q, s);
         if constexpr (SPLIT == 2) {  // the sum over the other half of the channels
             lds_char *mine = lds + 2 * S::BUF + wave * 4096 + lane * 16;
             lds_char *other = lds + 2 * S::BUF + (wave ^ 1) * 4096 + lane * 16;
@@ -166,14 +169,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
             }
         }
         if (look) {
-            const bool later = later_tiles && base + TK > wave_min;
-            if (later || valid != kAll) hide_scores<TT>(s, valid, later_tiles ? lim - base : TK, lane);
+            if (later_tiles || valid != kAll)
+                hide_scores<TT>(s, valid, later_tiles ? lim - base : TK, lane);
             soften<TT, DT>(s, m, l, o, sl);
-            // A value that is no number must not reach rows that do not see its token (0 * inf).
-            if (later && any_odd<T>(vt, TK * S::CHV, lane))
-                add_values_apart<T, TT, DT, S::CHV>(s, vt, part * DT, lim - base, lane, o);
-            else
-                add_values<T, TT, DT, S::CHV>(s, vt, part * DT, lane, o);
+            if (later_tiles && any_odd<T>(vt, TK * S::CHV, lane)) odd = true;
+            add_values<T, later_tiles>(s, vt, values, o);
         }
         valid = next_valid;
     };
@@ -186,6 +186,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
     }
     for (; t < plain; ++t) step(t, std::false_type{});
     for (; t < nt; ++t) step(t, std::true_type{});
+    if (odd) add_others<T>(a.pages, own_table, LATENT ? kc : vc, base_of(plain), end1, part * DT, lim, lane, o);
 
     if (!active) return;
     const int r = 32 * group + (lane & 31);

@@ -247,13 +247,16 @@ AttnPlan attn_plan(int64_t tokens, int64_t num_seqs, bool packed, int64_t q_head
     }
     if (pre_units > 0)
         p.prefix_splits = cut(p.prefix_few ? slots / kv_heads : slots / (kv_heads * tiles), pre_units);
-    if (own_units > 0) {
-        // one in flight for each place, and lengths over 1024 tokens cut so that ragged ones even out
-        const int64_t base = kv_heads * num_seqs * (p.few_rows ? 1 : (most + 127) / 128);
-        int64_t want = (2 * slots + base - 1) / base;
-        const int64_t even = own_units / 8 < 4 ? own_units / 8 : 4;
-        if (p.few_rows && want < even) want = even;
-        p.own_splits = cut(want, own_units);
+    if (own_units > 0 && p.few_rows > 0) {
+        // twice as many as run at once, and lengths over 1024 tokens cut so that ragged ones even out
+        const int64_t base = kv_heads * num_seqs, even = own_units / 8 < 4 ? own_units / 8 : 4;
+        const int64_t want = (2 * slots + base - 1) / base;
+        p.own_splits = cut(want < even ? even : want, own_units);
+    } else if (own_units > 0) {
+        // a part of many rows is large beside the tokens it stands for: only where workgroups lack
+        const int64_t base = kv_heads * num_seqs * ((most + p.tile_rows - 1) / p.tile_rows);
+        const int64_t left = slots - kv_heads * tiles * p.prefix_splits;
+        p.own_splits = cut(left / base, own_units);
     }
     return p;
 }
