@@ -25,7 +25,7 @@ LIB = os.path.join(HERE, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_chunk.hip", "kda_seq.hip", "kda_segment.hip",
            "kda_bwd.hip", "kda_bwd_chain.hip", "layer_api.cpp", "conv.hip", "qk_norm.hip",
            "ssm_scan.hip", "ssm_step.hip", "ssm_bwd.hip", "cache_api.cpp", "cache_append.hip",
-           "attn_tile.hip", "attn_few.hip"]
+           "attn.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-mcode-object-version=5",

@@ -1,0 +1,191 @@
+// attn.hip -- the launches of the attention over a shared prefix and each session's
+// own tokens.
+#include "attn_few.h"
+#include "attn_tile.h"
+
+namespace kda {
+namespace {
+
+constexpr int kTurn = 256;
+
+// What a launch is made of: `few` blocks for few rows (own_few of them own tokens, the others
+// prefix), and those of the tile grid.
+struct MixGrid {
+    int few, own_few;
+    TileGrid tile;
+};
+
+// Per-head caches: both walks in one launch, so that the one bound by memory and the one bound
+// by the matrix units share each CU.
+template <typename T, int D, int TK, int PLACES> struct MixShape {
+    static constexpr int A = TileShape<T, D, D, false, 1, 4, TK>::LDS;
+    static constexpr int B = FewShape<T, D, 4, PLACES>::LDS;
+    static constexpr int LDS = A > B ? A : B;
+};
+template <typename T, int D, int TK, int PLACES>
+__global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a, MixGrid g) {
+    __shared__ __attribute__((aligned(1024))) char smem[MixShape<T, D, TK, PLACES>::LDS];
+    const int tiles = g.tile.prefix_blocks + g.tile.own_blocks;
+    // of both kinds in turn, kTurn blocks each, while there are both
+    const int both = g.few < tiles ? g.few : tiles, turns = both / kTurn * kTurn;
+    int b = blockIdx.x;
+    bool few;
+    if (b < 2 * turns) {
+        few = b / kTurn % 2 == 1;
+        b = b / (2 * kTurn) * kTurn + b % kTurn;
+    } else {
+        b -= turns;  // the rest of the tiles, then of the others
+        few = b >= tiles;
+        if (few) b -= tiles - turns;
+    }
+    if (few)
+        few_walk<T, D, 4, PLACES>(a, g.own_few, b, smem);
+    else
+        tile_walk<T, D, D, false, 1, 4, TK>(a, g.tile, b, smem);
+}
+
+__global__ __launch_bounds__(512, 2) void attn_latent_kernel(AttnArgs a, TileGrid g) {
+    typedef TileShape<bf16, 576, 512, true, 2, 8, 32> S;
+    __shared__ __attribute__((aligned(1024))) char smem[S::LDS];
+    tile_walk<bf16, 576, 512, true, 2, 8, 32>(a, g, blockIdx.x, smem);
+}
+
+// One workgroup per row (token, head): DV / 4 lanes hold a row's values, the 1024 / DV groups
+// of them take every so many-th part, and are added up in their order.  Its time is one chain
+// of loads (lengths, statistics, parts), so everything that does not depend on another load is
+// read at once.
+template <typename T, int DV> __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
+    constexpr int LANES = DV / 4, GROUPS = 256 / LANES, SLOTS = 128;
+    __shared__ float2 stat[SLOTS];
+    __shared__ f32x4 sums[GROUPS][LANES];
+    const int64_t at = blockIdx.x, rows = (int64_t)a.seqs.tokens * a.heads;
+    const int token = (int)(at / a.heads), h = (int)(at % a.heads);
+    const int tid = threadIdx.x, lane = tid & 63, group = tid / LANES, c = 4 * (tid % LANES);
+    const AttnPlan &p = a.plan;
+    // statistics of every slot, whether a part was written or not
+    const int slots = p.prefix_splits + p.own_splits;
+    float2 mine = {0.f, 0.f};
+    if (tid < slots) mine = a.stat[tid * rows + at];
+    const int s = a.seqs.cu ? session_search(a.seqs, token, lane, [](int first, int) { return first; })
+                            : token / a.seqs.each;
+    const int first = session_first(a.seqs, s), last = session_first(a.seqs, s + 1);
+    if (token < first || token >= last) return;  // in no session
+    const int L = own_tokens(a.seqs, a.pages, s), P = prefix_tokens(a);
+    const bool any = P > 0 || L - (last - token) + 1 > 0;
+
+    // which slots hold a part: the first n0 of the prefix's, the first n1 of the own ones
+    const int pu = units_of(P), lu = units_of(L);
+    const int u0 = p.joint ? pu + lu : pu, per0 = split_units(u0, p.prefix_splits);
+    const int n0 = per0 > 0 ? (u0 + per0 - 1) / per0 : 0;
+    const int per1 = p.joint ? 0 : split_units(lu, p.own_splits);
+    const int n1 = per1 > 0 ? (lu + per1 - 1) / per1 : 0, n = n0 + n1;
+    const int slot = tid < p.prefix_splits ? tid : tid - p.prefix_splits + n0;
+    if (tid < slots && (tid < p.prefix_splits ? tid < n0 : slot < n)) stat[slot] = mine;
+    __syncthreads();
+    float top = -__builtin_inff();
+    for (int k = 0; k < n; ++k) top = __builtin_fmaxf(top, stat[k].x);
+    float sum = 0.f;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < n; ++k) sum += stat[k].y * part_weight(stat[k], top);
+#pragma unroll 4
+    for (int k = group; k < n; k += GROUPS) {
+        const int64_t from = k < n0 ? k : p.prefix_splits + k - n0;
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(a.part + (from * rows + at) * DV + c);
+        const float f = part_weight(stat[k], top);
+        if (f != 0.f) y += w * f;  // a part of which nothing was seen holds anything
+    }
+    sums[group][tid % LANES] = y;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) y += sums[g][tid];
+    const float inv = any ? 1.f / sum : 0.f;
+    T *out = static_cast<T *>(a.out) + token * a.out_stride + (int64_t)h * DV + c;
+    store4(out, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    if (a.lse && c == 0)
+        a.lse[at] = any ? (usable(top) + __builtin_log2f(sum)) * kLn2 : -__builtin_inff();
+}
+
+// Blocks of the launch; -1 where they are too many for one.
+int64_t tile_grid(const AttnArgs &a, TileGrid *g) {
+    const AttnPlan &p = a.plan;
+    const int64_t rows = (int64_t)a.seqs.tokens * a.group;
+    int64_t r0 = 0, t0 = 0, r1 = 0, t1 = 0;
+    if (p.prefix_splits > 0 && !p.joint && !p.prefix_few) {
+        r0 = (int64_t)a.kv_heads * p.prefix_splits;
+        t0 = (rows + p.tile_rows - 1) / p.tile_rows;
+    }
+    if (p.joint || (p.own_splits > 0 && p.own_tiles)) {
+        r1 = (int64_t)a.kv_heads * (p.joint ? p.prefix_splits : p.own_splits);
+        t1 = rows / p.tile_rows + a.seqs.num;  // a session's first one: its first row's / tile_rows + its number
+    }
+    constexpr int64_t kMost = (int64_t)1 << 22;  // 512 threads each
+    if (r0 > kMost || t0 > kMost || r1 > kMost || t1 > kMost) return -1;
+    const int64_t b0 = (r0 * t0 + 7) / 8 * 8, b1 = (r1 * t1 + 7) / 8 * 8;
+    if (b0 + b1 > kMost) return -1;
+    *g = {(int)r0, (int)t0, (int)b0, (int)r1, (int)t1, (int)b1};
+    return b0 + b1;
+}
+
+int64_t few_blocks(const AttnArgs &a, int64_t *own) {
+    const AttnPlan &p = a.plan;
+    *own = p.few_rows > 0 && !p.joint ? (int64_t)a.seqs.num * a.kv_heads * p.own_splits : 0;
+    return *own + (p.prefix_few ? (int64_t)a.kv_heads * p.prefix_splits : 0);
+}
+
+
+template <typename T, int D, int TK, int PLACES>
+int mixed(const AttnArgs &a, const MixGrid &g, int64_t blocks, hipStream_t stream) {
+    hipLaunchKernelGGL((attn_kernel<T, D, TK, PLACES>), dim3((unsigned)blocks), dim3(256), 0, stream, a, g);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+// Blocks of the launch in all, -1 where they are too many for one.
+int64_t mix_grid(const AttnArgs &a, MixGrid *g) {
+    int64_t own;
+    const int64_t few = few_blocks(a, &own), tile = tile_grid(a, &g->tile);
+    if (tile < 0 || few + tile > (1 << 23)) return -1;
+    g->few = (int)few, g->own_few = (int)own;
+    return few + tile;
+}
+
+}  // namespace
+
+int64_t attn_threads(const AttnArgs &a) {
+    MixGrid g;
+    const int64_t n = mix_grid(a, &g);
+    return n < 0 ? kMostThreads + 1 : n * 512;
+}
+int64_t attn_merge_threads(const AttnArgs &a) { return (int64_t)a.seqs.tokens * a.heads * 256; }
+
+int launch_attn(const AttnArgs &a, hipStream_t stream) {
+    MixGrid g;
+    const int64_t n = mix_grid(a, &g);
+    if (n <= 0) return (int)n;
+    if (a.d == 576) {
+        hipLaunchKernelGGL(attn_latent_kernel, dim3((unsigned)n), dim3(512), 0, stream, a, g.tile);
+        return hipGetLastError() == hipSuccess ? 0 : -1;
+    }
+    if (a.dtype == kDtypeF32)
+        return a.d == 64 ? mixed<float, 64, 32, 2>(a, g, n, stream)
+                         : mixed<float, 128, 32, 1>(a, g, n, stream);
+    return a.d == 64 ? mixed<bf16, 64, 64, 2>(a, g, n, stream)
+                     : mixed<bf16, 128, 64, 2>(a, g, n, stream);
+}
+
+int launch_attn_merge(const AttnArgs &a, hipStream_t stream) {
+    const dim3 grid((unsigned)(attn_merge_threads(a) / 256));
+    if (a.dv == 512)
+        hipLaunchKernelGGL((attn_merge_kernel<bf16, 512>), grid, dim3(256), 0, stream, a);
+    else if (a.dtype == kDtypeF32 && a.dv == 64)
+        hipLaunchKernelGGL((attn_merge_kernel<float, 64>), grid, dim3(256), 0, stream, a);
+    else if (a.dtype == kDtypeF32)
+        hipLaunchKernelGGL((attn_merge_kernel<float, 128>), grid, dim3(256), 0, stream, a);
+    else if (a.dv == 64)
+        hipLaunchKernelGGL((attn_merge_kernel<bf16, 64>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((attn_merge_kernel<bf16, 128>), grid, dim3(256), 0, stream, a);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+}  // namespace kda

@@ -1,9 +1,10 @@
-// attn_tile.hip -- attention of many query rows over a shared prefix, over a
+// attn_tile.h -- attention of many query rows over a shared prefix, over a
 // session's own tokens, or over both: matrix products fed from LDS.
+#pragma once
+
 #include "attn_device.h"
 
 namespace kda {
-namespace {
 
 template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK> struct TileShape {
     static constexpr int E = sizeof(T), C = D * E / 16, CV = DV * E / 16;
@@ -22,19 +23,18 @@ struct TileGrid {
 };
 
 template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK>
-__global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileGrid g) {
+__device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, int block, char *smem) {
     typedef TileShape<T, D, DV, LATENT, SPLIT, NW, TK> S;
     // A wave's share: 32 rows, KS chunk pairs of their channels, DT * 32 of their values.
     constexpr int TT = TK / 32, DT = DV / 32 / SPLIT, KS = S::C / 2 / SPLIT;
     constexpr uint64_t kAll = ~0ull >> (64 - TK);
-    __shared__ __attribute__((aligned(1024))) char smem[S::LDS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, group = wave / SPLIT, part = wave % SPLIT;
 
     // Blocks in the order of their ranges (kv head, split), an eighth of them on each XCD:
     // those that read the same tokens share an L2.
-    const bool pre = (int)blockIdx.x < g.prefix_blocks;
-    const int b = pre ? blockIdx.x : blockIdx.x - g.prefix_blocks;
+    const bool pre = block < g.prefix_blocks;
+    const int b = pre ? block : block - g.prefix_blocks;
     const int tiles = pre ? g.prefix_tiles : g.own_tiles;
     const int unit = b % 8 * (pre ? g.prefix_blocks / 8 : g.own_blocks / 8) + b / 8;
     const int range = unit / tiles;
@@ -220,54 +220,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_tile_kernel(AttnArgs a, TileG
         if (a.lse && first)
             a.lse[at] = any ? (usable(m) * sl + __builtin_log2f(l)) * kLn2 : -__builtin_inff();
     }
-}
-
-template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK>
-int launch(const AttnArgs &a, const TileGrid &g, int64_t blocks, hipStream_t stream) {
-    auto kernel = attn_tile_kernel<T, D, DV, LATENT, SPLIT, NW, TK>;
-    if (blocks > 0)
-        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * NW), 0, stream, a, g);
-    return hipGetLastError() == hipSuccess ? 0 : -1;
-}
-
-// Blocks of the launch; -1 where they are too many for one.
-int64_t grid_of(const AttnArgs &a, TileGrid *g) {
-    const AttnPlan &p = a.plan;
-    const int64_t rows = (int64_t)a.seqs.tokens * a.group;
-    int64_t r0 = 0, t0 = 0, r1 = 0, t1 = 0;
-    if (p.prefix_splits > 0 && !p.joint && !p.prefix_few) {
-        r0 = (int64_t)a.kv_heads * p.prefix_splits;
-        t0 = (rows + p.tile_rows - 1) / p.tile_rows;
-    }
-    if (p.joint || (p.own_splits > 0 && p.own_tiles)) {
-        r1 = (int64_t)a.kv_heads * (p.joint ? p.prefix_splits : p.own_splits);
-        t1 = rows / p.tile_rows + a.seqs.num;  // a session's first one: its first row's / tile_rows + its number
-    }
-    constexpr int64_t kMost = (int64_t)1 << 22;  // 512 threads each
-    if (r0 > kMost || t0 > kMost || r1 > kMost || t1 > kMost) return -1;
-    const int64_t b0 = (r0 * t0 + 7) / 8 * 8, b1 = (r1 * t1 + 7) / 8 * 8;
-    if (b0 + b1 > kMost) return -1;
-    *g = {(int)r0, (int)t0, (int)b0, (int)r1, (int)t1, (int)b1};
-    return b0 + b1;
-}
-
-}  // namespace
-
-int64_t attn_tile_threads(const AttnArgs &a) {
-    TileGrid g;
-    const int64_t n = grid_of(a, &g);
-    return n < 0 ? kMostThreads + 1 : n * 512;
-}
-
-int launch_attn_tiles(const AttnArgs &a, hipStream_t stream) {
-    TileGrid g;
-    const int64_t n = grid_of(a, &g);
-    if (a.d == 576) return launch<bf16, 576, 512, true, 2, 8, 32>(a, g, n, stream);
-    if (a.dtype == kDtypeF32)
-        return a.d == 64 ? launch<float, 64, 64, false, 1, 4, 32>(a, g, n, stream)
-                         : launch<float, 128, 128, false, 1, 4, 32>(a, g, n, stream);
-    return a.d == 64 ? launch<bf16, 64, 64, false, 1, 4, 64>(a, g, n, stream)
-                     : launch<bf16, 128, 128, false, 1, 4, 64>(a, g, n, stream);
 }
 
 }  // namespace kda

@@ -392,7 +392,7 @@ int kda_prefix_attn_fwd(const void *q, const void *k_cache, const void *v_cache,
         a.part = static_cast<float *>(workspace);
         a.stat = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + values);
     }
-    if (kda::attn_tile_threads(a) > kda::kMostThreads || kda::attn_few_threads(a) > kda::kMostThreads ||
+    if (kda::attn_threads(a) > kda::kMostThreads ||
         (parts && kda::attn_merge_threads(a) > kda::kMostThreads))
         return KDA_ERR_UNSUPPORTED;
     if ((st = check_device()) != KDA_OK) return st;
@@ -400,8 +400,7 @@ int kda_prefix_attn_fwd(const void *q, const void *k_cache, const void *v_cache,
     if (debug_mode() &&
         (st = debug_check_offsets(cu_seqlens, num_seqs, tokens, stream, where)) != KDA_OK)
         return st;
-    int rc = kda::launch_attn_tiles(a, stream);
-    if (rc == 0) rc = kda::launch_attn_few(a, stream);
+    int rc = kda::launch_attn(a, stream);
     if (rc == 0 && parts) rc = kda::launch_attn_merge(a, stream);
     return launch_status(rc, stream, where);
 }

@@ -87,11 +87,9 @@ AttnPlan attn_plan(int64_t tokens, int64_t num_seqs, bool packed, int64_t q_head
                    int64_t kv_heads, int head_dim, int64_t own_tokens, int64_t prefix_tokens,
                    int dtype);
 // Threads of the launches that a call is made of, and those.
-int64_t attn_tile_threads(const AttnArgs &a);
-int64_t attn_few_threads(const AttnArgs &a);
+int64_t attn_threads(const AttnArgs &a);
 int64_t attn_merge_threads(const AttnArgs &a);
-int launch_attn_tiles(const AttnArgs &a, hipStream_t stream);
-int launch_attn_few(const AttnArgs &a, hipStream_t stream);
+int launch_attn(const AttnArgs &a, hipStream_t stream);
 int launch_attn_merge(const AttnArgs &a, hipStream_t stream);
 
 }  // namespace kda
