@@ -22,7 +22,7 @@ template <typename T, int D, int TK, int PLACES> struct MixShape {
     static constexpr int B = FewShape<T, D, 4, PLACES>::LDS;
     static constexpr int LDS = A > B ? A : B;
 };
-template <typename T, int D, int TK, int PLACES>
+template <typename T, int D, int TK, int PLACES, bool NEAR>
 __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a, MixGrid g) {
     __shared__ __attribute__((aligned(1024))) char smem[MixShape<T, D, TK, PLACES>::LDS];
     const int tiles = g.tile.prefix_blocks + g.tile.own_blocks;
@@ -39,15 +39,16 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a, MixGrid g) {
         if (few) b -= tiles - turns;
     }
     if (few)
-        few_walk<T, D, 4, PLACES>(a, g.own_few, b, smem);
+        few_walk<T, D, 4, PLACES, NEAR>(a, g.own_few, b, smem);
     else
-        tile_walk<T, D, D, false, 1, 4, TK>(a, g.tile, b, smem);
+        tile_walk<T, D, D, false, 1, 4, TK, NEAR>(a, g.tile, b, smem);
 }
 
+template <bool NEAR>
 __global__ __launch_bounds__(512, 2) void attn_latent_kernel(AttnArgs a, TileGrid g) {
     typedef TileShape<bf16, 576, 512, true, 2, 8, 32> S;
     __shared__ __attribute__((aligned(1024))) char smem[S::LDS];
-    tile_walk<bf16, 576, 512, true, 2, 8, 32>(a, g, blockIdx.x, smem);
+    tile_walk<bf16, 576, 512, true, 2, 8, 32, NEAR>(a, g, blockIdx.x, smem);
 }
 
 // One workgroup per row (token, head): DV / 4 lanes hold a row's values, the 1024 / DV groups
@@ -136,7 +137,12 @@ int64_t few_blocks(const AttnArgs &a, int64_t *own) {
 
 template <typename T, int D, int TK, int PLACES>
 int mixed(const AttnArgs &a, const MixGrid &g, int64_t blocks, hipStream_t stream) {
-    hipLaunchKernelGGL((attn_kernel<T, D, TK, PLACES>), dim3((unsigned)blocks), dim3(256), 0, stream, a, g);
+    if (a.pages.near)
+        hipLaunchKernelGGL((attn_kernel<T, D, TK, PLACES, true>), dim3((unsigned)blocks), dim3(256), 0,
+                           stream, a, g);
+    else
+        hipLaunchKernelGGL((attn_kernel<T, D, TK, PLACES, false>), dim3((unsigned)blocks), dim3(256), 0,
+                           stream, a, g);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
@@ -163,7 +169,12 @@ int launch_attn(const AttnArgs &a, hipStream_t stream) {
     const int64_t n = mix_grid(a, &g);
     if (n <= 0) return (int)n;
     if (a.d == 576) {
-        hipLaunchKernelGGL(attn_latent_kernel, dim3((unsigned)n), dim3(512), 0, stream, a, g.tile);
+        if (a.pages.near)
+            hipLaunchKernelGGL((attn_latent_kernel<true>), dim3((unsigned)n), dim3(512), 0, stream, a,
+                               g.tile);
+        else
+            hipLaunchKernelGGL((attn_latent_kernel<false>), dim3((unsigned)n), dim3(512), 0, stream, a,
+                               g.tile);
         return hipGetLastError() == hipSuccess ? 0 : -1;
     }
     if (a.dtype == kDtypeF32)

@@ -211,6 +211,13 @@ __device__ __forceinline__ void load_lds16(const char *from, uint32_t to) {
                  : "v"(from), "s"(to)
                  : "memory");
 }
+// The same from an address that is the wave's and an offset under 2^32 that is the lane's.
+__device__ __forceinline__ void load_lds16(const char *from, uint32_t offset, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0"
+                 :
+                 : "s"(from), "v"(offset), "s"(to)
+                 : "memory");
+}
 // Until at most N of this wave's loads are on their way.  The compiler knows this instruction:
 // it does not wait again for its own loads from before.
 template <int N> __device__ __forceinline__ void wait_loads() {
@@ -219,27 +226,43 @@ template <int N> __device__ __forceinline__ void wait_loads() {
     asm volatile("" ::: "memory");
 }
 
-// Rows of C chunks of ROWS tokens into a tile, 64 chunks a load, wave `wave` of NW taking
-// every NW-th load; place: each token's, at its lane.  TWO: the same rows of another cache
-// into the tile behind.
-template <int C, int ROWS, int NW, bool TWO>
-__device__ __forceinline__ void load_tile(const char *base, const char *second, uint32_t place,
-                                          int shift, lds_char *tile, int wave, int lane) {
-    constexpr int LOADS = ROWS * C / 64;
-#pragma unroll
-    for (int i = 0; i < (LOADS + NW - 1) / NW; ++i) {
-        const int load = NW * i + wave;
-        if (LOADS % NW != 0 && load >= LOADS) break;
-        // (rows that are no power of two: formed again each time, to keep registers free)
-        const int p = 64 * load + ((C & (C - 1)) != 0 ? here(lane) : lane), row = p / C;
-        const int chunk = (p % C) ^ tile_turn<C>(row);
-        const uint64_t at =
-            (uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(4 * row, (int)place) << shift;
-        const uint32_t to = (uint32_t)(uintptr_t)tile + 1024 * load;
-        load_lds16(base + chunk * 16 + at, to);
-        if (TWO) load_lds16(second + chunk * 16 + at, to + ROWS * C * 16);
+// The loads of rows of C chunks of ROWS tokens into a tile, 64 chunks each, wave `wave` of NW
+// taking every NW-th.  set(): from each token's place, at its lane; load(): from any cache of
+// that layout.  NEAR: every value of a head lies under 2^32 bytes behind its first.
+template <int C, int ROWS, int NW, bool NEAR> struct TileLoads {
+    static constexpr int LOADS = ROWS * C / 64, N = (LOADS + NW - 1) / NW;
+    uint32_t at[N];
+    __device__ static bool mine(int i, int wave) { return LOADS % NW == 0 || NW * i + wave < LOADS; }
+    // Row and byte in the row of what this lane reads with load i.  (Rows that are no power of
+    // two: formed again each time, to keep registers free.)
+    __device__ static void part(int i, int wave, int lane, int *row, int *byte) {
+        const int p = 64 * (NW * i + wave) + ((C & (C - 1)) != 0 ? here(lane) : lane);
+        *row = p / C, *byte = ((p % C) ^ tile_turn<C>(*row)) * 16;
     }
-}
+    __device__ __forceinline__ void set(const Pages &pages, uint32_t place, int wave, int lane) {
+        if (NEAR) place <<= pages.shift;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            int row, byte;
+            part(i, wave, lane, &row, &byte);
+            at[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (row < ROWS ? row : 0), (int)place);
+        }
+    }
+    __device__ __forceinline__ void load(const Pages &pages, const char *cache, lds_char *tile,
+                                         int wave, int lane) const {
+        const uint32_t to = (uint32_t)(uintptr_t)tile + 1024 * wave;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (!mine(i, wave)) break;
+            int row, byte;
+            part(i, wave, lane, &row, &byte);
+            if (NEAR)
+                load_lds16(cache, at[i] + byte, to + 1024 * NW * i);
+            else
+                load_lds16(cache + ((uint64_t)at[i] << pages.shift) + byte, to + 1024 * NW * i);
+        }
+    }
+};
 // Rows of tokens that are not there (valid) to zeros: their product with a probability of zero
 // has to be zero.  Each wave clears what it has loaded, once that has come.
 template <int C, int ROWS, int NW>
@@ -291,10 +314,10 @@ __device__ __forceinline__ void hide_scores(f32x16 (&s)[TT], uint64_t valid, int
     }
 }
 
-// Scores to probabilities relative to the running maximum m, their sum into l.
+// The running maximum m over a tile's scores; what stands against the old one moves with it.
 template <int TT, int DT>
-__device__ __forceinline__ void soften(f32x16 (&s)[TT], float &m, float &l, f32x16 (&o)[DT],
-                                       float sl) {
+__device__ __forceinline__ void move_maximum(const f32x16 (&s)[TT], float &m, float &l,
+                                             f32x16 (&o)[DT], float sl) {
     float top = s[0][0];
 #pragma unroll
     for (int j = 0; j < TT; ++j)
@@ -309,6 +332,10 @@ __device__ __forceinline__ void soften(f32x16 (&s)[TT], float &m, float &l, f32x
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= f;
     }
+}
+// Scores to probabilities relative to m, their sum into l.
+template <int TT>
+__device__ __forceinline__ void soften(f32x16 (&s)[TT], float m, float &l, float sl) {
     const float ms = usable(m) * sl;
 #pragma unroll
     for (int j = 0; j < TT; ++j)
@@ -324,9 +351,9 @@ template <typename T, int C, int TT, int KS>
 __device__ __forceinline__ void scores(lds_char *tile, const Keys<C> &keys, const u32x4 (&q)[KS],
                                        f32x16 (&s)[TT]) {
 #pragma unroll
-    for (int j = 0; j < TT; ++j)
+    for (int c = 0; c < KS; ++c)
 #pragma unroll
-        for (int c = 0; c < KS; ++c)
+        for (int j = 0; j < TT; ++j)
             s[j] = AttnMma<T>::chunk(keys.read(tile, j, c), q[c], c ? s[j] : f32x16(0.f));
 }
 
@@ -370,6 +397,55 @@ __device__ __forceinline__ void add_others(const Pages &pages, const int32_t *ta
                     const float x = to_f32(row[32 * (d0 + d) + 8 * k + 4 * half + i]);
                     o[d][4 * k + i] += see && !(__builtin_fabsf(x) < __builtin_inff()) ? x : 0.f;
                 }
+    }
+}
+
+// A tile's probabilities (s, against m) and their products with its values, and beside them the
+// scores of the next tile, in one stream that keeps the matrix unit fed: operands are read from
+// LDS kAhead products before they are used, and the exponentials stand between the products of
+// the next scores, which do not depend on them.  The fences keep the compiler from moving each
+// read to its product, where its latency would be waited for.  beside(i): what else is done
+// with product i of the values, which have little beside them.
+constexpr int kAhead = 4;
+template <typename T, int C, int TT, int KS, int DT, typename V, typename F>
+__device__ __forceinline__ void turn_over(lds_char *kt, lds_char *vt, const Keys<C> &keys,
+                                          const V &values, const u32x4 (&q)[KS], f32x16 (&s)[TT],
+                                          f32x16 (&next)[TT], float m, float &l, f32x16 (&o)[DT],
+                                          float sl, F beside) {
+    typedef AttnMma<T> M;
+    constexpr int QK = TT * KS, PV = 2 * TT * DT, E = 16 * TT;
+    static_assert(QK >= kAhead && PV >= kAhead, "operands ahead");
+    u32x4 k[kAhead];
+    typename M::Value v[kAhead];
+    typename M::Prob p[2 * TT];
+    const float ms = usable(m) * sl;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) k[i] = keys.read(kt, i % TT, i / TT);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < QK; ++i) {
+        const int j = i % TT, c = i / TT, to = i + kAhead;
+        next[j] = M::chunk(k[i % kAhead], q[c], c ? next[j] : f32x16(0.f));
+        if (to < QK)
+            k[i % kAhead] = keys.read(kt, to % TT, to / TT);
+        else
+            v[to - QK] = values.read(vt, (to - QK) / DT, (to - QK) % DT);
+#pragma unroll
+        for (int e = i * E / QK; e < (i + 1) * E / QK; ++e) {
+            const float x = fast_exp2(s[e / 16][e % 16] * sl - ms);
+            s[e / 16][e % 16] = x;
+            l += x;
+            if (e % 8 == 7) p[e / 8] = M::prob(s[e / 16], e / 8 % 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < PV; ++i) {
+        const int d = i % DT, to = i + kAhead;
+        o[d] = M::mma(v[i % kAhead], p[i / DT], o[d]);
+        if (to < PV) v[i % kAhead] = values.read(vt, to / DT, to % DT);
+        beside(i);
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 

@@ -24,7 +24,7 @@ template <typename T, int D, int NW, int PLACES> struct FewShape {
 };
 
 // One workgroup per (session, kv head, split), or per (kv head, split) of the prefix.
-template <typename T, int D, int NW, int PLACES>
+template <typename T, int D, int NW, int PLACES, bool NEAR>
 __device__ __forceinline__ void few_walk(const AttnArgs &a, int own_blocks, int block, char *smem) {
     typedef FewShape<T, D, NW, PLACES> S;
     constexpr int DT = D / 32, KS = S::C / 2;
@@ -92,9 +92,8 @@ __device__ __forceinline__ void few_walk(const AttnArgs &a, int own_blocks, int 
         *valid = (uint32_t)__ballot(there);
         return place;
     };
-    auto load = [&](const char *cache, uint32_t place, lds_char *to) {
-        load_tile<S::C, kFewTile, 1, false>(cache, nullptr, place, a.pages.shift, to, 0, lane);
-    };
+    TileLoads<S::C, kFewTile, 1, NEAR> loads;
+    auto load = [&](const char *cache, lds_char *to) { loads.load(a.pages, cache, to, 0, lane); };
 
     f32x16 o[DT];
     float m = -__builtin_inff(), l = 0.f;
@@ -103,12 +102,12 @@ __device__ __forceinline__ void few_walk(const AttnArgs &a, int own_blocks, int 
     const float sl = a.scale * kLog2e;
     const Keys<S::C> keys(0, lane);
     const typename AttnMma<T>::template Values<S::C> values(0, lane);
-    uint32_t valid = 0, next_valid = 0, place = 0;
-    if (count > 0) place = where(0, &valid);
+    uint32_t valid = 0, next_valid = 0;
+    if (count > 0) loads.set(a.pages, where(0, &valid), 0, lane);
     wait_loads<0>();  // the queries, which have come with the entries: not waited for again
     if (count > 0) {
-        load(kc, place, kt);
-        if (PLACES == 2) load(vc, place, vt);
+        load(kc, kt);
+        if (PLACES == 2) load(vc, vt);
     }
     bool odd = false;  // a value that is no number in a tile that not all rows see whole
     // One tile; LATER: some row may not see some token of it.
@@ -120,11 +119,12 @@ __device__ __forceinline__ void few_walk(const AttnArgs &a, int own_blocks, int 
         f32x16 s[1];
         scores<T, S::C, 1, KS>(kt, keys, q, s);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read, before they are loaded again
-        if (PLACES == 1) load(vc, place, vt);
-        if (more) place = where(k + 1, &next_valid);
-        if (PLACES == 2 && more) load(kc, place, kt);
+        if (PLACES == 1) load(vc, vt);
+        if (more) loads.set(a.pages, where(k + 1, &next_valid), 0, lane);
+        if (PLACES == 2 && more) load(kc, kt);
         if (later || valid != ~0u) hide_scores<1>(s, valid, later ? lim - base : kFewTile, lane);
-        soften<1, DT>(s, m, l, o, sl);
+        move_maximum<1, DT>(s, m, l, o, sl);
+        soften<1>(s, m, l, sl);
         if (PLACES == 2 && more)
             wait_loads<S::LOADS>();
         else
@@ -136,7 +136,7 @@ __device__ __forceinline__ void few_walk(const AttnArgs &a, int own_blocks, int 
         if (later && any_odd<T>(vt, kFewTile * S::C, lane)) odd = true;
         add_values<T, later>(s, vt, values, o);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (more) load(PLACES == 2 ? vc : kc, place, vt);
+        if (more) load(PLACES == 2 ? vc : kc, vt);
         valid = next_valid;
     };
     // tiles that all rows see whole first: those that end at the first row's last token or before

@@ -9,8 +9,10 @@ namespace kda {
 template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK> struct TileShape {
     static constexpr int E = sizeof(T), C = D * E / 16, CV = DV * E / 16;
     static constexpr int BM = 32 * NW / SPLIT;          // rows of a workgroup
-    static constexpr int KB = TK * C * 16, VB = LATENT ? 0 : TK * CV * 16, BUF = KB + VB;
-    static constexpr int LDS = 2 * BUF + (SPLIT == 2 ? 4096 * NW : 0);
+    static constexpr int KB = TK * C * 16, VB = LATENT ? 0 : TK * CV * 16;
+    // tiles of keys t + 1 and values t are read while keys t + 2 and values t + 1 come
+    static constexpr int SUMS = 2 * (KB + VB);
+    static constexpr int LDS = SUMS + (SPLIT == 2 ? 4096 * NW : 0);
     static constexpr int CHV = LATENT ? C : CV;         // chunks of a row that holds values
     static_assert(TK * C % 64 == 0 && TK * CV % 64 == 0, "whole loads");
 };
@@ -22,7 +24,7 @@ struct TileGrid {
     int own_ranges, own_tiles, own_blocks;
 };
 
-template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK>
+template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK, bool NEAR>
 __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, int block, char *smem) {
     typedef TileShape<T, D, DV, LATENT, SPLIT, NW, TK> S;
     // A wave's share: 32 rows, KS chunk pairs of their channels, DT * 32 of their values.
@@ -108,85 +110,188 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
     const char *kc = static_cast<const char *>(a.k_cache) + head;
     const char *vc = LATENT ? nullptr : static_cast<const char *>(a.v_cache) + head;
     lds_char *lds = (lds_char *)smem;
+    auto keys_of = [&](int t) { return lds + (t & 1) * S::KB; };
+    auto values_of = [&](int t) { return LATENT ? keys_of(t) : lds + 2 * S::KB + (t & 1) * S::VB; };
     auto base_of = [&](int t) { return t < n0 ? base0 + t * TK : base1 + (t - n0) * TK; };
-    // This lane's token of tile t: the entry of its page, -1 where there is none.
-    auto entry_of = [&](int t) {
-        const int tok = base_of(t) + lane;
-        if (t >= nt || lane >= TK || tok >= (t < n0 ? end0 : end1)) return -1;
-        return (t < n0 ? a.prefix_pages : own_table)[a.pages.by_size(tok)];
+
+    // The tile that is placed next and the entry of its page for this lane's token (one of the
+    // table's whether the token is there or not) and the token's number in the page; the same of
+    // the tile behind it, whose entry is on its way.  No branches: this stands in the stream of
+    // products.
+    int ahead = 0, in = 0, entry = 0, in2 = 0, entry2 = 0;
+    const int last0 = end0 > base0 ? a.pages.by_size(end0 - 1) : 0;
+    const int last1 = end1 > base1 ? a.pages.by_size(end1 - 1) : 0;
+    auto owned = [&](int t) { return n0 < nt && t >= n0; };
+    auto look_up = [&](int t) {
+        const int tok = base_of(t) + lane, idx = a.pages.by_size(tok);
+        const int last = owned(t) ? last1 : last0;
+        in = in2, entry = entry2;
+        in2 = tok - idx * a.pages.size;
+        entry2 = (owned(t) ? own_table : a.prefix_pages)[idx < last ? idx : last];
     };
-    auto issue = [&](int t, int entry) -> uint64_t {
-        bool there;
-        const uint32_t place = token_place(a.pages, entry, base_of(t) + lane, &there);
-        load_tile<S::C, TK, NW, !LATENT>(kc, vc, place, a.pages.shift, lds + (t & 1) * S::BUF, wave, lane);
-        return __ballot(there);
+    // That tile's loads, and which of its tokens there are.
+    auto place_tile = [&](TileLoads<S::C, TK, NW, NEAR> &loads, uint64_t *valid) {
+        const int end = ahead >= nt ? 0 : (owned(ahead) ? end1 : end0);
+        const bool there = (lane < TK) & (base_of(ahead) + lane < end) &
+                           ((unsigned)entry < (unsigned)a.pages.count);
+        const uint32_t place = (uint32_t)entry * a.pages.page_units + (uint32_t)in * a.pages.token_units;
+        *valid = __ballot(there);
+        loads.set(a.pages, there ? place : 0, wave, lane);
+        ++ahead;
+    };
+    auto load_keys = [&](int t, const TileLoads<S::C, TK, NW, NEAR> &loads) {
+        if (t < nt) loads.load(a.pages, kc, keys_of(t), wave, lane);
+    };
+    auto load_values = [&](int t, const TileLoads<S::C, TK, NW, NEAR> &loads) {
+        if (!LATENT && t < nt) loads.load(a.pages, vc, values_of(t), wave, lane);
     };
 
-    f32x16 o[DT];
+    f32x16 o[DT], s[TT];
     float m = -__builtin_inff(), l = 0.f;  // running maximum of q k; this lane's half of the sum
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16(0.f);
     const float sl = a.scale * kLog2e;  // scores in units of log 2
-
     const Keys<S::C> keys(part * KS, lane);
     const typename AttnMma<T>::template Values<S::CHV> values(part * DT, lane);
-
     bool odd = false;  // a value that is no number in a tile that not all rows see whole
-    uint64_t valid = 0, next_valid = 0;
-    int entry = -1;
-    if (nt > 0) {
-        valid = issue(0, entry_of(0));
-        entry = entry_of(1);
-    }
-    // One tile; LATER: some row may not see some token of it.
-    auto step = [&](int t, auto LATER) {
-        constexpr bool later_tiles = decltype(LATER)::value;
-        lds_char *kt = lds + (t & 1) * S::BUF, *vt = LATENT ? kt : kt + S::KB;
-        wait_loads<0>();
-        if (valid != kAll) clear_rows<S::CHV, TK, NW>(vt, valid, wave, lane);
-        __syncthreads();
-        if (t + 1 < nt) {
-            next_valid = issue(t + 1, entry);
-            entry = entry_of(t + 2);
-        }
-        const int base = base_of(t);
-        const bool look = active && !(later_tiles && base >= wave_max);
-        f32x16 s[TT];
-        if (SPLIT == 2 || look) scores<T, S::C, TT, KS>(kt, keys, q, s);
-        if constexpr (SPLIT == 2) {  // the sum over the other half of the channels
-            lds_char *mine = lds + 2 * S::BUF + wave * 4096 + lane * 16;
-            lds_char *other = lds + 2 * S::BUF + (wave ^ 1) * 4096 + lane * 16;
+
+    // SPLIT 2: the sums over the two halves of the channels meet in LDS.
+    lds_char *mine = lds + S::SUMS + wave * 4096 + lane * 16;
+    lds_char *other = lds + S::SUMS + (wave ^ 1) * 4096 + lane * 16;
+    auto give = [&](const f32x16 &x) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                *(lds_f32x4 *)(mine + 1024 * e) =
-                    f32x4{s[0][4 * e], s[0][4 * e + 1], s[0][4 * e + 2], s[0][4 * e + 3]};
-            lds_barrier();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const f32x4 w = *(lds_f32x4 *)(other + 1024 * e);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[0][4 * e + i] += w[i];
-            }
-        }
-        if (look) {
-            if (later_tiles || valid != kAll)
-                hide_scores<TT>(s, valid, later_tiles ? lim - base : TK, lane);
-            soften<TT, DT>(s, m, l, o, sl);
-            if (later_tiles && any_odd<T>(vt, TK * S::CHV, lane)) odd = true;
-            add_values<T, later_tiles>(s, vt, values, o);
-        }
-        valid = next_valid;
+        for (int e = 0; e < 4; ++e)
+            *(lds_f32x4 *)(mine + 1024 * e) = f32x4{x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]};
     };
-    wait_loads<0>();  // the queries among them
-    // tiles that all rows see whole first: of the prefix, and of own tokens up to the first row's
-    int t = 0, plain = nt;
+    auto take = [&](f32x16 &x) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f32x4 w = *(lds_f32x4 *)(other + 1024 * e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[4 * e + i] += w[i];
+        }
+    };
+
+    // tiles under `plain` are seen whole by all rows: of the prefix, and own ones up to the first row's
+    int plain = nt;
     if (!pre && end1 > base1) {
         const int whole = seen(0) > base1 ? (seen(0) - base1) / TK : 0;
         plain = n0 + whole < nt ? n0 + whole : nt;
     }
-    for (; t < plain; ++t) step(t, std::false_type{});
-    for (; t < nt; ++t) step(t, std::true_type{});
-    if (odd) add_others<T>(a.pages, own_table, LATENT ? kc : vc, base_of(plain), end1, part * DT, lim, lane, o);
+    // valid: which tokens of tile t there are; valid1, valid2: of the two behind it.
+    uint64_t valid = 0, valid1 = 0, valid2 = 0;
+    TileLoads<S::C, TK, NW, NEAR> loads, loads2;  // of tiles t + 1 and t + 2
+    int t = 0;
+    if (nt == 0) {
+        wait_loads<0>();
+    } else if constexpr (SPLIT == 1) {
+        look_up(0), look_up(1);
+        place_tile(loads, &valid);
+        load_keys(0, loads);
+        load_values(0, loads);
+        look_up(2);
+        place_tile(loads, &valid1);
+        load_keys(1, loads);
+        look_up(3);
+        place_tile(loads2, &valid2);
+        wait_loads<0>();  // the queries among them
+        __syncthreads();
+        if (nt > 0 && active) scores<T, S::C, TT, KS>(keys_of(0), keys, q, s);
+        // Tile t, whose scores are in x: probabilities and values, and beside them the scores of
+        // tile t + 1, to y.  LATER: some row may not see some token of it, or it is the last.
+        auto step = [&](f32x16 (&x)[TT], f32x16 (&y)[TT], auto LATER) {
+            constexpr bool later = decltype(LATER)::value;
+            lds_char *vt = values_of(t), *kt = keys_of(t + 1);
+            wait_loads<0>();
+            if (valid != kAll) clear_rows<S::CHV, TK, NW>(vt, valid, wave, lane);
+            __syncthreads();
+            load_values(t + 1, loads);
+            load_keys(t + 2, loads2);
+            look_up(t + 4);
+            const int base = base_of(t);
+            const bool own = t >= n0, look = active && !(later && own && base >= wave_max);
+            if (look && (later || valid != kAll))
+                hide_scores<TT>(x, valid, later && own ? lim - base : TK, lane);
+            if (later && look && any_odd<T>(vt, TK * S::CHV, lane)) odd = true;
+            valid = valid1, valid1 = valid2;
+            auto place_next = [&]() {
+                loads = loads2;
+                place_tile(loads2, &valid2);
+            };
+            if constexpr (!later) {
+                if (active) {
+                    move_maximum<TT, DT>(x, m, l, o, sl);
+                    turn_over<T>(kt, vt, keys, values, q, x, y, m, l, o, sl, [&](int i) {
+                        if (i == 2) place_next();
+                    });
+                } else {
+                    place_next();
+                }
+            } else {
+                place_next();
+                if (active && t + 1 < nt) scores<T, S::C, TT, KS>(kt, keys, q, y);
+                if (look) {
+                    move_maximum<TT, DT>(x, m, l, o, sl);
+                    soften<TT>(x, m, l, sl);
+                    add_values<T, true>(x, vt, values, o);
+                }
+            }
+            ++t;
+        };
+        f32x16 s2[TT];
+        while (t + 1 < plain && t + 2 < nt) {
+            step(s, s2, std::false_type{});
+            step(s2, s, std::false_type{});
+        }
+        while (t < nt) {
+            step(s, s2, std::true_type{});
+#pragma unroll
+            for (int j = 0; j < TT; ++j) s[j] = s2[j];
+        }
+    } else {
+        look_up(0), look_up(1);
+        place_tile(loads, &valid);
+        load_keys(0, loads);
+        look_up(2);
+        place_tile(loads, &valid1);
+        wait_loads<0>();  // the queries among them
+        auto step = [&](auto LATER) {
+            constexpr bool later = decltype(LATER)::value;
+            lds_char *kt = keys_of(t);
+            wait_loads<0>();
+            if (valid != kAll) clear_rows<S::CHV, TK, NW>(kt, valid, wave, lane);
+            __syncthreads();
+            load_keys(t + 1, loads);
+            look_up(t + 3);
+            const int base = base_of(t);
+            const bool own = t >= n0, look = active && !(later && own && base >= wave_max);
+            if (active) {
+                scores<T, S::C, TT, KS>(kt, keys, q, s);
+                give(s[0]);
+            }
+            lds_barrier();
+            if (look) {
+                take(s[0]);
+                if (later || valid != kAll)
+                    hide_scores<TT>(s, valid, later && own ? lim - base : TK, lane);
+                if (later && any_odd<T>(kt, TK * S::CHV, lane)) odd = true;
+                move_maximum<TT, DT>(s, m, l, o, sl);
+                soften<TT>(s, m, l, sl);
+                add_values<T, later>(s, kt, values, o);
+            }
+            place_tile(loads, &valid2);
+            valid = valid1, valid1 = valid2;
+            ++t;
+        };
+        while (t < plain) step(std::false_type{});
+        while (t < nt) step(std::true_type{});
+    }
+    if (odd) {  // from the first of those tiles on: all own tokens, or the last of the prefix
+        const int from = plain < nt ? plain : nt - 1;
+        const bool own = from >= n0;
+        add_others<T>(a.pages, own ? own_table : a.prefix_pages, LATENT ? kc : vc, base_of(from),
+                      own ? end1 : end0, part * DT, own ? lim : end0, lane, o);
+    }
 
     if (!active) return;
     const int r = 32 * group + (lane & 31);

@@ -59,7 +59,7 @@ int check_pages(int32_t num_pages, int32_t page_size, int32_t heads, int32_t d, 
             return KDA_ERR_SHAPE;
     }
     *p = {num_pages, page_size, kda::Divisor((uint32_t)page_size), page_stride * esz,
-          token_stride * esz, head_stride * esz, 0, 0, 4};
+          token_stride * esz, head_stride * esz, 0, 0, 4, 0};
     // the largest power of two that divides both (16 bytes at least: checked with the alignment)
     const uint64_t page = num_pages > 1 ? (uint64_t)p->page : 0;
     const uint64_t token = page_size > 1 ? (uint64_t)p->token : 0, bits = page | token;
@@ -68,6 +68,7 @@ int check_pages(int32_t num_pages, int32_t page_size, int32_t heads, int32_t d, 
                           (token >> p->shift) * (page_size - 1);
     if (most > UINT32_MAX) return KDA_ERR_UNSUPPORTED;
     p->page_units = (uint32_t)(page >> p->shift), p->token_units = (uint32_t)(token >> p->shift);
+    p->near = ((most << p->shift) + (uint64_t)d * esz) >> 32 == 0;
     return KDA_OK;
 }
 

@@ -42,6 +42,7 @@ struct Pages {
     // the first two in units of 2^shift bytes: every token's place of a head fits 32 bits
     uint32_t page_units, token_units;
     int32_t shift;
+    int32_t near;  // every value of a head lies under 2^32 bytes behind its first: places in bytes
 };
 
 struct AppendArgs {
