@@ -13,8 +13,29 @@ from typing import Optional, Tuple
 import torch
 
 from ._lib import lib
-from .layer import _call, _dtype, _expect, _fits, _out_rows, _rows, _sizes_fit, _workspace
+from .layer import _MOST, _call, _dtype, _expect, _fits, _rows, _sizes_fit, _workspace
 from .ops import _DTYPES, _ptr
+
+
+_INT32, _FLOAT32 = torch.int32, torch.float32
+
+
+def _row_stride(t, name, dtype, T, H, d, device) -> int:
+    """``_rows`` of a [T, H, d] tensor with the common cases first."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (T, H, d) and t.device == device:
+        row, head, one = t.stride()
+        if one == 1 and head == d and row >= H * d and T > 1 and H > 0:
+            return row
+    return _rows(t, name, dtype, torch.Size((T, H, d)), device, 1)
+
+
+def _ints(t, name, shape, device):
+    """Check a dense int32 tensor."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _INT32 and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        if t is None:
+            raise TypeError(f"{name} must be a tensor")
+        _expect(t, name, _INT32, shape, device)
 
 
 def _cache(t, name, dtype, device, heads, d):
@@ -25,14 +46,13 @@ def _cache(t, name, dtype, device, heads, d):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    shape = t.shape
-    if len(shape) != 4 or shape[2] != heads or shape[3] != d:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected (pages, page_size, {heads}, {d})")
+    if t.dim() != 4 or t.shape[2:] != (heads, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (pages, page_size, {heads}, {d})")
+    n, page = t.shape[:2]
     s = t.stride()
     if s[3] != 1 and d != 1:
         raise ValueError(f"{name}: the channels of a head must be contiguous")
-    n, page = shape[0], shape[1]
-    if n > 0x7fffffff or not 1 <= page <= 0x7fffffff:
+    if n > _MOST or not 1 <= page <= _MOST:
         _sizes_fit(name, n, page)
         raise ValueError(f"{name}: a page holds at least one token")
     return (n, page, s[0] if n > 1 else 0, s[1] if page > 1 else 0, s[2] if heads > 1 else 0)
@@ -40,23 +60,27 @@ def _cache(t, name, dtype, device, heads, d):
 
 def _caches(k_cache, v_cache, dtype, device, heads, d):
     k = _cache(k_cache, "k_cache", dtype, device, heads, d)
-    if v_cache is not None and _cache(v_cache, "v_cache", dtype, device, heads, d) != k:
-        raise ValueError("k_cache and v_cache must have one shape and one order in memory")
+    if v_cache is not None:
+        if (isinstance(v_cache, torch.Tensor) and v_cache.shape == k_cache.shape
+                and v_cache.dtype is dtype and v_cache.stride() == k_cache.stride()
+                and v_cache.device == device):
+            return k
+        if _cache(v_cache, "v_cache", dtype, device, heads, d) != k:
+            raise ValueError("k_cache and v_cache must have one shape and one order in memory")
     return k
 
 
 def _sessions(page_table, lens, cu_seqlens, tokens, device):
     """Check the sessions' table, lengths and offsets; returns (sessions, table width)."""
-    for t, name, dim in ((page_table, "page_table", 2), (lens, "lens", 1)):
-        if not isinstance(t, torch.Tensor) or t.dim() != dim:
-            raise ValueError(f"{name} must be a {dim}-D tensor")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a 2-D tensor")
     n, width = page_table.shape
-    if n > 0x7fffffff or width > 0x7fffffff or tokens > 0x7fffffff:
+    if n > _MOST or width > _MOST or tokens > _MOST:
         _sizes_fit("page_table", n, width, tokens)
-    _expect(page_table, "page_table", torch.int32, (n, width), device)
-    _expect(lens, "lens", torch.int32, (n,), device)
+    _ints(page_table, "page_table", (n, width), device)
+    _ints(lens, "lens", (n,), device)
     if cu_seqlens is not None:
-        _expect(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), device)
+        _ints(cu_seqlens, "cu_seqlens", (n + 1,), device)
     elif tokens % n if n else tokens:
         raise ValueError(f"{tokens} tokens are not the same number for each of {n} sessions")
     return n, width
@@ -89,9 +113,9 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Tens
     dev, dtype = k.device, k.dtype
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
-    ks = _rows(k, "k", dtype, k.shape, dev, 1)
-    vs = 0 if v is None else _rows(v, "v", dtype, k.shape, dev, 1)
-    pages = _caches(k_cache, v_cache, dtype, dev, H, d)
+    ks = _row_stride(k, "k", dtype, T, H, d, dev)
+    vs = 0 if v is None else _row_stride(v, "v", dtype, T, H, d, dev)
+    pages, page, *strides = _caches(k_cache, v_cache, dtype, dev, H, d)
     n, width = _sessions(page_table, lens, cu_seqlens, T, dev)
     hq = qs = os = 0
     if q is not None:
@@ -99,8 +123,11 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Tens
             raise ValueError("q must be [T, Hq, d]")
         hq = q.shape[1]
         _fits(q, "q")
-        qs = _rows(q, "q", dtype, (T, hq, d), dev, 1)
-        out_q, os = _out_rows(out_q, "out_q", q, dev, 1)
+        qs = _row_stride(q, "q", dtype, T, hq, d, dev)
+        if out_q is None:
+            out_q, os = torch.empty((T, hq, d), dtype=dtype, device=dev), hq * d
+        else:
+            os = _row_stride(out_q, "out_q", dtype, T, hq, d, dev)
     elif out_q is not None:
         raise ValueError("out_q needs q")
     rot = rows = 0
@@ -111,13 +138,14 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Tens
             raise ValueError("table must be [rows, rotary_dim]")
         rows, rot = table.shape
         _fits(table, "table")
-        _expect(table, "table", torch.float32, (rows, rot), dev)
-        _expect(positions, "positions", torch.int32, (T,), dev)
-    _sizes_fit("rotary_offset", rotary_offset)
-    _call("kda_cache_append", dev, _ptr(q), _ptr(k), _ptr(v), _ptr(table), _ptr(positions),
-          _ptr(page_table), _ptr(lens), _ptr(cu_seqlens), _ptr(out_q), _ptr(k_cache),
-          _ptr(v_cache), T, n, hq, H, d, rot, rotary_offset, rows, pages[0], pages[1], width, qs,
-          ks, vs, os, *pages[2:], int(bool(interleaved)), dt)
+        _expect(table, "table", _FLOAT32, (rows, rot), dev)
+        _ints(positions, "positions", (T,), dev)
+    if not -_MOST <= rotary_offset <= _MOST:
+        _sizes_fit("rotary_offset", abs(rotary_offset))
+    _call("kda_cache_append", dev, _ptr(q), k.data_ptr(), _ptr(v), _ptr(table), _ptr(positions),
+          page_table.data_ptr(), lens.data_ptr(), _ptr(cu_seqlens), _ptr(out_q), k_cache.data_ptr(),
+          _ptr(v_cache), T, n, hq, H, d, rot, rotary_offset, rows, pages, page, width, qs, ks, vs, os,
+          *strides, 1 if interleaved else 0, dt)
     return out_q
 
 
@@ -171,12 +199,15 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[t
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages, page_size, heads, d]")
     H = k_cache.shape[2]
-    if hq % max(H, 1) or (hq and not H):
+    if hq % H if H else hq:
         raise ValueError(f"{hq} query heads cannot share {H} heads of the cache")
-    pages = _caches(k_cache, v_cache, dtype, dev, H, d)
+    if H > _MOST:
+        _sizes_fit("k_cache", H)
+    pages, page, *strides = _caches(k_cache, v_cache, dtype, dev, H, d)
     dv = v_dim if v_dim is not None else (512 if v_cache is None and d == 576 else d)
-    _sizes_fit("prefix_attention", H, dv)
-    qs = _rows(q, "q", dtype, q.shape, dev, 1)
+    if not 0 <= dv <= _MOST:
+        raise ValueError(f"v_dim is {dv}")
+    qs = _row_stride(q, "q", dtype, T, hq, d, dev)
     n, width = _sessions(page_table, lens, cu_seqlens, T, dev)
     P = 0
     if (prefix_pages is None) != (prefix_len is None):
@@ -185,20 +216,25 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[t
         if not isinstance(prefix_pages, torch.Tensor) or prefix_pages.dim() != 1:
             raise ValueError("prefix_pages must be a 1-D tensor")
         P = prefix_pages.shape[0]
-        _sizes_fit("prefix_pages", P)
-        _expect(prefix_pages, "prefix_pages", torch.int32, (P,), dev)
-        _expect(prefix_len, "prefix_len", torch.int32, (1,), dev)
+        if P > _MOST:
+            _sizes_fit("prefix_pages", P)
+        _ints(prefix_pages, "prefix_pages", (P,), dev)
+        _ints(prefix_len, "prefix_len", (1,), dev)
     if out is None:
         out, os = torch.empty((T, hq, dv), dtype=dtype, device=dev), hq * dv
     else:
-        os = _rows(out, "out", dtype, (T, hq, dv), dev, 1)
-    if lse is None and output_lse:
-        lse = torch.empty((T, hq), dtype=torch.float32, device=dev)
-    _expect(lse, "lse", torch.float32, (T, hq), dev)
-    need = lib().kda_prefix_attn_workspace_size(T, n, hq, H, d, dv, pages[1], width, P, dt)
-    ws = _workspace(workspace, max(need, 0), dev) if need > 0 or workspace is not None else None
-    _call("kda_prefix_attn_fwd", dev, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
-          _ptr(lens), _ptr(prefix_pages), _ptr(prefix_len), _ptr(cu_seqlens), _ptr(out), _ptr(lse),
-          T, n, hq, H, d, dv, pages[0], pages[1], width, P, qs, os, *pages[2:],
-          d ** -0.5 if scale is None else scale, dt, _ptr(ws), 0 if ws is None else ws.numel())
+        os = _row_stride(out, "out", dtype, T, hq, dv, dev)
+    if lse is not None:
+        _expect(lse, "lse", _FLOAT32, (T, hq), dev)
+    elif output_lse:
+        lse = torch.empty((T, hq), dtype=_FLOAT32, device=dev)
+    need = lib().kda_prefix_attn_workspace_size(T, n, hq, H, d, dv, page, width, P, dt)
+    ws, room = None, 0
+    if need > 0 or workspace is not None:
+        ws = _workspace(workspace, max(need, 0), dev)
+        room = ws.numel()
+    _call("kda_prefix_attn_fwd", dev, q.data_ptr(), k_cache.data_ptr(), _ptr(v_cache),
+          page_table.data_ptr(), lens.data_ptr(), _ptr(prefix_pages), _ptr(prefix_len),
+          _ptr(cu_seqlens), out.data_ptr(), _ptr(lse), T, n, hq, H, d, dv, pages, page, width, P, qs,
+          os, *strides, d ** -0.5 if scale is None else scale, dt, _ptr(ws), room)
     return out, lse
