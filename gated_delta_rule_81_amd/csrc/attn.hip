@@ -44,11 +44,10 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a, MixGrid g) {
         tile_walk<T, D, D, false, 1, 4, TK, NEAR>(a, g.tile, b, smem);
 }
 
-template <bool NEAR>
 __global__ __launch_bounds__(512, 2) void attn_latent_kernel(AttnArgs a, TileGrid g) {
     typedef TileShape<bf16, 576, 512, true, 2, 8, 32> S;
     __shared__ __attribute__((aligned(1024))) char smem[S::LDS];
-    tile_walk<bf16, 576, 512, true, 2, 8, 32, NEAR>(a, g, blockIdx.x, smem);
+    tile_walk<bf16, 576, 512, true, 2, 8, 32, true>(a, g, blockIdx.x, smem);
 }
 
 // One workgroup per row (token, head): DV / 4 lanes hold a row's values, the 1024 / DV groups
@@ -169,12 +168,7 @@ int launch_attn(const AttnArgs &a, hipStream_t stream) {
     const int64_t n = mix_grid(a, &g);
     if (n <= 0) return (int)n;
     if (a.d == 576) {
-        if (a.pages.near)
-            hipLaunchKernelGGL((attn_latent_kernel<true>), dim3((unsigned)n), dim3(512), 0, stream, a,
-                               g.tile);
-        else
-            hipLaunchKernelGGL((attn_latent_kernel<false>), dim3((unsigned)n), dim3(512), 0, stream, a,
-                               g.tile);
+        hipLaunchKernelGGL(attn_latent_kernel, dim3((unsigned)n), dim3(512), 0, stream, a, g.tile);
         return hipGetLastError() == hipSuccess ? 0 : -1;
     }
     if (a.dtype == kDtypeF32)

@@ -346,15 +346,14 @@ __device__ __forceinline__ void soften(f32x16 (&s)[TT], float m, float &l, float
         }
 }
 
-// S^T of 32 * TT tokens: KS chunk pairs of their rows with those of q.
-template <typename T, int C, int TT, int KS>
-__device__ __forceinline__ void scores(lds_char *tile, const Keys<C> &keys, const u32x4 (&q)[KS],
-                                       f32x16 (&s)[TT]) {
+// S^T of 32 * TT tokens: KS chunk pairs of their rows with those of the queries, q(pair).
+template <typename T, int KS, int C, int TT, typename Q>
+__device__ __forceinline__ void scores(lds_char *tile, const Keys<C> &keys, Q q, f32x16 (&s)[TT]) {
 #pragma unroll
     for (int c = 0; c < KS; ++c)
 #pragma unroll
         for (int j = 0; j < TT; ++j)
-            s[j] = AttnMma<T>::chunk(keys.read(tile, j, c), q[c], c ? s[j] : f32x16(0.f));
+            s[j] = AttnMma<T>::chunk(keys.read(tile, j, c), q(c), c ? s[j] : f32x16(0.f));
 }
 
 // o += V^T P^T over a tile's tokens, DT * 32 channels.  NUMBERS: what is no number (an infinity
@@ -445,6 +444,54 @@ __device__ __forceinline__ void turn_over(lds_char *kt, lds_char *vt, const Keys
         o[d] = M::mma(v[i % kAhead], p[i / DT], o[d]);
         if (to < PV) v[i % kAhead] = values.read(vt, to / DT, to % DT);
         beside(i);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// The two halves of that on their own.  Scores of 32 tokens, operands read kNear products
+// ahead (registers are few here); keys(pair) reads one.
+constexpr int kNear = 3;
+template <typename T, int KS, typename K, typename Q>
+__device__ __forceinline__ void scores_ahead(K keys, Q q, f32x16 &s) {
+    u32x4 k[kNear];
+#pragma unroll
+    for (int c = 0; c < kNear; ++c) k[c] = keys(c);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int c = 0; c < KS; ++c) {
+        s = AttnMma<T>::chunk(k[c % kNear], q(c), c ? s : f32x16(0.f));
+        if (c + kNear < KS) k[c % kNear] = keys(c + kNear);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+// Probabilities of 32 tokens and their products with the values; the second sixteen tokens'
+// exponentials stand beside the products of the first.
+template <typename T, int DT, typename V>
+__device__ __forceinline__ void values_ahead(lds_char *vt, const V &values, f32x16 &s, float m,
+                                             float &l, f32x16 (&o)[DT], float sl) {
+    typedef AttnMma<T> M;
+    const float ms = usable(m) * sl;
+    auto soften1 = [&](int e) {
+        s[e] = fast_exp2(s[e] * sl - ms);
+        l += s[e];
+    };
+    typename M::Value v[kNear];
+#pragma unroll
+    for (int i = 0; i < kNear; ++i) v[i] = values.read(vt, i / DT, i % DT);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) soften1(e);
+    typename M::Prob p = M::prob(s, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 2 * DT; ++i) {
+        const int to = i + kNear;
+        if (i == DT) p = M::prob(s, 1);
+        o[i % DT] = M::mma(v[i % kNear], p, o[i % DT]);
+        if (to < 2 * DT) v[i % kNear] = values.read(vt, to / DT, to % DT);
+        if (i < DT) {
+#pragma unroll
+            for (int e = 8 + i * 8 / DT; e < 8 + (i + 1) * 8 / DT; ++e) soften1(e);
+        }
         __builtin_amdgcn_sched_barrier(0);
     }
 }

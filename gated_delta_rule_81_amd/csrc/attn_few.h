@@ -117,7 +117,7 @@ __device__ __forceinline__ void few_walk(const AttnArgs &a, int own_blocks, int 
         const int base = base_of(k);
         wait_loads<PLACES == 2 ? S::LOADS : 0>();  // the keys; the values are behind them
         f32x16 s[1];
-        scores<T, S::C, 1, KS>(kt, keys, q, s);
+        scores<T, KS>(kt, keys, [&](int c) { return q[c]; }, s);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read, before they are loaded again
         if (PLACES == 1) load(vc, vt);
         if (more) loads.set(a.pages, where(k + 1, &next_valid), 0, lane);

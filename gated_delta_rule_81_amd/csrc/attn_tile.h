@@ -7,12 +7,17 @@
 namespace kda {
 
 template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK> struct TileShape {
-    static constexpr int E = sizeof(T), C = D * E / 16, CV = DV * E / 16;
+    // Chunks of a row in LDS; of a latent row, its values alone: the channels behind them are a
+    // tile of their own, of REST chunks a row.
+    static constexpr int E = sizeof(T), C = (LATENT ? DV : D) * E / 16, CV = DV * E / 16;
+    static constexpr int REST = LATENT ? (D - DV) * E / 16 : 0;
     static constexpr int BM = 32 * NW / SPLIT;          // rows of a workgroup
-    static constexpr int KB = TK * C * 16, VB = LATENT ? 0 : TK * CV * 16;
+    static constexpr int KB = TK * (C + REST) * 16, VB = LATENT ? 0 : TK * CV * 16;
     // tiles of keys t + 1 and values t are read while keys t + 2 and values t + 1 come
     static constexpr int SUMS = 2 * (KB + VB);
-    static constexpr int LDS = SUMS + (SPLIT == 2 ? 4096 * NW : 0);
+    // SPLIT 2: scores on their way to the other half, and what of the queries has no registers
+    static constexpr int PARKED = SPLIT == 2 ? 6 : 0, PARK = SUMS + (SPLIT == 2 ? 4096 * NW : 0);
+    static constexpr int LDS = PARK + PARKED * 1024 * NW;
     static constexpr int CHV = LATENT ? C : CV;         // chunks of a row that holds values
     static_assert(TK * C % 64 == 0 && TK * CV % 64 == 0, "whole loads");
 };
@@ -28,7 +33,7 @@ template <typename T, int D, int DV, bool LATENT, int SPLIT, int NW, int TK, boo
 __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, int block, char *smem) {
     typedef TileShape<T, D, DV, LATENT, SPLIT, NW, TK> S;
     // A wave's share: 32 rows, KS chunk pairs of their channels, DT * 32 of their values.
-    constexpr int TT = TK / 32, DT = DV / 32 / SPLIT, KS = S::C / 2 / SPLIT;
+    constexpr int TT = TK / 32, DT = DV / 32 / SPLIT, KS = D * S::E / 32 / SPLIT;
     constexpr uint64_t kAll = ~0ull >> (64 - TK);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, group = wave / SPLIT, part = wave % SPLIT;
@@ -87,7 +92,12 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
     const int32_t *own_table = pre ? nullptr : a.seqs.table + (int64_t)session * a.seqs.width;
 
     // this wave's queries; rows behind the last one are computed as the last one's
-    u32x4 q[KS];
+    constexpr int KR = KS - S::PARKED;  // chunk pairs in registers; the others in LDS
+    u32x4 q[KR];
+    lds_char *park = (lds_char *)smem + S::PARK + wave * (S::PARKED * 1024) + lane * 16;
+    auto query = [&](int c) -> u32x4 {
+        return c < KR ? q[c < KR ? c : 0] : *(lds_u32x4 *)(park + 1024 * (c - KR));
+    };
     const bool active = 32 * group <= last;
     int lim = 0, wave_max = 0;  // own tokens that a row sees, and the wave's last
     {
@@ -97,9 +107,17 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
         const T *src = static_cast<const T *>(a.q) + (tok0 + row / G) * a.q_stride +
                        ((int64_t)hk * G + row % G) * D;
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
-            q[s] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(src) +
-                                                    16 * (2 * (part * KS + s) + half));
+        for (int s = 0; s < KS; ++s) {
+            // with SPLIT 2 a half of the values' channels and a half of those behind them
+            constexpr int KV = KS - S::REST / 2 / SPLIT;
+            const int pair = s < KV ? part * KV + s : S::C / 2 + part * (KS - KV) + s - KV;
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(src) +
+                                                             16 * (2 * pair + half));
+            if (s < KR)
+                q[s < KR ? s : 0] = x;
+            else
+                *(lds_u32x4 *)(park + 1024 * (s - KR)) = x;
+        }
         if (!pre) {
             lim = seen(r);
             wave_max = seen(32 * group + 31 < last ? 32 * group + 31 : last);
@@ -129,15 +147,19 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
         in2 = tok - idx * a.pages.size;
         entry2 = (owned(t) ? own_table : a.prefix_pages)[idx < last ? idx : last];
     };
-    // That tile's loads, and which of its tokens there are.
-    auto place_tile = [&](TileLoads<S::C, TK, NW, NEAR> &loads, uint64_t *valid) {
+    // That tile's place of this lane's token (0 where there is none: the first page's first, which
+    // is there), and which of its tokens there are.
+    auto place_token = [&](uint64_t *valid) -> uint32_t {
         const int end = ahead >= nt ? 0 : (owned(ahead) ? end1 : end0);
         const bool there = (lane < TK) & (base_of(ahead) + lane < end) &
                            ((unsigned)entry < (unsigned)a.pages.count);
         const uint32_t place = (uint32_t)entry * a.pages.page_units + (uint32_t)in * a.pages.token_units;
         *valid = __ballot(there);
-        loads.set(a.pages, there ? place : 0, wave, lane);
         ++ahead;
+        return there ? place : 0;
+    };
+    auto place_tile = [&](TileLoads<S::C, TK, NW, NEAR> &loads, uint64_t *valid) {
+        loads.set(a.pages, place_token(valid), wave, lane);
     };
     auto load_keys = [&](int t, const TileLoads<S::C, TK, NW, NEAR> &loads) {
         if (t < nt) loads.load(a.pages, kc, keys_of(t), wave, lane);
@@ -151,8 +173,6 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x16(0.f);
     const float sl = a.scale * kLog2e;  // scores in units of log 2
-    const Keys<S::C> keys(part * KS, lane);
-    const typename AttnMma<T>::template Values<S::CHV> values(part * DT, lane);
     bool odd = false;  // a value that is no number in a tile that not all rows see whole
 
     // SPLIT 2: the sums over the two halves of the channels meet in LDS.
@@ -180,11 +200,13 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
     }
     // valid: which tokens of tile t there are; valid1, valid2: of the two behind it.
     uint64_t valid = 0, valid1 = 0, valid2 = 0;
-    TileLoads<S::C, TK, NW, NEAR> loads, loads2;  // of tiles t + 1 and t + 2
     int t = 0;
     if (nt == 0) {
         wait_loads<0>();
     } else if constexpr (SPLIT == 1) {
+        const Keys<S::C> keys(0, lane);
+        const typename AttnMma<T>::template Values<S::CHV> values(0, lane);
+        TileLoads<S::C, TK, NW, NEAR> loads, loads2;  // of tiles t + 1 and t + 2
         look_up(0), look_up(1);
         place_tile(loads, &valid);
         load_keys(0, loads);
@@ -196,7 +218,7 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
         place_tile(loads2, &valid2);
         wait_loads<0>();  // the queries among them
         __syncthreads();
-        if (nt > 0 && active) scores<T, S::C, TT, KS>(keys_of(0), keys, q, s);
+        if (nt > 0 && active) scores<T, KS>(keys_of(0), keys, query, s);
         // Tile t, whose scores are in x: probabilities and values, and beside them the scores of
         // tile t + 1, to y.  LATER: some row may not see some token of it, or it is the last.
         auto step = [&](f32x16 (&x)[TT], f32x16 (&y)[TT], auto LATER) {
@@ -229,7 +251,7 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
                 }
             } else {
                 place_next();
-                if (active && t + 1 < nt) scores<T, S::C, TT, KS>(kt, keys, q, y);
+                if (active && t + 1 < nt) scores<T, KS>(kt, keys, query, y);
                 if (look) {
                     move_maximum<TT, DT>(x, m, l, o, sl);
                     soften<TT>(x, m, l, sl);
@@ -249,11 +271,44 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
             for (int j = 0; j < TT; ++j) s[j] = s2[j];
         }
     } else {
+        // Few registers are left beside a wave's share of the queries and the outputs: a tile is
+        // placed when it is loaded, its scores are formed when it is there, and where its operands
+        // lie is formed again for each.  The 64 chunks of a row's values are one load, whose row
+        // is the wave's; the channels behind them are four loads of eight rows each.
+        static_assert(LATENT && S::C == 64 && S::REST == 8 && TK == 32 && NW == 8, "a latent row");
+        auto issue = [&](int t, uint64_t *valid) {
+            const uint32_t place = place_token(valid);
+            if (t >= nt) return;
+            lds_char *tile = keys_of(t);
+            const int ln = here(lane);
+#pragma unroll
+            for (int i = 0; i < TK / NW; ++i) {
+                const int row = NW * i + wave;
+                const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)place, row)
+                                    << a.pages.shift;
+                load_lds16(kc + at, (uint32_t)((ln ^ tile_turn<S::C>(row)) * 16),
+                           (uint32_t)(uintptr_t)tile + 1024 * row);
+            }
+            if (wave < 4) {
+                const int row = 8 * wave + (ln >> 3);
+                const uint64_t at =
+                    (uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(4 * row, (int)place) << a.pages.shift;
+                load_lds16(kc + at + 1024 + ((ln & 7) ^ tile_turn<8>(row)) * 16,
+                           (uint32_t)(uintptr_t)tile + TK * S::C * 16 + 1024 * wave);
+            }
+        };
+        auto both_scores = [&](lds_char *tile) {
+            constexpr int KV = KS - 2;
+            const Keys<S::C> keys(part * KV, here(lane));
+            const Keys<8> rest(part * 2, here(lane));
+            scores_ahead<T, KS>(
+                [&](int c) {
+                    return c < KV ? keys.read(tile, 0, c) : rest.read(tile + TK * S::C * 16, 0, c - KV);
+                },
+                query, s[0]);
+        };
         look_up(0), look_up(1);
-        place_tile(loads, &valid);
-        load_keys(0, loads);
-        look_up(2);
-        place_tile(loads, &valid1);
+        issue(0, &valid);
         wait_loads<0>();  // the queries among them
         auto step = [&](auto LATER) {
             constexpr bool later = decltype(LATER)::value;
@@ -261,12 +316,12 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
             wait_loads<0>();
             if (valid != kAll) clear_rows<S::CHV, TK, NW>(kt, valid, wave, lane);
             __syncthreads();
-            load_keys(t + 1, loads);
-            look_up(t + 3);
+            look_up(t + 2);
+            issue(t + 1, &valid1);
             const int base = base_of(t);
             const bool own = t >= n0, look = active && !(later && own && base >= wave_max);
             if (active) {
-                scores<T, S::C, TT, KS>(kt, keys, q, s);
+                both_scores(kt);
                 give(s[0]);
             }
             lds_barrier();
@@ -276,11 +331,15 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
                     hide_scores<TT>(s, valid, later && own ? lim - base : TK, lane);
                 if (later && any_odd<T>(kt, TK * S::CHV, lane)) odd = true;
                 move_maximum<TT, DT>(s, m, l, o, sl);
-                soften<TT>(s, m, l, sl);
-                add_values<T, later>(s, kt, values, o);
+                const typename AttnMma<T>::template Values<S::CHV> values(part * DT, here(lane));
+                if constexpr (later) {
+                    soften<TT>(s, m, l, sl);
+                    add_values<T, true>(s, kt, values, o);
+                } else {
+                    values_ahead<T>(kt, values, s[0], m, l, o, sl);
+                }
             }
-            place_tile(loads, &valid2);
-            valid = valid1, valid1 = valid2;
+            valid = valid1;
             ++t;
         };
         while (t < plain) step(std::false_type{});

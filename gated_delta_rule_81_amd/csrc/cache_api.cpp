@@ -246,8 +246,14 @@ AttnPlan attn_plan(int64_t tokens, int64_t num_seqs, bool packed, int64_t q_head
         p.prefix_splits = cut(slots / (kv_heads * tiles), pre_units + own_units);
         return p;
     }
-    if (pre_units > 0)
-        p.prefix_splits = cut(p.prefix_few ? slots / kv_heads : slots / (kv_heads * tiles), pre_units);
+    // workgroups of the sessions' own tokens, where those go tile by tile
+    const int64_t own_tiles =
+        own_units > 0 && !p.few_rows ? kv_heads * num_seqs * ((most + p.tile_rows - 1) / p.tile_rows) : 0;
+    if (pre_units > 0) {
+        // as many parts as fill the places that those leave, if they leave enough
+        const int64_t one = p.prefix_few ? kv_heads : kv_heads * tiles, left = slots - own_tiles;
+        p.prefix_splits = cut((left >= one ? left : slots) / one, pre_units);
+    }
     if (own_units > 0 && p.few_rows > 0) {
         // twice as many as run at once, and lengths over 1024 tokens cut so that ragged ones even out
         const int64_t base = kv_heads * num_seqs, even = own_units / 8 < 4 ? own_units / 8 : 4;
@@ -255,9 +261,7 @@ AttnPlan attn_plan(int64_t tokens, int64_t num_seqs, bool packed, int64_t q_head
         p.own_splits = cut(want < even ? even : want, own_units);
     } else if (own_units > 0) {
         // a part of many rows is large beside the tokens it stands for: only where workgroups lack
-        const int64_t base = kv_heads * num_seqs * ((most + p.tile_rows - 1) / p.tile_rows);
-        const int64_t left = slots - kv_heads * tiles * p.prefix_splits;
-        p.own_splits = cut(left / base, own_units);
+        p.own_splits = cut((slots - kv_heads * tiles * p.prefix_splits) / own_tiles, own_units);
     }
     return p;
 }
