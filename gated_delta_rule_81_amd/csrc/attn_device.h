@@ -37,6 +37,13 @@ template <int C> __device__ __forceinline__ int tile_at(int row, int chunk) {
     return (row * C + (chunk ^ tile_turn<C>(row))) * 16;
 }
 
+// The lane number as a value the compiler cannot trace: what is formed from it in a rare
+// path is formed there and does not fill the registers as a constant of the loop around.
+__device__ __forceinline__ int here(int lane) {
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 __device__ __forceinline__ float half_max(float x) {
     const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
                                                     false);
@@ -134,19 +141,23 @@ template <> struct AttnMma<float> {
                                                      0, 0, 0);
         return c;
     }
+    // Row 8 (e / 4) + 4 (l / 32) + e % 4, channel l % 32 on from 32 d.  What of turn(row) the
+    // lane does not set is a constant, whose XOR with the lane's part is formed at each read: kept,
+    // those of all reads would fill the registers.
     template <int CH> struct Values {
-        int d0, lane;
-        __device__ __forceinline__ Values(int d0_, int lane_) : d0(d0_), lane(lane_) {}
+        static_assert(CH % 16 == 0, "rows over all banks");
+        int base;
+        __device__ __forceinline__ Values(int d0, int lane)
+            : base((((lane & 31) >> 2) ^ (lane >> 5)) * 16 + (lane & 3) * 4 +
+                   4 * (lane >> 5) * CH * 16 + d0 * 128) {}  // d0 even
         __device__ __forceinline__ Value read(lds_char *tile, int j, int d) const {
             typedef __attribute__((address_space(3))) float lds_float;
             Value v;
-            const int col = 32 * (d0 + d) + (lane & 31);
+            const int at = here(base);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int row = 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
-                v.a[e] = *(lds_float *)(tile + 16 * j * CH * 16 + tile_at<CH>(row, col >> 2) +
-                                        (col & 3) * 4);
-            }
+            for (int e = 0; e < 8; ++e)
+                v.a[e] = *(lds_float *)(tile + (at ^ (((e % 4) << 2 ^ e / 4 << 1 ^ (d & 1) << 3) * 16)) +
+                                        (16 * j + 8 * (e / 4) + e % 4) * CH * 16 + d / 2 * 256);
             return v;
         }
     };
@@ -185,13 +196,6 @@ __device__ __forceinline__ int prefix_tokens(const AttnArgs &a) {
     const int64_t most = (int64_t)a.prefix_width * a.pages.size;
     const int n = word_at(a.prefix_len, 0);
     return n < 0 ? 0 : (n > most ? (int)most : n);
-}
-
-// The lane number as a value the compiler cannot trace: what is formed from it in a rare
-// path is formed there and does not fill the registers as a constant of the loop around.
-__device__ __forceinline__ int here(int lane) {
-    asm volatile("" : "+v"(lane));
-    return lane;
 }
 
 // Place of token `tok` in the page `entry`, in units of 2^shift bytes behind the start of its
