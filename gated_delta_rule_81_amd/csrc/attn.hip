@@ -50,26 +50,36 @@ __global__ __launch_bounds__(512, 2) void attn_latent_kernel(AttnArgs a, TileGri
     tile_walk<bf16, 576, 512, true, 2, 8, 32, true>(a, g, blockIdx.x, smem);
 }
 
-// One workgroup per row (token, head): DV / 4 lanes hold a row's values, the 1024 / DV groups
-// of them take every so many-th part, and are added up in their order.  Its time is one chain
-// of loads (lengths, statistics, parts), so everything that does not depend on another load is
-// read at once.
-template <typename T, int DV> __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
-    constexpr int LANES = DV / 4, GROUPS = 256 / LANES, SLOTS = 128;
-    __shared__ float2 stat[SLOTS];
-    __shared__ f32x4 sums[GROUPS][LANES];
-    const int64_t at = blockIdx.x, rows = (int64_t)a.seqs.tokens * a.heads;
-    const int token = (int)(at / a.heads), h = (int)(at % a.heads);
-    const int tid = threadIdx.x, lane = tid & 63, group = tid / LANES, c = 4 * (tid % LANES);
+// Row (token, head): the parts of its splits.  W waves a row; DV / 4 lanes hold its values, the
+// groups of them take every so many-th part and are added up in their order.  Its time is one
+// chain of loads (lengths, statistics, parts), so what does not depend on another load is read at
+// once, and rows are many at once: 8192 rows of 10 parts of 128 take 15 us with one wave a row
+// and 26 with four; 64 rows of 67 parts 10 with four.
+template <typename T, int DV, int W> __global__ __launch_bounds__(256) void attn_merge_kernel(AttnArgs a) {
+    constexpr int LANES = DV / 4, GROUPS = 64 * W / LANES, SLOTS = 128, ROWS = 4 / W;
+    static_assert(GROUPS >= 1 && 64 * W * GROUPS % LANES == 0, "whole groups");
+    __shared__ float2 stat_all[ROWS][SLOTS];
+    __shared__ f32x4 sums_all[ROWS][GROUPS][LANES];
+    const int tid = threadIdx.x % (64 * W), mine = threadIdx.x / (64 * W);
+    const int64_t rows = (int64_t)a.seqs.tokens * a.heads, at = (int64_t)blockIdx.x * ROWS + mine;
+    float2 *stat = stat_all[mine];
+    const bool row = at < rows;
+    const int token = row ? (int)(at / a.heads) : 0, h = row ? (int)(at % a.heads) : 0;
+    const int group = tid / LANES, c = 4 * (tid % LANES);
     const AttnPlan &p = a.plan;
     // statistics of every slot, whether a part was written or not
     const int slots = p.prefix_splits + p.own_splits;
-    float2 mine = {0.f, 0.f};
-    if (tid < slots) mine = a.stat[tid * rows + at];
-    const int s = a.seqs.cu ? session_search(a.seqs, token, lane, [](int first, int) { return first; })
+    float2 got[SLOTS / 64 / W > 0 ? SLOTS / 64 / W : 1];
+#pragma unroll
+    for (int i = 0; i * 64 * W < SLOTS; ++i) {
+        const int k = tid + i * 64 * W;
+        got[i] = row && k < slots ? a.stat[k * rows + at] : float2{0.f, 0.f};
+    }
+    const int s = a.seqs.cu ? session_search(a.seqs, token, threadIdx.x & 63,
+                                             [](int first, int) { return first; })
                             : token / a.seqs.each;
     const int first = session_first(a.seqs, s), last = session_first(a.seqs, s + 1);
-    if (token < first || token >= last) return;  // in no session
+    const bool held = row && token >= first && token < last;  // in a session
     const int L = own_tokens(a.seqs, a.pages, s), P = prefix_tokens(a);
     const bool any = P > 0 || L - (last - token) + 1 > 0;
 
@@ -79,26 +89,30 @@ template <typename T, int DV> __global__ __launch_bounds__(256) void attn_merge_
     const int n0 = per0 > 0 ? (u0 + per0 - 1) / per0 : 0;
     const int per1 = p.joint ? 0 : split_units(lu, p.own_splits);
     const int n1 = per1 > 0 ? (lu + per1 - 1) / per1 : 0, n = n0 + n1;
-    const int slot = tid < p.prefix_splits ? tid : tid - p.prefix_splits + n0;
-    if (tid < slots && (tid < p.prefix_splits ? tid < n0 : slot < n)) stat[slot] = mine;
-    __syncthreads();
-    float top = -__builtin_inff();
-    for (int k = 0; k < n; ++k) top = __builtin_fmaxf(top, stat[k].x);
-    float sum = 0.f;
-    f32x4 y = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < n; ++k) sum += stat[k].y * part_weight(stat[k], top);
-#pragma unroll 4
-    for (int k = group; k < n; k += GROUPS) {
-        const int64_t from = k < n0 ? k : p.prefix_splits + k - n0;
-        const f32x4 w = *reinterpret_cast<const f32x4 *>(a.part + (from * rows + at) * DV + c);
-        const float f = part_weight(stat[k], top);
-        if (f != 0.f) y += w * f;  // a part of which nothing was seen holds anything
-    }
-    sums[group][tid % LANES] = y;
-    __syncthreads();
-    if (group > 0) return;
 #pragma unroll
-    for (int g = 1; g < GROUPS; ++g) y += sums[g][tid];
+    for (int i = 0; i * 64 * W < SLOTS; ++i) {
+        const int k = tid + i * 64 * W, to = k < p.prefix_splits ? k : k - p.prefix_splits + n0;
+        if (k < slots && (k < p.prefix_splits ? k < n0 : to < n)) stat[to] = got[i];
+    }
+    __syncthreads();
+    float top = -__builtin_inff(), sum = 0.f;
+    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+    if (held) {
+        for (int k = 0; k < n; ++k) top = __builtin_fmaxf(top, stat[k].x);
+        for (int k = 0; k < n; ++k) sum += stat[k].y * part_weight(stat[k], top);
+#pragma unroll 4
+        for (int k = group; k < n; k += GROUPS) {
+            const int64_t from = k < n0 ? k : p.prefix_splits + k - n0;
+            const f32x4 w = *reinterpret_cast<const f32x4 *>(a.part + (from * rows + at) * DV + c);
+            const float f = part_weight(stat[k], top);
+            if (f != 0.f) y += w * f;  // a part of which nothing was seen holds anything
+        }
+    }
+    sums_all[mine][group][tid % LANES] = y;
+    __syncthreads();
+    if (group > 0 || !held) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) y += sums_all[mine][g][tid];
     const float inv = any ? 1.f / sum : 0.f;
     T *out = static_cast<T *>(a.out) + token * a.out_stride + (int64_t)h * DV + c;
     store4(out, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
@@ -178,19 +192,27 @@ int launch_attn(const AttnArgs &a, hipStream_t stream) {
                      : mixed<bf16, 128, 64, 2>(a, g, n, stream);
 }
 
-int launch_attn_merge(const AttnArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)(attn_merge_threads(a) / 256));
-    if (a.dv == 512)
-        hipLaunchKernelGGL((attn_merge_kernel<bf16, 512>), grid, dim3(256), 0, stream, a);
-    else if (a.dtype == kDtypeF32 && a.dv == 64)
-        hipLaunchKernelGGL((attn_merge_kernel<float, 64>), grid, dim3(256), 0, stream, a);
-    else if (a.dtype == kDtypeF32)
-        hipLaunchKernelGGL((attn_merge_kernel<float, 128>), grid, dim3(256), 0, stream, a);
-    else if (a.dv == 64)
-        hipLaunchKernelGGL((attn_merge_kernel<bf16, 64>), grid, dim3(256), 0, stream, a);
+namespace {
+
+template <typename T, int DV> int merge(const AttnArgs &a, hipStream_t stream) {
+    constexpr int FEW = DV == 512 ? 2 : 1;  // waves that hold a row
+    const int64_t rows = (int64_t)a.seqs.tokens * a.heads;
+    // more rows than workgroups of four waves run at once (8 a CU)
+    if (rows > 2048)
+        hipLaunchKernelGGL((attn_merge_kernel<T, DV, FEW>), dim3((unsigned)((rows * FEW + 3) / 4)),
+                           dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((attn_merge_kernel<bf16, 128>), grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attn_merge_kernel<T, DV, 4>), dim3((unsigned)rows), dim3(256), 0, stream, a);
     return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+int launch_attn_merge(const AttnArgs &a, hipStream_t stream) {
+    if (a.dv == 512) return merge<bf16, 512>(a, stream);
+    if (a.dtype == kDtypeF32)
+        return a.dv == 64 ? merge<float, 64>(a, stream) : merge<float, 128>(a, stream);
+    return a.dv == 64 ? merge<bf16, 64>(a, stream) : merge<bf16, 128>(a, stream);
 }
 
 }  // namespace kda
