@@ -255,8 +255,8 @@ AttnPlan attn_plan(int64_t tokens, int64_t num_seqs, bool packed, int64_t q_head
         p.prefix_splits = cut((left >= one ? left : slots) / one, pre_units);
     }
     if (own_units > 0 && p.few_rows > 0) {
-        // twice as many as run at once, and lengths over 1024 tokens cut so that ragged ones even out
-        const int64_t base = kv_heads * num_seqs, even = own_units / 8 < 4 ? own_units / 8 : 4;
+        // twice as many as run at once, and lengths over 2048 tokens cut so that ragged ones even out
+        const int64_t base = kv_heads * num_seqs, even = own_units / 16 < 4 ? own_units / 16 : 4;
         const int64_t want = (2 * slots + base - 1) / base;
         p.own_splits = cut(want < even ? even : want, own_units);
     } else if (own_units > 0) {
