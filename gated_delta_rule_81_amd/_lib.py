@@ -7,6 +7,7 @@ There is no fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
@@ -120,6 +121,29 @@ def lib():
             fn.restype = res
         _lib = handle
     return _lib
+
+
+_calls = None
+
+
+def cache_calls():
+    """The CPython module of the operators on a paged cache (csrc/py_cache.cpp),
+    loaded once and given the library's entry points."""
+    global _calls
+    if _calls is None:
+        handle = lib()  # torch first: the module's names are torch's
+        path = os.path.join(os.path.dirname(LIB_PATH), "_cache_calls.so")
+        if not os.path.exists(path):
+            raise RuntimeError(
+                f"{path} is not built; run `python -m gated_delta_rule_81_amd.build`")
+        spec = importlib.util.spec_from_file_location("_cache_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(handle, name), ctypes.c_void_p).value
+                      for name in ("kda_cache_append", "kda_prefix_attn_fwd",
+                                   "kda_prefix_attn_workspace_size")))
+        _calls = module
+    return _calls
 
 
 def check(status: int, where: str) -> None:

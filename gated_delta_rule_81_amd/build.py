@@ -3,7 +3,8 @@
 Usage:  python -m gated_delta_rule_81_amd.build   (or ``build()`` from Python)
 
 Every HIP source is compiled separately (in parallel) and linked into one
-shared library next to this file.  Flags:
+shared library next to this file; beside it the CPython module ``_cache_calls.so``
+(csrc/py_cache.cpp, host code on torch's headers).  Flags:
   --offload-arch=gfx950       MI355X only
   -packed-fp32-ops (disabled) keep the compiler from emitting packed fp32 ops
   -mcode-object-version=5     loadable by the HIP runtime PyTorch bundles
@@ -13,6 +14,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkda.so")
+CALLS = os.path.join(HERE, "_cache_calls.so")
 
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_chunk.hip", "kda_seq.hip", "kda_segment.hip",
            "kda_bwd.hip", "kda_bwd_chain.hip", "layer_api.cpp", "conv.hip", "qk_norm.hip",
@@ -55,11 +58,33 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _calls(verbose: bool) -> None:
+    """The CPython module.  torch's libraries are found by name when it is imported:
+    torch has loaded them by then."""
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    paths = [*include_paths(), sysconfig.get_paths()["include"]]
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for p in paths for x in ("-isystem", p)], os.path.join(CSRC, "py_cache.cpp"), "-o", tmp,
+           *[f"-L{p}" for p in library_paths()], "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed for py_cache.cpp:\n" + res.stderr)
+    if verbose and res.stderr:
+        print(res.stderr, file=sys.stderr)
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source and link ``libkda.so``; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        calls = pool.submit(_calls, verbose)
         objs = list(pool.map(lambda s: _compile(s, verbose), SOURCES))
+        calls.result()
     tmp = LIB + ".tmp"
     subprocess.run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs],
                    check=True, capture_output=not verbose)

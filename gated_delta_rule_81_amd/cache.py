@@ -1,5 +1,6 @@
 """PyTorch front end of the operators on a paged cache (include/kda_cache.h):
-argument marshalling only, as in ``ops``.
+argument marshalling only, as in ``ops``.  The common case is marshalled by a
+CPython module (csrc/py_cache.cpp): the checks here take longer than a small call.
 
 A cache is [pages, page_size, heads, d], in any order in memory that keeps a
 head's d channels contiguous and places apart: [pages, heads, page_size, d]
@@ -12,12 +13,19 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._lib import lib
+from ._lib import cache_calls, check, lib
 from .layer import _MOST, _call, _dtype, _expect, _fits, _rows, _sizes_fit, _workspace
 from .ops import _DTYPES, _ptr
 
 
 _INT32, _FLOAT32 = torch.int32, torch.float32
+_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on_current_device(t) -> bool:
+    """Whether a call on ``t`` may go through csrc/py_cache.cpp, which does not
+    change the device (it returns None where an argument needs a word said)."""
+    return isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == torch.cuda.current_device()
 
 
 def _row_stride(t, name, dtype, T, H, d, device) -> int:
@@ -108,6 +116,13 @@ def cache_append(k: torch.Tensor, v: Optional[torch.Tensor], k_cache: torch.Tens
     (2 i, 2 i + 1) with ``interleaved``.  Returns the rotated q [T, Hq, d]
     (``out_q``, which may be ``q`` itself), or None without q.
     """
+    if out_q is None and _on_current_device(k):
+        done = cache_calls().append(_stream(k.get_device()), k, v, k_cache, v_cache, page_table, lens,
+                                    cu_seqlens, q, table, positions, rotary_offset, interleaved)
+        if done is not None:
+            if done[0]:
+                check(done[0], "kda_cache_append")
+            return done[1]
     dt = _dtype_of_rows(k, "k")
     T, H, d = k.shape
     dev, dtype = k.device, k.dtype
@@ -193,6 +208,16 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[t
     (out [T, Hq, v_dim], lse [T, Hq] fp32, the log of each token's sum of
     exponentials, or None): 0 and -inf where a token sees nothing.
     """
+    if out is None and lse is None and workspace is None and _on_current_device(q):
+        d = q.shape[-1]
+        done = cache_calls().attention(
+            _stream(q.get_device()), q, k_cache, v_cache, page_table, lens, prefix_pages, prefix_len,
+            cu_seqlens, d ** -0.5 if scale is None else scale,
+            v_dim if v_dim is not None else (512 if v_cache is None and d == 576 else d), output_lse)
+        if done is not None:
+            if done[0]:
+                check(done[0], "kda_prefix_attn_fwd")
+            return done[1], done[2]
     dt = _dtype_of_rows(q, "q")
     T, hq, d = q.shape
     dev, dtype = q.device, q.dtype
