@@ -14,7 +14,10 @@
  *     values.  The value at (page, token, head, channel) lies page * page_stride +
  *     token * token_stride + head * head_stride + channel elements behind the
  *     start, the same in k_cache and v_cache; strides are multiples of 16 bytes
- *     and two places never share a byte.  A page may hold its tokens' heads
+ *     and two places never share a byte.  A head's places are counted in units of
+ *     the largest power of two that divides page_stride and token_stride (in
+ *     bytes): 2^32 of them are the most (1 TB where it is 256 bytes), a cache that
+ *     holds more is refused (KDA_ERR_UNSUPPORTED).  A page may hold its tokens' heads
  *     together or its heads' tokens; the caches may be two tensors or halves of
  *     each page of one.
  *   - Latent cache: v_cache NULL.  A token's values are then the first v_dim
