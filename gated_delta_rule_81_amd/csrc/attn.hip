@@ -25,18 +25,21 @@ template <typename T, int D, int TK, int PLACES> struct MixShape {
 template <typename T, int D, int TK, int PLACES, bool NEAR>
 __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a, MixGrid g) {
     __shared__ __attribute__((aligned(1024))) char smem[MixShape<T, D, TK, PLACES>::LDS];
-    const int tiles = g.tile.prefix_blocks + g.tile.own_blocks;
-    // of both kinds in turn, kTurn blocks each, while there are both
-    const int both = g.few < tiles ? g.few : tiles, turns = both / kTurn * kTurn;
+    // Turns of kTurn tile blocks, one for each CU, with an equal share of the others behind each:
+    // those are short, and take up the second place of every CU while the tiles last.
+    const int tiles = g.tile.prefix_blocks + g.tile.own_blocks, turns = tiles / kTurn;
+    const int share = turns > 0 ? g.few / turns / 8 * 8 : 0, turn = kTurn + share;
     int b = blockIdx.x;
     bool few;
-    if (b < 2 * turns) {
-        few = b / kTurn % 2 == 1;
-        b = b / (2 * kTurn) * kTurn + b % kTurn;
-    } else {
-        b -= turns;  // the rest of the tiles, then of the others
-        few = b >= tiles;
-        if (few) b -= tiles - turns;
+    if (b < turns * turn) {
+        const int r = b % turn;
+        few = r >= kTurn;
+        b = b / turn * (few ? share : kTurn) + (few ? r - kTurn : r);
+    } else {  // what is left of the tiles, then of the others
+        b -= turns * turn;
+        const int left = tiles - turns * kTurn;
+        few = b >= left;
+        b += few ? turns * share - left : turns * kTurn;
     }
     if (few)
         few_walk<T, D, 4, PLACES, NEAR>(a, g.own_few, b, smem);
