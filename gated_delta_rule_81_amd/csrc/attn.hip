@@ -1,11 +1,19 @@
 // attn.hip -- the launches of the attention over a shared prefix and each session's
-// own tokens.
+// own tokens, and the join of what its splits leave.
+//
+//   o = sum_j p_j v_j / sum_j p_j,   p_j = 2^(scale log2(e) q k_j - m)
+//
+// A part holds its maximum m, its sum and its unscaled output; parts are joined by 2^(m - max m).
+// Measured with one token of 256 sessions, 32 heads (8 of keys) of 128, behind 16K shared tokens and up to
+// 2000 own ones (1.1 GB and 0.07 TFLOP): 272 us and 15 for the join; in two launches,
+// prefix then own tokens, 386 in all.
 #include "attn_few.h"
 #include "attn_tile.h"
 
 namespace kda {
 namespace {
 
+// Tile blocks of a turn (see attn_kernel): as many as there are CUs.
 constexpr int kTurn = 256;
 
 // What a launch is made of: `few` blocks for few rows (own_few of them own tokens, the others
@@ -26,7 +34,8 @@ template <typename T, int D, int TK, int PLACES, bool NEAR>
 __global__ __launch_bounds__(256, 2) void attn_kernel(AttnArgs a, MixGrid g) {
     __shared__ __attribute__((aligned(1024))) char smem[MixShape<T, D, TK, PLACES>::LDS];
     // Turns of kTurn tile blocks, one for each CU, with an equal share of the others behind each:
-    // those are short, and take up the second place of every CU while the tiles last.
+    // those are short, and take up the second place of every CU while the tiles last.  (256
+    // tokens behind 16K: 300 us; all tiles first, two of them on every CU, 312.)
     const int tiles = g.tile.prefix_blocks + g.tile.own_blocks, turns = tiles / kTurn;
     const int share = turns > 0 ? g.few / turns / 8 * 8 : 0, turn = kTurn + share;
     int b = blockIdx.x;
@@ -134,7 +143,8 @@ int64_t tile_grid(const AttnArgs &a, TileGrid *g) {
     }
     if (p.joint || (p.own_splits > 0 && p.own_tiles)) {
         r1 = (int64_t)a.kv_heads * (p.joint ? p.prefix_splits : p.own_splits);
-        t1 = rows / p.tile_rows + a.seqs.num;  // a session's first one: its first row's / tile_rows + its number
+        // a session's first one: its first row's / tile_rows + its number
+        t1 = rows / p.tile_rows + a.seqs.num;
     }
     constexpr int64_t kMost = (int64_t)1 << 22;  // 512 threads each
     if (r0 > kMost || t0 > kMost || r1 > kMost || t1 > kMost) return -1;
@@ -150,7 +160,8 @@ int64_t few_blocks(const AttnArgs &a, int64_t *own) {
     return *own + (p.prefix_few ? (int64_t)a.kv_heads * p.prefix_splits : 0);
 }
 
-
+// NEAR: places of a head's values in 32 bits, drafts over 32K 173 us against 181 with 64 bits,
+// prompts 624 against 666.
 template <typename T, int D, int TK, int PLACES>
 int mixed(const AttnArgs &a, const MixGrid &g, int64_t blocks, hipStream_t stream) {
     if (a.pages.near)

@@ -76,7 +76,6 @@ template <int C> struct Keys {
 template <typename T> struct AttnMma;
 
 template <> struct AttnMma<bf16> {
-    static constexpr int kOps = 1;  // products that use one Value
     struct Value { bf16x8 a; };
     typedef bf16x8 Prob;
     __device__ static f32x16 chunk(u32x4 a, u32x4 b, f32x16 c) {

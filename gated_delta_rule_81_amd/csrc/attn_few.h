@@ -1,5 +1,17 @@
 // attn_few.h -- attention of few query rows (at most 32: one token's heads of a group, or a
 // few tokens') over a long cache.
+//
+// Every key and value is read once and meets few rows, so memory bounds it: what counts is bytes
+// on their way.  The rows are one operand of 32 columns (empty ones repeat the last row: the
+// matrix unit has room).  A wave streams tiles of 32 tokens of its own through LDS, without
+// barriers; four waves share a workgroup, each taking every fourth tile, and join their
+// (maximum, sum, output) at the end; two workgroups a CU.  With keys and values each in a place
+// of their own, one comes while the other is read.
+//
+// Measured: bf16, one token of 128 sessions of 500 to 7900 own tokens, 8 heads of 128, 2.2 GB:
+// 386 us and 6 for the join, 5.6 TB/s (through the tile walk of many rows, whose waves share
+// a tile: 458).  fp32, 24 sessions of up to 700 tokens behind 2001 shared, 16 heads of 128, with the
+// prefix in the tile walk: 49 and 6 us; 124 with both there.
 #pragma once
 
 #include "attn_device.h"

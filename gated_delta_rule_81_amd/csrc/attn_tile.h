@@ -1,5 +1,32 @@
 // attn_tile.h -- attention of many query rows over a shared prefix, over a
 // session's own tokens, or over both: matrix products fed from LDS.
+//
+// A row is (token, head of the group), so the heads of a group and the tokens of all sessions
+// (of one, over its own tokens) share what is read.  A workgroup takes 128 rows, 32 a wave with
+// queries, maximum, sum and output in registers, and walks the tokens of its split in tiles of TK
+// that all of its waves read; two workgroups a CU.  Keys and values take two places each: while
+// tile t is worked on, the keys of t + 2 and the values of t + 1 come.  One barrier a tile.
+// What bounds it is issue: for a tile of 64 tokens a wave issues 32 products (32 cycles each)
+// beside 32 exponentials of a lane, their scaling, sum and rounding, and the maximum of as many scores.
+// The scores of tile t + 1 are formed before the values of tile t are added, so that
+// exponentials stand beside products that do not wait for them (turn_over): 675 us to 640 for the
+// prompts below.
+//
+// A latent row (576 channels, the first 512 of them the values) has one place for both.  Its
+// queries and outputs are too many for a wave: two waves share 32 rows, each with half of the channels
+// of both products (SPLIT 2), whose partial scores meet in LDS behind a second barrier; 6 of 18
+// pieces of the queries stay in LDS.  One workgroup of eight waves a CU.
+//
+// Tiles that some row does not see whole (the own tokens' last ones, and the last of all) go through a
+// loop of their own: there a value that is no number is left out of the product, where a
+// probability of zero would not hide it, and added behind the walk for the rows that see it.
+//
+// Measured, bf16: six prompts of up to 1500 tokens x 32 heads (8 of keys) of 128 behind 6000
+// shared ones, 0.56 TFLOP: 631 us, 890 TFLOP/s; the matrix unit is busy in 42% of the cycles, the
+// vector unit in 45%, at 1.96 GHz.  Four drafts of 64 sessions behind 32K, 0.14 TFLOP: 159 us
+// and 13 for the join (870 TFLOP/s).  Latent, 64 sessions x 96 heads behind 8192, 0.12 TFLOP:
+// 183 us and 16 (matrix unit 26%: the waves stand at the same barriers, and the quarter of the
+// CUs that takes own tokens ends early).
 #pragma once
 
 #include "attn_device.h"

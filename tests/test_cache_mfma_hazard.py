@@ -1,6 +1,6 @@
 """The kernels on a paged cache chain no bf16 MFMA shape's result into the other's
 accumulator too soon (tests/mfma_hazard.py), hold no packed fp32 instruction, and
-spill nothing where a spill's reload would wait for the tiles on their way.  CPU only."""
+set m0 right before each load from memory to LDS.  CPU only."""
 import os
 import re
 
