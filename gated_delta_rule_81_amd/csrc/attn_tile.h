@@ -227,7 +227,7 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
     }
     // valid: which tokens of tile t there are; valid1, valid2: of the two behind it.
     uint64_t valid = 0, valid1 = 0, valid2 = 0;
-    int t = 0;
+    int t = 0, from = 0;  // from: the first tile of the loop that leaves out what is no number
     if (nt == 0) {
         wait_loads<0>();
     } else if constexpr (SPLIT == 1) {
@@ -292,6 +292,7 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
             step(s, s2, std::false_type{});
             step(s2, s, std::false_type{});
         }
+        from = t;
         while (t < nt) {
             step(s, s2, std::true_type{});
 #pragma unroll
@@ -370,13 +371,16 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
             ++t;
         };
         while (t < plain) step(std::false_type{});
+        from = t;
         while (t < nt) step(std::true_type{});
     }
-    if (odd) {  // from the first of those tiles on: all own tokens, or the last of the prefix
-        const int from = plain < nt ? plain : nt - 1;
-        const bool own = from >= n0;
-        add_others<T>(a.pages, own ? own_table : a.prefix_pages, LATENT ? kc : vc, base_of(from),
-                      own ? end1 : end0, part * DT, own ? lim : end0, lane, o);
+    if (odd) {  // in the tiles from `from` on: the prefix's last ones, which all rows see, own ones
+        const char *values = LATENT ? kc : vc;
+        if (from < n0)
+            add_others<T>(a.pages, a.prefix_pages, values, base_of(from), end0, part * DT, end0, lane, o);
+        if (n0 < nt)
+            add_others<T>(a.pages, own_table, values, base_of(from > n0 ? from : n0), end1, part * DT,
+                          lim, lane, o);
     }
 
     if (!active) return;
