@@ -208,7 +208,7 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[t
     (out [T, Hq, v_dim], lse [T, Hq] fp32, the log of each token's sum of
     exponentials, or None): 0 and -inf where a token sees nothing.
     """
-    if out is None and lse is None and workspace is None and _on_current_device(q):
+    if out is None and lse is None and workspace is None and _on_current_device(q) and q.dim() == 3:
         d = q.shape[-1]
         done = cache_calls().attention(
             _stream(q.get_device()), q, k_cache, v_cache, page_table, lens, prefix_pages, prefix_len,

@@ -141,3 +141,26 @@ def test_both_ways_through_python(d, dtype):
         assert given is None or y is given
         both.append((y, kc) if vc is None else (y, kc, vc))
     assert all(torch.equal(a, b) for a, b in zip(*both))
+
+
+@pytest.mark.gpu
+def test_shapes_that_the_common_case_leaves():
+    """Tensors on the device whose shapes are no call's: said in words, nothing launched."""
+    c = case((2, 1), (2, 1), 20, 16, 4, 2, 64)
+    x = attention_inputs(c)
+    to = lambda t: t.to(DEV)
+    k, v, table, lens = to(x["k"]), to(x["v"]), to(x["table"]), to(x["lens"])
+    q = torch.randn(2, 4, 64, device=DEV).bfloat16()
+    for bad in (q[0, 0, 0], q[0], q[None]):
+        with pytest.raises(ValueError):
+            kda.prefix_attention(bad, k, v, table, lens)
+        with pytest.raises(ValueError):
+            kda.cache_append(bad, bad, k, v, table, lens)
+    with pytest.raises(ValueError):
+        kda.prefix_attention(q, k[0], v[0], table, lens)
+    with pytest.raises(ValueError):
+        kda.prefix_attention(q, k, v, table[0], lens)
+    with pytest.raises((TypeError, ValueError)):
+        kda.prefix_attention(q.half(), k, v, table, lens)
+    out, lse = kda.prefix_attention(q[:0], k, v, table[:0], lens[:0], output_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
