@@ -26,8 +26,8 @@
 // shared ones, 0.56 TFLOP: 631 us, 890 TFLOP/s; the matrix unit is busy in 42% of the cycles, the
 // vector unit in 45%, at 1.96 GHz.  Four drafts of 64 sessions behind 32K, 0.14 TFLOP: 159 us
 // and 13 for the join (870 TFLOP/s).  Latent, 64 sessions x 96 heads behind 8192, 0.12 TFLOP:
-// 183 us and 16 (matrix unit 26%: the waves stand at the same barriers, and the quarter of the
-// CUs that takes own tokens ends early).
+// 166 us and 16 (matrix unit 29%: two barriers a tile, and the quarter of the CUs that takes own
+// tokens ends early).
 #pragma once
 
 #include "attn_device.h"
