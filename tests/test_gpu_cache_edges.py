@@ -76,6 +76,29 @@ def test_a_nan_that_is_seen(c, where):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("c", [
+    case((1,) * 5, (50, 33, 64, 65, 200), 300, 8, 96, 1, 576),
+    case((60, 3, 20), (60, 170, 90), 150, 8, 8, 2, 576),
+    case((150, 190), (150, 333), 260, 8, 4, 2, 128),
+    case((1, 1, 1), (140, 130, 257), 300, 8, 8, 2, 64, "f32"),
+], ids=lambda c: f"{c['new'][:3]}-{c['d']}-{c['dtype']}")
+def test_pages_that_are_none_among_others(c):
+    """Every third page of the prefix and of each session is none; the first page, which is looked at
+    in their place, holds NaN and is nobody's."""
+    x = attention_inputs(c, 8)
+    for t in [x["k"]] + ([] if x["v"] is None else [x["v"]]):
+        t[0] = float("nan")
+    for pages in (x["table"], x["prefix_pages"]):
+        pages[pages == 0] = -1
+        flat = pages.view(-1)
+        flat[1::3] = torch.tensor([-1, x["k"].shape[0], 2 ** 31 - 1])[torch.arange(len(flat[1::3])) % 3].int()
+    say("prefix_attention: pages that are none among others", c)
+    got = attend(kda, x, c)
+    torch.cuda.synchronize()
+    compare(got, x, c, "pages that are none")
+
+
+@pytest.mark.gpu
 def test_thousands_of_sessions():
     """Packed, most of them empty, the first and the last among them; and the same of one token each."""
     g = torch.Generator().manual_seed(1)
