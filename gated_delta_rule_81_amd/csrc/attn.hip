@@ -93,7 +93,7 @@ template <typename T, int DV, int W> __global__ __launch_bounds__(256) void attn
     const int first = session_first(a.seqs, s), last = session_first(a.seqs, s + 1);
     const bool held = row && token >= first && token < last;  // in a session
     const int L = own_tokens(a.seqs, a.pages, s), P = prefix_tokens(a);
-    const bool any = P > 0 || L - (last - token) + 1 > 0;
+    const int lim = L - (last - token) + 1;  // own tokens that the row sees
 
     // which slots hold a part: the first n0 of the prefix's, the first n1 of the own ones
     const int pu = units_of(P), lu = units_of(L);
@@ -108,10 +108,17 @@ template <typename T, int DV, int W> __global__ __launch_bounds__(256) void attn
     }
     __syncthreads();
     float top = -__builtin_inff(), sum = 0.f;
+    bool any = true;  // whether the row sees a token
     f32x4 y = {0.f, 0.f, 0.f, 0.f};
     if (held) {
         for (int k = 0; k < n; ++k) top = __builtin_fmaxf(top, stat[k].x);
         for (int k = 0; k < n; ++k) sum += stat[k].y * part_weight(stat[k], top);
+        if (sum == 0.f) {  // the same in all lanes
+            const int lane = threadIdx.x & 63;
+            const int32_t *table = a.seqs.table + (int64_t)s * a.seqs.width;
+            const bool shared = first_there(a.pages, a.prefix_pages, P, lane) < P;
+            any = shared || first_there(a.pages, table, L, lane) < lim;
+        }
 #pragma unroll 4
         for (int k = group; k < n; k += GROUPS) {
             const int64_t from = k < n0 ? k : p.prefix_splits + k - n0;

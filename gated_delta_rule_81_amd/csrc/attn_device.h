@@ -205,6 +205,21 @@ __device__ __forceinline__ uint32_t token_place(const Pages &p, int entry, int t
     return *there ? (uint32_t)entry * p.page_units + in * p.token_units : 0;
 }
 
+// The first of `len` tokens (of a prefix, or of a session's own) whose page is there, len if none
+// is.  A row whose exponentials come to a sum of zero asks this: it sees nothing where that token
+// is not under its limit, and otherwise scores of -inf alone, whose softmax is no number.  64
+// entries a step; called by whole waves with the same table and length.
+__device__ __forceinline__ int first_there(const Pages &p, const int32_t *table, int len, int lane) {
+    const int n = len > 0 ? p.by_size(len - 1) + 1 : 0;
+#pragma unroll 1
+    for (int i = 0; i < n; i += 64) {
+        const int entry = i + lane < n ? table[i + lane] : -1;
+        const unsigned long long m = __ballot(entry >= 0 && entry < p.count);
+        if (m) return (i + __builtin_ctzll(m)) * p.size;
+    }
+    return len;
+}
+
 // 16 bytes a lane from memory to LDS at `to` + 16 * lane.  In assembly, so that the compiler
 // does not wait for all loads on their way before each read of LDS; what is read is
 // waited for by wait_loads().  m0 is read one wait state after it is written.

@@ -175,6 +175,16 @@ __device__ __forceinline__ void few_walk(const AttnArgs &a, int own_blocks, int 
         if (half == 0) stat[wave * 32 + lane] = float2{m * sl, l};
     }
     __syncthreads();
+    uint32_t nothing = 0;  // rows that see nothing
+    if (!a.part) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) sum += stat[w * 32 + row].y;
+        if (__ballot(sum == 0.f)) {
+            const int first = first_there(a.pages, table, len, lane);
+            nothing = (uint32_t)__ballot(sum == 0.f && first >= lim);
+        }
+    }
     for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * NW) {
         const int r = i / (D / 4), c = 4 * (i % (D / 4));
         float top = -__builtin_inff(), sum = 0.f;
@@ -196,7 +206,7 @@ __device__ __forceinline__ void few_walk(const AttnArgs &a, int own_blocks, int 
             *reinterpret_cast<f32x4 *>(a.part + to * D + c) = y;
             if (c == 0) a.stat[to] = float2{top, sum};
         } else {
-            const bool any = seen(r) > 0;
+            const bool any = !((nothing >> r) & 1);
             const float inv = any ? 1.f / sum : 0.f;
             T *out = static_cast<T *>(a.out) + token * a.out_stride + h * D + c;
             store4(out, y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);

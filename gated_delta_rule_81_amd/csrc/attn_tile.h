@@ -408,9 +408,15 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
     }
 
     if (!active) return;
+    l = half_sum(l);
+    bool any = true;  // whether this lane's row sees a token
+    if (!a.part && __ballot(l == 0.f)) {
+        const bool shared = first_there(a.pages, a.prefix_pages, P, lane) < P;
+        const int first = first_there(a.pages, own_table, L, lane);
+        any = l != 0.f || shared || first < lim;
+    }
     const int r = 32 * group + (lane & 31);
     if (r > last) return;
-    l = half_sum(l);
     const int64_t row = row0 + r, token = tok0 + row / G, h = (int64_t)hk * G + row % G;
     const int64_t at = token * a.heads + h;
     const int c0 = 32 * part * DT + 4 * half;  // first channel of this lane
@@ -427,7 +433,6 @@ __device__ __forceinline__ void tile_walk(const AttnArgs &a, const TileGrid &g, 
                 store4(dst + 32 * d + 8 * e, o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2],
                        o[d][4 * e + 3]);
     } else {
-        const bool any = P > 0 || lim > 0;
         const float inv = any ? 1.f / l : 0.f;
         T *dst = static_cast<T *>(a.out) + token * a.out_stride + h * DV + c0;
 #pragma unroll
