@@ -157,7 +157,14 @@ __device__ __forceinline__ void few_walk(const AttnArgs &a, int own_blocks, int 
     int k = 0;
     for (; k < plain && k < count; ++k) step(k, std::false_type{});
     for (; k < count; ++k) step(k, std::true_type{});
-    if (odd) add_others<T>(a.pages, table, vc, beg + whole * kFewTile, end, 0, lim, lane, o);
+    // Of this wave's tiles alone: for a row that sees nothing of them its part counts nothing, and
+    // an infinity of another wave's tile times that would be no number.
+    if (odd)
+        for (k = plain; k < count; ++k) {
+            const int base = base_of(k);
+            add_others<T>(a.pages, table, vc, base, base + kFewTile < end ? base + kFewTile : end, 0, lim,
+                          lane, o);
+        }
 
     // the waves' parts are joined through LDS, in wave order
     l = half_sum(l);
