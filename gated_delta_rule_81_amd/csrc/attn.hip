@@ -196,7 +196,17 @@ int64_t attn_threads(const AttnArgs &a) {
     const int64_t n = mix_grid(a, &g);
     return n < 0 ? kMostThreads + 1 : n * 512;
 }
-int64_t attn_merge_threads(const AttnArgs &a) { return (int64_t)a.seqs.tokens * a.heads * 256; }
+// Workgroups of the join, and waves a row: all four of a workgroup, or where rows are more than
+// workgroups run at once (8 a CU) as many as hold a row.
+static int64_t merge_grid(const AttnArgs &a, int *waves) {
+    const int64_t rows = (int64_t)a.seqs.tokens * a.heads;
+    *waves = rows <= 2048 ? 4 : (a.dv == 512 ? 2 : 1);
+    return (rows * *waves + 3) / 4;
+}
+int64_t attn_merge_threads(const AttnArgs &a) {
+    int waves;
+    return merge_grid(a, &waves) * 256;
+}
 
 int launch_attn(const AttnArgs &a, hipStream_t stream) {
     MixGrid g;
@@ -216,14 +226,13 @@ int launch_attn(const AttnArgs &a, hipStream_t stream) {
 namespace {
 
 template <typename T, int DV> int merge(const AttnArgs &a, hipStream_t stream) {
-    constexpr int FEW = DV == 512 ? 2 : 1;  // waves that hold a row
-    const int64_t rows = (int64_t)a.seqs.tokens * a.heads;
-    // more rows than workgroups of four waves run at once (8 a CU)
-    if (rows > 2048)
-        hipLaunchKernelGGL((attn_merge_kernel<T, DV, FEW>), dim3((unsigned)((rows * FEW + 3) / 4)),
-                           dim3(256), 0, stream, a);
+    constexpr int FEW = DV == 512 ? 2 : 1;
+    int waves;
+    const dim3 grid((unsigned)merge_grid(a, &waves));
+    if (waves == FEW)
+        hipLaunchKernelGGL((attn_merge_kernel<T, DV, FEW>), grid, dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((attn_merge_kernel<T, DV, 4>), dim3((unsigned)rows), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attn_merge_kernel<T, DV, 4>), grid, dim3(256), 0, stream, a);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -94,7 +94,10 @@ int kda_cache_append(const void *q, const void *k, const void *v, const float *t
  *
  * (head_dim, v_dim): (64, 64), (128, 128) with v_cache, bf16 or fp32, or (576, 512)
  * with v_cache NULL, bf16.  scale > 0 and finite.  Row starts and caches are
- * 16-byte aligned.
+ * 16-byte aligned.  A call of more than 2^22 workgroups of 128 rows, or of 2^23 with
+ * those of the sessions of few rows (key heads x parts of each), is refused
+ * (KDA_ERR_UNSUPPORTED), and where parts are joined one of 2^26 tokens x q_heads or
+ * more (2^25 with v_dim 512).
  */
 int64_t kda_prefix_attn_workspace_size(int32_t tokens, int32_t num_seqs, int32_t q_heads,
                                        int32_t kv_heads, int32_t head_dim, int32_t v_dim,

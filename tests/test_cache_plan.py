@@ -41,3 +41,15 @@ def test_long_prompts_without_a_prefix_are_not_refused():
                num_pages=4096, **heads(96, 8, 128))
     assert call(ATTN, **big) == DEVICE
     assert call(ATTN, **big, workspace=None, workspace_bytes=0) == DEVICE
+
+
+def test_rows_that_one_join_holds():
+    """Parts of 2^24 rows and more: a wave a row (two with 512 channels), 2^32 threads at most."""
+    step = lambda n, **kw: call(ATTN, tokens=n, num_seqs=n, num_pages=1 << 20, table_width=1, **kw)
+    one = heads(128, 8, 128)
+    assert step(1 << 17, **one) == DEVICE and step(1 << 18, **one) == DEVICE
+    assert step((1 << 19) - 1, **one) == DEVICE  # 2^26 rows less one token's
+    assert step(1 << 19, **one) == UNSUP
+    latent = {**LATENT, "q_heads": 64, "q_stride": 64 * 576, "out_stride": 64 * 512}
+    assert step(1 << 18, **latent) == DEVICE and step((1 << 19) - 1, **latent) == DEVICE
+    assert step(1 << 19, **latent) == UNSUP
