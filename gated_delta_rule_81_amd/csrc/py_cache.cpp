@@ -52,6 +52,13 @@ int32_t size32(int64_t n) {
     return (int32_t)n;
 }
 
+// Other Python threads run while this lives: the allocations and the launches, and in debug mode the
+// wait for the stream, touch no Python object.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // What every tensor of a call shares.
 struct Kind {
     c10::Device device;
@@ -155,13 +162,18 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *stream = PyLong_AsVoidPtr(a[0]);
         must(!PyErr_Occurred());
         at::Tensor out;
-        if (q) out = at::empty({T, hq, d}, k->options());
-        const int status = append_fn(
-            pointer(q), pointer(k), pointer(v), static_cast<const float *>(pointer(table)),
-            static_cast<const int32_t *>(pointer(positions)), s.table, s.lens, s.cu,
-            q ? out.data_ptr() : nullptr, pointer(kc), pointer(vc), size32(T), s.n, size32(hq),
-            size32(H), size32(d), size32(rot), (int32_t)at_channel, size32(table_rows), c.pages, c.size,
-            s.width, qs, ks, vs, q ? hq * d : 0, c.page, c.token, c.head, interleaved, kind.code, stream);
+        int status;
+        {
+            const Unlocked unlocked;
+            if (q) out = at::empty({T, hq, d}, k->options());
+            status = append_fn(
+                pointer(q), pointer(k), pointer(v), static_cast<const float *>(pointer(table)),
+                static_cast<const int32_t *>(pointer(positions)), s.table, s.lens, s.cu,
+                q ? out.data_ptr() : nullptr, pointer(kc), pointer(vc), size32(T), s.n, size32(hq),
+                size32(H), size32(d), size32(rot), (int32_t)at_channel, size32(table_rows), c.pages,
+                c.size, s.width, qs, ks, vs, q ? hq * d : 0, c.page, c.token, c.head, interleaved,
+                kind.code, stream);
+        }
         return result(status, out, nullptr);
     } catch (...) {
         PyErr_Clear();
@@ -195,21 +207,26 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int want = PyObject_IsTrue(a[11]);
         void *stream = PyLong_AsVoidPtr(a[0]);
         must(!PyErr_Occurred() && dv > 0 && dv <= INT32_MAX && want >= 0);
-        const int64_t need =
-            workspace_fn(size32(T), s.n, size32(hq), size32(H), size32(d), (int32_t)dv, c.size, s.width,
-                         size32(P), kind.code);
-        must(need >= 0);
-        const at::Tensor out = at::empty({T, hq, dv}, q->options());
-        at::Tensor lse, workspace;
-        if (want) lse = at::empty({T, hq}, q->options().dtype(at::kFloat));
-        if (need) workspace = at::empty({need}, q->options().dtype(at::kByte));
-        const int status = attn_fn(
-            pointer(q), pointer(kc), pointer(vc), s.table, s.lens,
-            static_cast<const int32_t *>(pointer(pages)), static_cast<const int32_t *>(pointer(length)),
-            s.cu, out.data_ptr(), want ? static_cast<float *>(lse.data_ptr()) : nullptr, size32(T), s.n,
-            size32(hq), size32(H), size32(d), (int32_t)dv, c.pages, c.size, s.width, size32(P), qs,
-            hq * dv, c.page, c.token, c.head, (float)scale, kind.code,
-            need ? workspace.data_ptr() : nullptr, need, stream);
+        at::Tensor out, lse, workspace;
+        int status;
+        {
+            const Unlocked unlocked;
+            const int64_t need =
+                workspace_fn(size32(T), s.n, size32(hq), size32(H), size32(d), (int32_t)dv, c.size,
+                             s.width, size32(P), kind.code);
+            must(need >= 0);
+            out = at::empty({T, hq, dv}, q->options());
+            if (want) lse = at::empty({T, hq}, q->options().dtype(at::kFloat));
+            if (need) workspace = at::empty({need}, q->options().dtype(at::kByte));
+            status = attn_fn(
+                pointer(q), pointer(kc), pointer(vc), s.table, s.lens,
+                static_cast<const int32_t *>(pointer(pages)),
+                static_cast<const int32_t *>(pointer(length)), s.cu, out.data_ptr(),
+                want ? static_cast<float *>(lse.data_ptr()) : nullptr, size32(T), s.n, size32(hq),
+                size32(H), size32(d), (int32_t)dv, c.pages, c.size, s.width, size32(P), qs, hq * dv,
+                c.page, c.token, c.head, (float)scale, kind.code, need ? workspace.data_ptr() : nullptr,
+                need, stream);
+        }
         return result(status, out, &lse);
     } catch (...) {
         PyErr_Clear();
