@@ -208,7 +208,8 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[t
     (out [T, Hq, v_dim], lse [T, Hq] fp32, the log of each token's sum of
     exponentials, or None): 0 and -inf where a token sees nothing.
     """
-    if out is None and lse is None and workspace is None and _on_current_device(q) and q.dim() == 3:
+    if (out is None and lse is None and workspace is None and _on_current_device(q) and q.dim() == 3
+            and q.shape[-1]):
         d = q.shape[-1]
         done = cache_calls().attention(
             _stream(q.get_device()), q, k_cache, v_cache, page_table, lens, prefix_pages, prefix_len,
@@ -220,6 +221,8 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[t
             return done[1], done[2]
     dt = _dtype_of_rows(q, "q")
     T, hq, d = q.shape
+    if not d:
+        raise ValueError("q: a head has no channels")
     dev, dtype = q.device, q.dtype
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages, page_size, heads, d]")
