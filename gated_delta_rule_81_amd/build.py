@@ -79,16 +79,21 @@ def _calls(verbose: bool) -> None:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link ``libkda.so``; returns its path."""
+    """Compile every source and link ``libkda.so``; returns its path.  Where the
+    module beside it cannot be built, the library is there all the same, no older module
+    is left to call it, and the error is raised."""
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
         calls = pool.submit(_calls, verbose)
         objs = list(pool.map(lambda s: _compile(s, verbose), SOURCES))
-        calls.result()
     tmp = LIB + ".tmp"
     subprocess.run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs],
                    check=True, capture_output=not verbose)
     os.replace(tmp, LIB)
+    if calls.exception() is not None:
+        if os.path.exists(CALLS):
+            os.remove(CALLS)
+        raise calls.exception()
     return LIB
 
 
