@@ -195,8 +195,8 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[t
                      output_lse: bool = False
                      ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Softmax attention of the new tokens of a batch of sessions over a prefix
-    that they share, read once for all of them, and each session's own tokens up
-    to the new one itself (``kda_prefix_attn_fwd``).
+    that they share (read once for every 128 of their rows) and each session's own
+    tokens up to the new one itself (``kda_prefix_attn_fwd``).
 
     q: [T, Hq, d] (may be a slice of wider rows), Hq a multiple of the cache's
     heads, whose head j query heads Hq / H * j .. read; caches, page_table, lens
@@ -206,7 +206,8 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[t
     or 576 with v_cache None and v_dim 512 (bfloat16): the values are then the
     first 512 channels of the keys.  ``scale`` is d ** -0.5 by default.  Returns
     (out [T, Hq, v_dim], lse [T, Hq] fp32, the log of each token's sum of
-    exponentials, or None): 0 and -inf where a token sees nothing.
+    exponentials, or None): 0 and -inf where a token sees nothing, be it that the
+    lengths are zero or that no page it could see is there.
     """
     if (out is None and lse is None and workspace is None and _on_current_device(q) and q.dim() == 3
             and q.shape[-1]):

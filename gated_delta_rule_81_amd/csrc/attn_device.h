@@ -109,6 +109,10 @@ template <> struct AttnMma<bf16> {
             return {__builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7)};
         }
     };
+    // Rounded once, by at most 2^-8 of each: an output is off by 2^-8 of sum p |v| at most beside
+    // its own rounding (2.3e-3 of it on average against 1.7e-3).  A second part of what that leaves
+    // out and a product more for it cost prompts 634 to 930 us, drafts 173 to 241, latent rows 170 to
+    // 201, and of few rows alone 256K 208 to 213, 256 sessions behind 16K 271 to 289.
     __device__ static Prob prob(const f32x16 &s, int step) {
         Prob p;
 #pragma unroll

@@ -16,7 +16,8 @@ struct Sessions {
     int32_t num, each, tokens, width;  // width: columns of the page table
 };
 
-// x / d for 0 <= x < 2^31 as a product's upper half and two shifts.
+// x / d for 0 <= x < 2^31 as a product's upper half and two shifts (division by an invariant
+// integer, Granlund and Montgomery 1994).
 struct Divisor {
     uint32_t mul, sh1, sh2;
     Divisor() = default;

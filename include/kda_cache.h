@@ -5,9 +5,11 @@
  *
  *   - new keys and values appended to the cache, rotated by position on the way
  *     (kda_cache_append);
- *   - attention of a batch of sessions over a prefix that all of them share, read
- *     once for all, and each session's own tokens (kda_prefix_attn_*): single
- *     tokens, a few at a time, or prompts.
+ *   - attention of a batch of sessions over a prefix that all of them share and
+ *     each session's own tokens (kda_prefix_attn_*): single tokens, a few at a
+ *     time, or prompts.  The prefix is read once for every 128 rows (tokens x heads
+ *     of a group): of all sessions together, or, where a session has that many on
+ *     average, of each.
  *
  * Conventions shared by both (those of kda_layer.h otherwise):
  *   - Cache: num_pages pages of page_size tokens of kv_heads heads of head_dim
@@ -87,8 +89,10 @@ int kda_cache_append(const void *q, const void *k, const void *v, const float *t
  *   lse          [tokens, q_heads] or NULL    fp32
  *   prefix_pages [prefix_width] int32, prefix_len [1] int32 (prefix_width 0: no
  *                prefix, neither is read); a prefix_len over the pages counts as theirs
- * A token that sees nothing gets out = 0 and lse = -inf.  What a token does not
- * see never reaches it, NaN and infinities included.  Scores, sums and the output
+ * A token that sees nothing, because no length or no page shows it anything, gets
+ * out = 0 and lse = -inf; one whose scores are all -inf gets NaN and -inf, as the
+ * formula has it.  What a token does not see never reaches it, NaN and infinities
+ * included.  Scores, sums and the output
  * are held in fp32; bf16: each exp(..) enters its product with v rounded to bf16
  * once, the sum of them does not.
  *
